@@ -54,7 +54,7 @@ class DecState(ctypes.Structure):
                 ("internal", ctypes.c_void_p)]
 
 
-_P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_P, _I, _F, _S, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
 _SIGNATURES = {
     "dec_last_error": (ctypes.c_char_p, []),
     "dec_version": (ctypes.c_char_p, []),
@@ -69,6 +69,13 @@ _SIGNATURES = {
     "dec_lmhead_workspace_size": (_S, [_I]),
     "dec_lmhead_argmax": (_I, [_P, _P, _F, _P, _P, _P, _P, _S, _I, _I, _I, _P]),
     "dec_select_tokens": (_I, [_P, _P, _I, _F, _F, _I, _F, _P, _P, _I, _I, _P]),
+    "dec_kv4_store": (_I, [_P, _P, _I, _L, _L, _L, _I, _I, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "dec_kv4_load": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _L, _L, _L, _I, _I, _I, _I, _I, _P]),
+    "dec_long_attn_workspace_size": (_S, [_I, _I, _I]),
+    "dec_kv4_decode_attn": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _S, _I, _I, _I, _I, _I, _I, _P]),
+    "dec_block_bounds": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P]),
+    "dec_select_blocks": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "dec_block_decode_attn": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _S, _I, _I, _I, _I, _I, _P]),
     "dec_state_workspace_size": (_S, [ctypes.POINTER(DecModel), _I, _I]),
     "dec_state_init": (_I, [ctypes.POINTER(DecModel), ctypes.POINTER(DecState), _P]),
     "dec_state_release": (_I, [ctypes.POINTER(DecState)]),
@@ -221,6 +228,164 @@ def dec_select_tokens(logits, token_out, u=None, prev_tokens=None, repetition_pe
     _check(lib().dec_select_tokens(_ptr(logits, _f32, "logits"), _ptr(prev_tokens, _i32, "prev_tokens"), n_prev,
                                    repetition_penalty, temperature, top_k, top_p, _ptr(u, _f32, "u"),
                                    _ptr(token_out, _i32, "token_out"), B, V, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- long caches
+
+BLOCK_KEYS = 64  # keys of a selectable block
+_f16, _u8 = torch.float16, torch.uint8
+
+
+def _expect(ok: bool, what: str):
+    if not ok:
+        raise DecError(DEC_EINVAL, what)
+
+
+def _on_device(dev, stream):
+    """The stream's handle for tensors on ``dev``; the caller has made ``dev`` current."""
+    if isinstance(stream, torch.cuda.Stream):
+        _expect(stream.device == dev, f"the stream is on {stream.device}, the tensors are on {dev}")
+        return stream.cuda_stream
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else int(stream)
+
+
+def _gpu(t, dtype, shape, dev, name):
+    """Pointer of a contiguous tensor of this dtype and shape on CUDA device ``dev``."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        _expect(t.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        _expect(t.device == dev, f"{name} is on {t.device}, the other tensors are on {dev}")
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _run(dev, stream, name, *args):
+    """Calls the library on the tensors' device, whichever device is current."""
+    _expect(dev.type == "cuda", f"the tensors must be on a CUDA device, not on {dev}")
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, _on_device(dev, stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _on_device(dev, stream))
+    if rc != DEC_OK:
+        _check(rc)
+
+
+def _kv4(k_codes, k_params, v_codes, v_params):
+    """Pointers and sizes of a 4-bit cache."""
+    _expect(k_codes.dim() == 4 and k_params.dim() == 5, "codes must be [B, Hkv, S_max, D/2], params "
+                                                        "[B, Hkv, S_max, D/group, 2]")
+    B, Hkv, S, half = k_codes.shape
+    NG = k_params.shape[3]
+    D = 2 * half
+    _expect(NG >= 1 and D % NG == 0, f"{NG} groups do not divide head_dim {D}")
+    dev, cs, ps = k_codes.device, k_codes.shape, (B, Hkv, S, NG, 2)
+    return (_gpu(k_codes, _u8, cs, dev, "k_codes"), _gpu(k_params, _f16, ps, dev, "k_params"),
+            _gpu(v_codes, _u8, cs, dev, "v_codes"), _gpu(v_params, _f16, ps, dev, "v_params")), \
+        (B, Hkv, D, D // NG, S), dev
+
+
+def _rows(k, v, B, Hkv, D, dev, names):
+    """Pointers, type and strides of K and V rows [B, T, Hkv, D], strided alike."""
+    for t, name in zip((k, v), names):
+        if t.dtype != _f32 and t.dtype != _bf16:
+            raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+        _expect(t.dim() == 4 and t.shape[0] == B and t.shape[2:] == (Hkv, D) and (t.shape[1] == 0 or t.stride(3) == 1),
+                f"{name} must be rows [{B}, T, {Hkv}, {D}] with contiguous values, got {tuple(t.shape)} "
+                f"strided {t.stride()}")
+        _expect(t.device == dev, f"{name} is on {t.device}, the cache is on {dev}")
+    _expect(k.dtype == v.dtype and k.shape == v.shape, f"{names[0]} and {names[1]} must be of one type and shape")
+    st = tuple(s if n > 1 else 0 for s, n in zip(k.stride()[:3], k.shape))
+    _expect(st == tuple(s if n > 1 else 0 for s, n in zip(v.stride()[:3], v.shape)),
+            f"{names[0]} and {names[1]} must be strided alike")
+    return k.data_ptr(), v.data_ptr(), int(k.dtype == _bf16), st
+
+
+def dec_kv4_store(k, v, pos, k_codes, k_params, v_codes, v_params, tokens=None, lens=None, from_cache: bool = False,
+                  stream=None):
+    """Quantises K and V rows (views [B, T, Hkv, D], float32 or bf16) into the 4-bit cache at slots
+    ``pos[b] ..``.  ``from_cache``: the rows are a cache's, indexed by slot (``cache.transpose(1, 2)``), and
+    ``tokens`` of them are taken from ``pos[b]`` on.  ``lens`` (int32 [B]): tokens of each row, at most ``tokens``."""
+    held, (B, Hkv, D, group, S), dev = _kv4(k_codes, k_params, v_codes, v_params)
+    kp, vp, bf16, st = _rows(k, v, B, Hkv, D, dev, ("k", "v"))
+    T = k.shape[1] if tokens is None else int(tokens)
+    _run(dev, stream, "dec_kv4_store", kp, vp, bf16, *st, int(from_cache), k.shape[1],
+         _gpu(pos, _i32, (B,), dev, "pos"), None if lens is None else _gpu(lens, _i32, (B,), dev, "lens"), T, *held, B, Hkv,
+         D, group, S)
+
+
+def dec_kv4_load(k_codes, k_params, v_codes, v_params, pos, k_out, v_out, lens=None, stream=None):
+    """Reads slots ``pos[b] ..`` of the 4-bit cache into ``k_out`` and ``v_out`` (views [B, T, Hkv, D], float32 or
+    bf16); rows ``t >= lens[b]`` are left as they are."""
+    held, (B, Hkv, D, group, S), dev = _kv4(k_codes, k_params, v_codes, v_params)
+    kp, vp, bf16, st = _rows(k_out, v_out, B, Hkv, D, dev, ("k_out", "v_out"))
+    _run(dev, stream, "dec_kv4_load", *held, _gpu(pos, _i32, (B,), dev, "pos"),
+         None if lens is None else _gpu(lens, _i32, (B,), dev, "lens"), k_out.shape[1], kp, vp, bf16, *st, B, Hkv, D, group, S)
+
+
+def long_attn_workspace_size(Hq, Hkv, D) -> int:
+    return int(lib().dec_long_attn_workspace_size(Hq, Hkv, D))
+
+
+def _long_ws(ws, Hq, Hkv, D, dev):
+    if ws is None:
+        need = long_attn_workspace_size(Hq, Hkv, D)
+        if need == 0:
+            raise DecError(DEC_EINVAL, lib().dec_last_error().decode())
+        return torch.empty(need, dtype=_u8, device=dev)
+    _expect(ws.device == dev and ws.is_contiguous(), f"ws must be contiguous memory on {dev}")
+    return ws
+
+
+def dec_kv4_decode_attn(q, k_codes, k_params, v_codes, v_params, pos, o, ws=None, stream=None):
+    """GQA decode attention over a 4-bit cache; returns the workspace, for the next call."""
+    held, (B, Hkv, D, group, S), dev = _kv4(k_codes, k_params, v_codes, v_params)
+    Hq = q.shape[1] if q.dim() == 3 else 0
+    ws = _long_ws(ws, Hq, Hkv, D, dev)
+    _run(dev, stream, "dec_kv4_decode_attn", _gpu(q, _f32, (B, Hq, D), dev, "q"), *held, _gpu(pos, _i32, (B,), dev, "pos"),
+         _gpu(o, _f32, (B, Hq, D), dev, "o"), ws.data_ptr(), ws.nbytes, B, Hq, Hkv, D, group, S)
+    return ws
+
+
+def dec_block_bounds(k_cache, pos, bounds, tokens: int = 1, stream=None):
+    """Channel bounds (bf16 [B, Hkv, ceil(S_max/64), 2, D]) of the blocks that slots
+    ``pos[b] .. pos[b] + tokens - 1`` of the bf16 key cache touch."""
+    _expect(k_cache.dim() == 4, "k_cache must be [B, Hkv, S_max, D]")
+    B, Hkv, S, D = k_cache.shape
+    dev = k_cache.device
+    _run(dev, stream, "dec_block_bounds", _gpu(k_cache, _bf16, k_cache.shape, dev, "k_cache"),
+         _gpu(pos, _i32, (B,), dev, "pos"), int(tokens),
+         _gpu(bounds, _bf16, (B, Hkv, (S + BLOCK_KEYS - 1) // BLOCK_KEYS, 2, D), dev, "bounds"), B, Hkv, D, S)
+
+
+def dec_select_blocks(q, bounds, pos, blocks, n_first: int = 1, n_last: int = 1, stream=None):
+    """Fills ``blocks`` (int32 [B, Hkv, n_select]) with the blocks of the largest score bounds, ascending, -1 behind
+    the last; the first ``n_first`` and last ``n_last`` blocks of a row are always among them."""
+    _expect(q.dim() == 3 and bounds.dim() == 5 and blocks.dim() == 3, "q must be [B, Hq, D], bounds "
+            "[B, Hkv, blocks, 2, D], blocks [B, Hkv, n_select]")
+    B, Hq, D = q.shape
+    Hkv, NB, n = bounds.shape[1], bounds.shape[2], blocks.shape[2]
+    dev = q.device
+    _run(dev, stream, "dec_select_blocks", _gpu(q, _f32, q.shape, dev, "q"),
+         _gpu(bounds, _bf16, (B, Hkv, NB, 2, D), dev, "bounds"), _gpu(pos, _i32, (B,), dev, "pos"),
+         _gpu(blocks, _i32, (B, Hkv, n), dev, "blocks"), n, int(n_first), int(n_last), B, Hq, Hkv, D, NB * BLOCK_KEYS)
+
+
+def dec_block_decode_attn(q, k_cache, v_cache, pos, blocks, o, ws=None, stream=None):
+    """GQA decode attention over the listed 64-key blocks of a bf16 cache; returns the workspace."""
+    _expect(q.dim() == 3 and k_cache.dim() == 4 and blocks.dim() == 3, "q must be [B, Hq, D], the caches "
+            "[B, Hkv, S_max, D], blocks [B, Hkv, n_select]")
+    B, Hkv, S, D = k_cache.shape
+    Hq, n = q.shape[1], blocks.shape[2]
+    dev = k_cache.device
+    ws = _long_ws(ws, Hq, Hkv, D, dev)
+    _run(dev, stream, "dec_block_decode_attn", _gpu(q, _f32, (B, Hq, D), dev, "q"),
+         _gpu(k_cache, _bf16, k_cache.shape, dev, "k_cache"), _gpu(v_cache, _bf16, k_cache.shape, dev, "v_cache"),
+         _gpu(pos, _i32, (B,), dev, "pos"), _gpu(blocks, _i32, (B, Hkv, n), dev, "blocks"), n,
+         _gpu(o, _f32, (B, Hq, D), dev, "o"), ws.data_ptr(), ws.nbytes, B, Hq, Hkv, D, S)
+    return ws
 
 
 # ----------------------------------------------------------------------------- model / state

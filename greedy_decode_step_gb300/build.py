@@ -14,8 +14,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdec.so")
 UNITS = ["api.cu", "gemv_qkv.cu", "gemv_glu.cu", "gemv_resid.cu", "gemv_head.cu", "attn.cu", "step.cu", "prefill.cu",
-         "select.cu", "tcgemm.cu"]
-HEADERS = ["dec_common.cuh", "dec_kernels.cuh", "dec_attn.cuh", "dec_step.cuh", "dec_launch.cuh"]
+         "select.cu", "tcgemm.cu", "kv4.cu", "long_attn.cu", "blocks.cu", "long_api.cu"]
+HEADERS = ["dec_common.cuh", "dec_kernels.cuh", "dec_attn.cuh", "dec_step.cuh", "dec_launch.cuh", "dec_long.cuh",
+           "dec_host.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

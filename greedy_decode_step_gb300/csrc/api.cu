@@ -13,7 +13,9 @@
 #include <mutex>
 #include <string>
 
+#include "dec_host.cuh"
 #include "dec_launch.cuh"
+#include "dec_long.cuh"
 #include "libdec.h"
 
 using namespace dec;
@@ -167,6 +169,8 @@ int device_info(DeviceInfo** out) {
     DEC_CUDA(allow_smem_step());
     DEC_CUDA(allow_smem_tcgemm());
     DEC_CUDA(allow_smem_select());
+    DEC_CUDA(allow_smem_long());
+    DEC_CUDA(allow_smem_blocks());
     DEC_CUDA(prefer_max_carveout(add_rmsnorm_kernel));
     DEC_CUDA(prefer_max_carveout(advance_kernel));
     DEC_CUDA(prefer_max_carveout(set_tokens_kernel));
@@ -175,6 +179,29 @@ int device_info(DeviceInfo** out) {
   *out = &d;
   return DEC_OK;
 }
+
+}  // namespace
+
+// Services for the other units with entry points (dec_host.cuh).
+int dec::host_fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return code;
+}
+
+int dec::host_device(int* sms, uint32_t** err) {
+  DeviceInfo* d;
+  DEC_TRY(device_info(&d));
+  *sms = d->sms;
+  *err = d->err;
+  return DEC_OK;
+}
+
+namespace {
 
 // ------------------------------------------------------------------------------- checks
 

@@ -1,0 +1,842 @@
+// Decode attention over a long cache: a cache held in 4 bits, or the listed
+// 64-key blocks of a bf16 cache.
+//
+//   o[h] = sum_j softmax_j(q[h] . k_j / sqrt(D)) v_j
+//
+// One pass over the keys with a running maximum and sum.  The keys of all
+// (row, KV head) items are cut into units (32 keys of the 4-bit cache, 16 of
+// the bf16 one), laid end to end, and every CTA takes an equal run of them;
+// warp w of a CTA takes the run's units w, w + 8, ...  Each warp has a ring of
+// its own in shared memory that it fills with cp.async, so no warp waits for
+// another inside an item.  At an item's end the warps' states are merged; an
+// item cut between CTAs leaves one partial per CTA, which a second, small
+// launch joins (it starts by programmatic launch while the first one runs).
+//
+// Tensor cores (mma.sync m16n8k16): a decode step has few query rows per KV
+// head, so the keys take the M side and the N side holds 4 query heads twice,
+// the value's upper part and its remainder in neighbouring columns.  For up to
+// 4 heads per group one instruction so does the work of both parts, and each
+// lane holds the score of one head: S^T = K Q^T (keys x heads),
+// O^T = V^T P^T (dims x heads), P^T transposed in registers (movmatrix).
+//
+// 4-bit operands.  A masked nibble pair (w & 0x000F000F) read as two halves is
+// c * 2^-24 exactly (a subnormal), the next nibble (w & 0x00F000F0) is
+// 16 c * 2^-24: the scores need one logic operation for two codes, the powers
+// of two sit in the query operand, and each group's sum is scaled in fp32 by
+// its (s, z).  For the values the codes are centred, (1024 + c) - 1032 in half
+// arithmetic, exactly: uncentred ones would sum to numbers far above the
+// result.  Each key's s multiplies the probability before it is rounded to
+// two halves; a power of two C per warp, from the largest s seen, keeps that
+// product near the top of the half range.  The z part is a plain fp32 sum.
+#include <cuda_fp16.h>
+
+#include "dec_launch.cuh"
+#include "dec_long.cuh"
+
+namespace dec {
+namespace {
+
+constexpr int kW = 8;                 // warps of a CTA
+constexpr int kThreads = 32 * kW;
+constexpr int kMaxG = 16;             // query heads per KV head
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(live ? BYTES : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// D += A (16x16 half, row) * B (16x8 half, col), fp32 accumulate
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float half_lo(uint32_t w) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(w & 0xFFFFu)));
+}
+__device__ __forceinline__ float half_hi(uint32_t w) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16)));
+}
+// The leading 11 significant bits of x: exact in half while |x| is at least
+// 2^-14 and below 2^16; the conversion rounds smaller ones (to 2^-25).
+__device__ __forceinline__ float top11(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
+
+// ----------------------------------------------------------------------------- formats
+
+// 4-bit cache: a unit of 32 keys, rows of D/2 bytes.
+template <int D_, int GROUP>
+struct Kv4 {
+  static constexpr bool kQuant = true;
+  static constexpr int D = D_, NG = D / GROUP, kUnit = 32;
+  static constexpr int kRow = D / 2, kChunks = kRow / 16, kQWords = D / 32 * 4;  // 16-byte chunks: 32 dims each
+  static constexpr int kKOff = 0, kVOff = kUnit * kRow, kKpOff = 2 * kUnit * kRow, kVpOff = kKpOff + kUnit * NG * 4;
+  static constexpr int kStage = kVpOff + kUnit * NG * 4;
+  // chunk j of row r: the eight rows of an ldmatrix phase fall on distinct banks
+  static __device__ __forceinline__ uint32_t at(int r, int j) {
+    return static_cast<uint32_t>(r * kRow + ((j ^ (kChunks == 4 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4));
+  }
+};
+
+// bf16 cache: a unit of 16 keys, rows of 2 D bytes.
+template <int D_>
+struct Bf16 {
+  static constexpr bool kQuant = false;
+  static constexpr int D = D_, NG = 1, kUnit = 16;
+  static constexpr int kRow = 2 * D, kChunks = kRow / 16, kQWords = D / 16 * 2;
+  static constexpr int kKOff = 0, kVOff = kUnit * kRow, kStage = 2 * kUnit * kRow;
+  static __device__ __forceinline__ uint32_t at(int r, int j) {
+    return static_cast<uint32_t>(r * kRow + ((j ^ (r & 7)) << 4));
+  }
+};
+
+// ----------------------------------------------------------------------------- plan
+
+// Units of all items end to end: row b's Hkv items hold pre[b] .. pre[b + 1].
+// CTA c of n takes units [T c / n, T (c + 1) / n).
+__device__ __forceinline__ int run_start(int c, int n, int T) {
+  return static_cast<int>(static_cast<long long>(T) * c / n);
+}
+// the CTA whose run holds unit x
+__device__ __forceinline__ int run_of(int x, int n, int T) {
+  return static_cast<int>(((static_cast<long long>(x) + 1) * n - 1) / T);
+}
+// CTAs that work: each warp of a CTA gets a unit before the next CTA does
+__device__ __forceinline__ int runs(int n_cta, int T) { return min(n_cta, (T + kW - 1) / kW); }
+
+template <class F>
+__device__ __forceinline__ int row_units(const LongAttnArgs& a, int p) {
+  if (p < 0 || p >= a.S_max) return 0;
+  if constexpr (F::kQuant) return (p + F::kUnit) / F::kUnit;
+  else return a.n_select * (kBlockKeys / F::kUnit);
+}
+
+// pre[0 .. B] by one warp.
+template <class F>
+__device__ __forceinline__ void prefix_rows(const LongAttnArgs& a, int* pre, bool report) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  if (lane == 0) pre[0] = 0;
+  for (int base = 0; base < a.B; base += 32) {
+    const int b = base + lane;
+    int v = 0;
+    if (b < a.B) {
+      const int p = a.pos[b];
+      v = row_units<F>(a, p) * a.Hkv;
+      if (report && (p < -1 || p >= a.S_max)) atomicOr(a.err, kErrPosRange);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (b < a.B) pre[b + 1] = carry + v;
+    carry += __shfl_sync(0xffffffffu, v, 31);
+  }
+}
+
+struct Item {
+  int b, h;        // row, KV head
+  int start, end;  // its units
+  int len;         // keys of the row
+};
+
+// The item that holds unit t.
+__device__ __forceinline__ Item item_at(const LongAttnArgs& a, const int* pre, int t) {
+  int lo = 0, hi = a.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  Item it;
+  it.b = lo;
+  const int per = (pre[lo + 1] - pre[lo]) / a.Hkv;
+  it.h = (t - pre[lo]) / per;
+  it.start = pre[lo] + it.h * per;
+  it.end = it.start + per;
+  it.len = a.pos[lo] + 1;
+  return it;
+}
+
+// ----------------------------------------------------------------------------- query operand
+
+// Heads 4 nt .. 4 nt + 3 of a group as B fragments, by one warp.  Lane (g, c)
+// holds column g: head g / 2, its upper part (g even) or the remainder.
+//  * 4-bit: per chunk j four half pairs that meet the nibble pairs (0, 4),
+//    (1, 5), (2, 6), (3, 7) of word c, dims 32 j + 8 c + nibble, the odd
+//    nibbles' (16 times larger) with a factor 1/16.  The head is scaled by a
+//    power of two to [2^13, 2^14); f takes it back along with the codes'
+//    2^-24.  qs: each group's sum of q, for the z part.
+//  * bf16: per 16 dims two pairs, as the instruction lays them out.
+template <class F>
+__device__ __forceinline__ void stage_query(const float* q, int G, int nt, float scale_log2, uint32_t* words, float* f,
+                                            float* qs) {
+  constexpr int D = F::D;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int head = 4 * nt + (g >> 1);
+  const bool rest = g & 1;
+  if constexpr (F::kQuant) {
+    constexpr int NJ = D / 32, NG = F::NG;
+    float v[NJ][8];
+    float mx = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (head < G) {
+        const float4* p = reinterpret_cast<const float4*>(q + static_cast<size_t>(head) * D + 32 * j + 8 * c);
+        x = __ldg(p);
+        y = __ldg(p + 1);
+      }
+      v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+      v[j][4] = y.x, v[j][5] = y.y, v[j][6] = y.z, v[j][7] = y.w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[j][i]));
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+    const int e = mx > 0.f ? min(max(13 - ex, -100), 100) : 0;
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = gr * NJ / NG; j < (gr + 1) * NJ / NG; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += v[j][i];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (c == 0 && !rest) qs[head * 4 + gr] = s * scale_log2;
+    }
+    if (c == 0 && !rest) f[head] = __uint_as_float(static_cast<uint32_t>(127 + 24 - e) << 23) * scale_log2;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float k = (i & 1) ? up * 0.0625f : up;
+        const float x0 = v[j][i] * k, x1 = v[j][i + 4] * k;
+        const float h0 = top11(x0), h1 = top11(x1);
+        w[i] = rest ? pack_f16(x0 - h0, x1 - h1) : pack_f16(h0, h1);
+      }
+      *reinterpret_cast<uint4*>(words + ((nt * NJ + j) * 32 + lane) * 4) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    constexpr int NJ = D / 16;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      uint32_t w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float2 x = make_float2(0.f, 0.f);
+        if (head < G)
+          x = __ldg(reinterpret_cast<const float2*>(q + static_cast<size_t>(head) * D + 16 * j + 8 * i + 2 * c));
+        const uint32_t hi = pack_bf16(x.x, x.y);
+        w[i] = rest ? pack_bf16(x.x - bf16lo(hi), x.y - bf16hi(hi)) : hi;
+      }
+      *reinterpret_cast<uint2*>(words + ((nt * NJ + j) * 32 + lane) * 2) = make_uint2(w[0], w[1]);
+    }
+    if (c == 0 && !rest) f[head] = scale_log2;
+  }
+}
+
+// ----------------------------------------------------------------------------- one unit
+
+// A warp's running state.  Lane (g, c) of n-tile nt serves head 4 nt + c: m
+// the running maximum (log2 units; the same in the eight lanes of a head), mu
+// the value subtracted (0 while m is -inf), l and zs this lane's share of the
+// sums; o[nt][..][e] rows of O^T, columns (upper part, remainder) of the head.
+template <class F, int NT>
+struct State {
+  float o[NT][F::D / 16][4];
+  float m[NT], mu[NT], l[NT];
+  float zs[NT][F::NG];
+  float c, bound;  // 4-bit: factor on the scaled probabilities, every s seen is at most bound
+};
+
+template <class F, int NT>
+__device__ __forceinline__ void state_init(State<F, NT>& st) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < F::D / 16; ++i) st.o[nt][i][0] = st.o[nt][i][1] = st.o[nt][i][2] = st.o[nt][i][3] = 0.f;
+#pragma unroll
+    for (int g = 0; g < F::NG; ++g) st.zs[nt][g] = 0.f;
+    st.m[nt] = -INFINITY;
+    st.mu[nt] = st.l[nt] = 0.f;
+  }
+  st.c = 1.f;
+  st.bound = 0.f;
+}
+
+// NG (s, z) pairs of key r
+template <int NG>
+__device__ __forceinline__ void load_pairs(const unsigned char* base, int r, uint32_t (&w)[NG]) {
+  if constexpr (NG == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(base + r * 16);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else if constexpr (NG == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(base + r * 8);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(base + r * 4);
+  }
+}
+
+// New maxima and, for the 4-bit cache, a new bound on s: the state's sums go
+// over to them.  All 32 lanes; x: this lane's largest score per n-tile.
+template <class F, int NT>
+__device__ __forceinline__ void raise(State<F, NT>& st, const float (&x)[NT], float s_max) {
+  float ratio = 1.f;
+  if constexpr (F::kQuant) {
+    s_max = warp_max(s_max);
+    if (s_max > st.bound) {
+      const uint32_t e = __float_as_uint(s_max) >> 23;  // s_max in [2^(e-127), 2^(e-126))
+      st.bound = __uint_as_float((e + 1u) << 23);
+      const float c = __uint_as_float((127u + 14u + 127u - e) << 23);  // s c below 2^15
+      ratio = c / st.c;
+      st.c = c;
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float mx = x[nt];
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    mx = fmaxf(mx, st.m[nt]);
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    const float corr = ex2(st.m[nt] - mu);
+    st.m[nt] = mx;
+    st.mu[nt] = mu;
+    st.l[nt] *= corr;
+#pragma unroll
+    for (int g = 0; g < F::NG; ++g) st.zs[nt][g] *= corr;
+#pragma unroll
+    for (int i = 0; i < F::D / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.o[nt][i][e] *= corr * ratio;
+  }
+}
+
+// 32 keys of the 4-bit cache, of which the first nk count.
+template <class F, int NT>
+__device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t stage_addr, int nk, const uint32_t* words,
+                                         const float* fs, const float* qss, State<F, NT>& st) {
+  constexpr int NJ = F::D / 32, NG = F::NG, PER = NJ / NG;  // chunks per group
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int lrow = (lane & 7) + (lane & 8), lchunk = lane >> 4;
+  float s[NT][4];
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    uint32_t p0[NG], p1[NG];
+    load_pairs<NG>(stage + F::kKpOff, 16 * hh + g, p0);
+    load_pairs<NG>(stage + F::kKpOff, 16 * hh + g + 8, p1);
+    float acc[NT][NG][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) acc[nt][gr][0] = acc[nt][gr][1] = acc[nt][gr][2] = acc[nt][gr][3] = 0.f;
+#pragma unroll
+    for (int jj = 0; jj < NJ; jj += 2) {
+      uint32_t r[4];
+      ldsm_x4(r, stage_addr + F::kKOff + F::at(16 * hh + lrow, jj + lchunk));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int j = jj + t, gr = j / PER;
+        const uint32_t w0 = r[2 * t], w1 = r[2 * t + 1], x0 = w0 >> 8, x1 = w1 >> 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 b = *reinterpret_cast<const uint4*>(words + ((nt * NJ + j) * 32 + lane) * 4);
+          mma_f16_16816(acc[nt][gr], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x, b.y);
+          mma_f16_16816(acc[nt][gr], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u, b.z, b.w);
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float f = fs[4 * nt + c];
+      float a0 = 0.f, a1 = 0.f, z0 = 0.f, z1 = 0.f;
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        const float qs = qss[(4 * nt + c) * 4 + gr];
+        const float sc0 = half_lo(p0[gr]), sc1 = half_lo(p1[gr]);
+        a0 = fmaf(sc0, acc[nt][gr][0] + acc[nt][gr][1], a0);
+        a1 = fmaf(sc1, acc[nt][gr][2] + acc[nt][gr][3], a1);
+        z0 = fmaf(fmaf(-8.f, sc0, half_hi(p0[gr])), qs, z0);
+        z1 = fmaf(fmaf(-8.f, sc1, half_hi(p1[gr])), qs, z1);
+      }
+      s[nt][2 * hh] = fmaf(a0, f, z0);
+      s[nt][2 * hh + 1] = fmaf(a1, f, z1);
+    }
+  }
+  uint32_t vp[4][NG];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load_pairs<NG>(stage + F::kVpOff, 8 * i + g, vp[i]);
+  if (nk < 32) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (8 * i + g >= nk) s[nt][i] = -INFINITY;
+  }
+  // a larger score or scale than before anywhere in the warp?
+  float mx[NT];
+  bool more = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    mx[nt] = fmaxf(fmaxf(s[nt][0], s[nt][1]), fmaxf(s[nt][2], s[nt][3]));
+    more |= mx[nt] > st.m[nt];
+  }
+  __half2 sm = *reinterpret_cast<const __half2*>(&vp[0][0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) sm = __hmax2(sm, *reinterpret_cast<const __half2*>(&vp[i][gr]));
+  const float s_max = __low2float(sm);
+  more |= s_max > st.bound;
+  if (__any_sync(0xffffffffu, more)) raise<F, NT>(st, mx, s_max);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[nt][i] = ex2(s[nt][i] - st.mu[nt]);
+    st.l[nt] += (s[nt][0] + s[nt][1]) + (s[nt][2] + s[nt][3]);
+  }
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+    for (int jj = 0; jj < NJ; jj += 2) {
+      uint32_t r[4], b0[NT], b1[NT];
+      ldsm_x4_trans(r, stage_addr + F::kVOff + F::at(16 * hh + lrow, jj + lchunk));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int j = jj + t, gr = j / PER;
+        if (j % PER == 0) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float q0 = s[nt][2 * hh], q1 = s[nt][2 * hh + 1];
+            const float x0 = q0 * (half_lo(vp[2 * hh][gr]) * st.c), x1 = q1 * (half_lo(vp[2 * hh + 1][gr]) * st.c);
+            st.zs[nt][gr] = fmaf(q0, half_hi(vp[2 * hh][gr]), fmaf(q1, half_hi(vp[2 * hh + 1][gr]), st.zs[nt][gr]));
+            const float h0 = top11(x0), h1 = top11(x1);
+            b0[nt] = movmatrix_trans(pack_f16(h0, x0 - h0));
+            b1[nt] = movmatrix_trans(pack_f16(h1, x1 - h1));
+          }
+        }
+        const uint32_t w0 = r[2 * t], w1 = r[2 * t + 1], y0 = w0 >> 8, y1 = w1 >> 8;
+        const uint32_t e0 = add_f16x2((w0 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);  // c - 8
+        const uint32_t e1 = add_f16x2((w0 & 0x00F000F0u) | 0x64006400u, 0xE480E480u);  // 16 (c - 8)
+        const uint32_t e2 = add_f16x2((w1 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
+        const uint32_t e3 = add_f16x2((w1 & 0x00F000F0u) | 0x64006400u, 0xE480E480u);
+        const uint32_t f0 = add_f16x2((y0 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
+        const uint32_t f1 = add_f16x2((y0 & 0x00F000F0u) | 0x64006400u, 0xE480E480u);
+        const uint32_t f2 = add_f16x2((y1 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
+        const uint32_t f3 = add_f16x2((y1 & 0x00F000F0u) | 0x64006400u, 0xE480E480u);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16_16816(st.o[nt][2 * j], e0, e1, e2, e3, b0[nt], b1[nt]);
+          mma_f16_16816(st.o[nt][2 * j + 1], f0, f1, f2, f3, b0[nt], b1[nt]);
+        }
+      }
+    }
+  }
+}
+
+// 16 keys of a bf16 cache, of which the first nk count.
+template <class F, int NT>
+__device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uint32_t* words, const float* fs,
+                                          State<F, NT>& st) {
+  constexpr int NJ = F::D / 16;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  float acc[NT][2][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[nt][0][e] = acc[nt][1][e] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    uint32_t r[4];
+    ldsm_x4(r, stage_addr + F::kKOff + F::at(lane & 15, 2 * j + (lane >> 4)));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint2 b = *reinterpret_cast<const uint2*>(words + ((nt * NJ + j) * 32 + lane) * 2);
+      mma_bf16_16816(acc[nt][j & 1], r, b.x, b.y);
+    }
+  }
+  float s[NT][2], mx[NT];
+  bool more = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float f = fs[4 * nt + c];
+    s[nt][0] = ((acc[nt][0][0] + acc[nt][1][0]) + (acc[nt][0][1] + acc[nt][1][1])) * f;
+    s[nt][1] = ((acc[nt][0][2] + acc[nt][1][2]) + (acc[nt][0][3] + acc[nt][1][3])) * f;
+    if (g >= nk) s[nt][0] = -INFINITY;
+    if (g + 8 >= nk) s[nt][1] = -INFINITY;
+    mx[nt] = fmaxf(s[nt][0], s[nt][1]);
+    more |= mx[nt] > st.m[nt];
+  }
+  if (__any_sync(0xffffffffu, more)) raise<F, NT>(st, mx, 0.f);
+  uint32_t b0[NT], b1[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float x0 = ex2(s[nt][0] - st.mu[nt]), x1 = ex2(s[nt][1] - st.mu[nt]);
+    st.l[nt] += x0 + x1;
+    const uint32_t h = pack_bf16(x0, x1);
+    const uint32_t l = pack_bf16(x0 - bf16lo(h), x1 - bf16hi(h));
+    b0[nt] = movmatrix_trans(__byte_perm(h, l, 0x5410));
+    b1[nt] = movmatrix_trans(__byte_perm(h, l, 0x7632));
+  }
+  const int vrow = (lane & 7) + ((lane >> 4) << 3), vchunk = (lane >> 3) & 1;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    uint32_t r[4];
+    ldsm_x4_trans(r, stage_addr + F::kVOff + F::at(vrow, 2 * j + vchunk));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(st.o[nt][j], r, b0[nt], b1[nt]);
+  }
+}
+
+// ----------------------------------------------------------------------------- kernel
+
+template <class F, int STAGES>
+struct Smem {
+  static __host__ __device__ uint32_t ring(int B, int G, int NT) { return obuf(B, NT) + kW * G * (F::D + 4) * 4; }
+  static __host__ __device__ uint32_t words(int B) { return ((B + 1) * 4 + 127) / 128 * 128; }
+  static __host__ __device__ uint32_t f(int B, int NT) { return words(B) + NT * F::kQWords * 32 * 4; }
+  static __host__ __device__ uint32_t qs(int B, int NT) { return f(B, NT) + kMaxG * 4; }
+  static __host__ __device__ uint32_t ms(int B, int NT) { return qs(B, NT) + kMaxG * 4 * 4; }
+  static __host__ __device__ uint32_t ls(int B, int NT) { return ms(B, NT) + kW * kMaxG * 4; }
+  static __host__ __device__ uint32_t obuf(int B, int NT) { return ls(B, NT) + kW * kMaxG * 4; }
+  static __host__ __device__ uint32_t bytes(int B, int G, int NT) {
+    return (ring(B, G, NT) + 127) / 128 * 128 + kW * STAGES * F::kStage;
+  }
+};
+
+template <class F, int NT, int STAGES>
+__global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
+    long_attn_kernel(const __grid_constant__ LongAttnArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  using L = Smem<F, STAGES>;
+  constexpr int D = F::D;
+  const int G = a.Hq / a.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int* pre = reinterpret_cast<int*>(smem);
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::words(a.B));
+  float* fs = reinterpret_cast<float*>(smem + L::f(a.B, NT));
+  float* qss = reinterpret_cast<float*>(smem + L::qs(a.B, NT));
+  float* ms = reinterpret_cast<float*>(smem + L::ms(a.B, NT));
+  float* ls = reinterpret_cast<float*>(smem + L::ls(a.B, NT));
+  float* obuf = reinterpret_cast<float*>(smem + L::obuf(a.B, NT));
+  unsigned char* ring = smem + (L::ring(a.B, G, NT) + 127) / 128 * 128 + warp * (STAGES * F::kStage);
+  const uint32_t ring_addr = smem_addr(ring);
+
+  pdl_launch_dependents();
+  if (warp == 0) prefix_rows<F>(a, pre, blockIdx.x == 0);
+  __syncthreads();
+  const int T = pre[a.B], n = runs(a.n_cta, T);
+  const int cta = blockIdx.x;
+  if (cta >= n) return;  // the same verdict in every thread
+  const int t0 = run_start(cta, n, T), t1 = run_start(cta + 1, n, T);
+
+  // ---- loads: this warp's units t0 + warp + kW k, in order
+  Item li = item_at(a, pre, t0);  // the item being loaded
+  int list_k = 0;                 // listed blocks: units list_k .. list_k + 31 of this warp have their ids in the lanes
+  int ids = 0, ids_next = 0;
+  auto fetch_ids = [&](int k) {   // lane i: the block of unit k + i of this warp
+    const int t = t0 + warp + kW * (k + lane);
+    if (t >= t1) return -1;
+    const Item it = item_at(a, pre, t);
+    const size_t base = (static_cast<size_t>(it.b) * a.Hkv + it.h) * a.n_select;
+    return __ldg(a.blocks + base + (t - it.start) / (kBlockKeys / F::kUnit));
+  };
+  if constexpr (!F::kQuant) {
+    ids = fetch_ids(0);
+    ids_next = fetch_ids(32);
+  }
+  int ring_nk[STAGES];  // keys of the units in flight
+  auto issue = [&](int k, int slot) -> int {
+    const int t = t0 + warp + kW * k;
+    int nk = 0;
+    if (t < t1) {
+      if (t >= li.end) li = item_at(a, pre, t);
+      int k0;
+      if constexpr (F::kQuant) {
+        k0 = (t - li.start) * F::kUnit;
+        nk = min(F::kUnit, li.len - k0);
+      } else {
+        if (k - list_k == 32) {
+          list_k += 32;
+          ids = ids_next;
+          ids_next = fetch_ids(list_k + 32);
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, k - list_k);
+        const bool bad = id < -1 || id > (a.S_max - 1) / kBlockKeys;
+        if (bad && lane == 0) atomicOr(a.err, kErrPosRange);
+        k0 = bad || id < 0 ? li.len : id * kBlockKeys + (t - li.start) % (kBlockKeys / F::kUnit) * F::kUnit;
+        nk = max(0, min(F::kUnit, li.len - k0));
+      }
+      if (nk > 0) {
+        const size_t row = (static_cast<size_t>(li.b) * a.Hkv + li.h) * a.S_max + k0;
+        const unsigned char* kb = static_cast<const unsigned char*>(a.k) + row * F::kRow;
+        const unsigned char* vb = static_cast<const unsigned char*>(a.v) + row * F::kRow;
+        const uint32_t dst = ring_addr + slot * F::kStage;
+#pragma unroll
+        for (int i = 0; i < F::kUnit * F::kChunks / 32; ++i) {
+          const int e = lane + 32 * i, r = e / F::kChunks, j = e % F::kChunks;
+          const bool live = r < nk;
+          const size_t off = live ? static_cast<size_t>(e) * 16 : 0;
+          cp_async16(dst + F::kKOff + F::at(r, j), kb + off, live);
+          cp_async16(dst + F::kVOff + F::at(r, j), vb + off, live);
+        }
+        if constexpr (F::kQuant) {
+          const bool live = lane < nk;
+          const size_t off = (row + (live ? lane : 0)) * F::NG;
+          cp_async_small<F::NG * 4>(dst + F::kKpOff + lane * F::NG * 4, a.kp + off, live);
+          cp_async_small<F::NG * 4>(dst + F::kVpOff + lane * F::NG * 4, a.vp + off, live);
+        }
+      }
+    }
+    cp_async_commit();
+    return nk;
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) ring_nk[i] = issue(i, i);
+
+  // ---- items of this run
+  int k = 0, slot = 0;
+  for (int t = t0; t < t1;) {
+    const Item it = item_at(a, pre, t);
+    const int seg_end = min(t1, it.end);
+    if (warp < NT)
+      stage_query<F>(a.q + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D, G, warp,
+                     a.scale_log2, words, fs, qss);
+    __syncthreads();
+    State<F, NT> st;
+    state_init(st);
+    for (; t0 + warp + kW * k < seg_end; ++k) {
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+      int nk = ring_nk[0];
+#pragma unroll
+      for (int i = 1; i < STAGES; ++i) nk = slot == i ? ring_nk[i] : nk;
+      if (nk > 0) {
+        if constexpr (F::kQuant)
+          unit_kv4<F, NT>(ring + slot * F::kStage, ring_addr + slot * F::kStage, nk, words, fs, qss, st);
+        else
+          unit_bf16<F, NT>(ring_addr + slot * F::kStage, nk, words, fs, st);
+      }
+      __syncwarp();
+      nk = issue(k + STAGES, slot);
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i)
+        if (slot == i) ring_nk[i] = nk;
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+    }
+    // the warps' states, each relative to its own maximum
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = 4 * nt + c;
+      float l = st.l[nt], zs[F::NG];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+      for (int gr = 0; gr < F::NG; ++gr) {
+        zs[gr] = st.zs[nt][gr];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) zs[gr] += __shfl_xor_sync(0xffffffffu, zs[gr], o);
+      }
+      if (g == 0) {
+        ms[warp * kMaxG + h] = st.m[nt];
+        ls[warp * kMaxG + h] = l;
+      }
+      if (h < G) {
+        float* to = obuf + (warp * G + h) * (D + 4);
+        if constexpr (F::kQuant) {
+          const float u0 = 1.f / st.c, u1 = u0 * 0.0625f;  // powers of two
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const float z = zs[i / 2 / (D / 32 / F::NG)];
+            *reinterpret_cast<float2*>(to + 32 * (i >> 1) + 4 * g + 2 * (i & 1)) =
+                make_float2(fmaf(st.o[nt][i][0] + st.o[nt][i][1], u0, z), fmaf(st.o[nt][i][2] + st.o[nt][i][3], u1, z));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            to[16 * i + g] = st.o[nt][i][0] + st.o[nt][i][1];
+            to[16 * i + g + 8] = st.o[nt][i][2] + st.o[nt][i][3];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = run_of(it.start, n, T) == cta && run_of(it.end - 1, n, T) == cta;
+    float* part = a.part + static_cast<size_t>(2 * cta + (it.start <= t0 ? 0 : 1)) * (G * (D + 2));
+    float* out = a.o + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D;
+    for (int e = tid; e < G * D; e += kThreads) {
+      const int h = e / D, d = e - h * D;
+      float M = -INFINITY, sum = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) M = fmaxf(M, ms[w * kMaxG + h]);
+      const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        const float x = ex2(ms[w * kMaxG + h] - mu);
+        l = fmaf(x, ls[w * kMaxG + h], l);
+        sum = fmaf(x, obuf[(w * G + h) * (D + 4) + d], sum);
+      }
+      if (whole) {
+        out[e] = l == 0.f ? 0.f : sum / l;
+      } else {
+        part[e] = sum;
+        if (d == 0) {
+          part[G * D + h] = M;
+          part[G * D + G + h] = l;
+        }
+      }
+    }
+    __syncthreads();
+    t = seg_end;
+  }
+  cp_async_wait<0>();
+}
+
+// Joins the partials of the items that are cut between CTAs, and writes the
+// zeros of rows without keys.  Grid (Hq, B), one thread per dim.
+template <class F>
+__global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant__ LongAttnArgs a) {
+  extern __shared__ __align__(16) int pre[];
+  constexpr int D = F::D;
+  const int G = a.Hq / a.Hkv, head = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  if (threadIdx.x < 32) prefix_rows<F>(a, pre, false);
+  __syncthreads();
+  const int T = pre[a.B], units = (pre[b + 1] - pre[b]) / a.Hkv;
+  pdl_wait();
+  float* out = a.o + (static_cast<size_t>(b) * a.Hq + head) * D + d;
+  if (units == 0) {
+    if (a.pos[b] == -1) *out = 0.f;
+    return;
+  }
+  const int n = runs(a.n_cta, T), g = head / G, h = head - g * G;
+  const int start = pre[b] + g * units;
+  const int c0 = run_of(start, n, T), c1 = run_of(start + units - 1, n, T);
+  if (c0 == c1) return;  // written by its CTA
+  const size_t stride = static_cast<size_t>(G) * (D + 2);
+  float M = -INFINITY, L = 0.f, sum = 0.f;
+  constexpr int kBatch = 8;
+  for (int c = c0; c <= c1; c += kBatch) {
+    float m[kBatch], l[kBatch], x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      m[i] = -INFINITY;
+      l[i] = x[i] = 0.f;
+      if (c + i <= c1) {
+        const float* p = a.part + (2 * (c + i) + (start <= run_start(c + i, n, T) ? 0 : 1)) * stride;
+        m[i] = __ldcg(p + G * D + h);
+        l[i] = __ldcg(p + G * D + G + h);
+        x[i] = __ldcg(p + h * D + d);
+      }
+    }
+    float mx = M;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, m[i]);
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    const float back = ex2(M - mu);
+    L *= back;
+    sum *= back;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float w = ex2(m[i] - mu);
+      L = fmaf(w, l[i], L);
+      sum = fmaf(w, x[i], sum);
+    }
+    M = mx;
+  }
+  *out = L == 0.f ? 0.f : sum / L;
+}
+
+// Units in flight per warp: what shared memory holds beside the merge buffer.
+template <class F, int NT>
+constexpr int stages() {
+  return F::kQuant || NT > 1 ? 2 : 3;
+}
+
+template <class F, int NT>
+cudaError_t run(const LongAttnArgs& a, cudaStream_t st) {
+  const uint32_t smem = Smem<F, stages<F, NT>()>::bytes(a.B, a.Hq / a.Hkv, NT);
+  cudaError_t e = launch(long_attn_kernel<F, NT, stages<F, NT>()>, dim3(a.n_cta), dim3(kThreads), smem, st, false, a);
+  if (e != cudaSuccess) return e;
+  return launch(long_merge_kernel<F>, dim3(a.Hq, a.B), dim3(F::D), (a.B + 1) * 4, st, true, a);
+}
+template <class F>
+cudaError_t run_format(const LongAttnArgs& a, cudaStream_t st) {
+  const int G = a.Hq / a.Hkv;
+  if (G <= 4) return run<F, 1>(a, st);
+  if (G <= 8) return run<F, 2>(a, st);
+  return run<F, 4>(a, st);
+}
+template <class F>
+cudaError_t allow_format() {
+  cudaError_t e = allow_smem(long_attn_kernel<F, 1, stages<F, 1>()>);
+  if (e == cudaSuccess) e = allow_smem(long_attn_kernel<F, 2, stages<F, 2>()>);
+  if (e == cudaSuccess) e = allow_smem(long_attn_kernel<F, 4, stages<F, 4>()>);
+  return e;
+}
+
+}  // namespace
+
+// Two CTAs fit an SM for the 4-bit cache with up to 4 heads per group.
+int long_attn_ctas(int Hq, int Hkv, bool quant, int sms) {
+  return min(kLongMaxCtas, quant && Hq / Hkv <= 4 ? 2 * sms : sms);
+}
+
+cudaError_t launch_long_attn(const LongAttnArgs& a, int D, int group, cudaStream_t st) {
+  if (a.blocks) return D == 64 ? run_format<Bf16<64>>(a, st) : run_format<Bf16<128>>(a, st);
+  if (D == 64) return group == 32 ? run_format<Kv4<64, 32>>(a, st) : run_format<Kv4<64, 64>>(a, st);
+  if (group == 32) return run_format<Kv4<128, 32>>(a, st);
+  if (group == 64) return run_format<Kv4<128, 64>>(a, st);
+  return run_format<Kv4<128, 128>>(a, st);
+}
+
+cudaError_t allow_smem_long() {
+  cudaError_t e = allow_format<Kv4<64, 32>>();
+  if (e == cudaSuccess) e = allow_format<Kv4<64, 64>>();
+  if (e == cudaSuccess) e = allow_format<Kv4<128, 32>>();
+  if (e == cudaSuccess) e = allow_format<Kv4<128, 64>>();
+  if (e == cudaSuccess) e = allow_format<Kv4<128, 128>>();
+  if (e == cudaSuccess) e = allow_format<Bf16<64>>();
+  if (e == cudaSuccess) e = allow_format<Bf16<128>>();
+  return e;
+}
+
+}  // namespace dec

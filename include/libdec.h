@@ -30,7 +30,8 @@
  *    limit) set bits in a per-device error word read by dec_device_error().
  *  - Numerics: fp32 accumulation of bf16 weights; RMSNorm, RoPE, softmax and
  *    SiLU in fp32 (RoPE angles reduced in fp64); the KV cache stores bf16.
- *  - Batch B is 1..16.  head_dim D is 64 or 128; Hq/Hkv is an integer <= 16.
+ *  - Batch B is 1..16 (token selection and the long-cache calls take more).
+ *    head_dim D is 64 or 128; Hq/Hkv is an integer <= 16.
  */
 #ifndef LIBDEC_H
 #define LIBDEC_H
@@ -203,6 +204,119 @@ int dec_lmhead_argmax(const float* residual, const void* final_norm, float eps, 
 int dec_select_tokens(const float* logits, const int32_t* prev_tokens, int n_prev, float repetition_penalty,
                       float temperature, int top_k, float top_p, const float* u, int32_t* token_out, int B, int V,
                       void* stream);
+
+/* ------------------------------------------------------------------ long caches */
+
+/*
+ * Operators for caches that no longer pay for being read whole in bf16 at
+ * every step: a KV cache held in 4 bits, and attention over selected 64-key
+ * blocks of a bf16 cache.  They are single calls beside dec_gqa_decode_attn
+ * (the captured decode loop keeps its bf16 cache).  The paper has no
+ * counterpart of them.  Limits shared by all: B is 1..1024, Hkv 1..4096, D 64
+ * or 128, Hq/Hkv an integer <= 16, B * Hkv * S_max < 2^31.  The GPU sets error
+ * bit 4 for a position, count or block id outside its range.
+ *
+ * The 4-bit cache of one of K and V:
+ *   codes   uint8 [B][Hkv][S_max][D/2]: dim 2i in the low nibble of byte i,
+ *           dim 2i + 1 in the high one
+ *   params  half  [B][Hkv][S_max][D/group][2]: scale s and middle z of each
+ *           group of `group` dims (32, 64 or 128, at most D)
+ * A code c stands for z + s (c - 8): 4.5 bits a value at group 64.  A group
+ * with extremes lo and hi gets, in float32 operations,
+ *   s = half((hi - lo) / 15),  z = half(lo + 8 s),
+ *   c = clamp(rint((x - z) / s) + 8, 0, 15)      (c = 8 where s = 0)
+ * with s and z clamped to +-65504; a group that holds an infinity or a NaN
+ * reads back as NaN whole.
+ */
+
+/*
+ * Quantises the K and V rows of T tokens into the cache as they are written:
+ * row b's token t goes to slot pos[b] + t, t < lens[b] (lens NULL: t < T).
+ * k, v: float32 (bf16 == 0) or bf16 (bf16 != 0) rows of D contiguous values;
+ * element (b, t, h) begins at b * stride_row + t * stride_token +
+ * h * stride_head elements (multiples of 16 bytes), the same for k and v.
+ *   from_cache == 0: t counts from the first row given (e.g. the k and v
+ *     columns of a fused projection's output); src_tokens >= T rows
+ *   from_cache != 0: the source is itself a cache, indexed by slot: token t of
+ *     row b is read at pos[b] + t; src_tokens is its slots (e.g. the bf16
+ *     cache that dec_prefill or dec_qkv_gemv_rope filled)
+ * T == 1: one decode step.  A row whose slots would leave either cache, or
+ * whose lens[b] lies outside [0, T], is left as it was (error bit 4).  Slots
+ * outside the written range keep their contents.
+ */
+int dec_kv4_store(const void* k, const void* v, int bf16, int64_t stride_row, int64_t stride_token,
+                  int64_t stride_head, int from_cache, int src_tokens, const int32_t* pos, const int32_t* lens, int T,
+                  void* k_codes, void* k_params, void* v_codes, void* v_params, int B, int Hkv, int D, int group,
+                  int S_max, void* stream);
+
+/*
+ * Reads the range back: slot pos[b] + t of the cache, t < lens[b], as rows
+ * of float32 or bf16 (one rounding of z + s (c - 8)) at the given strides.
+ * Rows t >= lens[b], and rows refused as above, keep their contents.
+ */
+int dec_kv4_load(const void* k_codes, const void* k_params, const void* v_codes, const void* v_params,
+                 const int32_t* pos, const int32_t* lens, int T, void* k_out, void* v_out, int bf16,
+                 int64_t stride_row, int64_t stride_token, int64_t stride_head, int B, int Hkv, int D, int group,
+                 int S_max, void* stream);
+
+/* Workspace bytes of dec_kv4_decode_attn and dec_block_decode_attn, whatever B and S_max (0: sizes refused). */
+size_t dec_long_attn_workspace_size(int Hq, int Hkv, int D);
+
+/*
+ * dec_gqa_decode_attn over a 4-bit cache: for each row b and query head h,
+ * with g = floor(h / (Hq/Hkv)) and keys j = 0 .. pos[b],
+ *   o[b][h] = sum_j softmax_j(q[b][h] . K[b][g][j] / sqrt(D)) V[b][g][j]
+ * K and V the values that the codes stand for, nothing rounded to 16 bits on
+ * the way.  pos[b] == -1 is a row without keys: its output is zero.  A row
+ * with any other pos outside [0, S_max) is not written (error bit 4).  Slots
+ * behind pos[b] are not read.  q is taken up to 2^114 in magnitude.  ws: device
+ * workspace of dec_long_attn_workspace_size() bytes, 256-byte aligned, any
+ * contents; calls that can overlap on the GPU need one each.  Results are
+ * reproducible bit for bit.
+ */
+int dec_kv4_decode_attn(const float* q, const void* k_codes, const void* k_params, const void* v_codes,
+                        const void* v_params, const int32_t* pos, float* o, void* ws, size_t ws_bytes, int B, int Hq,
+                        int Hkv, int D, int group, int S_max, void* stream);
+
+/*
+ * Channel bounds of a bf16 key cache [B][Hkv][S_max][D], per block of 64
+ * slots: bounds bf16 [B][Hkv][ceil(S_max/64)][2][D], [0] the largest and [1]
+ * the smallest value of each dim (NaNs are passed over).  Call it after the T
+ * tokens at slots pos[b] .. pos[b] + T - 1 were written (T == 1: a decode
+ * step): every block that holds one of them is computed anew over its slots up
+ * to pos[b] + T - 1; the other blocks keep theirs.  A row whose slots leave
+ * the cache is left as it was (error bit 4).
+ */
+int dec_block_bounds(const void* k_cache, const int32_t* pos, int T, void* bounds, int B, int Hkv, int D, int S_max,
+                     void* stream);
+
+/*
+ * The blocks that each (row, KV head) attends to, by a cheap upper bound of
+ * its scores.  Over blocks j = 0 .. floor(pos[b] / 64), with the group's
+ * query heads h and bounds hi, lo of the block,
+ *   score(j) = sum_h sum_d max(q[b][h][d] hi[d], q[b][h][d] lo[d])
+ * the first n_first and last n_last blocks and then the best-scored others
+ * are taken, n_select in all (all blocks where there are no more).  Blocks are
+ * ranked by their exact scores, not by float32 roundings of them; equal ones by
+ * the lower index; a NaN score counts as -infinity.
+ * blocks: int32 [B][Hkv][n_select], ascending, -1 in unused places (pos[b] ==
+ * -1: all).  n_first + n_last <= n_select <= 8192; S_max <= 524,288.  A row
+ * with any other pos outside [0, S_max) is not written (error bit 4).
+ */
+int dec_select_blocks(const float* q, const void* bounds, const int32_t* pos, int32_t* blocks, int n_select,
+                      int n_first, int n_last, int B, int Hq, int Hkv, int D, int S_max, void* stream);
+
+/*
+ * dec_gqa_decode_attn over listed blocks: the keys of (row b, KV head g) are
+ * the slots 64 i .. 64 i + 63, up to pos[b], of every block i of
+ * blocks[b][g][0 .. n_select) (-1: none), in any order; a block listed twice
+ * counts twice.  A row or head without any key gets zeros.  A block id outside
+ * [-1, ceil(S_max/64)) is passed over (error bit 4).  pos, ws and
+ * reproducibility as in dec_kv4_decode_attn.
+ */
+int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cache, const int32_t* pos,
+                          const int32_t* blocks, int n_select, float* o, void* ws, size_t ws_bytes, int B, int Hq,
+                          int Hkv, int D, int S_max, void* stream);
 
 /* ------------------------------------------------------------------ whole step */
 
