@@ -58,14 +58,26 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// D += A (16x16 half, row) * B (16x8 half, col), fp32 accumulate
+// D += A (16x16 half, row) * B (16x8 half, col), fp32 accumulate; and from zero
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                   uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D = A (16x8 half, row) * B (8x8 half, col)
+__device__ __forceinline__ void mma_f16_1688_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
@@ -80,6 +92,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ float half_lo(uint32_t w) {
@@ -103,7 +130,7 @@ struct Kv4 {
   static constexpr int kKOff = 0, kVOff = kUnit * kRow, kKpOff = 2 * kUnit * kRow, kVpOff = kKpOff + kUnit * NG * 4;
   static constexpr int kStage = kVpOff + kUnit * NG * 4;
   // chunk j of row r: the eight rows of an ldmatrix phase fall on distinct banks
-  static __device__ __forceinline__ uint32_t at(int r, int j) {
+  static __host__ __device__ constexpr uint32_t at(int r, int j) {
     return static_cast<uint32_t>(r * kRow + ((j ^ (kChunks == 4 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4));
   }
 };
@@ -115,7 +142,7 @@ struct Bf16 {
   static constexpr int D = D_, NG = 1, kUnit = 16;
   static constexpr int kRow = 2 * D, kChunks = kRow / 16, kQWords = D / 16 * 2;
   static constexpr int kKOff = 0, kVOff = kUnit * kRow, kStage = 2 * kUnit * kRow;
-  static __device__ __forceinline__ uint32_t at(int r, int j) {
+  static __host__ __device__ constexpr uint32_t at(int r, int j) {
     return static_cast<uint32_t>(r * kRow + ((j ^ (r & 7)) << 4));
   }
 };
@@ -197,11 +224,12 @@ __device__ __forceinline__ Item item_at(const LongAttnArgs& a, const int* pre, i
 //    (1, 5), (2, 6), (3, 7) of word c, dims 32 j + 8 c + nibble, the odd
 //    nibbles' (16 times larger) with a factor 1/16.  The head is scaled by a
 //    power of two to [2^13, 2^14); f takes it back along with the codes'
-//    2^-24.  qs: each group's sum of q, for the z part.
+//    2^-24.  zq: for the (s, z) pair of group c, (-8 Q, Q) with Q the group's
+//    sum of q, scaled by another 2^-10.
 //  * bf16: per 16 dims two pairs, as the instruction lays them out.
 template <class F>
 __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float scale_log2, uint32_t* words, float* f,
-                                            float* qs) {
+                                            uint32_t* zq) {
   constexpr int D = F::D;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int head = 4 * nt + (g >> 1);
@@ -228,6 +256,7 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
     const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
     const int e = mx > 0.f ? min(max(13 - ex, -100), 100) : 0;
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    float mine = 0.f;
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
       float s = 0.f;
@@ -237,8 +266,11 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
         for (int i = 0; i < 8; ++i) s += v[j][i];
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if (c == 0 && !rest) qs[head * 4 + gr] = s * scale_log2;
+      if (gr == c) mine = s;
     }
+    mine *= up * 0x1p-10f;
+    const float top = top11(mine), part = rest ? mine - top : top;
+    zq[nt * 32 + lane] = pack_f16(-8.f * part, part);
     if (c == 0 && !rest) f[head] = __uint_as_float(static_cast<uint32_t>(127 + 24 - e) << 23) * scale_log2;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -275,14 +307,19 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
 
 // A warp's running state.  Lane (g, c) of n-tile nt serves head 4 nt + c: m
 // the running maximum (log2 units; the same in the eight lanes of a head), mu
-// the value subtracted (0 while m is -inf), l and zs this lane's share of the
-// sums; o[nt][..][e] rows of O^T, columns (upper part, remainder) of the head.
+// the value subtracted (0 while m is -inf; 15 less for the 4-bit cache, whose
+// probabilities so fill the half range), l this lane's share of the sum;
+// o[nt][..][e] rows of O^T, columns (upper part, remainder) of the head.
+// zs: likewise sum_j p_j times the words of key j's (s, z) pairs, row g the
+// g-th half word, so that row 2 i + 1 is the z sum of group i.
 template <class F, int NT>
 struct State {
+  static constexpr float kUp = 15.f;
   float o[NT][F::D / 16][4];
   float m[NT], mu[NT], l[NT];
-  float zs[NT][F::NG];
-  float c, bound;  // 4-bit: factor on the scaled probabilities, every s seen is at most bound
+  float zs[NT][4];
+  float c, bound;  // 4-bit: factor on the scales, of which every one seen is at most bound
+  uint32_t c2;     // the factor as two halves
 };
 
 template <class F, int NT>
@@ -291,12 +328,13 @@ __device__ __forceinline__ void state_init(State<F, NT>& st) {
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < F::D / 16; ++i) st.o[nt][i][0] = st.o[nt][i][1] = st.o[nt][i][2] = st.o[nt][i][3] = 0.f;
-#pragma unroll
-    for (int g = 0; g < F::NG; ++g) st.zs[nt][g] = 0.f;
+    st.zs[nt][0] = st.zs[nt][1] = st.zs[nt][2] = st.zs[nt][3] = 0.f;
     st.m[nt] = -INFINITY;
-    st.mu[nt] = st.l[nt] = 0.f;
+    st.mu[nt] = F::kQuant ? -State<F, NT>::kUp : 0.f;
+    st.l[nt] = 0.f;
   }
   st.c = 1.f;
+  st.c2 = 0x3C003C00u;
   st.bound = 0.f;
 }
 
@@ -324,7 +362,9 @@ __device__ __forceinline__ void raise(State<F, NT>& st, const float (&x)[NT], fl
     if (s_max > st.bound) {
       const uint32_t e = __float_as_uint(s_max) >> 23;  // s_max in [2^(e-127), 2^(e-126))
       st.bound = __uint_as_float((e + 1u) << 23);
-      const float c = __uint_as_float((127u + 14u + 127u - e) << 23);  // s c below 2^15
+      const uint32_t up = min(126u - e + 127u, 127u + 15u);  // s c at most 1
+      const float c = __uint_as_float(up << 23);
+      st.c2 = pack_f16(c, c);
       ratio = c / st.c;
       st.c = c;
     }
@@ -339,10 +379,10 @@ __device__ __forceinline__ void raise(State<F, NT>& st, const float (&x)[NT], fl
     const float mu = mx == -INFINITY ? 0.f : mx;
     const float corr = ex2(st.m[nt] - mu);
     st.m[nt] = mx;
-    st.mu[nt] = mu;
+    st.mu[nt] = F::kQuant ? mu - State<F, NT>::kUp : mu;
     st.l[nt] *= corr;
 #pragma unroll
-    for (int g = 0; g < F::NG; ++g) st.zs[nt][g] *= corr;
+    for (int e = 0; e < 4; ++e) st.zs[nt][e] *= corr;
 #pragma unroll
     for (int i = 0; i < F::D / 16; ++i)
 #pragma unroll
@@ -350,24 +390,47 @@ __device__ __forceinline__ void raise(State<F, NT>& st, const float (&x)[NT], fl
   }
 }
 
+// Half words (row g) of the (s, z) pairs of keys 8 i + 2 c and + 1, i = 0 .. 3.
+template <int NG>
+__device__ __forceinline__ void load_pairs_trans(const unsigned char* base, uint32_t addr, uint32_t (&w)[4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  if constexpr (NG == 4) {
+    ldsm_x4_trans(w, addr + lane * 16);
+  } else {
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(base);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = (8 * i + 2 * c) * 2 * NG + (g < 2 * NG ? g : 0);
+      w[i] = static_cast<uint32_t>(h[at]) | (static_cast<uint32_t>(h[at + 2 * NG]) << 16);
+    }
+  }
+}
+
 // 32 keys of the 4-bit cache, of which the first nk count.
 template <class F, int NT>
 __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t stage_addr, int nk, const uint32_t* words,
-                                         const float* fs, const float* qss, State<F, NT>& st) {
+                                         const float (&fs)[NT], const uint32_t (&zq)[NT], State<F, NT>& st) {
   constexpr int NJ = F::D / 32, NG = F::NG, PER = NJ / NG;  // chunks per group
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int lrow = (lane & 7) + (lane & 8), lchunk = lane >> 4;
+  // the lane's own pair (group c) of keys 8 i + g
+  uint32_t kw[4], vw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = ((8 * i + g) * NG + (c < NG ? c : 0)) * 4;
+    kw[i] = *reinterpret_cast<const uint32_t*>(stage + F::kKpOff + at);
+    vw[i] = *reinterpret_cast<const uint32_t*>(stage + F::kVpOff + at);
+    if (NG < 4 && c >= NG) kw[i] = 0;
+  }
   float s[NT][4];
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
     uint32_t p0[NG], p1[NG];
     load_pairs<NG>(stage + F::kKpOff, 16 * hh + g, p0);
     load_pairs<NG>(stage + F::kKpOff, 16 * hh + g + 8, p1);
-    float acc[NT][NG][4];
+    float acc[NT][NG][4], zp[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) acc[nt][gr][0] = acc[nt][gr][1] = acc[nt][gr][2] = acc[nt][gr][3] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) mma_f16_1688_zero(zp[nt], kw[2 * hh], kw[2 * hh + 1], zq[nt]);
 #pragma unroll
     for (int jj = 0; jj < NJ; jj += 2) {
       uint32_t r[4];
@@ -379,31 +442,27 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint4 b = *reinterpret_cast<const uint4*>(words + ((nt * NJ + j) * 32 + lane) * 4);
-          mma_f16_16816(acc[nt][gr], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x, b.y);
+          if (j % PER == 0)
+            mma_f16_16816_zero(acc[nt][gr], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x,
+                               b.y);
+          else
+            mma_f16_16816(acc[nt][gr], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x, b.y);
           mma_f16_16816(acc[nt][gr], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u, b.z, b.w);
         }
       }
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float f = fs[4 * nt + c];
-      float a0 = 0.f, a1 = 0.f, z0 = 0.f, z1 = 0.f;
+      float a0 = (zp[nt][0] + zp[nt][1]) * 0x1p-14f, a1 = (zp[nt][2] + zp[nt][3]) * 0x1p-14f;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        const float qs = qss[(4 * nt + c) * 4 + gr];
-        const float sc0 = half_lo(p0[gr]), sc1 = half_lo(p1[gr]);
-        a0 = fmaf(sc0, acc[nt][gr][0] + acc[nt][gr][1], a0);
-        a1 = fmaf(sc1, acc[nt][gr][2] + acc[nt][gr][3], a1);
-        z0 = fmaf(fmaf(-8.f, sc0, half_hi(p0[gr])), qs, z0);
-        z1 = fmaf(fmaf(-8.f, sc1, half_hi(p1[gr])), qs, z1);
+        a0 = fmaf(half_lo(p0[gr]), acc[nt][gr][0] + acc[nt][gr][1], a0);
+        a1 = fmaf(half_lo(p1[gr]), acc[nt][gr][2] + acc[nt][gr][3], a1);
       }
-      s[nt][2 * hh] = fmaf(a0, f, z0);
-      s[nt][2 * hh + 1] = fmaf(a1, f, z1);
+      s[nt][2 * hh] = a0 * fs[nt];
+      s[nt][2 * hh + 1] = a1 * fs[nt];
     }
   }
-  uint32_t vp[4][NG];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) load_pairs<NG>(stage + F::kVpOff, 8 * i + g, vp[i]);
   if (nk < 32) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -413,28 +472,33 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
   }
   // a larger score or scale than before anywhere in the warp?
   float mx[NT];
-  bool more = false;
+  const float s_max = half_lo(max_f16x2(max_f16x2(vw[0], vw[1]), max_f16x2(vw[2], vw[3])));
+  bool more = s_max > st.bound;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     mx[nt] = fmaxf(fmaxf(s[nt][0], s[nt][1]), fmaxf(s[nt][2], s[nt][3]));
     more |= mx[nt] > st.m[nt];
   }
-  __half2 sm = *reinterpret_cast<const __half2*>(&vp[0][0]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int gr = 0; gr < NG; ++gr) sm = __hmax2(sm, *reinterpret_cast<const __half2*>(&vp[i][gr]));
-  const float s_max = __low2float(sm);
-  more |= s_max > st.bound;
   if (__any_sync(0xffffffffu, more)) raise<F, NT>(st, mx, s_max);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[nt][i] = ex2(s[nt][i] - st.mu[nt]);
-    st.l[nt] += (s[nt][0] + s[nt][1]) + (s[nt][2] + s[nt][3]);
-  }
+  uint32_t vt[4];
+  load_pairs_trans<NG>(stage + F::kVpOff, stage_addr + F::kVpOff, vt);
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
+    // probabilities of keys g and g + 8 (times 2^15) as upper halves and remainders
+    uint32_t top[NT], rem[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float q0 = ex2(s[nt][2 * hh] - st.mu[nt]), q1 = ex2(s[nt][2 * hh + 1] - st.mu[nt]);
+      st.l[nt] += q0 + q1;
+      top[nt] = pack_f16(q0, q1);
+      rem[nt] = pack_f16(q0 - half_lo(top[nt]), q1 - half_hi(top[nt]));
+      mma_f16_16816(st.zs[nt], vt[2 * hh], 0u, vt[2 * hh + 1], 0u,
+                    movmatrix_trans(__byte_perm(top[nt], rem[nt], 0x5410)),
+                    movmatrix_trans(__byte_perm(top[nt], rem[nt], 0x7632)));
+    }
+    uint32_t p0[NG], p1[NG];
+    load_pairs<NG>(stage + F::kVpOff, 16 * hh + g, p0);
+    load_pairs<NG>(stage + F::kVpOff, 16 * hh + g + 8, p1);
 #pragma unroll
     for (int jj = 0; jj < NJ; jj += 2) {
       uint32_t r[4], b0[NT], b1[NT];
@@ -443,14 +507,14 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
       for (int t = 0; t < 2; ++t) {
         const int j = jj + t, gr = j / PER;
         if (j % PER == 0) {
+          // times the keys' scales: the product's upper half, its exact error, and the remainder's share
+          const uint32_t sc = mul_f16x2(__byte_perm(p0[gr], p1[gr], 0x5410), st.c2);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float q0 = s[nt][2 * hh], q1 = s[nt][2 * hh + 1];
-            const float x0 = q0 * (half_lo(vp[2 * hh][gr]) * st.c), x1 = q1 * (half_lo(vp[2 * hh + 1][gr]) * st.c);
-            st.zs[nt][gr] = fmaf(q0, half_hi(vp[2 * hh][gr]), fmaf(q1, half_hi(vp[2 * hh + 1][gr]), st.zs[nt][gr]));
-            const float h0 = top11(x0), h1 = top11(x1);
-            b0[nt] = movmatrix_trans(pack_f16(h0, x0 - h0));
-            b1[nt] = movmatrix_trans(pack_f16(h1, x1 - h1));
+            const uint32_t x = mul_f16x2(top[nt], sc);
+            const uint32_t y = fma_f16x2(rem[nt], sc, fma_f16x2(top[nt], sc, x ^ 0x80008000u));
+            b0[nt] = movmatrix_trans(__byte_perm(x, y, 0x5410));
+            b1[nt] = movmatrix_trans(__byte_perm(x, y, 0x7632));
           }
         }
         const uint32_t w0 = r[2 * t], w1 = r[2 * t + 1], y0 = w0 >> 8, y1 = w1 >> 8;
@@ -474,10 +538,10 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
 
 // 16 keys of a bf16 cache, of which the first nk count.
 template <class F, int NT>
-__device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uint32_t* words, const float* fs,
+__device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uint32_t* words, const float (&fs)[NT],
                                           State<F, NT>& st) {
   constexpr int NJ = F::D / 16;
-  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int lane = threadIdx.x & 31, g = lane >> 2;
   float acc[NT][2][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -497,7 +561,7 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
   bool more = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const float f = fs[4 * nt + c];
+    const float f = fs[nt];
     s[nt][0] = ((acc[nt][0][0] + acc[nt][1][0]) + (acc[nt][0][1] + acc[nt][1][1])) * f;
     s[nt][1] = ((acc[nt][0][2] + acc[nt][1][2]) + (acc[nt][0][3] + acc[nt][1][3])) * f;
     if (g >= nk) s[nt][0] = -INFINITY;
@@ -533,8 +597,8 @@ struct Smem {
   static __host__ __device__ uint32_t ring(int B, int G, int NT) { return obuf(B, NT) + kW * G * (F::D + 4) * 4; }
   static __host__ __device__ uint32_t words(int B) { return ((B + 1) * 4 + 127) / 128 * 128; }
   static __host__ __device__ uint32_t f(int B, int NT) { return words(B) + NT * F::kQWords * 32 * 4; }
-  static __host__ __device__ uint32_t qs(int B, int NT) { return f(B, NT) + kMaxG * 4; }
-  static __host__ __device__ uint32_t ms(int B, int NT) { return qs(B, NT) + kMaxG * 4 * 4; }
+  static __host__ __device__ uint32_t zq(int B, int NT) { return f(B, NT) + kMaxG * 4; }
+  static __host__ __device__ uint32_t ms(int B, int NT) { return zq(B, NT) + 4 * 32 * 4; }
   static __host__ __device__ uint32_t ls(int B, int NT) { return ms(B, NT) + kW * kMaxG * 4; }
   static __host__ __device__ uint32_t obuf(int B, int NT) { return ls(B, NT) + kW * kMaxG * 4; }
   static __host__ __device__ uint32_t bytes(int B, int G, int NT) {
@@ -552,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* pre = reinterpret_cast<int*>(smem);
   uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::words(a.B));
-  float* fs = reinterpret_cast<float*>(smem + L::f(a.B, NT));
-  float* qss = reinterpret_cast<float*>(smem + L::qs(a.B, NT));
+  float* f_smem = reinterpret_cast<float*>(smem + L::f(a.B, NT));
+  uint32_t* zq_smem = reinterpret_cast<uint32_t*>(smem + L::zq(a.B, NT));
   float* ms = reinterpret_cast<float*>(smem + L::ms(a.B, NT));
   float* ls = reinterpret_cast<float*>(smem + L::ls(a.B, NT));
   float* obuf = reinterpret_cast<float*>(smem + L::obuf(a.B, NT));
@@ -568,7 +632,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   if (cta >= n) return;  // the same verdict in every thread
   const int t0 = run_start(cta, n, T), t1 = run_start(cta + 1, n, T);
 
-  // ---- loads: this warp's units t0 + warp + kW k, in order
+  // ---- loads: this warp's units t0 + warp + kW k, in order.  A lane copies
+  // the 16-byte pieces lane, lane + 32, .. of a unit, at fixed places in shared
+  // memory (the swizzle has a period of 32 pieces)
+  static_assert(F::at(0, 0) == 0 && 32 % F::kChunks == 0, "lane-fixed pieces");
+  constexpr int kPieces = F::kUnit * F::kChunks / 32;
+  const uint32_t lane_at = F::at(lane / F::kChunks, lane % F::kChunks);
   Item li = item_at(a, pre, t0);  // the item being loaded
   int list_k = 0;                 // listed blocks: units list_k .. list_k + 31 of this warp have their ids in the lanes
   int ids = 0, ids_next = 0;
@@ -583,16 +652,54 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
     ids = fetch_ids(0);
     ids_next = fetch_ids(32);
   }
-  int ring_nk[STAGES];  // keys of the units in flight
+  const unsigned char *k_src = nullptr, *v_src = nullptr;  // 4-bit: this lane's first piece of slot 0 of the item
+  const uint32_t *kp_src = nullptr, *vp_src = nullptr;
+  auto item_sources = [&]() {
+    const size_t row = (static_cast<size_t>(li.b) * a.Hkv + li.h) * a.S_max;
+    k_src = static_cast<const unsigned char*>(a.k) + row * F::kRow + lane * 16;
+    v_src = static_cast<const unsigned char*>(a.v) + row * F::kRow + lane * 16;
+    kp_src = a.kp + (row + lane) * F::NG;
+    vp_src = a.vp + (row + lane) * F::NG;
+  };
+  if constexpr (F::kQuant) item_sources();
+  // issues unit k of this warp into a slot; returns its keys (bf16 only)
   auto issue = [&](int k, int slot) -> int {
     const int t = t0 + warp + kW * k;
     int nk = 0;
     if (t < t1) {
-      if (t >= li.end) li = item_at(a, pre, t);
-      int k0;
+      if (t >= li.end) {
+        li = item_at(a, pre, t);
+        if constexpr (F::kQuant) item_sources();
+      }
+      const uint32_t dst = ring_addr + slot * F::kStage + lane_at;
       if constexpr (F::kQuant) {
-        k0 = (t - li.start) * F::kUnit;
-        nk = min(F::kUnit, li.len - k0);
+        const int k0 = (t - li.start) * F::kUnit;
+        const unsigned char* ks = k_src + static_cast<size_t>(k0) * F::kRow;
+        const unsigned char* vs = v_src + static_cast<size_t>(k0) * F::kRow;
+        const uint32_t* kps = kp_src + static_cast<size_t>(k0) * F::NG;
+        const uint32_t* vps = vp_src + static_cast<size_t>(k0) * F::NG;
+        const uint32_t pdst = ring_addr + slot * F::kStage + lane * F::NG * 4;
+        nk = li.len - k0;
+        if (nk >= F::kUnit) {
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            cp_async16(dst + F::kKOff + 512 * i, ks + 512 * i, true);
+            cp_async16(dst + F::kVOff + 512 * i, vs + 512 * i, true);
+          }
+          cp_async_small<F::NG * 4>(pdst + F::kKpOff, kps, true);
+          cp_async_small<F::NG * 4>(pdst + F::kVpOff, vps, true);
+        } else {  // zeros behind the last key; their sources lie inside the unit's live part
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const bool live = lane / F::kChunks + 32 / F::kChunks * i < nk;
+            const size_t off = live ? 512 * i : 0;
+            cp_async16(dst + F::kKOff + 512 * i, (live ? ks : ks - lane * 16) + off, live);
+            cp_async16(dst + F::kVOff + 512 * i, (live ? vs : vs - lane * 16) + off, live);
+          }
+          const bool live = lane < nk;
+          cp_async_small<F::NG * 4>(pdst + F::kKpOff, live ? kps : kps - lane * F::NG, live);
+          cp_async_small<F::NG * 4>(pdst + F::kVpOff, live ? vps : vps - lane * F::NG, live);
+        }
       } else {
         if (k - list_k == 32) {
           list_k += 32;
@@ -602,33 +709,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
         const int id = __shfl_sync(0xffffffffu, ids, k - list_k);
         const bool bad = id < -1 || id > (a.S_max - 1) / kBlockKeys;
         if (bad && lane == 0) atomicOr(a.err, kErrPosRange);
-        k0 = bad || id < 0 ? li.len : id * kBlockKeys + (t - li.start) % (kBlockKeys / F::kUnit) * F::kUnit;
+        const int k0 =
+            bad || id < 0 ? li.len : id * kBlockKeys + (t - li.start) % (kBlockKeys / F::kUnit) * F::kUnit;
         nk = max(0, min(F::kUnit, li.len - k0));
-      }
-      if (nk > 0) {
-        const size_t row = (static_cast<size_t>(li.b) * a.Hkv + li.h) * a.S_max + k0;
-        const unsigned char* kb = static_cast<const unsigned char*>(a.k) + row * F::kRow;
-        const unsigned char* vb = static_cast<const unsigned char*>(a.v) + row * F::kRow;
-        const uint32_t dst = ring_addr + slot * F::kStage;
+        if (nk > 0) {
+          const size_t row = (static_cast<size_t>(li.b) * a.Hkv + li.h) * a.S_max + k0;
+          const unsigned char* ks = static_cast<const unsigned char*>(a.k) + row * F::kRow + lane * 16;
+          const unsigned char* vs = static_cast<const unsigned char*>(a.v) + row * F::kRow + lane * 16;
 #pragma unroll
-        for (int i = 0; i < F::kUnit * F::kChunks / 32; ++i) {
-          const int e = lane + 32 * i, r = e / F::kChunks, j = e % F::kChunks;
-          const bool live = r < nk;
-          const size_t off = live ? static_cast<size_t>(e) * 16 : 0;
-          cp_async16(dst + F::kKOff + F::at(r, j), kb + off, live);
-          cp_async16(dst + F::kVOff + F::at(r, j), vb + off, live);
-        }
-        if constexpr (F::kQuant) {
-          const bool live = lane < nk;
-          const size_t off = (row + (live ? lane : 0)) * F::NG;
-          cp_async_small<F::NG * 4>(dst + F::kKpOff + lane * F::NG * 4, a.kp + off, live);
-          cp_async_small<F::NG * 4>(dst + F::kVpOff + lane * F::NG * 4, a.vp + off, live);
+          for (int i = 0; i < kPieces; ++i) {
+            const bool live = lane / F::kChunks + 32 / F::kChunks * i < nk;
+            const size_t off = live ? 512 * i : 0;
+            const uint32_t at = ring_addr + slot * F::kStage +
+                                F::at(lane / F::kChunks + 32 / F::kChunks * i, lane % F::kChunks);
+            cp_async16(at + F::kKOff, (live ? ks : ks - lane * 16) + off, live);
+            cp_async16(at + F::kVOff, (live ? vs : vs - lane * 16) + off, live);
+          }
         }
       }
     }
     cp_async_commit();
     return nk;
   };
+  int ring_nk[STAGES];  // bf16: keys of the units in flight
 #pragma unroll
   for (int i = 0; i < STAGES; ++i) ring_nk[i] = issue(i, i);
 
@@ -639,27 +742,36 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
     const int seg_end = min(t1, it.end);
     if (warp < NT)
       stage_query<F>(a.q + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D, G, warp,
-                     a.scale_log2, words, fs, qss);
+                     a.scale_log2, words, f_smem, zq_smem);
     __syncthreads();
+    float fs[NT];
+    uint32_t zq[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      fs[nt] = f_smem[4 * nt + (lane & 3)];
+      zq[nt] = zq_smem[nt * 32 + lane];
+    }
     State<F, NT> st;
     state_init(st);
     for (; t0 + warp + kW * k < seg_end; ++k) {
       cp_async_wait<STAGES - 1>();
       __syncwarp();
-      int nk = ring_nk[0];
+      if constexpr (F::kQuant) {
+        const int nk = it.len - (t0 + warp + kW * k - it.start) * F::kUnit;
+        unit_kv4<F, NT>(ring + slot * F::kStage, ring_addr + slot * F::kStage, nk, words, fs, zq, st);
+        __syncwarp();
+        issue(k + STAGES, slot);
+      } else {
+        int nk = ring_nk[0];
 #pragma unroll
-      for (int i = 1; i < STAGES; ++i) nk = slot == i ? ring_nk[i] : nk;
-      if (nk > 0) {
-        if constexpr (F::kQuant)
-          unit_kv4<F, NT>(ring + slot * F::kStage, ring_addr + slot * F::kStage, nk, words, fs, qss, st);
-        else
-          unit_bf16<F, NT>(ring_addr + slot * F::kStage, nk, words, fs, st);
+        for (int i = 1; i < STAGES; ++i) nk = slot == i ? ring_nk[i] : nk;
+        if (nk > 0) unit_bf16<F, NT>(ring_addr + slot * F::kStage, nk, words, fs, st);
+        __syncwarp();
+        nk = issue(k + STAGES, slot);
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i)
+          if (slot == i) ring_nk[i] = nk;
       }
-      __syncwarp();
-      nk = issue(k + STAGES, slot);
-#pragma unroll
-      for (int i = 0; i < STAGES; ++i)
-        if (slot == i) ring_nk[i] = nk;
       slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
     // the warps' states, each relative to its own maximum
@@ -671,11 +783,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
-      for (int gr = 0; gr < F::NG; ++gr) {
-        zs[gr] = st.zs[nt][gr];
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) zs[gr] += __shfl_xor_sync(0xffffffffu, zs[gr], o);
-      }
+      for (int gr = 0; gr < F::NG; ++gr)
+        zs[gr] = __shfl_sync(0xffffffffu, st.zs[nt][0] + st.zs[nt][1], 4 * (2 * gr + 1) + c);
       if (g == 0) {
         ms[warp * kMaxG + h] = st.m[nt];
         ls[warp * kMaxG + h] = l;
