@@ -19,15 +19,17 @@
 // lane holds the score of one head: S^T = K Q^T (keys x heads),
 // O^T = V^T P^T (dims x heads), P^T transposed in registers (movmatrix).
 //
-// 4-bit operands.  A masked nibble pair (w & 0x000F000F) read as two halves is
-// c * 2^-24 exactly (a subnormal), the next nibble (w & 0x00F000F0) is
-// 16 c * 2^-24: the scores need one logic operation for two codes, the powers
-// of two sit in the query operand, and each group's sum is scaled in fp32 by
-// its (s, z).  For the values the codes are centred, (1024 + c) - 1032 in half
-// arithmetic, exactly: uncentred ones would sum to numbers far above the
-// result.  Each key's s multiplies the probability before it is rounded to
-// two halves; a power of two C per warp, from the largest s seen, keeps that
-// product near the top of the half range.  The z part is a plain fp32 sum.
+// 4-bit operands.  A nibble pair masked out of a word and joined to 1024 in each
+// half is 1024 + c, less 1032 exactly c - 8; the next nibble pair gives
+// 16 (c - 8).  The 16 is taken out of the query operand, or of the result.
+// Codes have to be centred: a sum of uncentred ones runs far above its result,
+// and the tensor core cuts each product at the last place of the running sum
+// (1.1e-6 of the result with uncentred keys, 0.4e-6 so; 3e-5 with uncentred
+// values).  The scores' group sums are scaled in fp32 by s.  For the values a
+// key's s multiplies its probability, held as two halves: the product's upper
+// half, and its exact error plus the lower half's product.  A power of two C
+// per warp, from the largest s seen, keeps s C at most 1.  The z parts are
+// products of their own, with the (s, z) words as the other operand.
 #include <cuda_fp16.h>
 
 #include "dec_launch.cuh"
@@ -104,6 +106,31 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
+// a b - c
+__device__ __forceinline__ uint32_t fms_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("{\n .reg .b32 n;\n neg.f16x2 n, %3;\n fma.rn.f16x2 %0, %1, %2, n;\n}" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// The codes of nibbles 0 and 4 of w (bits 0 and 16 on) as c - 8, those of
+// nibbles 1 and 5 as 16 (c - 8), exactly: 1024 + c less 1032.  magic is 1024 in
+// both halves, held in a register so that masking and joining is one operation.
+__device__ __forceinline__ uint32_t centred_lo(uint32_t w, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(d) : "r"(w), "r"(magic));
+  return add_f16x2(d, 0xE408E408u);
+}
+__device__ __forceinline__ uint32_t centred_hi(uint32_t w, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(d) : "r"(w), "r"(magic));
+  return add_f16x2(d, 0xE480E480u);
+}
+// 8x8 transpose of 16-bit values across the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -168,9 +195,9 @@ __device__ __forceinline__ int row_units(const LongAttnArgs& a, int p) {
   else return a.n_select * (kBlockKeys / F::kUnit);
 }
 
-// pre[0 .. B] by one warp.
+// pre[0 .. B], and each row's keys in len, by one warp.
 template <class F>
-__device__ __forceinline__ void prefix_rows(const LongAttnArgs& a, int* pre, bool report) {
+__device__ __forceinline__ void prefix_rows(const LongAttnArgs& a, int* pre, int* len, bool report) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
   if (lane == 0) pre[0] = 0;
@@ -180,6 +207,7 @@ __device__ __forceinline__ void prefix_rows(const LongAttnArgs& a, int* pre, boo
     if (b < a.B) {
       const int p = a.pos[b];
       v = row_units<F>(a, p) * a.Hkv;
+      len[b] = p + 1;
       if (report && (p < -1 || p >= a.S_max)) atomicOr(a.err, kErrPosRange);
     }
 #pragma unroll
@@ -199,7 +227,7 @@ struct Item {
 };
 
 // The item that holds unit t.
-__device__ __forceinline__ Item item_at(const LongAttnArgs& a, const int* pre, int t) {
+__device__ __forceinline__ Item item_at(const LongAttnArgs& a, const int* pre, const int* len, int t) {
   int lo = 0, hi = a.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -212,20 +240,20 @@ __device__ __forceinline__ Item item_at(const LongAttnArgs& a, const int* pre, i
   it.h = (t - pre[lo]) / per;
   it.start = pre[lo] + it.h * per;
   it.end = it.start + per;
-  it.len = a.pos[lo] + 1;
+  it.len = len[lo];
   return it;
 }
 
 // ----------------------------------------------------------------------------- query operand
 
-// Heads 4 nt .. 4 nt + 3 of a group as B fragments, by one warp.  Lane (g, c)
+// Heads 4 nt .. 4 nt + 3 of a group (q in shared memory) as B fragments, by one
+// warp.  Lane (g, c)
 // holds column g: head g / 2, its upper part (g even) or the remainder.
 //  * 4-bit: per chunk j four half pairs that meet the nibble pairs (0, 4),
 //    (1, 5), (2, 6), (3, 7) of word c, dims 32 j + 8 c + nibble, the odd
 //    nibbles' (16 times larger) with a factor 1/16.  The head is scaled by a
-//    power of two to [2^13, 2^14); f takes it back along with the codes'
-//    2^-24.  zq: for the (s, z) pair of group c, (-8 Q, Q) with Q the group's
-//    sum of q, scaled by another 2^-10.
+//    power of two to [2^13, 2^14); f takes it back.  zq: for the (s, z) pair of
+//    group c, (0, Q) with Q the group's sum of q, scaled by another 2^-10.
 //  * bf16: per 16 dims two pairs, as the instruction lays them out.
 template <class F>
 __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float scale_log2, uint32_t* words, float* f,
@@ -242,9 +270,9 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
     for (int j = 0; j < NJ; ++j) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
       if (head < G) {
-        const float4* p = reinterpret_cast<const float4*>(q + static_cast<size_t>(head) * D + 32 * j + 8 * c);
-        x = __ldg(p);
-        y = __ldg(p + 1);
+        const float4* p = reinterpret_cast<const float4*>(q + head * D + 32 * j + 8 * c);
+        x = p[0];
+        y = p[1];
       }
       v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
       v[j][4] = y.x, v[j][5] = y.y, v[j][6] = y.z, v[j][7] = y.w;
@@ -270,8 +298,8 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
     }
     mine *= up * 0x1p-10f;
     const float top = top11(mine), part = rest ? mine - top : top;
-    zq[nt * 32 + lane] = pack_f16(-8.f * part, part);
-    if (c == 0 && !rest) f[head] = __uint_as_float(static_cast<uint32_t>(127 + 24 - e) << 23) * scale_log2;
+    zq[nt * 32 + lane] = pack_f16(0.f, part);
+    if (c == 0 && !rest) f[head] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * scale_log2;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       uint32_t w[4];
@@ -293,7 +321,7 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
       for (int i = 0; i < 2; ++i) {
         float2 x = make_float2(0.f, 0.f);
         if (head < G)
-          x = __ldg(reinterpret_cast<const float2*>(q + static_cast<size_t>(head) * D + 16 * j + 8 * i + 2 * c));
+          x = *reinterpret_cast<const float2*>(q + head * D + 16 * j + 8 * i + 2 * c);
         const uint32_t hi = pack_bf16(x.x, x.y);
         w[i] = rest ? pack_bf16(x.x - bf16lo(hi), x.y - bf16hi(hi)) : hi;
       }
@@ -306,18 +334,21 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
 // ----------------------------------------------------------------------------- one unit
 
 // A warp's running state.  Lane (g, c) of n-tile nt serves head 4 nt + c: m
-// the running maximum (log2 units; the same in the eight lanes of a head), mu
-// the value subtracted (0 while m is -inf; 15 less for the 4-bit cache, whose
-// probabilities so fill the half range), l this lane's share of the sum;
+// the reference score (log2 units; the same in the eight lanes of a head), mu
+// the value subtracted (0 while m is -inf; kUp less for the 4-bit cache), l
+// this lane's share of the sum;
 // o[nt][..][e] rows of O^T, columns (upper part, remainder) of the head.
 // zs: likewise sum_j p_j times the words of key j's (s, z) pairs, row g the
 // g-th half word, so that row 2 i + 1 is the z sum of group i.
 template <class F, int NT>
 struct State {
-  static constexpr float kUp = 15.f;
+  // 4-bit: m follows a larger score only once it leads by kSlack, so that the
+  // sums are rescaled seldom; probabilities are at most 2^(kUp + kSlack), the
+  // top of the half range
+  static constexpr float kUp = F::kQuant ? 11.f : 0.f, kSlack = F::kQuant ? 4.f : 0.f;
   float o[NT][F::D / 16][4];
   float m[NT], mu[NT], l[NT];
-  float zs[NT][4];
+  float zs[NT];
   float c, bound;  // 4-bit: factor on the scales, of which every one seen is at most bound
   uint32_t c2;     // the factor as two halves
 };
@@ -328,9 +359,9 @@ __device__ __forceinline__ void state_init(State<F, NT>& st) {
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < F::D / 16; ++i) st.o[nt][i][0] = st.o[nt][i][1] = st.o[nt][i][2] = st.o[nt][i][3] = 0.f;
-    st.zs[nt][0] = st.zs[nt][1] = st.zs[nt][2] = st.zs[nt][3] = 0.f;
+    st.zs[nt] = 0.f;
     st.m[nt] = -INFINITY;
-    st.mu[nt] = F::kQuant ? -State<F, NT>::kUp : 0.f;
+    st.mu[nt] = -State<F, NT>::kUp;
     st.l[nt] = 0.f;
   }
   st.c = 1.f;
@@ -379,10 +410,9 @@ __device__ __forceinline__ void raise(State<F, NT>& st, const float (&x)[NT], fl
     const float mu = mx == -INFINITY ? 0.f : mx;
     const float corr = ex2(st.m[nt] - mu);
     st.m[nt] = mx;
-    st.mu[nt] = F::kQuant ? mu - State<F, NT>::kUp : mu;
+    st.mu[nt] = mu - State<F, NT>::kUp;
     st.l[nt] *= corr;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) st.zs[nt][e] *= corr;
+    st.zs[nt] *= corr;
 #pragma unroll
     for (int i = 0; i < F::D / 16; ++i)
 #pragma unroll
@@ -413,6 +443,8 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
   constexpr int NJ = F::D / 32, NG = F::NG, PER = NJ / NG;  // chunks per group
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int lrow = (lane & 7) + (lane & 8), lchunk = lane >> 4;
+  uint32_t magic;
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
   // the lane's own pair (group c) of keys 8 i + g
   uint32_t kw[4], vw[4];
 #pragma unroll
@@ -439,21 +471,22 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
       for (int t = 0; t < 2; ++t) {
         const int j = jj + t, gr = j / PER;
         const uint32_t w0 = r[2 * t], w1 = r[2 * t + 1], x0 = w0 >> 8, x1 = w1 >> 8;
+        const uint32_t e0 = centred_lo(w0, magic), e1 = centred_lo(w1, magic);
+        const uint32_t e2 = centred_hi(w0, magic), e3 = centred_hi(w1, magic);
+        const uint32_t f0 = centred_lo(x0, magic), f1 = centred_lo(x1, magic);
+        const uint32_t f2 = centred_hi(x0, magic), f3 = centred_hi(x1, magic);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint4 b = *reinterpret_cast<const uint4*>(words + ((nt * NJ + j) * 32 + lane) * 4);
-          if (j % PER == 0)
-            mma_f16_16816_zero(acc[nt][gr], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x,
-                               b.y);
-          else
-            mma_f16_16816(acc[nt][gr], w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, b.x, b.y);
-          mma_f16_16816(acc[nt][gr], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u, b.z, b.w);
+          if (j % PER == 0) mma_f16_16816_zero(acc[nt][gr], e0, e1, e2, e3, b.x, b.y);
+          else mma_f16_16816(acc[nt][gr], e0, e1, e2, e3, b.x, b.y);
+          mma_f16_16816(acc[nt][gr], f0, f1, f2, f3, b.z, b.w);
         }
       }
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float a0 = (zp[nt][0] + zp[nt][1]) * 0x1p-14f, a1 = (zp[nt][2] + zp[nt][3]) * 0x1p-14f;
+      float a0 = (zp[nt][0] + zp[nt][1]) * 0x1p10f, a1 = (zp[nt][2] + zp[nt][3]) * 0x1p10f;
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         a0 = fmaf(half_lo(p0[gr]), acc[nt][gr][0] + acc[nt][gr][1], a0);
@@ -477,14 +510,14 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     mx[nt] = fmaxf(fmaxf(s[nt][0], s[nt][1]), fmaxf(s[nt][2], s[nt][3]));
-    more |= mx[nt] > st.m[nt];
+    more |= mx[nt] > st.m[nt] + State<F, NT>::kSlack;
   }
   if (__any_sync(0xffffffffu, more)) raise<F, NT>(st, mx, s_max);
   uint32_t vt[4];
   load_pairs_trans<NG>(stage + F::kVpOff, stage_addr + F::kVpOff, vt);
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
-    // probabilities of keys g and g + 8 (times 2^15) as upper halves and remainders
+    // probabilities of keys g and g + 8 (times 2^kUp) as upper halves and remainders
     uint32_t top[NT], rem[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -492,9 +525,12 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
       st.l[nt] += q0 + q1;
       top[nt] = pack_f16(q0, q1);
       rem[nt] = pack_f16(q0 - half_lo(top[nt]), q1 - half_hi(top[nt]));
-      mma_f16_16816(st.zs[nt], vt[2 * hh], 0u, vt[2 * hh + 1], 0u,
-                    movmatrix_trans(__byte_perm(top[nt], rem[nt], 0x5410)),
-                    movmatrix_trans(__byte_perm(top[nt], rem[nt], 0x7632)));
+      // joined in fp32: the tensor core cuts each product at the last place of the
+      // running sum, and these sums are long (4e-6 of the result at 33k keys, 1e-6 so)
+      float z[4];
+      mma_f16_16816_zero(z, vt[2 * hh], 0u, vt[2 * hh + 1], 0u, transpose8(__byte_perm(top[nt], rem[nt], 0x5410)),
+                         transpose8(__byte_perm(top[nt], rem[nt], 0x7632)));
+      st.zs[nt] += z[0] + z[1];
     }
     uint32_t p0[NG], p1[NG];
     load_pairs<NG>(stage + F::kVpOff, 16 * hh + g, p0);
@@ -512,20 +548,16 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint32_t x = mul_f16x2(top[nt], sc);
-            const uint32_t y = fma_f16x2(rem[nt], sc, fma_f16x2(top[nt], sc, x ^ 0x80008000u));
-            b0[nt] = movmatrix_trans(__byte_perm(x, y, 0x5410));
-            b1[nt] = movmatrix_trans(__byte_perm(x, y, 0x7632));
+            const uint32_t y = fma_f16x2(rem[nt], sc, fms_f16x2(top[nt], sc, x));
+            b0[nt] = transpose8(__byte_perm(x, y, 0x5410));
+            b1[nt] = transpose8(__byte_perm(x, y, 0x7632));
           }
         }
         const uint32_t w0 = r[2 * t], w1 = r[2 * t + 1], y0 = w0 >> 8, y1 = w1 >> 8;
-        const uint32_t e0 = add_f16x2((w0 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);  // c - 8
-        const uint32_t e1 = add_f16x2((w0 & 0x00F000F0u) | 0x64006400u, 0xE480E480u);  // 16 (c - 8)
-        const uint32_t e2 = add_f16x2((w1 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
-        const uint32_t e3 = add_f16x2((w1 & 0x00F000F0u) | 0x64006400u, 0xE480E480u);
-        const uint32_t f0 = add_f16x2((y0 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
-        const uint32_t f1 = add_f16x2((y0 & 0x00F000F0u) | 0x64006400u, 0xE480E480u);
-        const uint32_t f2 = add_f16x2((y1 & 0x000F000Fu) | 0x64006400u, 0xE408E408u);
-        const uint32_t f3 = add_f16x2((y1 & 0x00F000F0u) | 0x64006400u, 0xE480E480u);
+        const uint32_t e0 = centred_lo(w0, magic), e1 = centred_hi(w0, magic);
+        const uint32_t e2 = centred_lo(w1, magic), e3 = centred_hi(w1, magic);
+        const uint32_t f0 = centred_lo(y0, magic), f1 = centred_hi(y0, magic);
+        const uint32_t f2 = centred_lo(y1, magic), f3 = centred_hi(y1, magic);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_f16_16816(st.o[nt][2 * j], e0, e1, e2, e3, b0[nt], b1[nt]);
@@ -577,8 +609,8 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
     st.l[nt] += x0 + x1;
     const uint32_t h = pack_bf16(x0, x1);
     const uint32_t l = pack_bf16(x0 - bf16lo(h), x1 - bf16hi(h));
-    b0[nt] = movmatrix_trans(__byte_perm(h, l, 0x5410));
-    b1[nt] = movmatrix_trans(__byte_perm(h, l, 0x7632));
+    b0[nt] = transpose8(__byte_perm(h, l, 0x5410));
+    b1[nt] = transpose8(__byte_perm(h, l, 0x7632));
   }
   const int vrow = (lane & 7) + ((lane >> 4) << 3), vchunk = (lane >> 3) & 1;
 #pragma unroll
@@ -594,8 +626,9 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
 
 template <class F, int STAGES>
 struct Smem {
-  static __host__ __device__ uint32_t ring(int B, int G, int NT) { return obuf(B, NT) + kW * G * (F::D + 4) * 4; }
-  static __host__ __device__ uint32_t words(int B) { return ((B + 1) * 4 + 127) / 128 * 128; }
+  static __host__ __device__ uint32_t ring(int B, int G, int NT) { return qraw(B, G, NT) + G * F::D * 4; }
+  static __host__ __device__ uint32_t qraw(int B, int G, int NT) { return obuf(B, NT) + kW * G * (F::D + 4) * 4; }
+  static __host__ __device__ uint32_t words(int B) { return ((2 * B + 1) * 4 + 127) / 128 * 128; }
   static __host__ __device__ uint32_t f(int B, int NT) { return words(B) + NT * F::kQWords * 32 * 4; }
   static __host__ __device__ uint32_t zq(int B, int NT) { return f(B, NT) + kMaxG * 4; }
   static __host__ __device__ uint32_t ms(int B, int NT) { return zq(B, NT) + 4 * 32 * 4; }
@@ -615,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   const int G = a.Hq / a.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* pre = reinterpret_cast<int*>(smem);
+  int* len = pre + a.B + 1;
   uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::words(a.B));
   float* f_smem = reinterpret_cast<float*>(smem + L::f(a.B, NT));
   uint32_t* zq_smem = reinterpret_cast<uint32_t*>(smem + L::zq(a.B, NT));
@@ -625,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   const uint32_t ring_addr = smem_addr(ring);
 
   pdl_launch_dependents();
-  if (warp == 0) prefix_rows<F>(a, pre, blockIdx.x == 0);
+  if (warp == 0) prefix_rows<F>(a, pre, len, blockIdx.x == 0);
   __syncthreads();
   const int T = pre[a.B], n = runs(a.n_cta, T);
   const int cta = blockIdx.x;
@@ -638,13 +672,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   static_assert(F::at(0, 0) == 0 && 32 % F::kChunks == 0, "lane-fixed pieces");
   constexpr int kPieces = F::kUnit * F::kChunks / 32;
   const uint32_t lane_at = F::at(lane / F::kChunks, lane % F::kChunks);
-  Item li = item_at(a, pre, t0);  // the item being loaded
+  Item li = item_at(a, pre, len, t0);  // the item being loaded
   int list_k = 0;                 // listed blocks: units list_k .. list_k + 31 of this warp have their ids in the lanes
   int ids = 0, ids_next = 0;
   auto fetch_ids = [&](int k) {   // lane i: the block of unit k + i of this warp
     const int t = t0 + warp + kW * (k + lane);
     if (t >= t1) return -1;
-    const Item it = item_at(a, pre, t);
+    const Item it = item_at(a, pre, len, t);
     const size_t base = (static_cast<size_t>(it.b) * a.Hkv + it.h) * a.n_select;
     return __ldg(a.blocks + base + (t - it.start) / (kBlockKeys / F::kUnit));
   };
@@ -668,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
     int nk = 0;
     if (t < t1) {
       if (t >= li.end) {
-        li = item_at(a, pre, t);
+        li = item_at(a, pre, len, t);
         if constexpr (F::kQuant) item_sources();
       }
       const uint32_t dst = ring_addr + slot * F::kStage + lane_at;
@@ -731,19 +765,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
     cp_async_commit();
     return nk;
   };
+  // the query rows of the item that holds unit t, without a commit of their own
+  float* qraw = reinterpret_cast<float*>(smem + L::qraw(a.B, G, NT));
+  auto fetch_query = [&](int t) {
+    const Item it = item_at(a, pre, len, t);
+    const float* q = a.q + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D;
+    for (int e = tid * 4; e < G * D; e += kThreads * 4) cp_async16(smem_addr(qraw + e), q + e, true);
+  };
+  fetch_query(t0);  // ahead of the stream: behind it they would wait for it
+  cp_async_commit();
   int ring_nk[STAGES];  // bf16: keys of the units in flight
-#pragma unroll
-  for (int i = 0; i < STAGES; ++i) ring_nk[i] = issue(i, i);
+  ring_nk[0] = issue(0, 0);
 
   // ---- items of this run
+  cp_async_wait<1>();
+  __syncthreads();
   int k = 0, slot = 0;
   for (int t = t0; t < t1;) {
-    const Item it = item_at(a, pre, t);
+    const Item it = item_at(a, pre, len, t);
     const int seg_end = min(t1, it.end);
     if (warp < NT)
-      stage_query<F>(a.q + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D, G, warp,
-                     a.scale_log2, words, f_smem, zq_smem);
+      stage_query<F>(qraw, G, warp, a.scale_log2, words, f_smem, zq_smem);
     __syncthreads();
+    if (t == t0) {
+#pragma unroll
+      for (int i = 1; i < STAGES; ++i) ring_nk[i] = issue(i, i);
+    }
+    if (seg_end < t1) fetch_query(seg_end);  // the next item's, with the next commit
     float fs[NT];
     uint32_t zq[NT];
 #pragma unroll
@@ -774,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
       }
       slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
+    if (seg_end < t1) cp_async_wait<0>();
     // the warps' states, each relative to its own maximum
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -784,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
       for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
       for (int gr = 0; gr < F::NG; ++gr)
-        zs[gr] = __shfl_sync(0xffffffffu, st.zs[nt][0] + st.zs[nt][1], 4 * (2 * gr + 1) + c);
+        zs[gr] = __shfl_sync(0xffffffffu, st.zs[nt], 4 * (2 * gr + 1) + c);
       if (g == 0) {
         ms[warp * kMaxG + h] = st.m[nt];
         ls[warp * kMaxG + h] = l;
@@ -847,13 +896,13 @@ __global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant_
   extern __shared__ __align__(16) int pre[];
   constexpr int D = F::D;
   const int G = a.Hq / a.Hkv, head = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
-  if (threadIdx.x < 32) prefix_rows<F>(a, pre, false);
+  if (threadIdx.x < 32) prefix_rows<F>(a, pre, pre + a.B + 1, false);
   __syncthreads();
   const int T = pre[a.B], units = (pre[b + 1] - pre[b]) / a.Hkv;
   pdl_wait();
   float* out = a.o + (static_cast<size_t>(b) * a.Hq + head) * D + d;
   if (units == 0) {
-    if (a.pos[b] == -1) *out = 0.f;
+    if (pre[a.B + 1 + b] == 0) *out = 0.f;
     return;
   }
   const int n = runs(a.n_cta, T), g = head / G, h = head - g * G;
@@ -905,7 +954,7 @@ cudaError_t run(const LongAttnArgs& a, cudaStream_t st) {
   const uint32_t smem = Smem<F, stages<F, NT>()>::bytes(a.B, a.Hq / a.Hkv, NT);
   cudaError_t e = launch(long_attn_kernel<F, NT, stages<F, NT>()>, dim3(a.n_cta), dim3(kThreads), smem, st, false, a);
   if (e != cudaSuccess) return e;
-  return launch(long_merge_kernel<F>, dim3(a.Hq, a.B), dim3(F::D), (a.B + 1) * 4, st, true, a);
+  return launch(long_merge_kernel<F>, dim3(a.Hq, a.B), dim3(F::D), (2 * a.B + 1) * 4, st, true, a);
 }
 template <class F>
 cudaError_t run_format(const LongAttnArgs& a, cudaStream_t st) {
