@@ -94,43 +94,71 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __gri
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 
-// Largest score first; a NaN counts as -infinity.
+// Larger score, larger key; a NaN counts as -infinity.
 __device__ __forceinline__ uint32_t score_key(float s) {
   return float_order_key(s == s ? s + 0.0f : -INFINITY);
 }
 
-// Sum over the CTA of one int per thread; every thread gets it.
-__device__ __forceinline__ int cta_sum(int v, int* red) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int s = 0;
+// The sums over LANES lanes of kBatch values per lane: lane i of the group
+// gets the sum of value i / (LANES / kBatch).  Each step exchanges half of the
+// values still held, so that the batch takes kBatch + 1 (or 2) shuffles, not
+// 4 or 5 for every value.
+constexpr int kBatch = 8;
+template <int LANES>
+__device__ __forceinline__ float batch_sum(float (&s)[kBatch]) {
+  const int lane = threadIdx.x & 31;
+  int width = kBatch;
 #pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) s += red[i];
-  return s;
+  for (int o = LANES / 2; o >= LANES / kBatch; o >>= 1) {
+    width >>= 1;
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < kBatch / 2; ++i) {
+      if (i < width) {
+        const float give = up ? s[i] : s[i + width], keep = up ? s[i + width] : s[i];
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = LANES / kBatch / 2; o > 0; o >>= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+  return s[0];
 }
 
 // One CTA per (row, KV head).  The row's blocks 0 .. pos / 64 are scored in
-// fp32; the cut is found by bisection over the order-preserving integer keys.
-// An fp32 score is within E of the exact one, so blocks more than 2 E above
-// the cut are in and those more than 2 E below are out whatever the rounding;
-// the few between are scored again in 64 bits and ranked (ties: the lower
-// block), so that the choice is that of the exact scores.
-// Bound by latency and, per CTA, by reading 4 D bytes per block.
+// fp32; the cut is found on order-preserving integer keys, four bits per round
+// (warp w counts the keys at or above the w-th of 15 trial cuts).  An fp32
+// score is within E of the exact one, so blocks more than 2 E above the cut are
+// in and those more than 2 E below are out whatever the rounding; the few
+// between are scored again in 64 bits and ranked (ties: the lower block), so
+// that the choice is that of the exact scores.
+// Bound by latency: the chain position, query, bounds, cut, list, each a few
+// hundred nanoseconds, and by one SM's reading of 4 D bytes per block.
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid_constant__ SelectBlocksArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int kVec = 2 * D / 8;                       // 16-byte vectors of a block's bounds
-  constexpr int kPerWarp = 32 / (kVec < 32 ? kVec : 32);  // blocks a warp scores side by side
+  constexpr int kVec = 2 * D / 8;       // 16-byte vectors of a block's bounds
+  constexpr int kPerWarp = 32 / kVec;   // blocks a warp scores side by side
   __shared__ float w32[2 * D];
   __shared__ float err_red[kSelWarps];
-  __shared__ int red[kSelWarps];
+  __shared__ int counts[2][kSelWarps];
+  __shared__ int n_near, n_over;
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
   const size_t item = static_cast<size_t>(b) * a.Hkv + h;
+  const float* q = a.q + (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * G) * D;
   int32_t* out = a.blocks + item * a.n_select;
   const int p = a.pos[b];
+  if (tid < D) {
+    float P = 0.f, N = 0.f;
+    for (int i = 0; i < G; ++i) {
+      const float x = __ldg(q + i * D + tid);
+      if (x > 0.f) P += x;
+      else N += x;  // a NaN goes here
+    }
+    w32[tid] = P;
+    w32[D + tid] = N;
+  }
   if (p < -1 || p >= a.S_max) {
     if (h == 0 && tid == 0) atomicOr(a.err, kErrPosRange);
     return;
@@ -140,37 +168,30 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
     for (int i = tid; i < a.n_select; i += kSelThreads) out[i] = i < nb ? i : -1;
     return;
   }
-  float* score = reinterpret_cast<float*>(smem);                                // [nb]
+  uint32_t* key = reinterpret_cast<uint32_t*>(smem);                            // [nb]
   double* exact = reinterpret_cast<double*>(smem + (a.NB * 4 + 15) / 16 * 16);  // [nb], of the blocks in `list`
   int* list = reinterpret_cast<int*>(exact + a.NB);                             // blocks near the cut
-  for (int d = tid; d < D; d += kSelThreads) {
-    double P = 0., N = 0.;
-    for (int i = 0; i < G; ++i) {
-      const double q = a.q[(static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * G + i) * D + d];
-      if (q > 0.) P += q;
-      else N += q;  // a NaN goes here
-    }
-    w32[d] = static_cast<float>(P);
-    w32[D + d] = static_cast<float>(N);
-  }
-  __syncthreads();
   // blocks lo_free .. hi_free - 1 compete; the others are taken
   const int lo_free = min(a.n_first, nb), hi_free = max(lo_free, nb - a.n_last);
   const int want = a.n_select - (nb - (hi_free - lo_free));
   const uint4* rows = reinterpret_cast<const uint4*>(a.bounds + item * a.NB * 2 * D);
   const int part = lane / kVec, vec = lane % kVec;  // D = 64: two blocks side by side
+  constexpr int kStep = kSelWarps * kPerWarp * kBatch;
+  uint4 u[kBatch];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      u[i] = __ldg(rows + static_cast<size_t>(min(j0 + i * kPerWarp + part, nb - 1)) * kVec + vec);
+  };
+  const int first = lo_free + warp * kPerWarp * kBatch;
+  if (first < hi_free) load(first);
+  if (tid == 0) n_near = n_over = 0;
+  __syncthreads();
   float w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = w32[8 * vec + i];
   float amax = 0.f;  // the largest sum of term magnitudes that this lane met
-  constexpr int kBatch = 8;
-  for (int j0 = lo_free + warp * kPerWarp * kBatch; j0 < hi_free; j0 += kSelWarps * kPerWarp * kBatch) {
-    uint4 u[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int j = min(j0 + i * kPerWarp + part, hi_free - 1);
-      u[i] = __ldg(rows + static_cast<size_t>(j) * kVec + vec);
-    }
+  for (int j0 = first; j0 < hi_free; j0 += kStep) {
     float s[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -186,18 +207,15 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
       s[i] = t;
       amax = fmaxf(amax, m == m ? m : INFINITY);
     }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-#pragma unroll
-      for (int o = kVec / 2; o > 0; o >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-      const int j = j0 + i * kPerWarp + part;
-      if (vec == 0 && j < hi_free) score[j] = s[i];
-    }
+    if (j0 + kStep < hi_free) load(j0 + kStep);
+    const float sum = batch_sum<kVec>(s);
+    const int j = j0 + vec / (kVec / kBatch) * kPerWarp + part;
+    if (vec % (kVec / kBatch) == 0 && j < hi_free) key[j] = score_key(sum);
   }
-  // E: the rounding of the weights, products and sums is below 16 * 2^-24 of
-  // the sum of magnitudes (8 fused steps, 5 additions, 1 rounding of w), and
-  // 256 results below the normal range lose 2^-149 each.  Not finite: every
-  // block counts as near the cut.
+  // E: the rounding of the weights (15 additions), products and sums (8 fused
+  // steps, 5 additions) is below 32 * 2^-24 of the sum of magnitudes, and 256
+  // results below the normal range lose 2^-149 each.  Not finite: every block
+  // counts as near the cut.
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax += __shfl_xor_sync(0xffffffffu, amax, o);
   if (lane == 0) err_red[warp] = amax;
@@ -205,43 +223,43 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   float E = 0.f;
 #pragma unroll
   for (int i = 0; i < kSelWarps; ++i) E = fmaxf(E, err_red[i]);
-  E = fmaf(E, 1.0f / (1 << 20), 1e-41f);
-  // the want-th largest score, bit by bit
+  E = fmaf(E, 1.0f / (1 << 19), 1e-41f);
+  // the want-th largest key
   uint32_t cut = 0;
   if (want > 0) {
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t trial = cut | (1u << bit);
-      int n = 0;
-      for (int j = lo_free + tid; j < hi_free; j += kSelThreads) n += score_key(score[j]) >= trial ? 1 : 0;
-      if (cta_sum(n, red) >= want) cut = trial;
+#pragma unroll 1
+    for (int shift = 28; shift >= 0; shift -= 4) {
+      int* c = counts[(shift >> 2) & 1];
+      if (warp < 15) {
+        const uint32_t trial = cut | (static_cast<uint32_t>(warp + 1) << shift);
+        int n = 0;
+        for (int j = lo_free + lane; j < hi_free; j += 32) n += key[j] >= trial ? 1 : 0;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) c[warp] = n;
+      }
+      __syncthreads();
+      int digit = 0;  // the counts fall with the trial
+#pragma unroll
+      for (int i = 0; i < 15; ++i) digit += c[i] >= want ? 1 : 0;
+      cut |= static_cast<uint32_t>(digit) << shift;
     }
   }
   const float tau = float_from_order_key(cut);
-  // above: in; near the cut: listed in block order
-  int taken = 0, near = 0;  // of the blocks before the chunk
-  for (int base = lo_free; base < hi_free; base += kSelThreads) {
-    const int j = base + tid;
-    const float s = j < hi_free ? score[j] : 0.f;
-    const bool over = j < hi_free && s > tau + 2.f * E;
-    const bool close = j < hi_free && !over && !(s < tau - 2.f * E);
-    const unsigned mine = __ballot_sync(0xffffffffu, close);
-    taken += cta_sum(over ? 1 : 0, red);
-    __syncthreads();
-    if (lane == 0) red[warp] = __popc(mine);
-    __syncthreads();
-    int before = near;
-    for (int i = 0; i < kSelWarps; ++i) {
-      if (i < warp) before += red[i];
-      near += red[i];
-    }
-    if (close) list[before + __popc(mine & ((1u << lane) - 1u))] = j;
-    // the score's place now says whether the block is in
-    if (j < hi_free) score[j] = over ? 1.f : 0.f;
+  // above: in; near the cut: listed, in any order
+  int over = 0;
+  for (int j = lo_free + tid; j < hi_free; j += kSelThreads) {
+    const float s = float_from_order_key(key[j]);
+    const bool in = want > 0 && s > tau + 2.f * E;
+    if (in) ++over;
+    else if (want > 0 && !(s < tau - 2.f * E)) list[atomicAdd(&n_near, 1)] = j;
+    key[j] = in ? 1u : 0u;  // from here on: whether the block is in
   }
+  over = __reduce_add_sync(0xffffffffu, over);
+  if (lane == 0 && over) atomicAdd(&n_over, over);
   __syncthreads();
-  const int rest = want - taken;  // of the near ones
+  const int near = n_near, rest = want - n_over;  // of the near ones
   if (rest >= near) {
-    for (int i = tid; i < near; i += kSelThreads) score[list[i]] = 1.f;
+    for (int i = tid; i < near; i += kSelThreads) key[list[i]] = 1u;
   } else if (rest > 0) {
     for (int i = warp; i < near; i += kSelWarps) {
       const uint16_t* r = a.bounds + (item * a.NB + list[i]) * 2 * D;
@@ -250,8 +268,8 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
         const double hi = __uint_as_float(static_cast<uint32_t>(r[d]) << 16);
         const double lo = __uint_as_float(static_cast<uint32_t>(r[D + d]) << 16);
         for (int e = 0; e < G; ++e) {  // the definition itself: it also holds for infinite bounds
-          const double q = a.q[(static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * G + e) * D + d];
-          const double x = q * hi, y = q * lo;
+          const double qd = q[e * D + d];
+          const double x = qd * hi, y = qd * lo;
           s += x > y || x != x ? x : y;
         }
       }
@@ -262,25 +280,27 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
     __syncthreads();
     for (int i = tid; i < near; i += kSelThreads) {
       const double s = exact[i];
+      const int j = list[i];
       int better = 0;
-      for (int e = 0; e < near; ++e) better += exact[e] > s || (exact[e] == s && e < i) ? 1 : 0;
-      if (better < rest) score[list[i]] = 1.f;
+      for (int e = 0; e < near; ++e) better += exact[e] > s || (exact[e] == s && list[e] < j) ? 1 : 0;
+      if (better < rest) key[j] = 1u;
     }
   }
-  __syncthreads();
   // the chosen blocks in order
-  int done = 0;
-  for (int base = 0; base < nb; base += kSelThreads) {
-    const int j = base + tid;
-    const bool in = j < nb && (j < lo_free || j >= hi_free || score[j] != 0.f);
-    const unsigned mine = __ballot_sync(0xffffffffu, in);
+  int done = 0, turn = 0;
+  for (int base = 0; base < nb; base += kSelThreads, turn ^= 1) {
     __syncthreads();
-    if (lane == 0) red[warp] = __popc(mine);
+    const int j = base + tid;
+    const bool in = j < nb && (j < lo_free || j >= hi_free || key[j] != 0u);
+    const unsigned mine = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) counts[turn][warp] = __popc(mine);
     __syncthreads();
     int before = done;
+#pragma unroll
     for (int i = 0; i < kSelWarps; ++i) {
-      if (i < warp) before += red[i];
-      done += red[i];
+      const int n = counts[turn][i];
+      before += i < warp ? n : 0;
+      done += n;
     }
     if (in) out[before + __popc(mine & ((1u << lane) - 1u))] = j;
   }
