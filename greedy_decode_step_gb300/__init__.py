@@ -2,7 +2,8 @@
 
 Argument marshalling only: every function here checks tensor dtypes and
 shapes, passes raw device pointers and sizes to the library and turns a
-non-zero status into ``DecError``.  All arithmetic runs in the CUDA kernels of
+non-zero status into ``DecError`` (for the long-cache calls a compiled module,
+``csrc/binding.cpp``, does it).  All arithmetic runs in the CUDA kernels of
 ``libdec.so``; if the library is missing, every call raises.
 
 PyTorch supplies device memory and streams.
@@ -233,7 +234,6 @@ def dec_select_tokens(logits, token_out, u=None, prev_tokens=None, repetition_pe
 # ----------------------------------------------------------------------------- long caches
 
 BLOCK_KEYS = 64  # keys of a selectable block
-_f16, _u8 = torch.float16, torch.uint8
 
 
 def _expect(ok: bool, what: str):
@@ -241,78 +241,30 @@ def _expect(ok: bool, what: str):
         raise DecError(DEC_EINVAL, what)
 
 
-# The handle of a device's current stream without the Stream object around it
-# (these calls are short enough for its construction to count).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+def _native():
+    """The compiled marshalling of the calls below (they are too short for this file's); raises if it is not built."""
+    global _nat
+    if _nat is None:
+        lib()
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"the native binding is not built ({_build.BINDING}); run greedy_decode_step_gb300.build()")
+        from . import _binding
+        _binding.set_error(DecError)
+        _nat = _binding
+    return _nat
 
 
-def _handle(stream, index):
-    """Stream handle for tensors on CUDA device ``index``, the current one."""
+_nat = None
+
+
+def _handle(stream, t):
+    """Stream handle (an int) for tensors like ``t``; None for their device's current stream."""
     if stream is None:
-        return _raw_stream(index)
+        return None
     if isinstance(stream, torch.cuda.Stream):
-        _expect(stream.device.index == index, f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+        _expect(stream.device == t.device, f"the stream is on {stream.device}, the tensors are on {t.device}")
         return stream.cuda_stream
     return int(stream)
-
-
-def _gpu(t, dtype, shape, index, name):
-    """Pointer of a contiguous tensor of this dtype and shape on CUDA device ``index``."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    _expect(t.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _expect(t.get_device() == index, f"{name} is on {t.device}, other tensors of the call are not")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _run(index, stream, fn, *args):
-    """Calls the library on the tensors' device, whichever device is current."""
-    _expect(index >= 0, "the tensors must be on a CUDA device")
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, _raw_stream(index) if stream is None else _handle(stream, index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, _handle(stream, index))
-    if rc != DEC_OK:
-        _check(rc)
-
-
-def _kv4(k_codes, k_params, v_codes, v_params):
-    """Pointers and sizes of a 4-bit cache."""
-    _expect(k_codes.dim() == 4 and k_params.dim() == 5, "codes must be [B, Hkv, S_max, D/2], params "
-                                                        "[B, Hkv, S_max, D/group, 2]")
-    B, Hkv, S, half = k_codes.shape
-    NG = k_params.shape[3]
-    D = 2 * half
-    _expect(NG >= 1 and D % NG == 0, f"{NG} groups do not divide head_dim {D}")
-    dev, cs, ps = k_codes.get_device(), k_codes.shape, (B, Hkv, S, NG, 2)
-    return (_gpu(k_codes, _u8, cs, dev, "k_codes"), _gpu(k_params, _f16, ps, dev, "k_params"),
-            _gpu(v_codes, _u8, cs, dev, "v_codes"), _gpu(v_params, _f16, ps, dev, "v_params")), \
-        (B, Hkv, D, D // NG, S), dev
-
-
-def _rows(k, v, B, Hkv, D, dev, names):
-    """Pointers, type and strides of K and V rows [B, T, Hkv, D], strided alike."""
-    shape, st = k.shape, k.stride()
-    if not (k.dtype is v.dtype and (k.dtype is _f32 or k.dtype is _bf16) and len(shape) == 4 and v.shape == shape and
-            shape[0] == B and shape[2] == Hkv and shape[3] == D and st[3] == 1 and v.stride() == st and
-            k.get_device() == dev and v.get_device() == dev):
-        for t, name in zip((k, v), names):
-            if t.dtype != _f32 and t.dtype != _bf16:
-                raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-            _expect(t.dim() == 4 and t.shape[0] == B and t.shape[2:] == (Hkv, D) and t.stride(3) == 1,
-                    f"{name} must be rows [{B}, T, {Hkv}, {D}] with contiguous values, got {tuple(t.shape)} "
-                    f"strided {t.stride()}")
-            _expect(t.get_device() == dev, f"{name} is on {t.device}, the cache is not")
-        _expect(k.dtype == v.dtype and k.shape == v.shape, f"{names[0]} and {names[1]} must be of one type and shape")
-        _expect(all(n <= 1 or x == y for n, x, y in zip(shape, st, v.stride())),
-                f"{names[0]} and {names[1]} must be strided alike")
-    # a dim of one element may carry any stride
-    return (k.data_ptr(), v.data_ptr(), 1 if k.dtype is _bf16 else 0, st[0] if B > 1 else 0,
-            st[1] if shape[1] > 1 else 0, st[2] if Hkv > 1 else 0)
 
 
 def dec_kv4_store(k, v, pos, k_codes, k_params, v_codes, v_params, tokens=None, lens=None, from_cache: bool = False,
@@ -320,91 +272,40 @@ def dec_kv4_store(k, v, pos, k_codes, k_params, v_codes, v_params, tokens=None, 
     """Quantises K and V rows (views [B, T, Hkv, D], float32 or bf16) into the 4-bit cache at slots
     ``pos[b] ..``.  ``from_cache``: the rows are a cache's, indexed by slot (``cache.transpose(1, 2)``), and
     ``tokens`` of them are taken from ``pos[b]`` on.  ``lens`` (int32 [B]): tokens of each row, at most ``tokens``."""
-    held, (B, Hkv, D, group, S), dev = _kv4(k_codes, k_params, v_codes, v_params)
-    rows, n = _rows(k, v, B, Hkv, D, dev, ("k", "v")), k.shape[1]
-    T = n if tokens is None else int(tokens)
-    _run(dev, stream, (_lib or lib()).dec_kv4_store, *rows, int(from_cache), n, _gpu(pos, _i32, (B,), dev, "pos"),
-         None if lens is None else _gpu(lens, _i32, (B,), dev, "lens"), T, *held, B, Hkv, D, group, S)
+    (_nat or _native()).kv4_store(k, v, pos, k_codes, k_params, v_codes, v_params, tokens, lens, from_cache,
+                                  _handle(stream, k_codes))
 
 
 def dec_kv4_load(k_codes, k_params, v_codes, v_params, pos, k_out, v_out, lens=None, stream=None):
     """Reads slots ``pos[b] ..`` of the 4-bit cache into ``k_out`` and ``v_out`` (views [B, T, Hkv, D], float32 or
     bf16); rows ``t >= lens[b]`` are left as they are."""
-    held, (B, Hkv, D, group, S), dev = _kv4(k_codes, k_params, v_codes, v_params)
-    kp, vp, bf16, *st = _rows(k_out, v_out, B, Hkv, D, dev, ("k_out", "v_out"))
-    _run(dev, stream, (_lib or lib()).dec_kv4_load, *held, _gpu(pos, _i32, (B,), dev, "pos"),
-         None if lens is None else _gpu(lens, _i32, (B,), dev, "lens"), k_out.shape[1], kp, vp, bf16, *st, B, Hkv, D,
-         group, S)
+    (_nat or _native()).kv4_load(k_codes, k_params, v_codes, v_params, pos, k_out, v_out, lens, _handle(stream, k_codes))
 
 
 def long_attn_workspace_size(Hq, Hkv, D) -> int:
     return int(lib().dec_long_attn_workspace_size(Hq, Hkv, D))
 
 
-def _long_ws(ws, Hq, Hkv, D, dev, stream):
-    if ws is None:
-        need = long_attn_workspace_size(Hq, Hkv, D)
-        if need == 0:
-            raise DecError(DEC_EINVAL, lib().dec_last_error().decode())
-        _expect(dev >= 0, "the tensors must be on a CUDA device")
-        if stream is None:
-            return torch.empty(need, dtype=_u8, device=dev)
-        # made on the stream that uses it, so that dropping it is safe
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
-        with torch.cuda.stream(s):
-            return torch.empty(need, dtype=_u8, device=dev)
-    _expect(ws.get_device() == dev and ws.is_contiguous(), "ws must be contiguous memory on the tensors' device")
-    return ws
-
-
 def dec_kv4_decode_attn(q, k_codes, k_params, v_codes, v_params, pos, o, ws=None, stream=None):
     """GQA decode attention over a 4-bit cache; returns the workspace, for the next call."""
-    held, (B, Hkv, D, group, S), dev = _kv4(k_codes, k_params, v_codes, v_params)
-    Hq = q.shape[1] if q.dim() == 3 else 0
-    ws = _long_ws(ws, Hq, Hkv, D, dev, stream)
-    _run(dev, stream, (_lib or lib()).dec_kv4_decode_attn, _gpu(q, _f32, (B, Hq, D), dev, "q"), *held,
-         _gpu(pos, _i32, (B,), dev, "pos"), _gpu(o, _f32, (B, Hq, D), dev, "o"), ws.data_ptr(), ws.nbytes, B, Hq,
-         Hkv, D, group, S)
-    return ws
+    return (_nat or _native()).kv4_decode_attn(q, k_codes, k_params, v_codes, v_params, pos, o, ws, _handle(stream, k_codes))
 
 
 def dec_block_bounds(k_cache, pos, bounds, tokens: int = 1, stream=None):
     """Channel bounds (bf16 [B, Hkv, ceil(S_max/64), 2, D]) of the blocks that slots
     ``pos[b] .. pos[b] + tokens - 1`` of the bf16 key cache touch."""
-    _expect(k_cache.dim() == 4, "k_cache must be [B, Hkv, S_max, D]")
-    B, Hkv, S, D = k_cache.shape
-    dev = k_cache.get_device()
-    _run(dev, stream, (_lib or lib()).dec_block_bounds, _gpu(k_cache, _bf16, k_cache.shape, dev, "k_cache"),
-         _gpu(pos, _i32, (B,), dev, "pos"), int(tokens),
-         _gpu(bounds, _bf16, (B, Hkv, (S + BLOCK_KEYS - 1) // BLOCK_KEYS, 2, D), dev, "bounds"), B, Hkv, D, S)
+    (_nat or _native()).block_bounds(k_cache, pos, bounds, tokens, _handle(stream, k_cache))
 
 
 def dec_select_blocks(q, bounds, pos, blocks, n_first: int = 1, n_last: int = 1, stream=None):
     """Fills ``blocks`` (int32 [B, Hkv, n_select]) with the blocks of the largest score bounds, ascending, -1 behind
     the last; the first ``n_first`` and last ``n_last`` blocks of a row are always among them."""
-    _expect(q.dim() == 3 and bounds.dim() == 5 and blocks.dim() == 3, "q must be [B, Hq, D], bounds "
-            "[B, Hkv, blocks, 2, D], blocks [B, Hkv, n_select]")
-    B, Hq, D = q.shape
-    Hkv, NB, n = bounds.shape[1], bounds.shape[2], blocks.shape[2]
-    dev = q.get_device()
-    _run(dev, stream, (_lib or lib()).dec_select_blocks, _gpu(q, _f32, q.shape, dev, "q"),
-         _gpu(bounds, _bf16, (B, Hkv, NB, 2, D), dev, "bounds"), _gpu(pos, _i32, (B,), dev, "pos"),
-         _gpu(blocks, _i32, (B, Hkv, n), dev, "blocks"), n, int(n_first), int(n_last), B, Hq, Hkv, D, NB * BLOCK_KEYS)
+    (_nat or _native()).select_blocks(q, bounds, pos, blocks, n_first, n_last, _handle(stream, q))
 
 
 def dec_block_decode_attn(q, k_cache, v_cache, pos, blocks, o, ws=None, stream=None):
     """GQA decode attention over the listed 64-key blocks of a bf16 cache; returns the workspace."""
-    _expect(q.dim() == 3 and k_cache.dim() == 4 and blocks.dim() == 3, "q must be [B, Hq, D], the caches "
-            "[B, Hkv, S_max, D], blocks [B, Hkv, n_select]")
-    B, Hkv, S, D = k_cache.shape
-    Hq, n = q.shape[1], blocks.shape[2]
-    dev = k_cache.get_device()
-    ws = _long_ws(ws, Hq, Hkv, D, dev, stream)
-    _run(dev, stream, (_lib or lib()).dec_block_decode_attn, _gpu(q, _f32, (B, Hq, D), dev, "q"),
-         _gpu(k_cache, _bf16, k_cache.shape, dev, "k_cache"), _gpu(v_cache, _bf16, k_cache.shape, dev, "v_cache"),
-         _gpu(pos, _i32, (B,), dev, "pos"), _gpu(blocks, _i32, (B, Hkv, n), dev, "blocks"), n,
-         _gpu(o, _f32, (B, Hq, D), dev, "o"), ws.data_ptr(), ws.nbytes, B, Hq, Hkv, D, S)
-    return ws
+    return (_nat or _native()).block_decode_attn(q, k_cache, v_cache, pos, blocks, o, ws, _handle(stream, k_cache))
 
 
 # ----------------------------------------------------------------------------- model / state

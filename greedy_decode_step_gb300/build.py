@@ -1,10 +1,12 @@
 """Build libdec.so (sm_103a) in place with nvcc: one object per translation
-unit, compiled in parallel, then linked against the shared CUDA runtime."""
+unit, compiled in parallel, then linked against the shared CUDA runtime; and
+with the host compiler the extension module ``_binding`` against torch."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -13,6 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdec.so")
+BINDING = os.path.join(HERE, "_binding.so")
 UNITS = ["api.cu", "gemv_qkv.cu", "gemv_glu.cu", "gemv_resid.cu", "gemv_head.cu", "attn.cu", "step.cu", "prefill.cu",
          "select.cu", "tcgemm.cu", "kv4.cu", "long_attn.cu", "blocks.cu", "long_api.cu"]
 HEADERS = ["dec_common.cuh", "dec_kernels.cuh", "dec_attn.cuh", "dec_step.cuh", "dec_launch.cuh", "dec_long.cuh",
@@ -29,6 +32,18 @@ def nvcc() -> str:
 def _flags():
     return [ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", CSRC, "-I", INCLUDE,
             "--expt-relaxed-constexpr"]
+
+
+def _binding_job(force: bool):
+    """The compile command of binding.cpp, or None, and its object (one per torch version)."""
+    import torch
+    src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "libdec.h")
+    obj = os.path.join(BUILD, f"binding_{torch.__version__}.o")
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    paths = [root, os.path.join(root, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda, INCLUDE]
+    cmd = ["g++", "-O2", "-fPIC", "-std=c++17", *(f"-I{p}" for p in paths), "-c", src, "-o", obj]
+    return (cmd if force or _stale(obj, [src, header, __file__]) else None), obj
 
 
 def _stale(target: str, deps) -> bool:
@@ -51,20 +66,32 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if force or _stale(obj, [src, __file__] + headers):
             jobs.append([nvcc(), *_flags(), *extra, "-c", src, "-o", obj])
 
+    binding_cmd, binding_obj = _binding_job(force)
+    if binding_cmd:
+        jobs.insert(0, binding_cmd)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
 
-    with ThreadPoolExecutor(max_workers=min(len(UNITS), os.cpu_count() or 1)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 1)) as ex:
         list(ex.map(run, jobs))
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cuda_lib = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "lib64")
         run([nvcc(), ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs, "-Xlinker", f"-rpath,{cuda_lib}"])
         os.replace(tmp, LIB)
+    if force or jobs or _stale(BINDING, [binding_obj, LIB]):
+        import torch
+        tmp = BINDING + f".tmp{os.getpid()}"
+        libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+        # torch is imported first, so its libraries are found by name; libdec.so lies beside the module
+        run(["g++", "-shared", "-o", tmp, binding_obj, "-L", HERE, "-l:libdec.so", "-L", libs, "-ltorch_python",
+             "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, BINDING)
     return LIB
 
 

@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __gri
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelMaxCluster = 4;
 
 // Larger score, larger key; a NaN counts as -infinity.
 __device__ __forceinline__ uint32_t score_key(float s) {
@@ -125,27 +126,104 @@ __device__ __forceinline__ float batch_sum(float (&s)[kBatch]) {
   return s[0];
 }
 
-// One CTA per (row, KV head).  The row's blocks 0 .. pos / 64 are scored in
-// fp32; the cut is found on order-preserving integer keys, four bits per round
-// (warp w counts the keys at or above the w-th of 15 trial cuts).  An fp32
-// score is within E of the exact one, so blocks more than 2 E above the cut are
-// in and those more than 2 E below are out whatever the rounding; the few
-// between are scored again in 64 bits and ranked (ties: the lower block), so
-// that the choice is that of the exact scores.
+// The want-th largest of n <= kSelThreads keys, by bisection in warp 0, whose
+// lanes hold them in registers; it ends once a trial splits off exactly `want`
+// keys (about log2 n + 2 rounds for unlike keys, 32 at most).
+__device__ __forceinline__ uint32_t kth_largest_warp(const uint32_t* key, int n, int want, uint32_t* result) {
+  if (threadIdx.x < 32) {
+    constexpr int kPer = kSelThreads / 32;
+    uint32_t k[kPer], most = 0, least = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = threadIdx.x + 32 * i;
+      k[i] = j < n ? key[j] : 0u;  // below every trial
+      most = max(most, k[i]);
+      least = min(least, j < n ? k[i] : 0xFFFFFFFFu);
+    }
+    uint32_t lo = __reduce_min_sync(0xffffffffu, least), hi = __reduce_max_sync(0xffffffffu, most);
+    // at least `want` keys reach lo; fewer reach hi + 1
+    while (lo < hi) {
+      const uint32_t trial = hi - (hi - lo) / 2;
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c += k[i] >= trial ? 1 : 0;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (c == want) {
+        uint32_t m = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) m = min(m, k[i] >= trial ? k[i] : 0xFFFFFFFFu);
+        lo = hi = __reduce_min_sync(0xffffffffu, m);
+      } else if (c > want) {
+        lo = trial;
+      } else {
+        hi = trial - 1;
+      }
+    }
+    if (threadIdx.x == 0) *result = lo;
+  }
+  __syncthreads();
+  return *result;
+}
+
+// The same for any n: four bits per round, warp w counting the keys at or
+// above the w-th of 15 trial cuts.
+__device__ __forceinline__ uint32_t kth_largest_cta(const uint32_t* key, int n, int want,
+                                                    int (*counts)[kSelWarps]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t cut = 0;
+#pragma unroll 1
+  for (int shift = 28; shift >= 0; shift -= 4) {
+    int* c = counts[(shift >> 2) & 1];
+    if (warp < 15) {
+      const uint32_t trial = cut | (static_cast<uint32_t>(warp + 1) << shift);
+      int m = 0;
+#pragma unroll 4
+      for (int j = lane; j < n; j += 32) m += key[j] >= trial ? 1 : 0;
+      m = __reduce_add_sync(0xffffffffu, m);
+      if (lane == 0) c[warp] = m;
+    }
+    __syncthreads();
+    int digit = 0;  // the counts fall with the trial
+#pragma unroll
+    for (int i = 0; i < 15; ++i) digit += c[i] >= want ? 1 : 0;
+    cut |= static_cast<uint32_t>(digit) << shift;
+  }
+  return cut;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores a word at CTA 0's copy of a shared-memory address.
+__device__ __forceinline__ void store_cta0(const void* p, uint32_t v) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(p)));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+// A cluster of CTAs per (row, KV head): all of them score the row's blocks
+// 0 .. pos / 64 in fp32, in turn, into CTA 0's shared memory, and CTA 0 goes on
+// alone.  The cut is found on order-preserving integer keys.  An fp32 score is
+// within E of the exact one, so blocks more than 2 E above the cut are in and
+// those more than 2 E below are out whatever the rounding; the few between are
+// scored again in 64 bits and ranked (ties: the lower block), so that the
+// choice is that of the exact scores.
 // Bound by latency: the chain position, query, bounds, cut, list, each a few
-// hundred nanoseconds, and by one SM's reading of 4 D bytes per block.
+// hundred nanoseconds; one SM alone takes 6 us to read 512 blocks' bounds.
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid_constant__ SelectBlocksArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int kVec = 2 * D / 8;       // 16-byte vectors of a block's bounds
   constexpr int kPerWarp = 32 / kVec;   // blocks a warp scores side by side
   __shared__ float w32[2 * D];
-  __shared__ float err_red[kSelWarps];
+  __shared__ float err_red[kSelMaxCluster][kSelWarps];
   __shared__ int counts[2][kSelWarps];
   __shared__ int n_near, n_over;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ uint32_t s_cut;
+  const int ctas = a.cluster, rank = blockIdx.x % ctas;
+  const int h = blockIdx.x / ctas, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
   const size_t item = static_cast<size_t>(b) * a.Hkv + h;
+  if (ctas > 1) cluster_arrive();  // before the others write here, CTA 0 has started
   const float* q = a.q + (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * G) * D;
   int32_t* out = a.blocks + item * a.n_select;
   const int p = a.pos[b];
@@ -159,13 +237,13 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
     w32[tid] = P;
     w32[D + tid] = N;
   }
-  if (p < -1 || p >= a.S_max) {
-    if (h == 0 && tid == 0) atomicOr(a.err, kErrPosRange);
-    return;
-  }
+  const bool refused = p < -1 || p >= a.S_max;
   const int nb = p < 0 ? 0 : p / kBlockKeys + 1;
-  if (nb <= a.n_select) {  // all of them
-    for (int i = tid; i < a.n_select; i += kSelThreads) out[i] = i < nb ? i : -1;
+  if (refused || nb <= a.n_select) {  // nothing, or all of them
+    if (refused && h == 0 && rank == 0 && tid == 0) atomicOr(a.err, kErrPosRange);
+    if (!refused && rank == 0)
+      for (int i = tid; i < a.n_select; i += kSelThreads) out[i] = i < nb ? i : -1;
+    if (ctas > 1) cluster_wait();
     return;
   }
   uint32_t* key = reinterpret_cast<uint32_t*>(smem);                            // [nb]
@@ -176,22 +254,23 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   const int want = a.n_select - (nb - (hi_free - lo_free));
   const uint4* rows = reinterpret_cast<const uint4*>(a.bounds + item * a.NB * 2 * D);
   const int part = lane / kVec, vec = lane % kVec;  // D = 64: two blocks side by side
-  constexpr int kStep = kSelWarps * kPerWarp * kBatch;
+  const int step = ctas * kSelWarps * kPerWarp * kBatch;
   uint4 u[kBatch];
   auto load = [&](int j0) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       u[i] = __ldg(rows + static_cast<size_t>(min(j0 + i * kPerWarp + part, nb - 1)) * kVec + vec);
   };
-  const int first = lo_free + warp * kPerWarp * kBatch;
+  const int first = lo_free + (rank * kSelWarps + warp) * kPerWarp * kBatch;
   if (first < hi_free) load(first);
   if (tid == 0) n_near = n_over = 0;
+  if (ctas > 1) cluster_wait();
   __syncthreads();
   float w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = w32[8 * vec + i];
   float amax = 0.f;  // the largest sum of term magnitudes that this lane met
-  for (int j0 = first; j0 < hi_free; j0 += kStep) {
+  for (int j0 = first; j0 < hi_free; j0 += step) {
     float s[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -207,10 +286,13 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
       s[i] = t;
       amax = fmaxf(amax, m == m ? m : INFINITY);
     }
-    if (j0 + kStep < hi_free) load(j0 + kStep);
+    if (j0 + step < hi_free) load(j0 + step);
     const float sum = batch_sum<kVec>(s);
     const int j = j0 + vec / (kVec / kBatch) * kPerWarp + part;
-    if (vec % (kVec / kBatch) == 0 && j < hi_free) key[j] = score_key(sum);
+    if (vec % (kVec / kBatch) == 0 && j < hi_free) {
+      if (ctas > 1) store_cta0(key + j, score_key(sum));
+      else key[j] = score_key(sum);
+    }
   }
   // E: the rounding of the weights (15 additions), products and sums (8 fused
   // steps, 5 additions) is below 32 * 2^-24 of the sum of magnitudes, and 256
@@ -218,32 +300,24 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   // counts as near the cut.
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax += __shfl_xor_sync(0xffffffffu, amax, o);
-  if (lane == 0) err_red[warp] = amax;
+  if (lane == 0) {
+    if (ctas > 1) store_cta0(&err_red[rank][warp], __float_as_uint(amax));
+    else err_red[0][warp] = amax;
+  }
+  if (ctas > 1) {
+    cluster_arrive();
+    cluster_wait();
+    if (rank) return;
+  }
   __syncthreads();
   float E = 0.f;
+  for (int i = 0; i < ctas; ++i)
 #pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) E = fmaxf(E, err_red[i]);
+    for (int j = 0; j < kSelWarps; ++j) E = fmaxf(E, err_red[i][j]);
   E = fmaf(E, 1.0f / (1 << 19), 1e-41f);
-  // the want-th largest key
-  uint32_t cut = 0;
-  if (want > 0) {
-#pragma unroll 1
-    for (int shift = 28; shift >= 0; shift -= 4) {
-      int* c = counts[(shift >> 2) & 1];
-      if (warp < 15) {
-        const uint32_t trial = cut | (static_cast<uint32_t>(warp + 1) << shift);
-        int n = 0;
-        for (int j = lo_free + lane; j < hi_free; j += 32) n += key[j] >= trial ? 1 : 0;
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) c[warp] = n;
-      }
-      __syncthreads();
-      int digit = 0;  // the counts fall with the trial
-#pragma unroll
-      for (int i = 0; i < 15; ++i) digit += c[i] >= want ? 1 : 0;
-      cut |= static_cast<uint32_t>(digit) << shift;
-    }
-  }
+  const uint32_t cut = want == 0                         ? 0u
+                       : hi_free - lo_free <= kSelThreads ? kth_largest_warp(key + lo_free, hi_free - lo_free, want, &s_cut)
+                                                          : kth_largest_cta(key + lo_free, hi_free - lo_free, want, counts);
   const float tau = float_from_order_key(cut);
   // above: in; near the cut: listed, in any order
   int over = 0;
@@ -316,10 +390,31 @@ cudaError_t launch_block_bounds(const BoundsArgs& a, int D, cudaStream_t st) {
                  : launch(block_bounds_kernel<128>, grid, dim3(kBoundThreads), 0, st, false, a);
 }
 
-cudaError_t launch_select_blocks(const SelectBlocksArgs& a, int D, cudaStream_t st) {
-  const dim3 grid(a.Hkv, a.B);
-  return D == 64 ? launch(select_blocks_kernel<64>, grid, dim3(kSelThreads), select_smem(a.NB), st, false, a)
-                 : launch(select_blocks_kernel<128>, grid, dim3(kSelThreads), select_smem(a.NB), st, false, a);
+// CTAs per item: as many as fit the GPU at one per SM beside the other items',
+// but no more than leave each warp its batch of blocks.  (b = 1, 8 heads, 512
+// blocks: 10.0 us with one, 8.7 with two, 8.0 with four.)
+int select_cluster(int items, int NB, int D, int sms) {
+  const int batch = kSelWarps * (32 / (2 * D / 8)) * kBatch;
+  int c = 1;
+  while (c < kSelMaxCluster && 2 * c * items <= 2 * sms && c * batch < NB) c *= 2;
+  return c;
+}
+
+cudaError_t launch_select_blocks(SelectBlocksArgs a, int D, int sms, cudaStream_t st) {
+  a.cluster = select_cluster(a.B * a.Hkv, a.NB, D, sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.Hkv * a.cluster, a.B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = select_smem(a.NB);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  return D == 64 ? cudaLaunchKernelEx(&cfg, select_blocks_kernel<64>, a)
+                 : cudaLaunchKernelEx(&cfg, select_blocks_kernel<128>, a);
 }
 
 cudaError_t allow_smem_blocks() {

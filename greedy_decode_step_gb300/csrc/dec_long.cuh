@@ -78,9 +78,10 @@ struct SelectBlocksArgs {
   const int32_t* pos;            // [B] last key
   int32_t* blocks;               // [B][Hkv][n_select]
   int B, Hq, Hkv, S_max, NB, n_select, n_first, n_last;
+  int cluster;                   // CTAs per (row, KV head): set by the launch
   uint32_t* err;
 };
-cudaError_t launch_select_blocks(const SelectBlocksArgs& a, int D, cudaStream_t st);
+cudaError_t launch_select_blocks(SelectBlocksArgs a, int D, int sms, cudaStream_t st);
 cudaError_t allow_smem_blocks();
 
 }  // namespace dec

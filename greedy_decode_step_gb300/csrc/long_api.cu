@@ -252,7 +252,7 @@ int dec_select_blocks(const float* q, const void* bounds, const int32_t* pos, in
   a.n_select = n_select;
   a.n_first = n_first;
   a.n_last = n_last;
-  DEC_LAUNCHED(launch_select_blocks(a, D, static_cast<cudaStream_t>(stream)), "block selection");
+  DEC_LAUNCHED(launch_select_blocks(a, D, sms, static_cast<cudaStream_t>(stream)), "block selection");
   return DEC_OK;
 }
 

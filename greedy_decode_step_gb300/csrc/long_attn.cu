@@ -177,16 +177,22 @@ struct Bf16 {
 // ----------------------------------------------------------------------------- plan
 
 // Units of all items end to end: row b's Hkv items hold pre[b] .. pre[b + 1].
-// CTA c of n takes units [T c / n, T (c + 1) / n).
-__device__ __forceinline__ int run_start(int c, int n, int T) {
-  return static_cast<int>(static_cast<long long>(T) * c / n);
-}
-// the CTA whose run holds unit x
-__device__ __forceinline__ int run_of(int x, int n, int T) {
-  return static_cast<int>(((static_cast<long long>(x) + 1) * n - 1) / T);
-}
-// CTAs that work: each warp of a CTA gets a unit before the next CTA does
-__device__ __forceinline__ int runs(int n_cta, int T) { return min(n_cta, (T + kW - 1) / kW); }
+// The T units are cut into n runs of q or q + 1, one per CTA; n is such that
+// each warp of a CTA gets a unit before the next CTA does.
+struct Runs {
+  int n, q, longer;  // runs 0 .. longer - 1 hold q + 1 units
+  __device__ __forceinline__ Runs(int n_cta, int T) {
+    n = min(n_cta, (T + kW - 1) / kW);
+    q = n ? T / n : 0;
+    longer = T - q * n;
+  }
+  __device__ __forceinline__ int start(int c) const { return c * q + min(c, longer); }
+  // the run that holds unit x
+  __device__ __forceinline__ int of(int x) const {
+    const int head = longer * (q + 1);
+    return x < head ? x / (q + 1) : longer + (x - head) / q;
+  }
+};
 
 template <class F>
 __device__ __forceinline__ int row_units(const LongAttnArgs& a, int p) {
@@ -661,10 +667,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   pdl_launch_dependents();
   if (warp == 0) prefix_rows<F>(a, pre, len, blockIdx.x == 0);
   __syncthreads();
-  const int T = pre[a.B], n = runs(a.n_cta, T);
+  const Runs runs(a.n_cta, pre[a.B]);
   const int cta = blockIdx.x;
-  if (cta >= n) return;  // the same verdict in every thread
-  const int t0 = run_start(cta, n, T), t1 = run_start(cta + 1, n, T);
+  if (cta >= runs.n) return;  // the same verdict in every thread
+  const int t0 = runs.start(cta), t1 = runs.start(cta + 1);
 
   // ---- loads: this warp's units t0 + warp + kW k, in order.  A lane copies
   // the 16-byte pieces lane, lane + 32, .. of a unit, at fixed places in shared
@@ -858,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
       }
     }
     __syncthreads();
-    const bool whole = run_of(it.start, n, T) == cta && run_of(it.end - 1, n, T) == cta;
+    const bool whole = it.start >= t0 && it.end <= t1;
     float* part = a.part + static_cast<size_t>(2 * cta + (it.start <= t0 ? 0 : 1)) * (G * (D + 2));
     float* out = a.o + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D;
     for (int e = tid; e < G * D; e += kThreads) {
@@ -890,55 +896,60 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
 }
 
 // Joins the partials of the items that are cut between CTAs, and writes the
-// zeros of rows without keys.  Grid (Hq, B), one thread per dim.
+// zeros of rows without keys.  Grid (Hq, B), one thread per dim.  Everything
+// that the positions decide is done before the wait for the attention launch
+// (plan and partial addresses behind it cost 2.5 us at 16 partials).
 template <class F>
 __global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant__ LongAttnArgs a) {
   extern __shared__ __align__(16) int pre[];
   constexpr int D = F::D;
   const int G = a.Hq / a.Hkv, head = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  int* at = pre + 2 * a.B + 1;  // [n_cta] partials of this item, in floats
+  float* ml = reinterpret_cast<float*>(at + a.n_cta);  // [2 n_cta] their maxima and sums
   if (threadIdx.x < 32) prefix_rows<F>(a, pre, pre + a.B + 1, false);
   __syncthreads();
-  const int T = pre[a.B], units = (pre[b + 1] - pre[b]) / a.Hkv;
+  const int units = (pre[b + 1] - pre[b]) / a.Hkv;
+  const int g = head / G, h = head - g * G, stride = G * (D + 2);
+  int parts = 0;
+  if (units > 0) {
+    const Runs runs(a.n_cta, pre[a.B]);
+    const int start = pre[b] + g * units;
+    const int c0 = runs.of(start);
+    parts = runs.of(start + units - 1) - c0 + 1;
+    if (parts > 1)
+      for (int i = d; i < parts; i += D) at[i] = (2 * (c0 + i) + (start <= runs.start(c0 + i) ? 0 : 1)) * stride;
+  }
+  const int len = pre[a.B + 1 + b];
+  __syncthreads();
   pdl_wait();
   float* out = a.o + (static_cast<size_t>(b) * a.Hq + head) * D + d;
   if (units == 0) {
-    if (pre[a.B + 1 + b] == 0) *out = 0.f;
+    if (len == 0) *out = 0.f;
     return;
   }
-  const int n = runs(a.n_cta, T), g = head / G, h = head - g * G;
-  const int start = pre[b] + g * units;
-  const int c0 = run_of(start, n, T), c1 = run_of(start + units - 1, n, T);
-  if (c0 == c1) return;  // written by its CTA
-  const size_t stride = static_cast<size_t>(G) * (D + 2);
+  if (parts == 1) return;  // written by its CTA
+  constexpr int kBatch = 16;
+  float x[kBatch];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) x[i] = base + i < parts ? __ldcg(a.part + at[base + i] + h * D + d) : 0.f;
+  };
+  load(0);
+  for (int i = d; i < 2 * parts; i += D) ml[i] = __ldcg(a.part + at[i >> 1] + G * D + (i & 1 ? G : 0) + h);
+  __syncthreads();
   float M = -INFINITY, L = 0.f, sum = 0.f;
-  constexpr int kBatch = 8;
-  for (int c = c0; c <= c1; c += kBatch) {
-    float m[kBatch], l[kBatch], x[kBatch];
+  for (int i = 0; i < parts; ++i) M = fmaxf(M, ml[2 * i]);
+  const float mu = M == -INFINITY ? 0.f : M;
+  for (int base = 0; base < parts; base += kBatch) {
+    if (base) load(base);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      m[i] = -INFINITY;
-      l[i] = x[i] = 0.f;
-      if (c + i <= c1) {
-        const float* p = a.part + (2 * (c + i) + (start <= run_start(c + i, n, T) ? 0 : 1)) * stride;
-        m[i] = __ldcg(p + G * D + h);
-        l[i] = __ldcg(p + G * D + G + h);
-        x[i] = __ldcg(p + h * D + d);
+      if (base + i < parts) {
+        const float w = ex2(ml[2 * (base + i)] - mu);
+        L = fmaf(w, ml[2 * (base + i) + 1], L);
+        sum = fmaf(w, x[i], sum);
       }
     }
-    float mx = M;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, m[i]);
-    const float mu = mx == -INFINITY ? 0.f : mx;
-    const float back = ex2(M - mu);
-    L *= back;
-    sum *= back;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float w = ex2(m[i] - mu);
-      L = fmaf(w, l[i], L);
-      sum = fmaf(w, x[i], sum);
-    }
-    M = mx;
   }
   *out = L == 0.f ? 0.f : sum / L;
 }
@@ -946,7 +957,7 @@ __global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant_
 // Units in flight per warp: what shared memory holds beside the merge buffer.
 template <class F, int NT>
 constexpr int stages() {
-  return F::kQuant || NT > 1 ? 2 : 3;
+  return 2;
 }
 
 template <class F, int NT>
@@ -954,7 +965,7 @@ cudaError_t run(const LongAttnArgs& a, cudaStream_t st) {
   const uint32_t smem = Smem<F, stages<F, NT>()>::bytes(a.B, a.Hq / a.Hkv, NT);
   cudaError_t e = launch(long_attn_kernel<F, NT, stages<F, NT>()>, dim3(a.n_cta), dim3(kThreads), smem, st, false, a);
   if (e != cudaSuccess) return e;
-  return launch(long_merge_kernel<F>, dim3(a.Hq, a.B), dim3(F::D), (2 * a.B + 1) * 4, st, true, a);
+  return launch(long_merge_kernel<F>, dim3(a.Hq, a.B), dim3(F::D), (2 * a.B + 1 + 3 * a.n_cta) * 4, st, true, a);
 }
 template <class F>
 cudaError_t run_format(const LongAttnArgs& a, cudaStream_t st) {
