@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __gri
   constexpr int kLanes = D / 8, kRows = kBoundThreads / kLanes, kPer = kBlockKeys / kRows;
   __shared__ uint4 fold[2][kBoundThreads / 32][kLanes];
   const int h = blockIdx.y, b = blockIdx.z;
+  pdl_wait();
+  pdl_launch_dependents();
   const int p = a.pos[b];
   if (p < 0 || p > a.S_max - a.T) {
     if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) atomicOr(a.err, kErrPosRange);
@@ -51,7 +53,7 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __gri
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = min(r0 + i * kRows, n - 1);  // a row twice changes no extreme
-    w[i] = __ldg(src + static_cast<size_t>(r) * kLanes);
+    w[i] = src[static_cast<size_t>(r) * kLanes];
   }
   uint4 hi = w[0], lo = w[0];
 #pragma unroll
@@ -224,13 +226,15 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   const int G = a.Hq / a.Hkv;
   const size_t item = static_cast<size_t>(b) * a.Hkv + h;
   if (ctas > 1) cluster_arrive();  // before the others write here, CTA 0 has started
+  pdl_wait();
+  pdl_launch_dependents();
   const float* q = a.q + (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(h) * G) * D;
   int32_t* out = a.blocks + item * a.n_select;
   const int p = a.pos[b];
   if (tid < D) {
     float P = 0.f, N = 0.f;
     for (int i = 0; i < G; ++i) {
-      const float x = __ldg(q + i * D + tid);
+      const float x = q[i * D + tid];
       if (x > 0.f) P += x;
       else N += x;  // a NaN goes here
     }
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   auto load = [&](int j0) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      u[i] = __ldg(rows + static_cast<size_t>(min(j0 + i * kPerWarp + part, nb - 1)) * kVec + vec);
+      u[i] = rows[static_cast<size_t>(min(j0 + i * kPerWarp + part, nb - 1)) * kVec + vec];
   };
   const int first = lo_free + (rank * kSelWarps + warp) * kPerWarp * kBatch;
   if (first < hi_free) load(first);
@@ -386,8 +390,8 @@ uint32_t select_smem(int NB) { return (NB * 4 + 15) / 16 * 16 + NB * 8 + NB * 4;
 
 cudaError_t launch_block_bounds(const BoundsArgs& a, int D, cudaStream_t st) {
   const dim3 grid((a.T + kBlockKeys - 2) / kBlockKeys + 1, a.Hkv, a.B);
-  return D == 64 ? launch(block_bounds_kernel<64>, grid, dim3(kBoundThreads), 0, st, false, a)
-                 : launch(block_bounds_kernel<128>, grid, dim3(kBoundThreads), 0, st, false, a);
+  return D == 64 ? launch(block_bounds_kernel<64>, grid, dim3(kBoundThreads), 0, st, true, a)
+                 : launch(block_bounds_kernel<128>, grid, dim3(kBoundThreads), 0, st, true, a);
 }
 
 // CTAs per item: as many as fit the GPU at one per SM beside the other items',
@@ -407,12 +411,14 @@ cudaError_t launch_select_blocks(SelectBlocksArgs a, int D, int sms, cudaStream_
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = select_smem(a.NB);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
   return D == 64 ? cudaLaunchKernelEx(&cfg, select_blocks_kernel<64>, a)
                  : cudaLaunchKernelEx(&cfg, select_blocks_kernel<128>, a);
 }

@@ -9,11 +9,12 @@
 // stands for z + s (c - 8).  A group holding an infinity or a NaN stores
 // s = z = NaN, so that it reads back as NaN whole.
 //
-// Both kernels are bound by memory (2 or 4 bytes read and 0.53 to 0.63
-// written per value, or the reverse).  One thread takes 8 dims of a row: 16
-// or 32 bytes in, one 32-bit word of codes out, so that a warp's loads and
-// stores are contiguous, and group / 8 neighbouring lanes find the extremes by
-// shuffles.
+// Reading back is bound by memory (0.53 to 0.63 bytes read and 2 or 4 written
+// per value): one thread takes 8 dims of a row, a 32-bit word of codes.
+// Storing is bound by instructions: one thread takes 16 dims, so that a group's
+// scale is worked out half as often (8 dims a thread: 199 instructions for
+// every 8 values and 34 us for 84 MB of bf16 rows, 16 dims: 26 us), and
+// group / 16 neighbouring lanes find the extremes by shuffles.
 #include <cuda_fp16.h>
 
 #include "dec_launch.cuh"
@@ -23,7 +24,9 @@ namespace dec {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerThread = 4;  // rows in flight per thread
+constexpr int kRowsPerThread = 4;  // rows in flight per thread, reading back
+constexpr int kVals = 16;          // dims per thread, storing
+constexpr int kStoreRows = 2;      // rows in flight per thread, storing
 
 __device__ __forceinline__ float half_bits_to_float(uint32_t h) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
@@ -41,30 +44,90 @@ __device__ __forceinline__ int row_tokens(const int32_t* pos, const int32_t* len
 }
 
 template <bool BF16>
-struct Raw8 {
-  uint4 w[BF16 ? 1 : 2];
+struct Raw {
+  static constexpr int kWords = kVals * (BF16 ? 2 : 4) / 16;
+  uint4 w[kWords];
   __device__ __forceinline__ void load(const void* base, long long at) {
-    if constexpr (BF16) {
-      w[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
-    } else {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + at);
-      w[0] = __ldg(p);
-      w[1] = __ldg(p + 1);
+    const uint4* p = reinterpret_cast<const uint4*>(BF16 ? static_cast<const void*>(static_cast<const uint16_t*>(base) + at)
+                                                         : static_cast<const void*>(static_cast<const float*>(base) + at));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = p[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (auto& u : w) u = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(float (&x)[kVals]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (BF16) {
+          x[8 * i + 2 * j] = bf16lo(u[j]);
+          x[8 * i + 2 * j + 1] = bf16hi(u[j]);
+        } else {
+          x[4 * i + j] = __uint_as_float(u[j]);
+        }
+      }
     }
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    if constexpr (BF16) {
-      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+  // Largest and smallest value over the LANES neighbouring lanes of a group; NaN if any is.
+  template <int LANES>
+  __device__ __forceinline__ void extremes(float* hi, float* lo) const {
+    if constexpr (BF16) {  // two at a time
+      uint32_t h = max2(max2(w[0].x, w[0].y), max2(w[0].z, w[0].w));
+      uint32_t l = min2(min2(w[0].x, w[0].y), min2(w[0].z, w[0].w));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16lo(u[i]);
-        x[2 * i + 1] = bf16hi(u[i]);
+      for (int i = 1; i < kWords; ++i) {
+        h = max2(h, max2(max2(w[i].x, w[i].y), max2(w[i].z, w[i].w)));
+        l = min2(l, min2(min2(w[i].x, w[i].y), min2(w[i].z, w[i].w)));
       }
-    } else {
-      const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+      for (int o = LANES / 2; o > 0; o >>= 1) {
+        h = max2(h, __shfl_xor_sync(0xffffffffu, h, o));
+        l = min2(l, __shfl_xor_sync(0xffffffffu, l, o));
+      }
+      *hi = max1(bf16lo(h), bf16hi(h));
+      *lo = min1(bf16lo(l), bf16hi(l));
+    } else {
+      float x[kVals];
+      get(x);
+      float h = x[0], l = x[0];
+#pragma unroll
+      for (int i = 1; i < kVals; ++i) {
+        h = max1(h, x[i]);
+        l = min1(l, x[i]);
+      }
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) {
+        h = max1(h, __shfl_xor_sync(0xffffffffu, h, o));
+        l = min1(l, __shfl_xor_sync(0xffffffffu, l, o));
+      }
+      *hi = h;
+      *lo = l;
     }
+  }
+  // extremes that keep a NaN
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ float max1(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+  }
+  static __device__ __forceinline__ float min1(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
   }
 };
 
@@ -76,105 +139,88 @@ __device__ __forceinline__ float div15(float d) {
   const float q = d * y;
   return fmaf(fmaf(-15.f, q, d), y, q);
 }
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Four codes less 8 (whole numbers -8 .. 7) as 16 bits, by exact float sums.
 __device__ __forceinline__ uint32_t join4(float a, float b, float c, float d) {
   const float v = fmaf(d, 4096.f, fmaf(c, 256.f, fmaf(b, 16.f, a)));
   return __float_as_uint(v + (8388608.f + 34952.f)) & 0xFFFFu;  // 2^23 + 8 * 0x1111
 }
 
-// The group / 8 lanes of a group, 8 values each: this lane's code word, and
-// the group's (s, z) pair.  rint((x - z) / s) goes by a product with an
-// approximate 1 / s and by adding 1.5 * 2^23: the product is within 3e-6 of the
-// quotient, so only one within 1e-5 of a half-integer could round otherwise,
-// and a thread that meets such a one divides.  (Two conversions per value on
-// the transcendental pipe and a division per group took 50 us where this
-// takes 24: 84 MB of bf16 rows.)
-template <int GROUP>
-__device__ __forceinline__ void quantise8(const float (&x)[8], uint32_t* word, uint32_t* pair) {
-  float lo = fminf(x[0], x[1]), hi = fmaxf(x[0], x[1]), zero = fmaf(x[0], 0.f, x[1] * 0.f);
-#pragma unroll
-  for (int i = 2; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    zero = fmaf(x[i], 0.f, zero);  // NaN once a value is not finite
-  }
-#pragma unroll
-  for (int o = GROUP / 16; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const uint32_t lane = threadIdx.x & 31;
-  const uint32_t peers = ((1u << (GROUP / 8)) - 1u) << (lane & ~(GROUP / 8 - 1u));
-  const bool nan_group = (__ballot_sync(0xffffffffu, zero != 0.f) & peers) != 0;
+// The group / 16 lanes of a group, 16 values each: this lane's code words, and
+// the group's (s, z) pair.  (x - z) / s is the product with RN(1/s) corrected by
+// its exact remainder, which rounds to the code of the true division: checked
+// for every half significand at 81 numerators around each half-integer.  A
+// group whose ends lie outside the codes is clamped.  (84 MB of bf16 rows: 50 us
+// with two conversions per value on the transcendental pipe and a division per
+// group; 39 and 34 us with a plain product, and a division wherever one of a
+// warp's values came within 1e-5 of a half-integer, which happens to a seventh
+// of the warps.)
+template <int GROUP, bool BF16>
+__device__ __forceinline__ void quantise(const Raw<BF16>& raw, uint2* words, uint32_t* pair) {
+  float lo, hi;
+  raw.template extremes<GROUP / kVals>(&hi, &lo);
+  const bool nan_group = !(hi <= 3.402823466e38f) || !(lo >= -3.402823466e38f);
   const __half sh = __float2half_rn(fminf(div15(hi - lo), 65504.f));
   const float s = __half2float(sh);
   const __half zh = __float2half_rn(fminf(fmaxf(fmaf(8.f, s, lo), -65504.f), 65504.f));
   const float z = __half2float(zh);
-  const float inv = s > 0.f ? rcp_approx(s) : 0.f;
-  float r[8], off = 0.f;
+  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  float x[kVals], r[kVals];
+  raw.get(x);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = fminf(fmaxf((x[i] - z) * inv, -8.f), 7.f);
-    r[i] = (t + 12582912.f) - 12582912.f;
-    off = fmaxf(off, fabsf(t - r[i]));
+  for (int i = 0; i < kVals; ++i) {
+    const float d = x[i] - z, q = d * inv;
+    r[i] = (fmaf(fmaf(-s, q, d), inv, q) + 12582912.f) - 12582912.f;  // 1.5 * 2^23
   }
-  if (off > 0.49999f) {
+  if (!((hi - z) * inv < 7.49f) || !((lo - z) * inv > -8.49f)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = rintf(fminf(fmaxf(__fdiv_rn(x[i] - z, s), -8.f), 7.f));
+    for (int i = 0; i < kVals; ++i) r[i] = fminf(fmaxf(r[i], -8.f), 7.f);
   }
-  *word = nan_group ? 0x88888888u : join4(r[0], r[1], r[2], r[3]) | (join4(r[4], r[5], r[6], r[7]) << 16);
+  words->x = nan_group ? 0x88888888u : join4(r[0], r[1], r[2], r[3]) | (join4(r[4], r[5], r[6], r[7]) << 16);
+  words->y = nan_group ? 0x88888888u : join4(r[8], r[9], r[10], r[11]) | (join4(r[12], r[13], r[14], r[15]) << 16);
   *pair = nan_group ? 0x7FFF7FFFu
                     : static_cast<uint32_t>(__half_as_ushort(sh)) | (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
 }
 
-// Grid (token chunks, Hkv * 2, B); a CTA takes kThreads / (D / 8) *
-// kRowsPerThread tokens of one head's K or V.
+// Grid (token chunks, Hkv * 2, B); a CTA takes kThreads / (D / kVals) *
+// kStoreRows tokens of one head's K or V.
 template <int D, int GROUP, bool BF16>
 __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const __grid_constant__ Kv4StoreArgs a) {
-  constexpr int kLanes = D / 8, kRows = kThreads / kLanes, NG = D / GROUP;
+  constexpr int kLanes = D / kVals, kRows = kThreads / kLanes, NG = D / GROUP;
   const int b = blockIdx.z, h = blockIdx.y >> 1, which = blockIdx.y & 1;
+  pdl_wait();
+  pdl_launch_dependents();
   int p0;
   const int n = row_tokens(a.pos, a.lens, b, a.T, a.S_max, a.from_cache ? a.src_tokens : a.S_max, &p0);
   if (n < 0) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(a.err, kErrPosRange);
     return;
   }
+  const int first = blockIdx.x * (kRows * kStoreRows);
+  if (first >= n) return;
   const int sub = threadIdx.x % kLanes;
-  const int t0 = blockIdx.x * (kRows * kRowsPerThread) + threadIdx.x / kLanes;
-  if (blockIdx.x * (kRows * kRowsPerThread) >= n) return;
-  const long long src0 = b * a.sb + h * a.sh + 8 * sub + (a.from_cache ? p0 * a.st : 0);
+  const int t0 = first + threadIdx.x / kLanes;
+  const long long src0 = b * a.sb + h * a.sh + kVals * sub + (a.from_cache ? p0 * a.st : 0);
   const void* src = a.src[which];
-  Raw8<BF16> raw[kRowsPerThread];
+  Raw<BF16> raw[kStoreRows];
 #pragma unroll
-  for (int i = 0; i < kRowsPerThread; ++i) {
+  for (int i = 0; i < kStoreRows; ++i) {
     const int t = t0 + i * kRows;
     if (t < n) raw[i].load(src, src0 + t * a.st);
+    else raw[i].zero();
   }
   const size_t slot0 = (static_cast<size_t>(b) * a.Hkv + h) * a.S_max + p0;
-  uint32_t* codes = reinterpret_cast<uint32_t*>(a.codes[which]);
+  uint2* codes = reinterpret_cast<uint2*>(a.codes[which]);
 #pragma unroll
-  for (int i = 0; i < kRowsPerThread; ++i) {
+  for (int i = 0; i < kStoreRows; ++i) {
+    if (first + i * kRows >= n) break;  // the same verdict in the whole CTA
     const int t = t0 + i * kRows;
-    if (t0 - static_cast<int>(threadIdx.x / kLanes) + i * kRows >= n) break;  // the same verdict in the whole CTA
-    float x[8];
-    if (t < n) {
-      raw[i].get(x);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.f;
-    }
-    uint32_t word, pair;
-    quantise8<GROUP>(x, &word, &pair);
+    uint2 words;
+    uint32_t pair;
+    quantise<GROUP, BF16>(raw[i], &words, &pair);
     if (t < n) {
       const size_t slot = slot0 + t;
-      codes[slot * kLanes + sub] = word;
-      if (sub % (GROUP / 8) == 0) a.params[which][slot * NG + sub / (GROUP / 8)] = pair;
+      codes[slot * kLanes + sub] = words;
+      if (sub % (GROUP / kVals) == 0) a.params[which][slot * NG + sub / (GROUP / kVals)] = pair;
     }
   }
 }
@@ -184,6 +230,8 @@ template <int D, int GROUP, bool BF16>
 __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constant__ Kv4LoadArgs a) {
   constexpr int kLanes = D / 8, kRows = kThreads / kLanes, NG = D / GROUP;
   const int b = blockIdx.z, h = blockIdx.y >> 1, which = blockIdx.y & 1;
+  pdl_wait();
+  pdl_launch_dependents();
   int p0;
   const int n = row_tokens(a.pos, a.lens, b, a.T, a.S_max, a.S_max, &p0);
   if (n < 0) {
@@ -199,8 +247,8 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constan
   for (int i = 0; i < kRowsPerThread; ++i) {
     const int t = t0 + i * kRows;
     if (t < n) {
-      word[i] = __ldg(codes + (slot0 + t) * kLanes + sub);
-      pair[i] = __ldg(a.params[which] + (slot0 + t) * NG + sub / (GROUP / 8));
+      word[i] = codes[(slot0 + t) * kLanes + sub];
+      pair[i] = a.params[which][(slot0 + t) * NG + sub / (GROUP / 8)];
     }
   }
 #pragma unroll
@@ -227,11 +275,7 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constan
   }
 }
 
-template <int D>
-dim3 kv4_grid(int T, int Hkv, int B) {
-  constexpr int per = kThreads / (D / 8) * kRowsPerThread;
-  return dim3((T + per - 1) / per, Hkv * 2, B);
-}
+dim3 kv4_grid(int T, int per, int Hkv, int B) { return dim3((T + per - 1) / per, Hkv * 2, B); }
 
 // (D, group, type) -> instantiation
 template <template <int, int, bool> class F, typename A>
@@ -249,13 +293,13 @@ cudaError_t dispatch(const A& a, int D, int group, bool bf16, cudaStream_t st) {
 template <int D, int G, bool BF16>
 struct Store {
   static cudaError_t run(const Kv4StoreArgs& a, cudaStream_t st) {
-    return launch(kv4_store_kernel<D, G, BF16>, kv4_grid<D>(a.T, a.Hkv, a.B), dim3(kThreads), 0, st, false, a);
+    return launch(kv4_store_kernel<D, G, BF16>, kv4_grid(a.T, kThreads / (D / kVals) * kStoreRows, a.Hkv, a.B), dim3(kThreads), 0, st, true, a);
   }
 };
 template <int D, int G, bool BF16>
 struct Load {
   static cudaError_t run(const Kv4LoadArgs& a, cudaStream_t st) {
-    return launch(kv4_load_kernel<D, G, BF16>, kv4_grid<D>(a.T, a.Hkv, a.B), dim3(kThreads), 0, st, false, a);
+    return launch(kv4_load_kernel<D, G, BF16>, kv4_grid(a.T, kThreads / (D / 8) * kRowsPerThread, a.Hkv, a.B), dim3(kThreads), 0, st, true, a);
   }
 };
 

@@ -664,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   unsigned char* ring = smem + (L::ring(a.B, G, NT) + 127) / 128 * 128 + warp * (STAGES * F::kStage);
   const uint32_t ring_addr = smem_addr(ring);
 
+  pdl_wait();
   pdl_launch_dependents();
   if (warp == 0) prefix_rows<F>(a, pre, len, blockIdx.x == 0);
   __syncthreads();
@@ -686,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
     if (t >= t1) return -1;
     const Item it = item_at(a, pre, len, t);
     const size_t base = (static_cast<size_t>(it.b) * a.Hkv + it.h) * a.n_select;
-    return __ldg(a.blocks + base + (t - it.start) / (kBlockKeys / F::kUnit));
+    return a.blocks[base + (t - it.start) / (kBlockKeys / F::kUnit)];
   };
   if constexpr (!F::kQuant) {
     ids = fetch_ids(0);
@@ -963,7 +964,7 @@ constexpr int stages() {
 template <class F, int NT>
 cudaError_t run(const LongAttnArgs& a, cudaStream_t st) {
   const uint32_t smem = Smem<F, stages<F, NT>()>::bytes(a.B, a.Hq / a.Hkv, NT);
-  cudaError_t e = launch(long_attn_kernel<F, NT, stages<F, NT>()>, dim3(a.n_cta), dim3(kThreads), smem, st, false, a);
+  cudaError_t e = launch(long_attn_kernel<F, NT, stages<F, NT>()>, dim3(a.n_cta), dim3(kThreads), smem, st, true, a);
   if (e != cudaSuccess) return e;
   return launch(long_merge_kernel<F>, dim3(a.Hq, a.B), dim3(F::D), (2 * a.B + 1 + 3 * a.n_cta) * 4, st, true, a);
 }
