@@ -54,10 +54,11 @@ struct LongAttnArgs {
   float* part;                   // [2 * n_cta][G * (D + 2)]
   int B, Hq, Hkv, S_max;
   int n_cta;                     // CTAs of the attention launch
+  int cluster;                   // CTAs per (row, KV head), or 1: set by the launch
   float scale_log2;              // log2(e) / sqrt(D)
   uint32_t* err;
 };
-cudaError_t launch_long_attn(const LongAttnArgs& a, int D, int group, cudaStream_t st);
+cudaError_t launch_long_attn(const LongAttnArgs& a, int D, int group, int sms, cudaStream_t st);
 int long_attn_ctas(int Hq, int Hkv, bool quant, int sms);
 cudaError_t allow_smem_long();
 

@@ -630,6 +630,8 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
 
 // ----------------------------------------------------------------------------- kernel
 
+// CL: a cluster of a.cluster CTAs per (row, KV head), each with an equal run of
+// its units, joined in CTA 0's shared memory: no partials, no second launch.
 template <class F, int STAGES>
 struct Smem {
   static __host__ __device__ uint32_t ring(int B, int G, int NT) { return qraw(B, G, NT) + G * F::D * 4; }
@@ -640,13 +642,25 @@ struct Smem {
   static __host__ __device__ uint32_t ms(int B, int NT) { return zq(B, NT) + 4 * 32 * 4; }
   static __host__ __device__ uint32_t ls(int B, int NT) { return ms(B, NT) + kW * kMaxG * 4; }
   static __host__ __device__ uint32_t obuf(int B, int NT) { return ls(B, NT) + kW * kMaxG * 4; }
-  static __host__ __device__ uint32_t bytes(int B, int G, int NT) {
+  static __host__ __device__ uint32_t join(int B, int G, int NT) {
     return (ring(B, G, NT) + 127) / 128 * 128 + kW * STAGES * F::kStage;
+  }
+  static __host__ __device__ uint32_t bytes(int B, int G, int NT, int cluster) {
+    return join(B, G, NT) + (cluster > 1 ? cluster * G * (F::D + 2) * 4 : 0);
   }
 };
 
-template <class F, int NT, int STAGES>
-__global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores a float at CTA 0's copy of a shared-memory address.
+__device__ __forceinline__ void store_cta0(float* p, float v) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(p)));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
+template <class F, int NT, int STAGES, bool CL>
+__global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
     long_attn_kernel(const __grid_constant__ LongAttnArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   using L = Smem<F, STAGES>;
@@ -666,12 +680,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
 
   pdl_wait();
   pdl_launch_dependents();
-  if (warp == 0) prefix_rows<F>(a, pre, len, blockIdx.x == 0);
-  __syncthreads();
-  const Runs runs(a.n_cta, pre[a.B]);
-  const int cta = blockIdx.x;
-  if (cta >= runs.n) return;  // the same verdict in every thread
-  const int t0 = runs.start(cta), t1 = runs.start(cta + 1);
+  int cta = blockIdx.x, T;
+  Item only{};  // CL: the cluster's item
+  if constexpr (CL) {
+    cluster_arrive();  // CTA 0 has started before anybody writes to it
+    const int item = blockIdx.x / a.cluster;
+    cta = blockIdx.x - item * a.cluster;
+    only.b = item / a.Hkv;
+    only.h = item - only.b * a.Hkv;
+    const int p = a.pos[only.b];
+    if ((p < -1 || p >= a.S_max) && only.h == 0 && cta == 0 && tid == 0) atomicOr(a.err, kErrPosRange);
+    only.len = p + 1;
+    only.end = T = row_units<F>(a, p);
+  } else {
+    if (warp == 0) prefix_rows<F>(a, pre, len, cta == 0);
+    __syncthreads();
+    T = pre[a.B];
+  }
+  const Runs runs(CL ? a.cluster : a.n_cta, T);
+  if (!CL && cta >= runs.n) return;  // the same verdict in every thread
+  const int t0 = cta < runs.n ? runs.start(cta) : T, t1 = cta < runs.n ? runs.start(cta + 1) : T;
+  auto locate = [&](int t) {
+    if constexpr (CL) return only;
+    else return item_at(a, pre, len, t);
+  };
 
   // ---- loads: this warp's units t0 + warp + kW k, in order.  A lane copies
   // the 16-byte pieces lane, lane + 32, .. of a unit, at fixed places in shared
@@ -679,13 +711,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   static_assert(F::at(0, 0) == 0 && 32 % F::kChunks == 0, "lane-fixed pieces");
   constexpr int kPieces = F::kUnit * F::kChunks / 32;
   const uint32_t lane_at = F::at(lane / F::kChunks, lane % F::kChunks);
-  Item li = item_at(a, pre, len, t0);  // the item being loaded
+  Item li = locate(t0);  // the item being loaded
   int list_k = 0;                 // listed blocks: units list_k .. list_k + 31 of this warp have their ids in the lanes
   int ids = 0, ids_next = 0;
   auto fetch_ids = [&](int k) {   // lane i: the block of unit k + i of this warp
     const int t = t0 + warp + kW * (k + lane);
     if (t >= t1) return -1;
-    const Item it = item_at(a, pre, len, t);
+    const Item it = locate(t);
     const size_t base = (static_cast<size_t>(it.b) * a.Hkv + it.h) * a.n_select;
     return a.blocks[base + (t - it.start) / (kBlockKeys / F::kUnit)];
   };
@@ -709,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
     int nk = 0;
     if (t < t1) {
       if (t >= li.end) {
-        li = item_at(a, pre, len, t);
+        li = locate(t);
         if constexpr (F::kQuant) item_sources();
       }
       const uint32_t dst = ring_addr + slot * F::kStage + lane_at;
@@ -775,11 +807,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   // the query rows of the item that holds unit t, without a commit of their own
   float* qraw = reinterpret_cast<float*>(smem + L::qraw(a.B, G, NT));
   auto fetch_query = [&](int t) {
-    const Item it = item_at(a, pre, len, t);
+    const Item it = locate(t);
     const float* q = a.q + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D;
     for (int e = tid * 4; e < G * D; e += kThreads * 4) cp_async16(smem_addr(qraw + e), q + e, true);
   };
-  fetch_query(t0);  // ahead of the stream: behind it they would wait for it
+  if (t0 < t1) fetch_query(t0);  // ahead of the stream: behind it they would wait for it
   cp_async_commit();
   int ring_nk[STAGES];  // bf16: keys of the units in flight
   ring_nk[0] = issue(0, 0);
@@ -789,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
   __syncthreads();
   int k = 0, slot = 0;
   for (int t = t0; t < t1;) {
-    const Item it = item_at(a, pre, len, t);
+    const Item it = locate(t);
     const int seg_end = min(t1, it.end);
     if (warp < NT)
       stage_query<F>(qraw, G, warp, a.scale_log2, words, f_smem, zq_smem);
@@ -866,7 +898,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
     }
     __syncthreads();
     const bool whole = it.start >= t0 && it.end <= t1;
+    float* join = reinterpret_cast<float*>(smem + L::join(a.B, G, NT)) + cta * G * (D + 2);
     float* part = a.part + static_cast<size_t>(2 * cta + (it.start <= t0 ? 0 : 1)) * (G * (D + 2));
+    if constexpr (CL) cluster_wait();
     float* out = a.o + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D;
     for (int e = tid; e < G * D; e += kThreads) {
       const int h = e / D, d = e - h * D;
@@ -882,6 +916,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
       }
       if (whole) {
         out[e] = l == 0.f ? 0.f : sum / l;
+      } else if constexpr (CL) {
+        store_cta0(join + e, sum);
+        if (d == 0) {
+          store_cta0(join + G * D + h, M);
+          store_cta0(join + G * D + G + h, l);
+        }
       } else {
         part[e] = sum;
         if (d == 0) {
@@ -894,7 +934,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant ? 2 : 1)
     t = seg_end;
   }
   cp_async_wait<0>();
+  if constexpr (CL) {
+    if (t0 >= t1) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+    if (cta > 0 || runs.n == 1) return;
+    float* out = a.o + (static_cast<size_t>(only.b) * a.Hq + static_cast<size_t>(only.h) * G) * D;
+    const float* join = reinterpret_cast<const float*>(smem + L::join(a.B, G, NT));
+    for (int e = tid; e < G * D; e += kThreads) {
+      const int h = e / D;
+      float M = -INFINITY, sum = 0.f, l = 0.f;
+      for (int i = 0; i < runs.n; ++i) M = fmaxf(M, join[i * G * (D + 2) + G * D + h]);
+      const float mu = M == -INFINITY ? 0.f : M;
+      for (int i = 0; i < runs.n; ++i) {
+        const float* p = join + i * G * (D + 2);
+        const float x = ex2(p[G * D + h] - mu);
+        l = fmaf(x, p[G * D + G + h], l);
+        sum = fmaf(x, p[e], sum);
+      }
+      if (runs.n > 0 || only.len == 0) out[e] = l == 0.f ? 0.f : sum / l;
+    }
+  }
 }
+
 
 // Joins the partials of the items that are cut between CTAs, and writes the
 // zeros of rows without keys.  Grid (Hq, B), one thread per dim.  Everything
@@ -961,25 +1023,66 @@ constexpr int stages() {
   return 2;
 }
 
+// CTAs per (row, KV head).  Clusters where every item's longest possible run is
+// short (at most four units per warp) and all of them fit the GPU at once, one
+// CTA per SM; otherwise (1) the balanced runs with their partials and second
+// launch.  One row of 4096 keys, 8 heads: XX us against 8.4; 64 listed blocks of
+// 8 heads: YY against 11.6.
 template <class F, int NT>
-cudaError_t run(const LongAttnArgs& a, cudaStream_t st) {
-  const uint32_t smem = Smem<F, stages<F, NT>()>::bytes(a.B, a.Hq / a.Hkv, NT);
-  cudaError_t e = launch(long_attn_kernel<F, NT, stages<F, NT>()>, dim3(a.n_cta), dim3(kThreads), smem, st, true, a);
+int cluster_size(const LongAttnArgs& a, int sms) {
+  const int items = a.B * a.Hkv;
+  const int units = F::kQuant ? (a.S_max + F::kUnit - 1) / F::kUnit : a.n_select * (kBlockKeys / F::kUnit);
+  int c = 1;
+  while (c < 8 && 2 * c * items <= sms &&
+         Smem<F, stages<F, NT>()>::bytes(a.B, a.Hq / a.Hkv, NT, 2 * c) <= kSmemMax)
+    c *= 2;
+  return units <= 4 * kW * c ? c : 1;
+}
+
+template <class F, int NT>
+cudaError_t run(LongAttnArgs a, int sms, cudaStream_t st) {
+  constexpr int S = stages<F, NT>();
+  const int G = a.Hq / a.Hkv;
+  a.cluster = cluster_size<F, NT>(a, sms);
+  if (a.cluster > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.B * a.Hkv * a.cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Smem<F, S>::bytes(a.B, G, NT, a.cluster);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, long_attn_kernel<F, NT, S, true>, a);
+  }
+  cudaError_t e = launch(long_attn_kernel<F, NT, S, false>, dim3(a.n_cta), dim3(kThreads), Smem<F, S>::bytes(a.B, G, NT, 1),
+                         st, true, a);
   if (e != cudaSuccess) return e;
   return launch(long_merge_kernel<F>, dim3(a.Hq, a.B), dim3(F::D), (2 * a.B + 1 + 3 * a.n_cta) * 4, st, true, a);
 }
 template <class F>
-cudaError_t run_format(const LongAttnArgs& a, cudaStream_t st) {
+cudaError_t run_format(const LongAttnArgs& a, int sms, cudaStream_t st) {
   const int G = a.Hq / a.Hkv;
-  if (G <= 4) return run<F, 1>(a, st);
-  if (G <= 8) return run<F, 2>(a, st);
-  return run<F, 4>(a, st);
+  if (G <= 4) return run<F, 1>(a, sms, st);
+  if (G <= 8) return run<F, 2>(a, sms, st);
+  return run<F, 4>(a, sms, st);
+}
+template <class F, int NT>
+cudaError_t allow() {
+  cudaError_t e = allow_smem(long_attn_kernel<F, NT, stages<F, NT>(), false>);
+  if (e == cudaSuccess) e = allow_smem(long_attn_kernel<F, NT, stages<F, NT>(), true>);
+  return e;
 }
 template <class F>
 cudaError_t allow_format() {
-  cudaError_t e = allow_smem(long_attn_kernel<F, 1, stages<F, 1>()>);
-  if (e == cudaSuccess) e = allow_smem(long_attn_kernel<F, 2, stages<F, 2>()>);
-  if (e == cudaSuccess) e = allow_smem(long_attn_kernel<F, 4, stages<F, 4>()>);
+  cudaError_t e = allow<F, 1>();
+  if (e == cudaSuccess) e = allow<F, 2>();
+  if (e == cudaSuccess) e = allow<F, 4>();
   return e;
 }
 
@@ -990,12 +1093,12 @@ int long_attn_ctas(int Hq, int Hkv, bool quant, int sms) {
   return min(kLongMaxCtas, quant && Hq / Hkv <= 4 ? 2 * sms : sms);
 }
 
-cudaError_t launch_long_attn(const LongAttnArgs& a, int D, int group, cudaStream_t st) {
-  if (a.blocks) return D == 64 ? run_format<Bf16<64>>(a, st) : run_format<Bf16<128>>(a, st);
-  if (D == 64) return group == 32 ? run_format<Kv4<64, 32>>(a, st) : run_format<Kv4<64, 64>>(a, st);
-  if (group == 32) return run_format<Kv4<128, 32>>(a, st);
-  if (group == 64) return run_format<Kv4<128, 64>>(a, st);
-  return run_format<Kv4<128, 128>>(a, st);
+cudaError_t launch_long_attn(const LongAttnArgs& a, int D, int group, int sms, cudaStream_t st) {
+  if (a.blocks) return D == 64 ? run_format<Bf16<64>>(a, sms, st) : run_format<Bf16<128>>(a, sms, st);
+  if (D == 64) return group == 32 ? run_format<Kv4<64, 32>>(a, sms, st) : run_format<Kv4<64, 64>>(a, sms, st);
+  if (group == 32) return run_format<Kv4<128, 32>>(a, sms, st);
+  if (group == 64) return run_format<Kv4<128, 64>>(a, sms, st);
+  return run_format<Kv4<128, 128>>(a, sms, st);
 }
 
 cudaError_t allow_smem_long() {
