@@ -1023,20 +1023,23 @@ constexpr int stages() {
   return 2;
 }
 
-// CTAs per (row, KV head).  Clusters where every item's longest possible run is
-// short (at most four units per warp) and all of them fit the GPU at once, one
-// CTA per SM; otherwise (1) the balanced runs with their partials and second
-// launch.  One row of 4096 keys, 8 heads: XX us against 8.4; 64 listed blocks of
-// 8 heads: YY against 11.6.
+// CTAs per (row, KV head): up to 8, while the clusters take at most two thirds
+// of the SMs (16 clusters of 8 wait for one another at 128 of 152: 9.3 us where
+// 64 CTAs take 7.4), or 1: the balanced runs with their partials and second
+// launch, about 3 us more, but all SMs.  A unit takes a warp about 1 us, so the
+// clusters win while a warp of theirs has at most 5 units more than one of the
+// balanced runs.  Measured, clusters against runs (b rows, query/KV heads, keys):
+// 1 32/8 4k 6.6 / 8.6 us, 16k 12.8 / 15.9, 32k 21.1 / 19.6; 8 12/3 8k 12.5 / 15.1,
+// 16k 20.6 / 20.7, 32k 35.8 / 29.7; 64 listed blocks 7.7 / 9.9, 256 17.6 / 18.5.
 template <class F, int NT>
 int cluster_size(const LongAttnArgs& a, int sms) {
   const int items = a.B * a.Hkv;
-  const int units = F::kQuant ? (a.S_max + F::kUnit - 1) / F::kUnit : a.n_select * (kBlockKeys / F::kUnit);
+  const long long units = F::kQuant ? (a.S_max + F::kUnit - 1) / F::kUnit : a.n_select * (kBlockKeys / F::kUnit);
   int c = 1;
-  while (c < 8 && 2 * c * items <= sms &&
+  while (c < 8 && 2 * c * items <= 2 * sms / 3 &&
          Smem<F, stages<F, NT>()>::bytes(a.B, a.Hq / a.Hkv, NT, 2 * c) <= kSmemMax)
     c *= 2;
-  return units <= 4 * kW * c ? c : 1;
+  return units * sms - units * items * c <= 5ll * kW * sms * c ? c : 1;
 }
 
 template <class F, int NT>
