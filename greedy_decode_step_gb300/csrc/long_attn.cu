@@ -167,7 +167,7 @@ template <int D_>
 struct Bf16 {
   static constexpr bool kQuant = false;
   static constexpr int D = D_, NG = 1, kUnit = 16;
-  static constexpr int kRow = 2 * D, kChunks = kRow / 16, kQWords = D / 16 * 2;
+  static constexpr int kRow = 2 * D, kChunks = kRow / 16, kQWords = D / 16 * 4;
   static constexpr int kKOff = 0, kVOff = kUnit * kRow, kStage = 2 * kUnit * kRow;
   static __host__ __device__ constexpr uint32_t at(int r, int j) {
     return static_cast<uint32_t>(r * kRow + ((j ^ (r & 7)) << 4));
@@ -194,10 +194,15 @@ struct Runs {
   }
 };
 
+// Keys of a row whose last one is at p; -1: a position outside the cache.
+__device__ __forceinline__ int row_keys(const LongAttnArgs& a, int p) { return p < -1 || p >= a.S_max ? -1 : p + 1; }
+
+// Units of an item of `len` keys.  Listed blocks: of any item, so that the plan
+// and the lists' loads need not wait for the positions (units without keys are
+// passed over).
 template <class F>
-__device__ __forceinline__ int row_units(const LongAttnArgs& a, int p) {
-  if (p < 0 || p >= a.S_max) return 0;
-  if constexpr (F::kQuant) return (p + F::kUnit) / F::kUnit;
+__device__ __forceinline__ int row_units(const LongAttnArgs& a, int len) {
+  if constexpr (F::kQuant) return len < 0 ? 0 : (len + F::kUnit - 1) / F::kUnit;
   else return a.n_select * (kBlockKeys / F::kUnit);
 }
 
@@ -211,10 +216,9 @@ __device__ __forceinline__ void prefix_rows(const LongAttnArgs& a, int* pre, int
     const int b = base + lane;
     int v = 0;
     if (b < a.B) {
-      const int p = a.pos[b];
-      v = row_units<F>(a, p) * a.Hkv;
-      len[b] = p + 1;
-      if (report && (p < -1 || p >= a.S_max)) atomicOr(a.err, kErrPosRange);
+      len[b] = row_keys(a, a.pos[b]);
+      v = row_units<F>(a, len[b]) * a.Hkv;
+      if (report && len[b] < 0) atomicOr(a.err, kErrPosRange);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -229,7 +233,7 @@ __device__ __forceinline__ void prefix_rows(const LongAttnArgs& a, int* pre, int
 struct Item {
   int b, h;        // row, KV head
   int start, end;  // its units
-  int len;         // keys of the row
+  int len;         // keys of the row, -1: refused
 };
 
 // The item that holds unit t.
@@ -260,7 +264,9 @@ __device__ __forceinline__ Item item_at(const LongAttnArgs& a, const int* pre, c
 //    nibbles' (16 times larger) with a factor 1/16.  The head is scaled by a
 //    power of two to [2^13, 2^14); f takes it back.  zq: for the (s, z) pair of
 //    group c, (0, Q) with Q the group's sum of q, scaled by another 2^-10.
-//  * bf16: per 16 dims two pairs, as the instruction lays them out.
+//  * bf16: per 16 dims two pairs, as the instruction lays them out, and two
+//    more whose upper-part columns hold a third part (24 bits in all; the
+//    remainder columns are zero).
 template <class F>
 __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float scale_log2, uint32_t* words, float* f,
                                             uint32_t* zq) {
@@ -322,16 +328,18 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
     constexpr int NJ = D / 16;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      uint32_t w[2];
+      uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float2 x = make_float2(0.f, 0.f);
-        if (head < G)
-          x = *reinterpret_cast<const float2*>(q + head * D + 16 * j + 8 * i + 2 * c);
+        if (head < G) x = *reinterpret_cast<const float2*>(q + head * D + 16 * j + 8 * i + 2 * c);
         const uint32_t hi = pack_bf16(x.x, x.y);
-        w[i] = rest ? pack_bf16(x.x - bf16lo(hi), x.y - bf16hi(hi)) : hi;
+        const float x0 = x.x - bf16lo(hi), x1 = x.y - bf16hi(hi);
+        const uint32_t mid = pack_bf16(x0, x1);
+        w[i] = rest ? mid : hi;
+        w[2 + i] = rest ? 0u : pack_bf16(x0 - bf16lo(mid), x1 - bf16hi(mid));
       }
-      *reinterpret_cast<uint2*>(words + ((nt * NJ + j) * 32 + lane) * 2) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint4*>(words + ((nt * NJ + j) * 32 + lane) * 4) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (c == 0 && !rest) f[head] = scale_log2;
   }
@@ -591,8 +599,9 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
     ldsm_x4(r, stage_addr + F::kKOff + F::at(lane & 15, 2 * j + (lane >> 4)));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const uint2 b = *reinterpret_cast<const uint2*>(words + ((nt * NJ + j) * 32 + lane) * 2);
-      mma_bf16_16816(acc[nt][j & 1], r, b.x, b.y);
+      const uint4 b = *reinterpret_cast<const uint4*>(words + ((nt * NJ + j) * 32 + lane) * 4);
+      mma_bf16_16816(acc[nt][0], r, b.x, b.y);
+      mma_bf16_16816(acc[nt][1], r, b.z, b.w);
     }
   }
   float s[NT][2], mx[NT];
@@ -608,15 +617,19 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
     more |= mx[nt] > st.m[nt];
   }
   if (__any_sync(0xffffffffu, more)) raise<F, NT>(st, mx, 0.f);
-  uint32_t b0[NT], b1[NT];
+  uint32_t b0[NT], b1[NT], c0[NT], c1[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float x0 = ex2(s[nt][0] - st.mu[nt]), x1 = ex2(s[nt][1] - st.mu[nt]);
     st.l[nt] += x0 + x1;
     const uint32_t h = pack_bf16(x0, x1);
-    const uint32_t l = pack_bf16(x0 - bf16lo(h), x1 - bf16hi(h));
+    const float y0 = x0 - bf16lo(h), y1 = x1 - bf16hi(h);
+    const uint32_t l = pack_bf16(y0, y1);
+    const uint32_t t = pack_bf16(y0 - bf16lo(l), y1 - bf16hi(l));
     b0[nt] = transpose8(__byte_perm(h, l, 0x5410));
     b1[nt] = transpose8(__byte_perm(h, l, 0x7632));
+    c0[nt] = transpose8(t & 0xFFFFu);  // the third part, in the upper parts' columns
+    c1[nt] = transpose8(t >> 16);
   }
   const int vrow = (lane & 7) + ((lane >> 4) << 3), vchunk = (lane >> 3) & 1;
 #pragma unroll
@@ -624,7 +637,10 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
     uint32_t r[4];
     ldsm_x4_trans(r, stage_addr + F::kVOff + F::at(vrow, 2 * j + vchunk));
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(st.o[nt][j], r, b0[nt], b1[nt]);
+    for (int nt = 0; nt < NT; ++nt) {
+      mma_bf16_16816(st.o[nt][j], r, b0[nt], b1[nt]);
+      mma_bf16_16816(st.o[nt][j], r, c0[nt], c1[nt]);
+    }
   }
 }
 
@@ -688,10 +704,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
     cta = blockIdx.x - item * a.cluster;
     only.b = item / a.Hkv;
     only.h = item - only.b * a.Hkv;
-    const int p = a.pos[only.b];
-    if ((p < -1 || p >= a.S_max) && only.h == 0 && cta == 0 && tid == 0) atomicOr(a.err, kErrPosRange);
-    only.len = p + 1;
-    only.end = T = row_units<F>(a, p);
+    only.len = row_keys(a, a.pos[only.b]);
+    if (only.len < 0 && only.h == 0 && cta == 0 && tid == 0) atomicOr(a.err, kErrPosRange);
+    only.end = T = row_units<F>(a, only.len);
+  } else if constexpr (!F::kQuant) {
+    if (cta == 0)
+      for (int b = tid; b < a.B; b += kThreads)
+        if (row_keys(a, a.pos[b]) < 0) atomicOr(a.err, kErrPosRange);
+    T = a.B * a.Hkv * row_units<F>(a, 0);
   } else {
     if (warp == 0) prefix_rows<F>(a, pre, len, cta == 0);
     __syncthreads();
@@ -701,8 +721,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
   if (!CL && cta >= runs.n) return;  // the same verdict in every thread
   const int t0 = cta < runs.n ? runs.start(cta) : T, t1 = cta < runs.n ? runs.start(cta + 1) : T;
   auto locate = [&](int t) {
-    if constexpr (CL) return only;
-    else return item_at(a, pre, len, t);
+    if constexpr (CL) {
+      return only;
+    } else if constexpr (!F::kQuant) {
+      const int per = row_units<F>(a, 0), item = t / per;
+      Item it;
+      it.b = item / a.Hkv;
+      it.h = item - it.b * a.Hkv;
+      it.start = item * per;
+      it.end = it.start + per;
+      it.len = row_keys(a, a.pos[it.b]);
+      return it;
+    } else {
+      return item_at(a, pre, len, t);
+    }
   };
 
   // ---- loads: this warp's units t0 + warp + kW k, in order.  A lane copies
@@ -711,20 +743,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
   static_assert(F::at(0, 0) == 0 && 32 % F::kChunks == 0, "lane-fixed pieces");
   constexpr int kPieces = F::kUnit * F::kChunks / 32;
   const uint32_t lane_at = F::at(lane / F::kChunks, lane % F::kChunks);
-  Item li = locate(t0);  // the item being loaded
   int list_k = 0;                 // listed blocks: units list_k .. list_k + 31 of this warp have their ids in the lanes
   int ids = 0, ids_next = 0;
   auto fetch_ids = [&](int k) {   // lane i: the block of unit k + i of this warp
     const int t = t0 + warp + kW * (k + lane);
     if (t >= t1) return -1;
-    const Item it = locate(t);
-    const size_t base = (static_cast<size_t>(it.b) * a.Hkv + it.h) * a.n_select;
-    return a.blocks[base + (t - it.start) / (kBlockKeys / F::kUnit)];
+    // unit t of all, or of the cluster's item
+    const size_t base = CL ? (static_cast<size_t>(only.b) * a.Hkv + only.h) * a.n_select : 0;
+    return a.blocks[base + t / (kBlockKeys / F::kUnit)];
   };
   if constexpr (!F::kQuant) {
     ids = fetch_ids(0);
     ids_next = fetch_ids(32);
   }
+  Item li = locate(t0);  // the item being loaded
   const unsigned char *k_src = nullptr, *v_src = nullptr;  // 4-bit: this lane's first piece of slot 0 of the item
   const uint32_t *kp_src = nullptr, *vp_src = nullptr;
   auto item_sources = [&]() {
@@ -783,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
         const bool bad = id < -1 || id > (a.S_max - 1) / kBlockKeys;
         if (bad && lane == 0) atomicOr(a.err, kErrPosRange);
         const int k0 =
-            bad || id < 0 ? li.len : id * kBlockKeys + (t - li.start) % (kBlockKeys / F::kUnit) * F::kUnit;
+            bad || id < 0 ? max(li.len, 0) : id * kBlockKeys + (t - li.start) % (kBlockKeys / F::kUnit) * F::kUnit;
         nk = max(0, min(F::kUnit, li.len - k0));
         if (nk > 0) {
           const size_t row = (static_cast<size_t>(li.b) * a.Hkv + li.h) * a.S_max + k0;
@@ -915,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
         sum = fmaf(x, obuf[(w * G + h) * (D + 4) + d], sum);
       }
       if (whole) {
-        out[e] = l == 0.f ? 0.f : sum / l;
+        if (it.len >= 0) out[e] = l == 0.f ? 0.f : sum / l;
       } else if constexpr (CL) {
         store_cta0(join + e, sum);
         if (d == 0) {
@@ -952,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
         l = fmaf(x, p[G * D + G + h], l);
         sum = fmaf(x, p[e], sum);
       }
-      if (runs.n > 0 || only.len == 0) out[e] = l == 0.f ? 0.f : sum / l;
+      if (only.len >= 0) out[e] = l == 0.f ? 0.f : sum / l;
     }
   }
 }
@@ -986,8 +1018,9 @@ __global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant_
   __syncthreads();
   pdl_wait();
   float* out = a.o + (static_cast<size_t>(b) * a.Hq + head) * D + d;
+  if (len < 0) return;  // refused
   if (units == 0) {
-    if (len == 0) *out = 0.f;
+    *out = 0.f;
     return;
   }
   if (parts == 1) return;  // written by its CTA
