@@ -10,7 +10,7 @@ namespace dec {
 
 constexpr int kLongMaxBatch = 1024;   // rows of one call
 constexpr int kBlockKeys = 64;        // keys of a selectable block
-constexpr int kLongMaxCtas = 320;     // CTAs of one attention launch (two per SM, or one)
+constexpr int kLongMaxCtas = 480;     // CTAs of one attention launch (three per SM, or one)
 constexpr int kSelMaxBlocks = 8192;   // blocks of a row that the selection holds in shared memory
 
 // 4-bit cache.  Per (row, KV head, slot): D/2 bytes of codes (dim 2i in the
@@ -53,13 +53,12 @@ struct LongAttnArgs {
   int n_select;
   float* part;                   // [2 * n_cta][G * (D + 2)]
   int B, Hq, Hkv, S_max;
-  int n_cta;                     // CTAs of the attention launch
+  int n_cta;                     // CTAs of the balanced launch: set by the launch
   int cluster;                   // CTAs per (row, KV head), or 1: set by the launch
   float scale_log2;              // log2(e) / sqrt(D)
   uint32_t* err;
 };
 cudaError_t launch_long_attn(const LongAttnArgs& a, int D, int group, int sms, cudaStream_t st);
-int long_attn_ctas(int Hq, int Hkv, bool quant, int sms);
 cudaError_t allow_smem_long();
 
 // Per-block channel bounds of a bf16 key cache: bounds[b][g][j][0] the

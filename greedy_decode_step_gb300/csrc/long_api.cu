@@ -193,7 +193,6 @@ int dec_kv4_decode_attn(const float* q, const void* k_codes, const void* k_param
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.S_max = S_max;
-  a.n_cta = long_attn_ctas(Hq, Hkv, true, sms);
   a.scale_log2 = softmax_scale(D);
   DEC_LAUNCHED(launch_long_attn(a, D, group, sms, static_cast<cudaStream_t>(stream)), "attention over the 4-bit cache");
   return DEC_OK;
@@ -286,7 +285,6 @@ int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cac
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.S_max = S_max;
-  a.n_cta = long_attn_ctas(Hq, Hkv, false, sms);
   a.scale_log2 = softmax_scale(D);
   DEC_LAUNCHED(launch_long_attn(a, D, 0, sms, static_cast<cudaStream_t>(stream)), "attention over listed blocks");
   return DEC_OK;

@@ -32,14 +32,14 @@
 // products of their own, with the (s, z) words as the other operand.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "dec_launch.cuh"
 #include "dec_long.cuh"
 
 namespace dec {
 namespace {
 
-constexpr int kW = 8;                 // warps of a CTA
-constexpr int kThreads = 32 * kW;
 constexpr int kMaxG = 16;             // query heads per KV head
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
@@ -181,8 +181,8 @@ struct Bf16 {
 // each warp of a CTA gets a unit before the next CTA does.
 struct Runs {
   int n, q, longer;  // runs 0 .. longer - 1 hold q + 1 units
-  __device__ __forceinline__ Runs(int n_cta, int T) {
-    n = min(n_cta, (T + kW - 1) / kW);
+  __device__ __forceinline__ Runs(int n_cta, int T, int warps) {
+    n = min(n_cta, (T + warps - 1) / warps);
     q = n ? T / n : 0;
     longer = T - q * n;
   }
@@ -646,9 +646,20 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
 
 // ----------------------------------------------------------------------------- kernel
 
+// Shape of a launch: warps of a CTA, units in flight per warp, CTAs of an SM.
+// Four-warp CTAs wait less at an item's end and share the SM more evenly than
+// larger ones (the 4-bit cache, 8 ragged rows to 32k keys: 12 warps as 3 x 4 with
+// 3 units each 42.5 us, 16 as 2 x 8 with 2 45.6, 16 in one CTA 61.2).  In a
+// cluster all warps of an SM work on one item.
+template <class F, int NT, bool CL>
+struct Shape {
+  static constexpr bool kSmall = F::kQuant && NT == 1 && !CL;
+  static constexpr int kW = kSmall ? 4 : 8, kStages = kSmall ? 3 : 2, kPerSm = kSmall ? 3 : 1;
+};
+
 // CL: a cluster of a.cluster CTAs per (row, KV head), each with an equal run of
 // its units, joined in CTA 0's shared memory: no partials, no second launch.
-template <class F, int STAGES>
+template <class F, int kW, int STAGES>
 struct Smem {
   static __host__ __device__ uint32_t ring(int B, int G, int NT) { return qraw(B, G, NT) + G * F::D * 4; }
   static __host__ __device__ uint32_t qraw(int B, int G, int NT) { return obuf(B, NT) + kW * G * (F::D + 4) * 4; }
@@ -675,11 +686,12 @@ __device__ __forceinline__ void store_cta0(float* p, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
-template <class F, int NT, int STAGES, bool CL>
-__global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
+template <class F, int NT, bool CL>
+__global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::kPerSm)
     long_attn_kernel(const __grid_constant__ LongAttnArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  using L = Smem<F, STAGES>;
+  constexpr int kW = Shape<F, NT, CL>::kW, kThreads = 32 * kW, STAGES = Shape<F, NT, CL>::kStages;
+  using L = Smem<F, kW, STAGES>;
   constexpr int D = F::D;
   const int G = a.Hq / a.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -717,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
     __syncthreads();
     T = pre[a.B];
   }
-  const Runs runs(CL ? a.cluster : a.n_cta, T);
+  const Runs runs(CL ? a.cluster : a.n_cta, T, kW);
   if (!CL && cta >= runs.n) return;  // the same verdict in every thread
   const int t0 = cta < runs.n ? runs.start(cta) : T, t1 = cta < runs.n ? runs.start(cta + 1) : T;
   auto locate = [&](int t) {
@@ -994,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && F::kQuant && !CL ? 2 : 1)
 // zeros of rows without keys.  Grid (Hq, B), one thread per dim.  Everything
 // that the positions decide is done before the wait for the attention launch
 // (plan and partial addresses behind it cost 2.5 us at 16 partials).
-template <class F>
+template <class F, int NT>
 __global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant__ LongAttnArgs a) {
   extern __shared__ __align__(16) int pre[];
   constexpr int D = F::D;
@@ -1007,7 +1019,7 @@ __global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant_
   const int g = head / G, h = head - g * G, stride = G * (D + 2);
   int parts = 0;
   if (units > 0) {
-    const Runs runs(a.n_cta, pre[a.B]);
+    const Runs runs(a.n_cta, pre[a.B], Shape<F, NT, false>::kW);
     const int start = pre[b] + g * units;
     const int c0 = runs.of(start);
     parts = runs.of(start + units - 1) - c0 + 1;
@@ -1050,12 +1062,6 @@ __global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant_
   *out = L == 0.f ? 0.f : sum / L;
 }
 
-// Units in flight per warp: what shared memory holds beside the merge buffer.
-template <class F, int NT>
-constexpr int stages() {
-  return 2;
-}
-
 // CTAs per (row, KV head): up to 8, while the clusters take at most two thirds
 // of the SMs (16 clusters of 8 wait for one another at 128 of 152: 9.3 us where
 // 64 CTAs take 7.4), or 1: the balanced runs with their partials and second
@@ -1066,25 +1072,26 @@ constexpr int stages() {
 // 16k 20.6 / 20.7, 32k 35.8 / 29.7; 64 listed blocks 7.7 / 9.9, 256 17.6 / 18.5.
 template <class F, int NT>
 int cluster_size(const LongAttnArgs& a, int sms) {
+  using S = Shape<F, NT, true>;
   const int items = a.B * a.Hkv;
   const long long units = F::kQuant ? (a.S_max + F::kUnit - 1) / F::kUnit : a.n_select * (kBlockKeys / F::kUnit);
   int c = 1;
   while (c < 8 && 2 * c * items <= 2 * sms / 3 &&
-         Smem<F, stages<F, NT>()>::bytes(a.B, a.Hq / a.Hkv, NT, 2 * c) <= kSmemMax)
+         Smem<F, S::kW, S::kStages>::bytes(a.B, a.Hq / a.Hkv, NT, 2 * c) <= kSmemMax)
     c *= 2;
-  return units * sms - units * items * c <= 5ll * kW * sms * c ? c : 1;
+  return units * sms - units * items * c <= 5ll * S::kW * sms * c ? c : 1;
 }
 
 template <class F, int NT>
 cudaError_t run(LongAttnArgs a, int sms, cudaStream_t st) {
-  constexpr int S = stages<F, NT>();
   const int G = a.Hq / a.Hkv;
   a.cluster = cluster_size<F, NT>(a, sms);
   if (a.cluster > 1) {
+    using S = Shape<F, NT, true>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.B * a.Hkv * a.cluster);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Smem<F, S>::bytes(a.B, G, NT, a.cluster);
+    cfg.blockDim = dim3(32 * S::kW);
+    cfg.dynamicSmemBytes = Smem<F, S::kW, S::kStages>::bytes(a.B, G, NT, a.cluster);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1094,12 +1101,14 @@ cudaError_t run(LongAttnArgs a, int sms, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, long_attn_kernel<F, NT, S, true>, a);
+    return cudaLaunchKernelEx(&cfg, long_attn_kernel<F, NT, true>, a);
   }
-  cudaError_t e = launch(long_attn_kernel<F, NT, S, false>, dim3(a.n_cta), dim3(kThreads), Smem<F, S>::bytes(a.B, G, NT, 1),
-                         st, true, a);
+  using S = Shape<F, NT, false>;
+  a.n_cta = std::min(kLongMaxCtas, S::kPerSm * sms);
+  cudaError_t e = launch(long_attn_kernel<F, NT, false>, dim3(a.n_cta), dim3(32 * S::kW),
+                         Smem<F, S::kW, S::kStages>::bytes(a.B, G, NT, 1), st, true, a);
   if (e != cudaSuccess) return e;
-  return launch(long_merge_kernel<F>, dim3(a.Hq, a.B), dim3(F::D), (2 * a.B + 1 + 3 * a.n_cta) * 4, st, true, a);
+  return launch(long_merge_kernel<F, NT>, dim3(a.Hq, a.B), dim3(F::D), (2 * a.B + 1 + 3 * a.n_cta) * 4, st, true, a);
 }
 template <class F>
 cudaError_t run_format(const LongAttnArgs& a, int sms, cudaStream_t st) {
@@ -1110,8 +1119,8 @@ cudaError_t run_format(const LongAttnArgs& a, int sms, cudaStream_t st) {
 }
 template <class F, int NT>
 cudaError_t allow() {
-  cudaError_t e = allow_smem(long_attn_kernel<F, NT, stages<F, NT>(), false>);
-  if (e == cudaSuccess) e = allow_smem(long_attn_kernel<F, NT, stages<F, NT>(), true>);
+  cudaError_t e = allow_smem(long_attn_kernel<F, NT, false>);
+  if (e == cudaSuccess) e = allow_smem(long_attn_kernel<F, NT, true>);
   return e;
 }
 template <class F>
@@ -1123,11 +1132,6 @@ cudaError_t allow_format() {
 }
 
 }  // namespace
-
-// Two CTAs fit an SM for the 4-bit cache with up to 4 heads per group.
-int long_attn_ctas(int Hq, int Hkv, bool quant, int sms) {
-  return min(kLongMaxCtas, quant && Hq / Hkv <= 4 ? 2 * sms : sms);
-}
 
 cudaError_t launch_long_attn(const LongAttnArgs& a, int D, int group, int sms, cudaStream_t st) {
   if (a.blocks) return D == 64 ? run_format<Bf16<64>>(a, sms, st) : run_format<Bf16<128>>(a, sms, st);
