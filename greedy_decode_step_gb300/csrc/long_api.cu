@@ -261,8 +261,8 @@ int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cac
   DEC_TRY(check_cache(B, Hkv, D, S_max));
   DEC_TRY(check_queries(Hq, Hkv));
   DEC_CHECK(n_select >= 1, DEC_EINVAL, "n_select must be >= 1");
-  DEC_CHECK(static_cast<long long>(B) * Hkv * n_select * 4 < (1ll << 31), DEC_EUNSUPPORTED,
-            "%lld listed blocks: below 2^29", static_cast<long long>(B) * Hkv * n_select);
+  DEC_CHECK(static_cast<long long>(B) * Hkv * (n_select * 4ll + 16) < (1ll << 31), DEC_EUNSUPPORTED,
+            "%lld listed blocks: below 2^29 - 2^23", static_cast<long long>(B) * Hkv * n_select);
   DEC_PTR(q);
   DEC_PTR(k_cache);
   DEC_PTR(v_cache);
