@@ -84,6 +84,16 @@ struct OnDevice {
   }
 };
 
+// A launch may wait for room in the stream: other Python threads run meanwhile.
+// The error message is this thread's own.
+template <typename Call>
+int without_gil(Call call) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int rc = call();
+  PyEval_RestoreThread(state);
+  return rc;
+}
+
 void done(int rc) {
   if (rc != DEC_OK) throw Failure{nullptr, rc, dec_last_error()};
 }
@@ -178,9 +188,12 @@ PyObject* kv4_store(PyObject* const* a) {
   const int32_t* pos = ints(a[2], c.B, c.dev, "pos");
   const int32_t* lens = ints(a[8], c.B, c.dev, "lens", true);
   const int from_cache = PyObject_IsTrue(a[9]);
+  if (from_cache < 0) throw Failure{nullptr, -1, ""};
   const OnDevice on(c.dev, a[10]);
-  done(dec_kv4_store(r.k, r.v, r.bf16, r.sb, r.st, r.sh, from_cache, static_cast<int>(r.T), pos, lens, T, c.kc, c.kp,
-                     c.vc, c.vp, c.B, c.Hkv, c.D, c.group(), c.S, on.stream));
+  done(without_gil([&] {
+    return dec_kv4_store(r.k, r.v, r.bf16, r.sb, r.st, r.sh, from_cache, static_cast<int>(r.T), pos, lens, T, c.kc, c.kp,
+                         c.vc, c.vp, c.B, c.Hkv, c.D, c.group(), c.S, on.stream);
+  }));
   Py_RETURN_NONE;
 }
 
@@ -191,8 +204,10 @@ PyObject* kv4_load(PyObject* const* a) {
   const int32_t* pos = ints(a[4], c.B, c.dev, "pos");
   const int32_t* lens = ints(a[7], c.B, c.dev, "lens", true);
   const OnDevice on(c.dev, a[8]);
-  done(dec_kv4_load(c.kc, c.kp, c.vc, c.vp, pos, lens, static_cast<int>(r.T), r.k, r.v, r.bf16, r.sb, r.st, r.sh, c.B,
-                    c.Hkv, c.D, c.group(), c.S, on.stream));
+  done(without_gil([&] {
+    return dec_kv4_load(c.kc, c.kp, c.vc, c.vp, pos, lens, static_cast<int>(r.T), r.k, r.v, r.bf16, r.sb, r.st, r.sh, c.B,
+                        c.Hkv, c.D, c.group(), c.S, on.stream);
+  }));
   Py_RETURN_NONE;
 }
 
@@ -202,6 +217,7 @@ PyObject* kv4_decode_attn(PyObject* const* a) {
   const at::Tensor& qt = tensor(a[0], "q");
   expect(qt.dim() == 3, "q must be [B, Hq, D], got " + str(qt.sizes()));
   const int64_t Hq = qt.size(1);
+  expect(Hq <= INT32_MAX, "too many heads");
   const void* q = gpu(a[0], at::kFloat, {c.B, Hq, c.D}, c.dev, "q");
   const int32_t* pos = ints(a[5], c.B, c.dev, "pos");
   void* o = gpu(a[6], at::kFloat, {c.B, Hq, c.D}, c.dev, "o");
@@ -209,8 +225,10 @@ PyObject* kv4_decode_attn(PyObject* const* a) {
   size_t bytes;
   PyObject* held = nullptr;
   void* ws = workspace(a[7], Hq, c.Hkv, c.D, c.dev, on, &bytes, &held);
-  const int rc = dec_kv4_decode_attn(static_cast<const float*>(q), c.kc, c.kp, c.vc, c.vp, pos, static_cast<float*>(o), ws,
-                                     bytes, c.B, Hq, c.Hkv, c.D, c.group(), c.S, on.stream);
+  const int rc = without_gil([&] {
+    return dec_kv4_decode_attn(static_cast<const float*>(q), c.kc, c.kp, c.vc, c.vp, pos, static_cast<float*>(o), ws,
+                               bytes, c.B, Hq, c.Hkv, c.D, c.group(), c.S, on.stream);
+  });
   if (rc != DEC_OK) Py_DECREF(held);
   done(rc);
   return held;
@@ -228,7 +246,7 @@ PyObject* block_bounds(PyObject* const* a) {
   void* bounds = gpu(a[2], at::kBFloat16, {B, Hkv, (S + 63) / 64, 2, D}, dev, "bounds");
   const int T = as_int(a[3]);
   const OnDevice on(dev, a[4]);
-  done(dec_block_bounds(kp, pos, T, bounds, B, Hkv, D, S, on.stream));
+  done(without_gil([&] { return dec_block_bounds(kp, pos, T, bounds, B, Hkv, D, S, on.stream); }));
   Py_RETURN_NONE;
 }
 
@@ -248,8 +266,10 @@ PyObject* select_blocks(PyObject* const* a) {
   void* blocks = gpu(a[3], at::kInt, {B, Hkv, n}, dev, "blocks");
   const int first = as_int(a[4]), last = as_int(a[5]);
   const OnDevice on(dev, a[6]);
-  done(dec_select_blocks(static_cast<const float*>(qp), bounds, pos, static_cast<int32_t*>(blocks), n, first, last, B, Hq,
-                         Hkv, D, NB * 64, on.stream));
+  done(without_gil([&] {
+    return dec_select_blocks(static_cast<const float*>(qp), bounds, pos, static_cast<int32_t*>(blocks), n, first, last, B,
+                             Hq, Hkv, D, NB * 64, on.stream);
+  }));
   Py_RETURN_NONE;
 }
 
@@ -272,8 +292,10 @@ PyObject* block_decode_attn(PyObject* const* a) {
   size_t bytes;
   PyObject* held = nullptr;
   void* ws = workspace(a[6], Hq, Hkv, D, dev, on, &bytes, &held);
-  const int rc = dec_block_decode_attn(static_cast<const float*>(q), kp, vp, pos, static_cast<const int32_t*>(blocks), n,
-                                       static_cast<float*>(o), ws, bytes, B, Hq, Hkv, D, S, on.stream);
+  const int rc = without_gil([&] {
+    return dec_block_decode_attn(static_cast<const float*>(q), kp, vp, pos, static_cast<const int32_t*>(blocks), n,
+                                 static_cast<float*>(o), ws, bytes, B, Hq, Hkv, D, S, on.stream);
+  });
   if (rc != DEC_OK) Py_DECREF(held);
   done(rc);
   return held;

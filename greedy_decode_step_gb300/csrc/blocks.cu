@@ -394,7 +394,7 @@ uint32_t select_smem(int NB) { return (NB * 4 + 15) / 16 * 16 + NB * 8 + NB * 4;
 }  // namespace
 
 cudaError_t launch_block_bounds(const BoundsArgs& a, int D, cudaStream_t st) {
-  const dim3 grid((a.T + kBlockKeys - 2) / kBlockKeys + 1, a.Hkv, a.B);
+  const dim3 grid((a.T - 1 + kBlockKeys - 1) / kBlockKeys + 1, a.Hkv, a.B);
   return D == 64 ? launch(block_bounds_kernel<64>, grid, dim3(kBoundThreads), 0, st, true, a)
                  : launch(block_bounds_kernel<128>, grid, dim3(kBoundThreads), 0, st, true, a);
 }

@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const __grid_constan
   }
 }
 
-dim3 kv4_grid(int T, int per, int Hkv, int B) { return dim3((T + per - 1) / per, Hkv * 2, B); }
+dim3 kv4_grid(int T, int per, int Hkv, int B) { return dim3((T - 1) / per + 1, Hkv * 2, B); }
 
 // (D, group, type) -> instantiation
 template <template <int, int, bool> class F, typename A>

@@ -36,8 +36,9 @@ int check_cache(int B, int Hkv, int D, int S_max) {
   DEC_CHECK(Hkv >= 1 && Hkv <= 4096, DEC_EUNSUPPORTED, "Hkv = %d outside 1..4096", Hkv);
   DEC_CHECK(D == 64 || D == 128, DEC_EUNSUPPORTED, "head_dim %d: supported 64 and 128", D);
   DEC_CHECK(S_max >= 1, DEC_EINVAL, "S_max must be >= 1");
-  DEC_CHECK(static_cast<long long>(B) * Hkv * S_max < (1ll << 31), DEC_EUNSUPPORTED,
-            "a cache of %lld (row, head, slot) entries: at most 2^31 - 1", static_cast<long long>(B) * Hkv * S_max);
+  // positions, and a CTA's tokens behind the last, stay in an int
+  DEC_CHECK(static_cast<long long>(B) * Hkv * S_max <= (1ll << 31) - 1024, DEC_EUNSUPPORTED,
+            "a cache of %lld (row, head, slot) entries: at most 2^31 - 1024", static_cast<long long>(B) * Hkv * S_max);
   return DEC_OK;
 }
 
@@ -50,6 +51,11 @@ int check_queries(int Hq, int Hkv) {
 int check_group(int D, int group) {
   DEC_CHECK((group == 32 || group == 64 || group == 128) && group <= D, DEC_EUNSUPPORTED,
             "group %d: supported 32, 64 and 128, at most head_dim", group);
+  return DEC_OK;
+}
+
+int check_tokens(int T) {
+  DEC_CHECK(T <= (1 << 30), DEC_EUNSUPPORTED, "T = %d tokens of a row: at most 2^30", T);
   return DEC_OK;
 }
 
@@ -85,6 +91,7 @@ int dec_kv4_store(const void* k, const void* v, int bf16, int64_t stride_row, in
   DEC_TRY(check_cache(B, Hkv, D, S_max));
   DEC_TRY(check_group(D, group));
   DEC_CHECK(T >= 0 && src_tokens >= 0, DEC_EINVAL, "T and src_tokens must be >= 0");
+  DEC_TRY(check_tokens(T));
   DEC_CHECK(T <= src_tokens, DEC_EINVAL, "T = %d tokens, but the source has %d", T, src_tokens);
   if (T == 0) return DEC_OK;
   DEC_PTR(k);
@@ -96,6 +103,7 @@ int dec_kv4_store(const void* k, const void* v, int bf16, int64_t stride_row, in
   DEC_PTR(k_params);
   DEC_PTR(v_codes);
   DEC_PTR(v_params);
+  DEC_CHECK(k_codes != v_codes && k_params != v_params, DEC_EINVAL, "K and V need caches of their own");
   Kv4StoreArgs a{};
   int sms;
   DEC_TRY(host_device(&sms, &a.err));
@@ -127,6 +135,7 @@ int dec_kv4_load(const void* k_codes, const void* k_params, const void* v_codes,
   DEC_TRY(check_cache(B, Hkv, D, S_max));
   DEC_TRY(check_group(D, group));
   DEC_CHECK(T >= 0, DEC_EINVAL, "T must be >= 0");
+  DEC_TRY(check_tokens(T));
   if (T == 0) return DEC_OK;
   DEC_PTR(k_codes);
   DEC_PTR(k_params);
@@ -136,7 +145,10 @@ int dec_kv4_load(const void* k_codes, const void* k_params, const void* v_codes,
   if (lens) DEC_INTS(lens);
   DEC_PTR(k_out);
   DEC_PTR(v_out);
+  DEC_CHECK(k_out != v_out, DEC_EINVAL, "k_out and v_out must differ");
   DEC_TRY(check_strides(stride_row, stride_token, stride_head, bf16));
+  DEC_CHECK((B == 1 || stride_row) && (T == 1 || stride_token) && (Hkv == 1 || stride_head), DEC_EINVAL,
+            "rows read back may not share memory (a stride of zero)");
   Kv4LoadArgs a{};
   int sms;
   DEC_TRY(host_device(&sms, &a.err));
@@ -261,8 +273,8 @@ int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cac
   DEC_TRY(check_cache(B, Hkv, D, S_max));
   DEC_TRY(check_queries(Hq, Hkv));
   DEC_CHECK(n_select >= 1, DEC_EINVAL, "n_select must be >= 1");
-  DEC_CHECK(static_cast<long long>(B) * Hkv * (n_select * 4ll + 16) < (1ll << 31), DEC_EUNSUPPORTED,
-            "%lld listed blocks: below 2^29 - 2^23", static_cast<long long>(B) * Hkv * n_select);
+  DEC_CHECK(static_cast<long long>(B) * Hkv * (n_select * 4ll + 16) < (1ll << 30), DEC_EUNSUPPORTED,
+            "%lld listed blocks and their heads: about 2^28 at most", static_cast<long long>(B) * Hkv * n_select);
   DEC_PTR(q);
   DEC_PTR(k_cache);
   DEC_PTR(v_cache);

@@ -679,7 +679,8 @@ template <class F, int kW, int STAGES>
 struct Smem {
   static __host__ __device__ uint32_t ring(int B, int G, int NT) { return qraw(B, G, NT) + G * F::D * 4; }
   static __host__ __device__ uint32_t qraw(int B, int G, int NT) { return obuf(B, NT) + kW * G * (F::D + 4) * 4; }
-  static __host__ __device__ uint32_t words(int B) { return ((2 * B + 1) * 4 + 127) / 128 * 128; }
+  // the plan of the 4-bit cache's balanced runs comes first
+  static __host__ __device__ uint32_t words(int B) { return F::kQuant ? ((2 * B + 1) * 4 + 127) / 128 * 128 : 0; }
   static __host__ __device__ uint32_t f(int B, int NT) { return words(B) + NT * F::kQWords * 32 * 4; }
   static __host__ __device__ uint32_t zq(int B, int NT) { return f(B, NT) + kMaxG * 4; }
   static __host__ __device__ uint32_t ms(int B, int NT) { return zq(B, NT) + 4 * 32 * 4; }

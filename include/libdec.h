@@ -213,7 +213,7 @@ int dec_select_tokens(const float* logits, const int32_t* prev_tokens, int n_pre
  * blocks of a bf16 cache.  They are single calls beside dec_gqa_decode_attn
  * (the captured decode loop keeps its bf16 cache).  The paper has no
  * counterpart of them.  Limits shared by all: B is 1..1024, Hkv 1..4096, D 64
- * or 128, Hq/Hkv an integer <= 16, B * Hkv * S_max < 2^31.  The GPU sets error
+ * or 128, Hq/Hkv an integer <= 16, B * Hkv * S_max <= 2^31 - 1024.  The GPU sets error
  * bit 4 for a position, count or block id outside its range.
  *
  * The 4-bit cache of one of K and V:
@@ -242,7 +242,8 @@ int dec_select_tokens(const float* logits, const int32_t* prev_tokens, int n_pre
  *     cache that dec_prefill or dec_qkv_gemv_rope filled)
  * T == 1: one decode step.  A row whose slots would leave either cache, or
  * whose lens[b] lies outside [0, T], is left as it was (error bit 4).  Slots
- * outside the written range keep their contents.
+ * outside the written range keep their contents.  A source may repeat rows (a
+ * stride of zero); the K and V caches are memory of their own.
  */
 int dec_kv4_store(const void* k, const void* v, int bf16, int64_t stride_row, int64_t stride_token,
                   int64_t stride_head, int from_cache, int src_tokens, const int32_t* pos, const int32_t* lens, int T,
@@ -252,7 +253,8 @@ int dec_kv4_store(const void* k, const void* v, int bf16, int64_t stride_row, in
 /*
  * Reads the range back: slot pos[b] + t of the cache, t < lens[b], as rows
  * of float32 or bf16 (one rounding of z + s (c - 8)) at the given strides.
- * Rows t >= lens[b], and rows refused as above, keep their contents.
+ * Rows t >= lens[b], and rows refused as above, keep their contents.  The rows
+ * written may not share memory.
  */
 int dec_kv4_load(const void* k_codes, const void* k_params, const void* v_codes, const void* v_params,
                  const int32_t* pos, const int32_t* lens, int T, void* k_out, void* v_out, int bf16,

@@ -267,6 +267,32 @@ def test_many_blocks_per_warp(gd):
     assert gd.device_error(clear=True) == 0
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,S,B,n", [(128, 16, 2, 700, 40, 5), (128, 16, 1, 300, 110, 3), (64, 24, 2, 900, 33, 7),
+                                            (128, 4, 4, 2000, 30, 12), (128, 16, 1, 100, 1024, 2)])
+def test_attention_of_many_rows(gd, D, Hq, Hkv, S, B, n):
+    """More (row, KV head) items than clusters fit: runs across items, cut items joined, every group width."""
+    k, v = make_k(B, Hkv, S, D, 61), make_k(B, Hkv, S, D, 63)
+    pos = [(37 * b * b + 11 * b) % (S + 1) - 1 for b in range(B)]
+    r = gen(19)
+    ids = torch.randint(-1, n_blocks(S), (B, Hkv, n), generator=r).to(torch.int32)
+    q = torch.randn(B, Hq, D, generator=gen(4)).cuda()
+    o = torch.full_like(q, float("nan"))
+    gd.dec_block_decode_attn(q, k, v, i32(pos), ids.cuda(), o)
+    check_attention(q, k, v, pos, ids.tolist(), o)
+    assert gd.device_error(clear=True) == 0
+
+
+def test_selection_of_many_rows(gd):
+    """One CTA per (row, KV head), where clusters of them do not fit."""
+    B, Hq, Hkv, D, S, n = 60, 8, 4, 64, 5000, 9
+    bd = torch.randn(B, Hkv, n_blocks(S), 2, D, generator=gen(1)).sort(3, descending=True).values.bfloat16().cuda()
+    q = torch.randn(B, Hq, D, generator=gen(3)).cuda()
+    pos = [(131 * b) % (S + 1) - 1 for b in range(B)]
+    got = run_select(gd, q, bd, pos, n, 1, 1)
+    assert gd.device_error(clear=True) == 0
+    check_select(got, q, bd, pos, n, 1, 1)
+
+
 def test_a_decode_step_with_selected_blocks(gd):
     """As a decode loop runs them: bounds of the prompt, then per step the new slot's bounds, the selection and
     the attention.  With every block listed it is dec_gqa_decode_attn; captured, it replays to the same bits."""

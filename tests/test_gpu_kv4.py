@@ -299,6 +299,20 @@ def test_attention_of_many_short_rows(gd, B):
     assert gd.device_error(clear=True) == 0
 
 
+@pytest.mark.parametrize("D,group,Hq,Hkv,S,B", [(128, 32, 18, 3, 500, 25), (128, 64, 24, 2, 401, 40), (64, 32, 16, 2, 230, 40),
+                                                (128, 128, 16, 1, 333, 101), (64, 64, 8, 8, 1200, 13),
+                                                (128, 32, 4, 1, 3000, 110), (128, 32, 16, 1, 40, 1024)])
+def test_attention_of_many_rows(gd, D, group, Hq, Hkv, S, B):
+    """More (row, KV head) items than clusters fit: runs across items, cut items joined, every group width."""
+    pos = [(37 * b * b + 11 * b) % (S + 1) - 1 for b in range(B)]
+    cache = make_cache(B, Hkv, S, D, group, pos, 55)
+    q = torch.randn(B, Hq, D, generator=gen(4)).cuda()
+    o = torch.full_like(q, float("nan"))
+    gd.dec_kv4_decode_attn(q, *cache, i32(pos), o)
+    check_attention(gd, q, cache, pos, o)
+    assert gd.device_error(clear=True) == 0
+
+
 def test_attention_of_rows_without_keys_and_refused_rows(gd):
     B, Hq, Hkv, D, S = 4, 4, 2, 64, 50
     cache = make_cache(B, Hkv, S, D, 32, [49] * B, 61)
@@ -366,6 +380,121 @@ def test_same_bits_in_every_call_on_another_stream_and_in_a_graph(gd):
     torch.cuda.synchronize()
     check_attention(gd, q, cache, [5, -1, 700], o)
     assert gd.device_error(clear=True) == 0
+
+
+def test_two_calls_at_once_with_workspaces_of_their_own(gd):
+    B, Hq, Hkv, D, S = 2, 16, 4, 128, 20000
+    cases = []
+    for i in range(2):
+        pos = [S - 1 - 500 * i, 9000 + i]
+        cache = tuple(torch.randint(0, 256, (B, Hkv, S, D // 2), dtype=torch.uint8, generator=gen(i + j)).cuda() if j % 2 == 0
+                      else torch.rand(B, Hkv, S, 4, 2, generator=gen(i + j)).half().cuda() for j in range(4))
+        q = torch.randn(B, Hq, D, generator=gen(i)).cuda()
+        ref = torch.empty_like(q)
+        gd.dec_kv4_decode_attn(q, *cache, i32(pos), ref)
+        cases.append((q, cache, i32(pos), ref, torch.empty_like(q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, cache, pos, ref, o, s in cases:
+            o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for q, cache, pos, ref, o, s in cases:
+                gd.dec_kv4_decode_attn(q, *cache, pos, o, stream=s)
+        torch.cuda.synchronize()
+        for q, cache, pos, ref, o, s in cases:
+            assert torch.equal(o, ref)
+
+
+def test_calls_wait_for_what_comes_before_them(gd):
+    """Chains of writes, stores, attention and reads without a wait of the host give what they give with one."""
+    B, Hq, Hkv, D, S, group = 3, 8, 2, 64, 90, 32
+
+    def chain(wait):
+        cache = empty_cache(B, Hkv, S, D, group, fill=0)
+        pos = i32([0, 0, 0])
+        g = torch.Generator("cuda").manual_seed(1)
+        o, ws, out = torch.empty(B, Hq, D, device="cuda"), None, []
+        kv = torch.empty(2, B, 1, Hkv, D, device="cuda")
+        q = torch.empty(B, Hq, D, device="cuda")
+        back = torch.empty(2, B, 1, Hkv, D, device="cuda")
+        for step in range(80):
+            kv.normal_(generator=g)
+            q.normal_(generator=g)
+            gd.dec_kv4_store(kv[0], kv[1], pos, *cache)
+            gd.dec_kv4_load(*cache, pos, back[0], back[1])
+            ws = gd.dec_kv4_decode_attn(q, *cache, pos, o, ws=ws)
+            if wait:
+                torch.cuda.synchronize()
+            out.append(o + back.sum())
+            pos += 1
+            kv.zero_()
+            q.zero_()
+        return torch.stack(out)
+
+    a, b = chain(True), chain(False)
+    assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+FIRST_CALL = """
+import sys, torch
+sys.path.insert(0, {root!r})
+import greedy_decode_step_gb300 as gd
+B, Hq, Hkv, D, S = 2, 8, 2, 128, 100
+c = [torch.zeros(B, Hkv, S, D // 2, dtype=torch.uint8, device="cuda") if i % 2 == 0 else
+     torch.ones(B, Hkv, S, 4, 2, dtype=torch.float16, device="cuda") for i in range(4)]
+k, v, q = (torch.randn(B, n, D, device="cuda") for n in (Hkv, Hkv, Hq))
+pos, o = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.empty(B, Hq, D, device="cuda")
+ws = torch.empty(gd.long_attn_workspace_size(Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+kc = torch.zeros(B, Hkv, S, D, dtype=torch.bfloat16, device="cuda")
+bd = torch.zeros(B, Hkv, 2, 2, D, dtype=torch.bfloat16, device="cuda")
+bl = torch.empty(B, Hkv, 2, dtype=torch.int32, device="cuda")
+o2 = torch.empty_like(o)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    gd.dec_kv4_store(k[:, None], v[:, None], pos, *c)
+    gd.dec_kv4_decode_attn(q, *c, pos, o, ws=ws)
+    gd.dec_block_bounds(kc, pos, bd)
+    gd.dec_select_blocks(q, bd, pos, bl)
+    gd.dec_block_decode_attn(q, kc, kc, pos, bl, o2, ws=ws)
+g.replay()
+torch.cuda.synchronize()
+back = torch.empty(2, B, 1, Hkv, D, device="cuda")
+gd.dec_kv4_load(*c, pos, back[0], back[1])
+assert torch.equal(o.view(B, Hkv, -1, D), back[1, :, 0][:, :, None].expand(-1, -1, Hq // Hkv, -1)), "one key: its value"
+assert torch.all(o2 == 0) and bl.tolist() == [[[0, -1]] * Hkv] * B
+assert gd.device_error() == 0
+print("ok")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured(gd):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
+
+
+def test_padded_and_repeated_source_rows(gd):
+    """T may be longer than the cache where lens are not, and a source may repeat one row (stride 0)."""
+    B, Hkv, S, D, T = 2, 2, 6, 64, 40
+    one = torch.randn(1, 1, Hkv, D, generator=gen(5)).cuda()
+    k = one.expand(B, T, Hkv, D)
+    cache = empty_cache(B, Hkv, S, D, 64)
+    gd.dec_kv4_store(k, k, i32([0, 2]), *cache, lens=i32([6, 3]))
+    torch.cuda.synchronize()
+    assert gd.device_error(clear=True) == 0
+    c, p = R.quantise(one[0, 0], 64)
+    for b, rows_ in ((0, range(6)), (1, range(2, 5))):
+        for t in range(S):
+            want = R.pack(c) if t in rows_ else torch.full((Hkv, D // 2), 0xAB, dtype=torch.uint8)
+            assert torch.equal(cache[0][b, :, t].cpu(), want) and torch.equal(cache[2][b, :, t].cpu(), want)
+    out = torch.empty(B, 3, Hkv, D, device="cuda")
+    with pytest.raises(gd.DecError, match="share memory"):
+        gd.dec_kv4_load(*cache, i32([0, 0]), out[:, :1].expand(B, 3, Hkv, D), out[:, 1:2].expand(B, 3, Hkv, D))
 
 
 def test_offsets_past_32_bits(gd):

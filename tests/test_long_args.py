@@ -25,9 +25,10 @@ def refused(gd, name, good, code, word, **change):
     assert rc == code and word in msg, (rc, msg)
 
 
-STORE = dict(k=P, v=P, bf16=0, sb=1024, st=512, sh=128, from_cache=0, src=4, pos=P, lens=None, T=4, kc=P, kp=P, vc=P, vp=P,
+Q = 0x2000
+STORE = dict(k=P, v=P, bf16=0, sb=1024, st=512, sh=128, from_cache=0, src=4, pos=P, lens=None, T=4, kc=P, kp=P, vc=Q, vp=Q,
              B=2, Hkv=4, D=128, group=32, S=64, stream=None)
-LOAD = dict(kc=P, kp=P, vc=P, vp=P, pos=P, lens=None, T=4, k=P, v=P, bf16=1, sb=1024, st=512, sh=128, B=2, Hkv=4, D=128,
+LOAD = dict(kc=P, kp=P, vc=P, vp=P, pos=P, lens=None, T=4, k=P, v=Q, bf16=1, sb=1024, st=512, sh=128, B=2, Hkv=4, D=128,
             group=32, S=64, stream=None)
 ATTN = dict(q=P, kc=P, kp=P, vc=P, vp=P, pos=P, o=P, ws=P, ws_bytes=1 << 40, B=2, Hq=8, Hkv=4, D=128, group=32, S=64,
             stream=None)
@@ -58,7 +59,7 @@ def test_sizes(gd, name, good):
 @pytest.mark.parametrize("name,good", ALL, ids=[n for n, _ in ALL])
 def test_pointers(gd, name, good):
     for arg, x in good.items():
-        if x == P:
+        if x in (P, Q):
             refused(gd, name, good, gd.DEC_EINVAL, "null", **{arg: None})
             refused(gd, name, good, gd.DEC_EINVAL, "aligned", **{arg: P + 2})
     if "lens" in good:
@@ -73,6 +74,12 @@ def test_particular_arguments(gd):
         refused(gd, "dec_kv4_store", STORE, gd.DEC_EINVAL, "strides", **{s: 130})
         refused(gd, "dec_kv4_load", LOAD, gd.DEC_EINVAL, "strides", **{s: 132})  # 264 bytes of bf16
         refused(gd, "dec_kv4_load", LOAD, gd.DEC_EINVAL, "strides", **{s: -8})
+        refused(gd, "dec_kv4_load", LOAD, gd.DEC_EINVAL, "share memory", **{s: 0})
+    refused(gd, "dec_kv4_load", LOAD, gd.DEC_EINVAL, "must differ", v=P)
+    refused(gd, "dec_kv4_store", STORE, gd.DEC_EINVAL, "of their own", vc=P)
+    refused(gd, "dec_kv4_store", STORE, gd.DEC_EINVAL, "of their own", vp=P)
+    for name, good in ALL[:2]:
+        refused(gd, name, good, gd.DEC_EUNSUPPORTED, "2^30", T=(1 << 30) + 1, **({"src": 2 ** 31 - 1} if "src" in good else {}))
     need = gd.long_attn_workspace_size(8, 4, 128)
     refused(gd, "dec_kv4_decode_attn", ATTN, gd.DEC_EINVAL, "needs", ws_bytes=need - 1)
     refused(gd, "dec_block_decode_attn", BLOCK, gd.DEC_EINVAL, "needs", ws_bytes=need - 1)
@@ -85,7 +92,7 @@ def test_particular_arguments(gd):
     refused(gd, "dec_select_blocks", SELECT, gd.DEC_EINVAL, "n_first", last=2 ** 31 - 1)
     refused(gd, "dec_select_blocks", SELECT, gd.DEC_EUNSUPPORTED, "524288", S=524289)
     refused(gd, "dec_block_decode_attn", BLOCK, gd.DEC_EINVAL, "n_select", n=0)
-    refused(gd, "dec_block_decode_attn", BLOCK, gd.DEC_EUNSUPPORTED, "2^29", n=1 << 27)
+    refused(gd, "dec_block_decode_attn", BLOCK, gd.DEC_EUNSUPPORTED, "2^28", n=1 << 27)
 
 
 def test_no_tokens_is_no_work(gd):
