@@ -5,12 +5,13 @@
 //
 // One pass over the keys with a running maximum and sum.  The keys of all
 // (row, KV head) items are cut into units (32 keys of the 4-bit cache, 16 of
-// the bf16 one), laid end to end, and every CTA takes an equal run of them;
-// warp w of a CTA takes the run's units w, w + 8, ...  Each warp has a ring of
-// its own in shared memory that it fills with cp.async, so no warp waits for
-// another inside an item.  At an item's end the warps' states are merged; an
-// item cut between CTAs leaves one partial per CTA, which a second, small
-// launch joins (it starts by programmatic launch while the first one runs).
+// the bf16 one), laid end to end, and every CTA takes an equal run of them; its
+// warps take the run's units in turn.  Each warp has a ring of its own in shared
+// memory that it fills with cp.async, so no warp waits for another inside an
+// item.  At an item's end the warps' states are merged; an item cut between
+// CTAs leaves one partial per CTA, which a second, small launch joins (it starts
+// by programmatic launch while the first one runs).  Few and short items go to
+// thread-block clusters instead, one launch.
 //
 // Tensor cores (mma.sync m16n8k16): a decode step has few query rows per KV
 // head, so the keys take the M side and the N side holds 4 query heads twice,
@@ -55,6 +56,8 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// every copy of this thread, of groups that are not committed too
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -366,9 +369,8 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
 // A warp's running state.  Lane (g, c) of n-tile nt serves head 4 nt + c: m
 // the reference score (log2 units; the same in the eight lanes of a head), mu
 // the value subtracted (0 while m is -inf; kUp less for the 4-bit cache), l
-// this lane's share of the sum;
-// o[nt][..][e] rows of O^T, columns (upper part, remainder) of the head.
-// zs: likewise sum_j p_j times the words of key j's (s, z) pairs, row g the
+// this lane's share of the sum, o[nt][..][e] rows of O^T, columns (upper part,
+// remainder) of the head.  zs: sum_j p_j times the words of key j's (s, z) pairs, row g the
 // g-th half word, so that row 2 i + 1 is the z sum of group i.
 template <class F, int NT>
 struct State {
@@ -868,7 +870,7 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
     cp_async_commit();
     return nk;
   };
-  // the query rows of the item that holds unit t, without a commit of their own
+  // an item's query rows, without a commit of their own
   float* qraw = reinterpret_cast<float*>(smem + L::qraw(a.B, G, NT));
   auto fetch_query = [&](const Item& it) {
     const float* q = a.q + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D;
@@ -926,7 +928,8 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
       }
       slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
-    if (seg_end < t1) cp_async_wait<0>();
+    // the next query has to be in; a warp without a unit here has not committed it
+    if (seg_end < t1) cp_async_wait_all();
     // the warps' states, each relative to its own maximum
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -998,7 +1001,7 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
     __syncthreads();
     t = seg_end;
   }
-  cp_async_wait<0>();
+  cp_async_wait_all();
   if constexpr (CL) {
     if (t0 >= t1) cluster_wait();
     cluster_arrive();
@@ -1086,11 +1089,12 @@ __global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant_
 // CTAs per (row, KV head): up to 8, while the clusters take at most two thirds
 // of the SMs (16 clusters of 8 wait for one another at 128 of 152: 9.3 us where
 // 64 CTAs take 7.4), or 1: the balanced runs with their partials and second
-// launch, about 3 us more, but all SMs.  A unit takes a warp about 1 us, so the
-// clusters win while a warp of theirs has at most 5 units more than one of the
-// balanced runs.  Measured, clusters against runs (b rows, query/KV heads, keys):
+// launch, about 3 us more, but all SMs.  A unit takes a warp about 1 us, NT times
+// that for wide groups, so the clusters win while a warp of theirs has at most
+// 5 / NT units more than one of the balanced runs.  Measured, clusters against runs (b rows, query/KV heads, keys):
 // 1 32/8 4k 6.6 / 8.6 us, 16k 12.8 / 15.9, 32k 21.1 / 19.6; 8 12/3 8k 12.5 / 15.1,
-// 16k 20.6 / 20.7, 32k 35.8 / 29.7; 64 listed blocks 7.7 / 9.9, 256 17.6 / 18.5.
+// 16k 20.6 / 20.7, 32k 35.8 / 29.7; 1 16/1 2k 9.9 / 9.7, 4k 11.9 / 10.2; 64 listed
+// blocks 7.7 / 9.9, 256 17.6 / 18.5.
 template <class F, int NT>
 int cluster_size(const LongAttnArgs& a, int sms) {
   using S = Shape<F, NT, true>;
@@ -1100,7 +1104,7 @@ int cluster_size(const LongAttnArgs& a, int sms) {
   while (c < 8 && 2 * c * items <= 2 * sms / 3 &&
          Smem<F, S::kW, S::kStages>::bytes(a.B, a.Hq / a.Hkv, NT, 2 * c) <= kSmemMax)
     c *= 2;
-  return units * sms - units * items * c <= 5ll * S::kW * sms * c ? c : 1;
+  return (units * sms - units * items * c) * NT <= 5ll * S::kW * sms * c ? c : 1;
 }
 
 template <class F, int NT>
