@@ -379,10 +379,10 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
 // g-th half word, so that row 2 i + 1 is the z sum of group i.
 template <class F, int NT>
 struct State {
-  // 4-bit: m follows a larger score only once it leads by kSlack, so that the
-  // sums are rescaled seldom; probabilities are at most 2^(kUp + kSlack), the
-  // top of the half range
-  static constexpr float kUp = F::kQuant ? 11.f : 0.f, kSlack = F::kQuant ? 4.f : 0.f;
+  // m follows a larger score only once it leads by kSlack, so that the sums are
+  // rescaled seldom; probabilities are at most 2^(kUp + kSlack), with the 4-bit
+  // cache the top of the half range
+  static constexpr float kUp = F::kQuant ? 11.f : 0.f, kSlack = 4.f;
   float o[NT][F::D / 16][4];
   float m[NT], mu[NT], l[NT];
   float zs[NT];
@@ -637,7 +637,7 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
     if (g >= nk) s[nt][0] = -INFINITY;
     if (g + 8 >= nk) s[nt][1] = -INFINITY;
     mx[nt] = fmaxf(s[nt][0], s[nt][1]);
-    more |= mx[nt] > st.m[nt];
+    more |= mx[nt] > st.m[nt] + State<F, NT>::kSlack;
   }
   if (__any_sync(0xffffffffu, more)) raise<F, NT>(st, mx, 0.f);
   uint32_t b0[NT], b1[NT], c0[NT], c1[NT];

@@ -298,9 +298,10 @@ int dec_block_bounds(const void* k_cache, const int32_t* pos, int T, void* bound
  * query heads h and bounds hi, lo of the block,
  *   score(j) = sum_h sum_d max(q[b][h][d] hi[d], q[b][h][d] lo[d])
  * the first n_first and last n_last blocks and then the best-scored others
- * are taken, n_select in all (all blocks where there are no more).  Blocks are
- * ranked by their exact scores, not by float32 roundings of them; equal ones by
- * the lower index; a NaN score counts as -infinity.
+ * are taken, n_select in all (all blocks where there are no more).  hi >= lo as
+ * dec_block_bounds writes them.  Blocks are ranked by their scores in 64 bits,
+ * not by float32 roundings of them; equal ones by the lower index; a NaN score
+ * counts as -infinity.
  * blocks: int32 [B][Hkv][n_select], ascending, -1 in unused places (pos[b] ==
  * -1: all).  n_first + n_last <= n_select <= 8192; S_max <= 524,288.  A row
  * with any other pos outside [0, S_max) is not written (error bit 4).

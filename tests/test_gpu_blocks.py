@@ -2,8 +2,8 @@
 attention over listed blocks, against plain forms in 64 bits.
 
 Bounds are values of the cache and the selection goes by exact scores: both
-must agree exactly.  Attention: query and probabilities are two bf16 parts
-(2^-17 of each value), tensor-core sums of 16 terms, so a score is within
+must agree exactly.  Attention: query and probabilities are three bf16 parts (two already leave
+2^-17 of each value), tensor-core sums of 16 terms, so a score is within
 2^-16 A of its value, A the largest sum of |q_d k_d| / sqrt(D) over the keys,
 a probability within 2^-15 A + 2^-16 relative, and with numerator and
 denominator |o - exact| <= 2^-14 (1 + A) sum_j p_j |v_j|.

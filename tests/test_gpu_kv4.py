@@ -478,6 +478,39 @@ def test_the_first_calls_of_a_process_may_be_captured(gd):
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
 
 
+def test_graphs_whose_calls_follow_copies_and_fills(gd):
+    """Every call directly behind a memory copy or fill node of the same graph sees its result."""
+    B, Hq, Hkv, D, S = 2, 8, 2, 64, 300
+    cache = make_cache(B, Hkv, S, D, 32, [S - 1] * B, 91, poison=False)
+    src = [torch.randn(B, 1, Hkv, D, generator=gen(i)).cuda() for i in (1, 2)]
+    q_src, pos_src = torch.randn(B, Hq, D, generator=gen(3)).cuda(), i32([290, 17])
+    k, v, q, pos = torch.zeros_like(src[0]), torch.zeros_like(src[1]), torch.zeros_like(q_src), torch.zeros_like(pos_src)
+    o, back = torch.empty_like(q), torch.empty(2, B, 1, Hkv, D, device="cuda")
+    ws = gd.dec_kv4_decode_attn(q, *cache, pos, o)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pos.copy_(pos_src)
+        k.copy_(src[0])
+        v.copy_(src[1])
+        gd.dec_kv4_store(k, v, pos, *cache)
+        back.zero_()
+        gd.dec_kv4_load(*cache, pos, back[0], back[1])
+        q.copy_(q_src)
+        gd.dec_kv4_decode_attn(q, *cache, pos, o, ws=ws)
+        pos.zero_()
+        q.zero_()
+    for _ in range(3):
+        o.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        c, p = R.quantise(src[i][:, 0], 32)
+        assert torch.equal(back[i][:, 0].cpu(), R.values(R.pack(c), p).float())
+    check_attention(gd, q_src, cache, [290, 17], o)
+    assert gd.device_error(clear=True) == 0
+
+
 def test_padded_and_repeated_source_rows(gd):
     """T may be longer than the cache where lens are not, and a source may repeat one row (stride 0)."""
     B, Hkv, S, D, T = 2, 2, 6, 64, 40
