@@ -93,9 +93,9 @@ __global__ void __launch_bounds__(kBoundThreads) block_bounds_kernel(const __gri
 
 // ----------------------------------------------------------------------------- selection
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelMaxCluster = 4;
+constexpr int kSelMaxCluster = 8;
 
 // Larger score, larger key; a NaN counts as -infinity.
 __device__ __forceinline__ uint32_t score_key(float s) {
@@ -128,13 +128,14 @@ __device__ __forceinline__ float batch_sum(float (&s)[kBatch]) {
   return s[0];
 }
 
-// The want-th largest of n <= kSelThreads keys, by a search of three trials a
+// The want-th largest of n <= kWarpKeys keys, by a search of three trials a
 // round in warp 0, whose lanes hold them in registers; it ends once a trial
 // splits off exactly `want` keys (about half of log2 n + 2 rounds for unlike
 // keys, 16 at most).
+constexpr int kWarpKeys = 512;
 __device__ __forceinline__ uint32_t kth_largest_warp(const uint32_t* key, int n, int want, uint32_t* result) {
   if (threadIdx.x < 32) {
-    constexpr int kPer = kSelThreads / 32;
+    constexpr int kPer = kWarpKeys / 32;
     uint32_t k[kPer], most = 0, least = 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -177,22 +178,21 @@ __device__ __forceinline__ uint32_t kth_largest_warp(const uint32_t* key, int n,
   return *result;
 }
 
-// The same for any n: four bits per round, warp w counting the keys at or
-// above the w-th of 15 trial cuts.
-__device__ __forceinline__ uint32_t kth_largest_cta(const uint32_t* key, int n, int want,
-                                                    int (*counts)[kSelWarps]) {
+// The same for any n: four bits per round, the warps counting the keys at or
+// above 15 trial cuts.
+__device__ __forceinline__ uint32_t kth_largest_cta(const uint32_t* key, int n, int want, int (*counts)[16]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t cut = 0;
 #pragma unroll 1
   for (int shift = 28; shift >= 0; shift -= 4) {
     int* c = counts[(shift >> 2) & 1];
-    if (warp < 15) {
-      const uint32_t trial = cut | (static_cast<uint32_t>(warp + 1) << shift);
+    for (int w = warp; w < 15; w += kSelWarps) {
+      const uint32_t trial = cut | (static_cast<uint32_t>(w + 1) << shift);
       int m = 0;
 #pragma unroll 4
       for (int j = lane; j < n; j += 32) m += key[j] >= trial ? 1 : 0;
       m = __reduce_add_sync(0xffffffffu, m);
-      if (lane == 0) c[warp] = m;
+      if (lane == 0) c[w] = m;
     }
     __syncthreads();
     int digit = 0;  // the counts fall with the trial
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   constexpr int kPerWarp = 32 / kVec;   // blocks a warp scores side by side
   __shared__ float w32[2 * D];
   __shared__ float err_red[kSelMaxCluster][kSelWarps];
-  __shared__ int counts[2][kSelWarps];
+  __shared__ int counts[2][16];
   __shared__ int n_near, n_over;
   __shared__ uint32_t s_cut;
   const int ctas = a.cluster, rank = blockIdx.x % ctas;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
     for (int j = 0; j < kSelWarps; ++j) E = fmaxf(E, err_red[i][j]);
   E = fmaf(E, 1.0f / (1 << 19), 1e-41f);
   const uint32_t cut = want == 0                         ? 0u
-                       : hi_free - lo_free <= kSelThreads ? kth_largest_warp(key + lo_free, hi_free - lo_free, want, &s_cut)
+                       : hi_free - lo_free <= kWarpKeys ? kth_largest_warp(key + lo_free, hi_free - lo_free, want, &s_cut)
                                                           : kth_largest_cta(key + lo_free, hi_free - lo_free, want, counts);
   const float tau = float_from_order_key(cut);
   // above: in; near the cut: listed, in any order
@@ -411,7 +411,8 @@ cudaError_t launch_block_bounds(const BoundsArgs& a, int D, cudaStream_t st) {
 
 // CTAs per item: as many as fit the GPU at one per SM beside the other items',
 // but no more than leave each warp its batch of blocks.  (b = 1, 8 heads, 512
-// blocks: 10.0 us with one, 8.7 with two, 8.0 with four.)
+// blocks: 9.6 us with one, 6.9 with four, 6.4 with eight; CTAs of 512 threads 9.2,
+// 6.9 and 6.9.)
 int select_cluster(int items, int NB, int D, int sms) {
   const int batch = kSelWarps * (32 / (2 * D / 8)) * kBatch;
   int c = 1;
