@@ -53,6 +53,7 @@ struct LongAttnArgs {
   int n_select;
   float* part;                   // [2 * n_cta][G * (D + 2)]
   int B, Hq, Hkv, S_max;
+  int G;                         // Hq / Hkv: set by the launch
   int n_cta;                     // CTAs of the balanced launch: set by the launch
   int cluster;                   // CTAs per (row, KV head), or 1: set by the launch
   float scale_log2;              // log2(e) / sqrt(D)

@@ -179,6 +179,16 @@ struct Bf16 {
 
 // ----------------------------------------------------------------------------- plan
 
+// x / d for x >= 0, d >= 1 by a float quotient and its correction: a division of
+// integers is 20 instructions, and at a launch's start each costs some 15 cycles.
+__device__ __forceinline__ int quot(int x, int d) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(d)));
+  int r = x - q * d;
+  while (r < 0) --q, r += d;
+  while (r >= d) ++q, r -= d;
+  return q;
+}
+
 // Units of all items end to end: row b's Hkv items hold pre[b] .. pre[b + 1].
 // Every item opens with kOpen units without keys, about what changing over to
 // an item costs a CTA (merging the warps' states, the next query), so that a run
@@ -190,7 +200,7 @@ struct Runs {
   int n, q, longer;  // runs 0 .. longer - 1 hold q + 1 units
   __device__ __forceinline__ Runs(int n_cta, int T, int warps) {
     n = min(n_cta, (T + warps - 1) / warps);
-    q = n ? T / n : 0;
+    q = n ? quot(T, n) : 0;
     longer = T - q * n;
   }
   __device__ __forceinline__ int start(int c) const { return c * q + min(c, longer); }
@@ -255,6 +265,7 @@ struct Item {
 };
 
 // The item that holds unit t, the same for the whole warp.
+template <class F>
 __device__ __forceinline__ Item item_at(const LongAttnArgs& a, const int* pre, const int* len, int t) {
   int lo = 0;
   if (a.B <= 32) {  // one look by the warp
@@ -270,8 +281,8 @@ __device__ __forceinline__ Item item_at(const LongAttnArgs& a, const int* pre, c
   }
   Item it;
   it.b = lo;
-  const int per = (pre[lo + 1] - pre[lo]) / a.Hkv;
-  it.h = (t - pre[lo]) / per;
+  const int per = row_places<F>(a, len[lo]);
+  it.h = quot(t - pre[lo], per);
   it.end = pre[lo] + (it.h + 1) * per;
   it.start = it.end - per + kOpen;
   it.len = len[lo];
@@ -717,7 +728,7 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
   constexpr int kW = Shape<F, NT, CL>::kW, kThreads = 32 * kW, STAGES = Shape<F, NT, CL>::kStages;
   using L = Smem<F, kW, STAGES>;
   constexpr int D = F::D;
-  const int G = a.Hq / a.Hkv;
+  const int G = a.G;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   int* pre = reinterpret_cast<int*>(smem);
   int* len = pre + a.B + 1;
@@ -736,9 +747,9 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
   Item only{};  // CL: the cluster's item
   if constexpr (CL) {
     cluster_arrive();  // CTA 0 has started before anybody writes to it
-    const int item = blockIdx.x / a.cluster;
+    const int item = quot(blockIdx.x, a.cluster);
     cta = blockIdx.x - item * a.cluster;
-    only.b = item / a.Hkv;
+    only.b = quot(item, a.Hkv);
     only.h = item - only.b * a.Hkv;
     only.len = row_keys(a, a.pos[only.b]);
     if (only.len < 0 && only.h == 0 && cta == 0 && tid == 0) atomicOr(a.err, kErrPosRange);
@@ -760,16 +771,16 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
     if constexpr (CL) {
       return only;
     } else if constexpr (!F::kQuant) {
-      const int per = row_places<F>(a, 0), item = t / per;
+      const int per = row_places<F>(a, 0), item = quot(t, per);
       Item it;
-      it.b = item / a.Hkv;
+      it.b = quot(item, a.Hkv);
       it.h = item - it.b * a.Hkv;
       it.end = (item + 1) * per;
       it.start = it.end - per + kOpen;
       it.len = row_keys(a, a.pos[it.b]);
       return it;
     } else {
-      return item_at(a, pre, len, t);
+      return item_at<F>(a, pre, len, t);
     }
   };
 
@@ -785,8 +796,8 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
     const int t = t0 + warp + kW * (k + lane);
     if (t >= t1) return -1;
     const int per = row_places<F>(a, 0);
-    const int item = CL ? only.b * a.Hkv + only.h : t / per, u = CL ? t : t % per - kOpen;
-    return u < 0 ? -1 : a.blocks[static_cast<size_t>(item) * a.n_select + u / (kBlockKeys / F::kUnit)];
+    const int item = CL ? only.b * a.Hkv + only.h : quot(t, per), u = CL ? t : t - item * per - kOpen;
+    return u < 0 ? -1 : a.blocks[static_cast<size_t>(item) * a.n_select + static_cast<unsigned>(u) / (kBlockKeys / F::kUnit)];
   };
   if constexpr (!F::kQuant) {
     ids = fetch_ids(0);
@@ -854,7 +865,7 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
         const bool bad = id < -1 || id > (a.S_max - 1) / kBlockKeys;
         if (bad && lane == 0) atomicOr(a.err, kErrPosRange);
         const int k0 =
-            bad || id < 0 ? max(li.len, 0) : id * kBlockKeys + (t - li.start) % (kBlockKeys / F::kUnit) * F::kUnit;
+            bad || id < 0 ? max(li.len, 0) : id * kBlockKeys + ((t - li.start) & (kBlockKeys / F::kUnit - 1)) * F::kUnit;
         nk = max(0, min(F::kUnit, li.len - k0));
         if (nk > 0) {
           const size_t row = (static_cast<size_t>(li.b) * a.Hkv + li.h) * a.S_max + k0;
@@ -1039,7 +1050,7 @@ template <class F, int NT>
 __global__ void __launch_bounds__(F::D) long_merge_kernel(const __grid_constant__ LongAttnArgs a) {
   extern __shared__ __align__(16) int pre[];
   constexpr int D = F::D;
-  const int G = a.Hq / a.Hkv, head = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  const int G = a.G, head = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
   int* at = pre + 2 * a.B + 1;  // [n_cta] partials of this item, in floats
   float* ml = reinterpret_cast<float*>(at + a.n_cta);  // [2 n_cta] their maxima and sums
   if (threadIdx.x < 32) prefix_rows<F>(a, pre, pre + a.B + 1, false);
@@ -1115,6 +1126,7 @@ int cluster_size(const LongAttnArgs& a, int sms) {
 template <class F, int NT>
 cudaError_t run(LongAttnArgs a, int sms, cudaStream_t st) {
   const int G = a.Hq / a.Hkv;
+  a.G = G;
   a.cluster = cluster_size<F, NT>(a, sms);
   if (a.cluster > 1) {
     using S = Shape<F, NT, true>;
