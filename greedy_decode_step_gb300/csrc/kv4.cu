@@ -13,7 +13,7 @@
 // per value): one thread takes 8 dims of a row, a 32-bit word of codes.
 // Storing is bound by instructions: one thread takes 16 dims, so that a group's
 // scale is worked out half as often (8 dims a thread: 199 instructions for
-// every 8 values and 34 us for 84 MB of bf16 rows, 16 dims: 24 us), and
+// every 8 values and 34 us for 84 MB of bf16 rows, 16 dims: 23 us), and
 // group / 16 neighbouring lanes find the extremes by shuffles.
 #include <cuda_fp16.h>
 
@@ -24,9 +24,9 @@ namespace dec {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerThread = 4;  // rows in flight per thread, reading back
+constexpr int kRowsPerThread = 8;  // rows in flight per thread, reading back
 constexpr int kVals = 16;          // dims per thread, storing
-constexpr int kStoreRows = 2;      // rows in flight per thread, storing
+constexpr int kStoreRows = 4;      // rows in flight per thread, storing
 
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 __device__ __forceinline__ float half_bits_to_float(uint32_t h) {
