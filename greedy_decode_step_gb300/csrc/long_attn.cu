@@ -741,9 +741,8 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
   unsigned char* ring = smem + (L::ring(a.B, G, NT) + 127) / 128 * 128 + warp * (STAGES * F::kStage);
   const uint32_t ring_addr = smem_addr(ring);
 
-  pdl_wait();
-  pdl_launch_dependents();
-  int cta = blockIdx.x, T;
+  // what needs no memory, while the launch before may still run
+  int cta = blockIdx.x, T = 0;
   Item only{};  // CL: the cluster's item
   if constexpr (CL) {
     cluster_arrive();  // CTA 0 has started before anybody writes to it
@@ -751,20 +750,26 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
     cta = blockIdx.x - item * a.cluster;
     only.b = quot(item, a.Hkv);
     only.h = item - only.b * a.Hkv;
+  }
+  if constexpr (!F::kQuant) T = CL ? row_units<F>(a, 0) : a.B * a.Hkv * row_places<F>(a, 0);
+  Runs runs(CL ? a.cluster : a.n_cta, T, kW);
+  pdl_wait();
+  pdl_launch_dependents();
+  if constexpr (CL) {
     only.len = row_keys(a, a.pos[only.b]);
     if (only.len < 0 && only.h == 0 && cta == 0 && tid == 0) atomicOr(a.err, kErrPosRange);
-    only.end = T = row_units<F>(a, only.len);
-  } else if constexpr (!F::kQuant) {
-    if (cta == 0)
-      for (int b = tid; b < a.B; b += kThreads)
-        if (row_keys(a, a.pos[b]) < 0) atomicOr(a.err, kErrPosRange);
-    T = a.B * a.Hkv * row_places<F>(a, 0);
-  } else {
+    only.end = row_units<F>(a, only.len);
+  } else if constexpr (F::kQuant) {
     if (warp == 0) prefix_rows<F>(a, pre, len, cta == 0);
     __syncthreads();
-    T = pre[a.B];
+  } else if (cta == 0) {
+    for (int b = tid; b < a.B; b += kThreads)
+      if (row_keys(a, a.pos[b]) < 0) atomicOr(a.err, kErrPosRange);
   }
-  const Runs runs(CL ? a.cluster : a.n_cta, T, kW);
+  if constexpr (F::kQuant) {  // units by the positions
+    T = CL ? only.end : pre[a.B];
+    runs = Runs(CL ? a.cluster : a.n_cta, T, kW);
+  }
   if (!CL && cta >= runs.n) return;  // the same verdict in every thread
   const int t0 = cta < runs.n ? runs.start(cta) : T, t1 = cta < runs.n ? runs.start(cta + 1) : T;
   auto locate = [&](int t) {
