@@ -753,9 +753,16 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
   }
   if constexpr (!F::kQuant) T = CL ? row_units<F>(a, 0) : a.B * a.Hkv * row_places<F>(a, 0);
   Runs runs(CL ? a.cluster : a.n_cta, T, kW);
+  // an item's query rows, without a commit of their own
+  float* qraw = reinterpret_cast<float*>(smem + L::qraw(a.B, G, NT));
+  auto fetch_query = [&](const Item& it) {
+    const float* q = a.q + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D;
+    for (int e = tid * 4; e < G * D; e += kThreads * 4) cp_async16(smem_addr(qraw + e), q + e, true);
+  };
   pdl_wait();
   pdl_launch_dependents();
   if constexpr (CL) {
+    fetch_query(only);
     only.len = row_keys(a, a.pos[only.b]);
     if (only.len < 0 && only.h == 0 && cta == 0 && tid == 0) atomicOr(a.err, kErrPosRange);
     only.end = row_units<F>(a, only.len);
@@ -891,13 +898,7 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
     cp_async_commit();
     return nk;
   };
-  // an item's query rows, without a commit of their own
-  float* qraw = reinterpret_cast<float*>(smem + L::qraw(a.B, G, NT));
-  auto fetch_query = [&](const Item& it) {
-    const float* q = a.q + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.h) * G) * D;
-    for (int e = tid * 4; e < G * D; e += kThreads * 4) cp_async16(smem_addr(qraw + e), q + e, true);
-  };
-  if (t0 < t1) fetch_query(li);  // ahead of the stream: behind it they would wait for it
+  if (!CL && t0 < t1) fetch_query(li);  // ahead of the stream: behind it they would wait for it
   cp_async_commit();
   int ring_nk[STAGES];  // bf16: keys of the units in flight
   ring_nk[0] = issue(0, 0);
