@@ -247,7 +247,8 @@ def _native():
     if _nat is None:
         lib()
         if not os.path.exists(_build.BINDING):
-            raise RuntimeError(f"the native binding is not built ({_build.BINDING}); run greedy_decode_step_gb300.build()")
+            raise RuntimeError(f"the native binding is not built ({_build.BINDING}); run "
+                               "greedy_decode_step_gb300.build()")
         from . import _binding
         _binding.set_error(DecError)
         _nat = _binding
@@ -288,7 +289,8 @@ def long_attn_workspace_size(Hq, Hkv, D) -> int:
 
 def dec_kv4_decode_attn(q, k_codes, k_params, v_codes, v_params, pos, o, ws=None, stream=None):
     """GQA decode attention over a 4-bit cache; returns the workspace, for the next call."""
-    return (_nat or _native()).kv4_decode_attn(q, k_codes, k_params, v_codes, v_params, pos, o, ws, _handle(stream, k_codes))
+    return (_nat or _native()).kv4_decode_attn(q, k_codes, k_params, v_codes, v_params, pos, o, ws,
+                                               _handle(stream, k_codes))
 
 
 def dec_block_bounds(k_cache, pos, bounds, tokens: int = 1, stream=None):

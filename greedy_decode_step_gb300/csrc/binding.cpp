@@ -50,11 +50,12 @@ int cuda_index(const at::Tensor& t) { return t.is_cuda() ? static_cast<int>(t.ge
 // Pointer of a contiguous tensor of this dtype and shape on CUDA device `index`.
 void* gpu(PyObject* o, at::ScalarType dtype, std::initializer_list<int64_t> shape, int index, const char* name) {
   const at::Tensor& t = tensor(o, name);
-  if (t.scalar_type() != dtype) throw Failure{PyExc_TypeError, 0, std::string(name) + " must be " + str(dtype) + ", got " +
-                                                                      str(t.scalar_type())};
+  if (t.scalar_type() != dtype)
+    throw Failure{PyExc_TypeError, 0, std::string(name) + " must be " + str(dtype) + ", got " + str(t.scalar_type())};
   const at::IntArrayRef want(shape.begin(), shape.size());
   if (t.sizes() != want) refuse(std::string(name) + " must have shape " + str(want) + ", got " + str(t.sizes()));
-  if (cuda_index(t) != index) refuse(std::string(name) + " is on " + t.device().str() + ", other tensors of the call are not");
+  if (cuda_index(t) != index)
+    refuse(std::string(name) + " is on " + t.device().str() + ", other tensors of the call are not");
   if (!t.is_contiguous()) throw Failure{PyExc_ValueError, 0, std::string(name) + " must be contiguous"};
   return t.data_ptr();
 }
@@ -347,8 +348,9 @@ PyMethodDef kMethods[] = {DEC_ENTRY(kv4_store, 11),
                           DEC_ENTRY(block_decode_attn, 8),
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", "Native marshalling of libdec's long-cache calls.", -1, kMethods,
-                       nullptr, nullptr, nullptr, nullptr};
+PyModuleDef kModule = {
+    PyModuleDef_HEAD_INIT, "_binding", "Native marshalling of libdec's long-cache calls.", -1, kMethods, nullptr, nullptr,
+    nullptr, nullptr};
 
 }  // namespace
 

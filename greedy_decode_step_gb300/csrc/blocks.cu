@@ -203,15 +203,6 @@ __device__ __forceinline__ uint32_t kth_largest_cta(const uint32_t* key, int n, 
   return cut;
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Stores a word at CTA 0's copy of a shared-memory address.
-__device__ __forceinline__ void store_cta0(const void* p, uint32_t v) {
-  uint32_t at;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(p)));
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
-}
-
 // A cluster of CTAs per (row, KV head): all of them score the row's blocks
 // 0 .. pos / 64 in fp32, in turn, into CTA 0's shared memory, and CTA 0 goes on
 // alone.  The cut is found on order-preserving integer keys.  An fp32 score is
@@ -334,9 +325,11 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
 #pragma unroll
     for (int j = 0; j < kSelWarps; ++j) E = fmaxf(E, err_red[i][j]);
   E = fmaf(E, 1.0f / (1 << 19), 1e-41f);
-  const uint32_t cut = want == 0                         ? 0u
-                       : hi_free - lo_free <= kWarpKeys ? kth_largest_warp(key + lo_free, hi_free - lo_free, want, &s_cut)
-                                                          : kth_largest_cta(key + lo_free, hi_free - lo_free, want, counts);
+  const int n_free = hi_free - lo_free;
+  uint32_t cut = 0;
+  if (want > 0)
+    cut = n_free <= kWarpKeys ? kth_largest_warp(key + lo_free, n_free, want, &s_cut)
+                              : kth_largest_cta(key + lo_free, n_free, want, counts);
   const float tau = float_from_order_key(cut);
   // above: in; near the cut: listed, in any order
   int over = 0;

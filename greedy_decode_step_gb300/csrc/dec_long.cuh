@@ -6,12 +6,24 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "dec_common.cuh"
+
 namespace dec {
 
 constexpr int kLongMaxBatch = 1024;   // rows of one call
 constexpr int kBlockKeys = 64;        // keys of a selectable block
 constexpr int kLongMaxCtas = 480;     // CTAs of one attention launch (three per SM, or one)
 constexpr int kSelMaxBlocks = 8192;   // blocks of a row that the selection holds in shared memory
+
+// Cluster barrier in two halves, and a store of a word at CTA 0's copy of a
+// shared-memory address.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void store_cta0(const void* p, uint32_t v) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(p)));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
 
 // 4-bit cache.  Per (row, KV head, slot): D/2 bytes of codes (dim 2i in the
 // low nibble of byte i, dim 2i + 1 in the high one) and per group of dims a

@@ -49,8 +49,7 @@ struct Raw {
   static constexpr int kWords = kVals * (BF16 ? 2 : 4) / 16;
   uint4 w[kWords];
   __device__ __forceinline__ void load(const void* base, long long at) {
-    const uint4* p = reinterpret_cast<const uint4*>(BF16 ? static_cast<const void*>(static_cast<const uint16_t*>(base) + at)
-                                                         : static_cast<const void*>(static_cast<const float*>(base) + at));
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) + at * (BF16 ? 2 : 4));
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = p[i];
   }
@@ -314,13 +313,15 @@ cudaError_t dispatch(const A& a, int D, int group, bool bf16, cudaStream_t st) {
 template <int D, int G, bool BF16>
 struct Store {
   static cudaError_t run(const Kv4StoreArgs& a, cudaStream_t st) {
-    return launch(kv4_store_kernel<D, G, BF16>, kv4_grid(a.T, kThreads / (D / kVals) * kStoreRows, a.Hkv, a.B), dim3(kThreads), 0, st, true, a);
+    const dim3 grid = kv4_grid(a.T, kThreads / (D / kVals) * kStoreRows, a.Hkv, a.B);
+    return launch(kv4_store_kernel<D, G, BF16>, grid, dim3(kThreads), 0, st, true, a);
   }
 };
 template <int D, int G, bool BF16>
 struct Load {
   static cudaError_t run(const Kv4LoadArgs& a, cudaStream_t st) {
-    return launch(kv4_load_kernel<D, G, BF16>, kv4_grid(a.T, kThreads / (D / 8) * kRowsPerThread, a.Hkv, a.B), dim3(kThreads), 0, st, true, a);
+    const dim3 grid = kv4_grid(a.T, kThreads / (D / 8) * kRowsPerThread, a.Hkv, a.B);
+    return launch(kv4_load_kernel<D, G, BF16>, grid, dim3(kThreads), 0, st, true, a);
   }
 };
 

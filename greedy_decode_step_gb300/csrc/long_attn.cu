@@ -193,7 +193,8 @@ __device__ __forceinline__ int quot(int x, int d) {
 // Every item opens with kOpen units without keys, about what changing over to
 // an item costs a CTA (merging the warps' states, the next query), so that a run
 // that meets many items holds fewer keys (8 ragged rows to 32k keys 39.4 us with
-// none, 36.6 with 12 or 16; 64 listed blocks each 26.0 and 25.0).  The T units are cut into n runs of q or q + 1, one per CTA; n is such that
+// none, 36.6 with 12 or 16; 64 listed blocks each 26.0 and 25.0).  The T units
+// are cut into n runs of q or q + 1, one per CTA; n is such that
 // each warp of a CTA gets a unit before the next CTA does.
 constexpr int kOpen = 16;
 struct Runs {
@@ -712,15 +713,6 @@ struct Smem {
   }
 };
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Stores a float at CTA 0's copy of a shared-memory address.
-__device__ __forceinline__ void store_cta0(float* p, float v) {
-  uint32_t at;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(p)));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
-}
-
 template <class F, int NT, bool CL>
 __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::kPerSm)
     long_attn_kernel(const __grid_constant__ LongAttnArgs a) {
@@ -809,7 +801,8 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
     if (t >= t1) return -1;
     const int per = row_places<F>(a, 0);
     const int item = CL ? only.b * a.Hkv + only.h : quot(t, per), u = CL ? t : t - item * per - kOpen;
-    return u < 0 ? -1 : a.blocks[static_cast<size_t>(item) * a.n_select + static_cast<unsigned>(u) / (kBlockKeys / F::kUnit)];
+    if (u < 0) return -1;
+    return a.blocks[static_cast<size_t>(item) * a.n_select + static_cast<unsigned>(u) / (kBlockKeys / F::kUnit)];
   };
   if constexpr (!F::kQuant) {
     ids = fetch_ids(0);
@@ -933,8 +926,8 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
       __syncwarp();
       if constexpr (F::kQuant) {
         const int u = t0 + warp + kW * k - it.start;
-        if (u >= 0)
-          unit_kv4<F, NT>(ring + slot * F::kStage, ring_addr + slot * F::kStage, it.len - u * F::kUnit, words, fs, zq, st);
+        const int at = slot * F::kStage;
+        if (u >= 0) unit_kv4<F, NT>(ring + at, ring_addr + at, it.len - u * F::kUnit, words, fs, zq, st);
         __syncwarp();
         issue(k + STAGES, slot);
       } else {
@@ -1007,10 +1000,10 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
       if (whole) {
         if (it.len >= 0) out[e] = l == 0.f ? 0.f : sum / l;
       } else if constexpr (CL) {
-        store_cta0(join + e, sum);
+        store_cta0(join + e, __float_as_uint(sum));
         if (d == 0) {
-          store_cta0(join + G * D + h, M);
-          store_cta0(join + G * D + G + h, l);
+          store_cta0(join + G * D + h, __float_as_uint(M));
+          store_cta0(join + G * D + G + h, __float_as_uint(l));
         }
       } else {
         part[e] = sum;
