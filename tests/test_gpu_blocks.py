@@ -109,6 +109,8 @@ def check_select(got, q, bd, pos, n, n_first, n_last):
     (128, 16, 1, 40000, 64, 2, 2, [39999]),
     (128, 8, 2, 3000, 7, 3, 4, [2999]),           # all places forced
     (128, 2, 1, 100000, 600, 1, 1, [99999]),      # more blocks than threads
+    (64, 2, 1, 524288, 64, 1, 1, [524287]),       # the longest row that is taken
+    (64, 3, 1, 524288, 8000, 0, 0, [524287 - 64 * 5]),
 ])
 def test_selection_equals_the_exact_ranking(gd, D, Hq, Hkv, S, n, first, last, pos):
     B = len(pos)
@@ -139,6 +141,9 @@ def test_scores_closer_than_float32_and_ties(gd):
         check_select(got, q, bd, [NB * 64 - 1], n, 0, 1)
     zero = torch.zeros_like(q).cuda()
     assert run_select(gd, zero, bd, [NB * 64 - 1], 6, 1, 1)[0, 0].tolist() == [0, 1, 2, 3, 4, NB - 1]
+    long = torch.ones(1, 1, 8192, 2, 64, dtype=torch.bfloat16, device="cuda")  # 8192 equal blocks
+    got = run_select(gd, torch.ones(1, 1, 64, device="cuda"), long, [524287], 100, 2, 3)
+    assert got[0, 0].tolist() == list(range(97)) + [8189, 8190, 8191]
 
 
 def test_selection_with_values_that_are_not_finite(gd):
