@@ -226,7 +226,7 @@ int dec_select_tokens(const float* logits, const int32_t* prev_tokens, int n_pre
  *   s = half((hi - lo) / 15),  z = half(lo + 8 s),
  *   c = clamp(rint((x - z) / s) + 8, 0, 15)      (c = 8 where s = 0)
  * with s and z clamped to +-65504; a group that holds an infinity or a NaN
- * reads back as NaN whole.
+ * reads back as NaN whole.  A cache filled by other means keeps s >= 0.
  */
 
 /*
@@ -314,7 +314,8 @@ int dec_select_blocks(const float* q, const void* bounds, const int32_t* pos, in
  * the slots 64 i .. 64 i + 63, up to pos[b], of every block i of
  * blocks[b][g][0 .. n_select) (-1: none), in any order; a block listed twice
  * counts twice.  A row or head without any key gets zeros.  A block id outside
- * [-1, ceil(S_max/64)) is passed over (error bit 4).  pos, ws and
+ * [-1, ceil(S_max/64)) is passed over (error bit 4).  An infinite or NaN key
+ * makes its group's outputs NaN, such a value its dim's.  pos, ws and
  * reproducibility as in dec_kv4_decode_attn.
  */
 int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cache, const int32_t* pos,

@@ -258,6 +258,31 @@ def test_lists_that_leave_a_row_empty_repeat_or_leave_the_cache(gd):
     assert gd.device_error(clear=True) == 4 and torch.all(o[1:3] == -5.0) and torch.all(o[0, :2] == 0.0)
 
 
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_keys_and_values_that_are_not_finite(gd, bad, n):
+    """They reach the outputs of what attends to them and no others, and none from slots behind the last."""
+    B, Hq, Hkv, D, S = 4, 8, 2, 64, 2560
+    g = gen(77)
+    k, v = (torch.randn(B, Hkv, S, D, generator=g).bfloat16().cuda() for _ in range(2))
+    q = torch.randn(B, Hq, D, generator=g).cuda()
+    k[0, 1, 70, 5] = bad         # listed
+    v[1, 0, 64, 9] = bad         # listed
+    k[2, 0, 151:, :] = bad       # behind the last key, the same block
+    v[2, 0, 151:, :] = bad
+    if n == 3:
+        k[3, 1, 64 * 30, 2] = bad  # not listed
+    blocks = torch.arange(n, dtype=torch.int32, device="cuda").expand(B, Hkv, -1).contiguous()
+    o = torch.empty(B, Hq, D, device="cuda")
+    gd.dec_block_decode_attn(q, k, v, i32([200, 200, 150, 2500]), blocks, o)
+    torch.cuda.synchronize()
+    assert gd.device_error(clear=True) == 0
+    want = torch.zeros(B, Hq, D, dtype=torch.bool, device="cuda")
+    want[0, 4:] = True
+    want[1, :4, 9] = True
+    assert torch.equal(o.isnan(), want) and torch.isfinite(o[~want]).all()
+
+
 def test_many_blocks_per_warp(gd):
     """Lists long enough that a warp walks more than 64 units, and every id is read once."""
     B, Hq, Hkv, D, S = 16, 4, 4, 64, 40000
