@@ -29,8 +29,9 @@
 // values).  The scores' group sums are scaled in fp32 by s.  For the values a
 // key's s multiplies its probability, held as two halves: the product's upper
 // half, and its exact error plus the lower half's product.  A power of two C
-// per warp, from the largest s seen, keeps s C at most 1.  The z parts are
-// products of their own, with the (s, z) words as the other operand.
+// per warp and group keeps s C below 1 and exact; a unit whose scales spread too
+// far for one C is taken in several passes, each over the keys that one serves.
+// The z parts are products of their own, with the (s, z) words as the other operand.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -398,8 +399,12 @@ struct State {
   float o[NT][F::D / 16][4];
   float m[NT], mu[NT], l[NT];
   float zs[NT];
-  float c, bound;  // 4-bit: factor on the scales, of which every one seen is at most bound
-  uint32_t c2;     // the factor as two halves
+  // 4-bit: the window of scales (below) of this lane's group (lane & 3), 0 at first.
+  // Where registers suffice it is held as its ends, half bits << 16, and every
+  // group's factor as two halves
+  static constexpr bool kHeld = NT < 4;
+  int window;                       // not kHeld
+  uint32_t lo, width, c2[F::NG];    // kHeld
 };
 
 template <class F, int NT>
@@ -413,9 +418,10 @@ __device__ __forceinline__ void state_init(State<F, NT>& st) {
     st.mu[nt] = -State<F, NT>::kUp;
     st.l[nt] = 0.f;
   }
-  st.c = 1.f;
-  st.c2 = 0x3C003C00u;
-  st.bound = 0.f;
+#pragma unroll
+  for (int gr = 0; gr < F::NG; ++gr) st.c2[gr] = 0x3C003C00u;
+  st.window = 0;
+  st.lo = st.width = 0u;
 }
 
 // NG (s, z) pairs of key r
@@ -432,23 +438,11 @@ __device__ __forceinline__ void load_pairs(const unsigned char* base, int r, uin
   }
 }
 
-// New maxima and, for the 4-bit cache, a new bound on s: the state's sums go
-// over to them.  All 32 lanes; x: this lane's largest score per n-tile.
+// New maxima: the state's sums go over to them, and to new factors of the groups,
+// `ratio` times the ones before.  All 32 lanes; x: this lane's largest score per
+// n-tile.
 template <class F, int NT>
-__device__ __forceinline__ void raise(State<F, NT>& st, const float (&x)[NT], float s_max) {
-  float ratio = 1.f;
-  if constexpr (F::kQuant) {
-    s_max = warp_max(s_max);
-    if (s_max > st.bound) {
-      const uint32_t e = __float_as_uint(s_max) >> 23;  // s_max in [2^(e-127), 2^(e-126))
-      st.bound = __uint_as_float((e + 1u) << 23);
-      const uint32_t up = min(126u - e + 127u, 127u + 15u);  // s c at most 1
-      const float c = __uint_as_float(up << 23);
-      st.c2 = pack_f16(c, c);
-      ratio = c / st.c;
-      st.c = c;
-    }
-  }
+__device__ __forceinline__ void raise(State<F, NT>& st, const float (&x)[NT], const float (&ratio)[F::NG]) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float mx = x[nt];
@@ -465,8 +459,128 @@ __device__ __forceinline__ void raise(State<F, NT>& st, const float (&x)[NT], fl
 #pragma unroll
     for (int i = 0; i < F::D / 16; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) st.o[nt][i][e] *= corr * ratio;
+      for (int e = 0; e < 4; ++e) st.o[nt][i][e] *= corr * ratio[i / (F::D / 16 / F::NG)];
   }
+}
+
+// Windows of scales.  Window e, 1 .. 31, holds s in [2^(e-21), 2^(e-15)), the first
+// one every s below 2^-14, and C = 2^(15-e) takes them below 1, exactly.  6 bits
+// hold the scales of alike keys (a factor of 2 to 3 apart in a unit) without a
+// change, and at the window's lower end still leave 2^-30 of a probability that
+// is held (in both of its halves) to 2^-36 of the largest one.
+constexpr int kWindow = 6;
+__device__ __forceinline__ uint32_t window_lo(int e) {  // half bits
+  return e > kWindow ? static_cast<uint32_t>(e - kWindow) << 10 : e > 1 ? 1u << (e + 9 - kWindow) : 1u;
+}
+// 1 / c of a power of two
+__device__ __forceinline__ float inverse(float c) { return __uint_as_float(0x7F000000u - __float_as_uint(c)); }
+__device__ __forceinline__ uint32_t window_factor(int e) {  // C as half bits; 1 without a window
+  return e == 0 ? 0x3C00u : e < 30 ? static_cast<uint32_t>(30 - e) << 10 : 0x400u >> (e - 29);
+}
+template <class F, int NT>
+__device__ __forceinline__ int window_of(const State<F, NT>& st) {
+  if constexpr (State<F, NT>::kHeld) return static_cast<int>((st.lo + st.width) >> 26);
+  else return st.window;
+}
+template <class F, int NT>
+__device__ __forceinline__ void window_ends(const State<F, NT>& st, uint32_t* lo, uint32_t* width) {
+  if constexpr (State<F, NT>::kHeld) {
+    *lo = st.lo;
+    *width = st.width;
+  } else {
+    *lo = st.window ? window_lo(st.window) << 16 : 0u;
+    *width = (static_cast<uint32_t>(st.window) << 26) - *lo;
+  }
+}
+// Group gr's factor as two halves.  All 32 lanes.
+template <class F, int NT>
+__device__ __forceinline__ uint32_t group_factor(const State<F, NT>& st, int gr) {
+  if constexpr (State<F, NT>::kHeld) return st.c2[gr];
+  else return __shfl_sync(0xffffffffu, window_factor(st.window) * 0x10001u, gr);
+}
+
+// Each lane's group goes over to window e; the sums have to be taken times
+// `ratio`.  All 32 lanes.
+template <class F, int NT>
+__device__ __forceinline__ void move_windows(State<F, NT>& st, int e, float (&ratio)[F::NG]) {
+  const int was = window_of(st);
+  const uint32_t both = window_factor(e) | static_cast<uint32_t>(127 + (was ? was : 15) - (e ? e : 15)) << 23;
+  if constexpr (State<F, NT>::kHeld) {
+    st.lo = e ? window_lo(e) << 16 : 0u;
+    st.width = (static_cast<uint32_t>(e) << 26) - st.lo;
+  } else {
+    st.window = e;
+  }
+#pragma unroll
+  for (int gr = 0; gr < F::NG; ++gr) {
+    const uint32_t w = __shfl_sync(0xffffffffu, both, gr);
+    ratio[gr] = __uint_as_float(w & 0x7F800000u);
+    if constexpr (State<F, NT>::kHeld) st.c2[gr] = __byte_perm(w, w, 0x1010);
+  }
+}
+
+// The pair of key r, of this lane's group.  vw: this lane's pairs of keys 8 i + g.
+__device__ __forceinline__ uint32_t pair_of(const uint32_t (&vw)[4], int r) {
+  const uint32_t mine = r < 16 ? (r < 8 ? vw[0] : vw[1]) : r < 24 ? vw[2] : vw[3];
+  return __shfl_sync(0xffffffffu, mine, 4 * (r & 7) + (threadIdx.x & 3));
+}
+
+// Of a unit whose scales do not all fit one window per group: the window of this
+// lane's group with the first live key's scale in its middle (where that is zero,
+// `next`), and the live keys, as bits, whose scales lie in the windows of all
+// groups.  Seldom run, so that it is a call.  (Such a unit in one pass, its
+// products in fp32 under a power of two of their own: the code beside the loop
+// costs the units that do not need it more, 16 rows of 8k keys 18.9 us where this
+// takes 17.9.)
+__device__ __noinline__ uint2 first_and_alike(uint4 pairs, uint32_t live, int next) {
+  const uint32_t vw[4] = {pairs.x, pairs.y, pairs.z, pairs.w};
+  const uint32_t s = pair_of(vw, __ffs(live) - 1) & 0x7FFFu;
+  if (s) next = s < 0x400u ? 1 : min(static_cast<int>(s >> 10) + 1 + kWindow / 2, 31);
+  uint32_t served = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = vw[i] & 0x7FFFu;
+    const bool in = x == 0u || x >= 0x7C00u || (x >= window_lo(next) && x < static_cast<uint32_t>(next) << 10);
+    uint32_t b = __ballot_sync(0xffffffffu, in);  // bits 4 g + c; all groups of key g to bit g
+    b &= b >> 1;
+    b = b & b >> 2 & 0x11111111u;
+    b = (b | b >> 3) & 0x03030303u;
+    b = (b | b >> 6) & 0x000F000Fu;
+    served |= ((b | b >> 12) & 0xFFu) << (8 * i);
+  }
+  return make_uint2(served & live, static_cast<uint32_t>(next));
+}
+
+// A unit with a scale outside its group's window (zeros are in none).  The windows
+// move to serve all its `live` keys where the scales of each group span no more
+// than a window, or else the first one and those like it.  Returns the keys that
+// are served, as bits.  vw as above, dead keys with a live one's.  All 32 lanes.
+template <class F, int NT>
+__device__ __forceinline__ uint32_t fit_windows(State<F, NT>& st, const uint32_t (&vw)[4], uint32_t live,
+                                                float (&ratio)[F::NG]) {
+  uint32_t most = 0u, less = ~0u;  // the largest scale; the smallest but zero, less 1
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t s = vw[i] << 16 & 0x7FFF0000u;
+    most = max(most, s < 0x7C000000u ? s : 0u);  // an infinity or a NaN needs no window
+    less = min(less, s - 0x10000u);
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    less = min(less, __shfl_xor_sync(0xffffffffu, less, o));
+  }
+  const uint32_t least = (less >> 16) + 1u;
+  const int now = window_of(st), own = most ? static_cast<int>(most >> 26) + 1 : now;
+  int next = own <= now && least >= window_lo(now) ? now : own;
+  uint32_t served = live;
+  if (!__all_sync(0xffffffffu, least >= window_lo(next))) {
+    const uint2 r = first_and_alike(make_uint4(vw[0], vw[1], vw[2], vw[3]), live, next);
+    served = r.x;
+    next = static_cast<int>(r.y);
+  }
+  move_windows(st, next, ratio);
+  return served;
 }
 
 // Half words (row g) of the (s, z) pairs of keys 8 i + 2 c and + 1, i = 0 .. 3.
@@ -485,10 +599,12 @@ __device__ __forceinline__ void load_pairs_trans(const unsigned char* base, uint
   }
 }
 
-// 32 keys of the 4-bit cache, of which the first nk count.
+// 32 keys of the 4-bit cache, of which those in `live` count.  Returns those that
+// are left for another pass.
 template <class F, int NT>
-__device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t stage_addr, int nk, const uint32_t* words,
-                                         const float (&fs)[NT], const uint32_t (&zq)[NT], State<F, NT>& st) {
+__device__ __forceinline__ uint32_t unit_kv4(const unsigned char* stage, uint32_t stage_addr, uint32_t live,
+                                             const uint32_t* words, const float (&fs)[NT], const uint32_t (&zq)[NT],
+                                             State<F, NT>& st) {
   constexpr int NJ = F::D / 32, NG = F::NG, PER = NJ / NG;  // chunks per group
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int lrow = (lane & 7) + (lane & 8), lchunk = lane >> 4;
@@ -545,23 +661,42 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
       s[nt][2 * hh + 1] = a1 * fs[nt];
     }
   }
-  if (nk < 32) {
+  uint32_t left = 0u;
+  auto drop = [&](uint32_t keys) {  // those without a bit
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (8 * i + g >= nk) s[nt][i] = -INFINITY;
+        if (!(keys >> (8 * i + g) & 1u)) s[nt][i] = -INFINITY;
+  };
+  if (live != ~0u) {
+    drop(live);
+    const uint32_t first = pair_of(vw, __ffs(live) - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(live >> (8 * i + g) & 1u)) vw[i] = first;
   }
-  // a larger score or scale than before anywhere in the warp?
+  // a larger score than before, or a scale outside its window, anywhere in the warp?
   float mx[NT];
-  const float s_max = half_lo(max_f16x2(max_f16x2(vw[0], vw[1]), max_f16x2(vw[2], vw[3])));
-  bool more = s_max > st.bound;
+  uint32_t off = 0u, lo, width;
+  window_ends(st, &lo, &width);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) off = max(off, (vw[i] << 16) - lo);
+  bool more = off >= width;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     mx[nt] = fmaxf(fmaxf(s[nt][0], s[nt][1]), fmaxf(s[nt][2], s[nt][3]));
     more |= mx[nt] > st.m[nt] + State<F, NT>::kSlack;
   }
-  if (__any_sync(0xffffffffu, more)) raise<F, NT>(st, mx, s_max);
+  if (__any_sync(0xffffffffu, more)) {
+    float ratio[NG];
+    const uint32_t served = fit_windows(st, vw, live, ratio);
+    raise<F, NT>(st, mx, ratio);
+    if (served != live) {
+      drop(served);
+      left = live & ~served;
+    }
+  }
   uint32_t vt[4];
   load_pairs_trans<NG>(stage + F::kVpOff, stage_addr + F::kVpOff, vt);
 #pragma unroll
@@ -593,7 +728,7 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
         const int j = jj + t, gr = j / PER;
         if (j % PER == 0) {
           // times the keys' scales: the product's upper half, its exact error, and the remainder's share
-          const uint32_t sc = mul_f16x2(__byte_perm(p0[gr], p1[gr], 0x5410), st.c2);
+          const uint32_t sc = mul_f16x2(__byte_perm(p0[gr], p1[gr], 0x5410), group_factor(st, gr));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint32_t x = mul_f16x2(top[nt], sc);
@@ -615,6 +750,7 @@ __device__ __forceinline__ void unit_kv4(const unsigned char* stage, uint32_t st
       }
     }
   }
+  return left;
 }
 
 // 16 keys of a bf16 cache, of which the first nk count.
@@ -651,7 +787,7 @@ __device__ __forceinline__ void unit_bf16(uint32_t stage_addr, int nk, const uin
     mx[nt] = fmaxf(s[nt][0], s[nt][1]);
     more |= mx[nt] > st.m[nt] + State<F, NT>::kSlack;
   }
-  if (__any_sync(0xffffffffu, more)) raise<F, NT>(st, mx, 0.f);
+  if (__any_sync(0xffffffffu, more)) raise<F, NT>(st, mx, {1.f});
   uint32_t b0[NT], b1[NT], c0[NT], c1[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -927,7 +1063,12 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
       if constexpr (F::kQuant) {
         const int u = t0 + warp + kW * k - it.start;
         const int at = slot * F::kStage;
-        if (u >= 0) unit_kv4<F, NT>(ring + at, ring_addr + at, it.len - u * F::kUnit, words, fs, zq, st);
+        if (u >= 0) {
+          const int nk = it.len - u * F::kUnit;
+          uint32_t live = nk < 32 ? (1u << nk) - 1u : ~0u;
+          do live = unit_kv4<F, NT>(ring + at, ring_addr + at, live, words, fs, zq, st);
+          while (live);
+        }
         __syncwarp();
         issue(k + STAGES, slot);
       } else {
@@ -947,6 +1088,11 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
     if (seg_end < t1) cp_async_wait_all();
     // the warps' states, each relative to its own maximum
     const int g = lane >> 2, c = lane & 3;
+    float units[F::NG];
+    if constexpr (F::kQuant) {
+#pragma unroll
+      for (int gr = 0; gr < F::NG; ++gr) units[gr] = inverse(half_lo(group_factor(st, gr)));
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int h = 4 * nt + c;
@@ -963,10 +1109,10 @@ __global__ void __launch_bounds__(32 * Shape<F, NT, CL>::kW, Shape<F, NT, CL>::k
       if (h < G) {
         float* to = obuf + (warp * G + h) * (D + 4);
         if constexpr (F::kQuant) {
-          const float u0 = 1.f / st.c, u1 = u0 * 0.0625f;  // powers of two
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            const float z = zs[i / 2 / (D / 32 / F::NG)];
+            const int gr = i / 2 / (D / 32 / F::NG);
+            const float z = zs[gr], u0 = units[gr], u1 = u0 * 0.0625f;
             *reinterpret_cast<float2*>(to + 32 * (i >> 1) + 4 * g + 2 * (i & 1)) =
                 make_float2(fmaf(st.o[nt][i][0] + st.o[nt][i][1], u0, z), fmaf(st.o[nt][i][2] + st.o[nt][i][3], u1, z));
           }
