@@ -299,8 +299,10 @@ __device__ __forceinline__ Item item_at(const LongAttnArgs& a, const int* pre, c
 //  * 4-bit: per chunk j four half pairs that meet the nibble pairs (0, 4),
 //    (1, 5), (2, 6), (3, 7) of word c, dims 32 j + 8 c + nibble, the odd
 //    nibbles' (16 times larger) with a factor 1/16.  The head is scaled by a
-//    power of two to [2^13, 2^14); f takes it back.  zq: for the (s, z) pair of
-//    group c, (0, Q) with Q the group's sum of q, scaled by another 2^-10.
+//    power of two to [2^14, 2^15); f takes it back.  zq: for the (s, z) pair of
+//    group c, (0, Q) with Q the group's mean of q so scaled.  Two parts leave
+//    2^-24 there: of the head's largest element 2^-34 for a dim's q, and 2^-38
+//    times the group's size for the sum over a group.
 //  * bf16: per 16 dims two pairs, as the instruction lays them out, and two
 //    more whose upper-part columns hold a third part (24 bits in all; the
 //    remainder columns are zero).
@@ -331,7 +333,7 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const int ex = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-    const int e = mx > 0.f ? min(max(13 - ex, -100), 100) : 0;
+    const int e = mx > 0.f ? min(max(14 - ex, -100), 100) : 0;
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     float mine = 0.f;
 #pragma unroll
@@ -345,7 +347,7 @@ __device__ __forceinline__ void stage_query(const float* q, int G, int nt, float
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       if (gr == c) mine = s;
     }
-    mine *= up * 0x1p-10f;
+    mine *= up * (1.f / (D / NG));
     const float top = top11(mine), part = rest ? mine - top : top;
     zq[nt * 32 + lane] = pack_f16(0.f, part);
     if (c == 0 && !rest) f[head] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * scale_log2;
@@ -651,7 +653,7 @@ __device__ __forceinline__ uint32_t unit_kv4(const unsigned char* stage, uint32_
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float a0 = (zp[nt][0] + zp[nt][1]) * 0x1p10f, a1 = (zp[nt][2] + zp[nt][3]) * 0x1p10f;
+      float a0 = (zp[nt][0] + zp[nt][1]) * (F::D / NG), a1 = (zp[nt][2] + zp[nt][3]) * (F::D / NG);
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
         a0 = fmaf(half_lo(p0[gr]), acc[nt][gr][0] + acc[nt][gr][1], a0);
