@@ -34,11 +34,17 @@ def _flags():
             "--expt-relaxed-constexpr"]
 
 
+def _binding_key() -> str:
+    """What the binding's object depends on beside its sources: the versions of torch and Python."""
+    import torch
+    return f"{torch.__version__}_{sysconfig.get_config_var('SOABI')}"
+
+
 def _binding_job(force: bool):
-    """The compile command of binding.cpp, or None, and its object (one per torch version)."""
+    """The compile command of binding.cpp, or None, and its object (one per torch and Python)."""
     import torch
     src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "libdec.h")
-    obj = os.path.join(BUILD, f"binding_{torch.__version__}.o")
+    obj = os.path.join(BUILD, f"binding_{_binding_key()}.o")
     root = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     paths = [root, os.path.join(root, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda, INCLUDE]
@@ -84,14 +90,24 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         cuda_lib = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "lib64")
         run([nvcc(), ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs, "-Xlinker", f"-rpath,{cuda_lib}"])
         os.replace(tmp, LIB)
-    if force or jobs or _stale(BINDING, [binding_obj, LIB]):
+    # the linked module has one name, so a note beside it says which object it was linked from
+    note = os.path.join(BUILD, "binding_linked")
+    linked = None
+    if os.path.exists(note):
+        with open(note) as f:
+            linked = f.read()
+    if force or jobs or linked != os.path.basename(binding_obj) or _stale(BINDING, [binding_obj, LIB]):
         import torch
         tmp = BINDING + f".tmp{os.getpid()}"
         libs = os.path.join(os.path.dirname(torch.__file__), "lib")
         # torch is imported first, so its libraries are found by name; libdec.so lies beside the module
         run(["g++", "-shared", "-o", tmp, binding_obj, "-L", HERE, "-l:libdec.so", "-L", libs, "-ltorch_python",
              "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+        if linked is not None:
+            os.remove(note)
         os.replace(tmp, BINDING)
+        with open(note, "w") as f:
+            f.write(os.path.basename(binding_obj))
     return LIB
 
 
