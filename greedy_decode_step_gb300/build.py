@@ -3,6 +3,7 @@ unit, compiled in parallel, then linked against the shared CUDA runtime; and
 with the host compiler the extension module ``_binding`` against torch."""
 from __future__ import annotations
 
+import contextlib
 import os
 import subprocess
 import sys
@@ -103,7 +104,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         # torch is imported first, so its libraries are found by name; libdec.so lies beside the module
         run(["g++", "-shared", "-o", tmp, binding_obj, "-L", HERE, "-l:libdec.so", "-L", libs, "-ltorch_python",
              "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
-        if linked is not None:
+        with contextlib.suppress(FileNotFoundError):  # another process may build as well
             os.remove(note)
         os.replace(tmp, BINDING)
         with open(note, "w") as f:
