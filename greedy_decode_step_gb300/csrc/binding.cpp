@@ -170,7 +170,11 @@ void* workspace(PyObject* given, int Hq, int Hkv, int D, int dev, const OnDevice
     return t.data_ptr();
   }
   *bytes = dec_long_attn_workspace_size(Hq, Hkv, D);
-  if (*bytes == 0) throw Failure{nullptr, DEC_EINVAL, dec_last_error()};
+  if (*bytes == 0) {  // sizes that the call itself refuses, with its own code
+    Py_INCREF(Py_None);
+    *out = Py_None;
+    return nullptr;
+  }
   const auto index = static_cast<c10::DeviceIndex>(dev);
   const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(on.stream, index));
   at::Tensor t = at::empty({static_cast<int64_t>(*bytes)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, index));

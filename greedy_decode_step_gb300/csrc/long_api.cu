@@ -30,11 +30,16 @@ bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_c
 #define DEC_PTR(p) DEC_CHECK(aligned(p, 16), DEC_EINVAL, "%s must be a non-null 16-byte aligned pointer", #p)
 #define DEC_INTS(p) DEC_CHECK(aligned(p, 4), DEC_EINVAL, "%s must be a non-null 4-byte aligned pointer", #p)
 
+int check_heads(int Hkv, int D) {
+  DEC_CHECK(Hkv >= 1 && Hkv <= 4096, DEC_EUNSUPPORTED, "Hkv = %d outside 1..4096", Hkv);
+  DEC_CHECK(D == 64 || D == 128, DEC_EUNSUPPORTED, "head_dim %d: supported 64 and 128", D);
+  return DEC_OK;
+}
+
 // Sizes shared by every call: a cache of B rows, Hkv heads, S_max slots.
 int check_cache(int B, int Hkv, int D, int S_max) {
   DEC_CHECK(B >= 1 && B <= kLongMaxBatch, DEC_EUNSUPPORTED, "batch %d outside 1..%d", B, kLongMaxBatch);
-  DEC_CHECK(Hkv >= 1 && Hkv <= 4096, DEC_EUNSUPPORTED, "Hkv = %d outside 1..4096", Hkv);
-  DEC_CHECK(D == 64 || D == 128, DEC_EUNSUPPORTED, "head_dim %d: supported 64 and 128", D);
+  DEC_TRY(check_heads(Hkv, D));
   DEC_CHECK(S_max >= 1, DEC_EINVAL, "S_max must be >= 1");
   // positions, and a CTA's tokens behind the last, stay in an int
   DEC_CHECK(static_cast<long long>(B) * Hkv * S_max <= (1ll << 31) - 1024, DEC_EUNSUPPORTED,
@@ -172,7 +177,7 @@ int dec_kv4_load(const void* k_codes, const void* k_params, const void* v_codes,
 }
 
 size_t dec_long_attn_workspace_size(int Hq, int Hkv, int D) {
-  if (Hkv < 1 || check_queries(Hq, Hkv) != DEC_OK || (D != 64 && D != 128)) return 0;
+  if (check_heads(Hkv, D) != DEC_OK || check_queries(Hq, Hkv) != DEC_OK) return 0;
   return part_bytes(Hq, Hkv, D);
 }
 
