@@ -299,10 +299,11 @@ def dec_block_bounds(k_cache, pos, bounds, tokens: int = 1, stream=None):
     (_nat or _native()).block_bounds(k_cache, pos, bounds, tokens, _handle(stream, k_cache))
 
 
-def dec_select_blocks(q, bounds, pos, blocks, n_first: int = 1, n_last: int = 1, stream=None):
+def dec_select_blocks(q, bounds, pos, blocks, n_first: int = 1, n_last: int = 1, stream=None, S_max=None):
     """Fills ``blocks`` (int32 [B, Hkv, n_select]) with the blocks of the largest score bounds, ascending, -1 behind
-    the last; the first ``n_first`` and last ``n_last`` blocks of a row are always among them."""
-    (_nat or _native()).select_blocks(q, bounds, pos, blocks, n_first, n_last, _handle(stream, q))
+    the last; the first ``n_first`` and last ``n_last`` blocks of a row are always among them.  ``S_max``: the
+    cache's slots, behind which positions are refused; the bounds alone tell them in whole blocks."""
+    (_nat or _native()).select_blocks(q, bounds, pos, blocks, n_first, n_last, S_max, _handle(stream, q))
 
 
 def dec_block_decode_attn(q, k_cache, v_cache, pos, blocks, o, ws=None, stream=None):

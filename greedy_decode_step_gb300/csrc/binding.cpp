@@ -255,7 +255,7 @@ PyObject* block_bounds(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
-// q, bounds, pos, blocks, n_first, n_last, stream
+// q, bounds, pos, blocks, n_first, n_last, S_max (None: whole blocks), stream
 PyObject* select_blocks(PyObject* const* a) {
   const at::Tensor &q = tensor(a[0], "q"), &bd = tensor(a[1], "bounds"), &bl = tensor(a[3], "blocks");
   expect(q.dim() == 3 && bd.dim() == 5 && bl.dim() == 3,
@@ -270,10 +270,13 @@ PyObject* select_blocks(PyObject* const* a) {
   const int32_t* pos = ints(a[2], B, dev, "pos");
   void* blocks = gpu(a[3], at::kInt, {B, Hkv, n}, dev, "blocks");
   const int first = as_int(a[4]), last = as_int(a[5]);
-  const OnDevice on(dev, a[6]);
+  const int S = a[6] == Py_None ? static_cast<int>(NB * 64) : as_int(a[6]);
+  expect(S >= 1 && (S - 1) / 64 + 1 == NB, std::to_string(NB) + " blocks of bounds do not match S_max = " +
+                                               std::to_string(S) + " slots");
+  const OnDevice on(dev, a[7]);
   done(without_gil([&] {
     return dec_select_blocks(static_cast<const float*>(qp), bounds, pos, static_cast<int32_t*>(blocks), n, first, last, B,
-                             Hq, Hkv, D, NB * 64, on.stream);
+                             Hq, Hkv, D, S, on.stream);
   }));
   Py_RETURN_NONE;
 }
@@ -348,7 +351,7 @@ PyMethodDef kMethods[] = {DEC_ENTRY(kv4_store, 11),
                           DEC_ENTRY(kv4_load, 9),
                           DEC_ENTRY(kv4_decode_attn, 9),
                           DEC_ENTRY(block_bounds, 5),
-                          DEC_ENTRY(select_blocks, 7),
+                          DEC_ENTRY(select_blocks, 8),
                           DEC_ENTRY(block_decode_attn, 8),
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};

@@ -33,3 +33,30 @@ def test_sizes_are_refused_alike_with_and_without_a_workspace(gd, Hq, Hkv, D, co
             with pytest.raises(gd.DecError, match=word) as e:
                 call()
             assert e.value.code == getattr(gd, code)
+
+
+def test_selection_slots_that_do_not_match_the_bounds(gd):  # noqa: F811
+    q, pos = torch.zeros(2, 4, 64), torch.zeros(2, dtype=torch.int32)
+    bounds, blocks = torch.zeros(2, 2, 3, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 2, dtype=torch.int32)
+    for slots in (128, 193, 0, -1):
+        with pytest.raises(gd.DecError, match="slots"):
+            gd.dec_select_blocks(q, bounds, pos, blocks, S_max=slots)
+    with pytest.raises(gd.DecError, match="CUDA device"):  # these match
+        gd.dec_select_blocks(q, bounds, pos, blocks, S_max=129)
+
+
+@pytest.mark.gpu
+def test_selection_refuses_positions_behind_the_cache(gd):  # noqa: F811
+    """The cache's slots may end inside its last block: a position behind them is outside the cache."""
+    S = 130
+    q = torch.zeros(3, 4, 64, device="cuda")
+    bounds = torch.zeros(3, 2, 3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    blocks = torch.full((3, 2, 3), -7, dtype=torch.int32, device="cuda")
+    pos = torch.tensor([129, 130, 191], dtype=torch.int32, device="cuda")
+    gd.dec_select_blocks(q, bounds, pos, blocks, S_max=S)
+    torch.cuda.synchronize()
+    assert gd.device_error(clear=True) == 4
+    assert blocks.tolist() == [[[0, 1, 2]] * 2] + [[[-7, -7, -7]] * 2] * 2
+    gd.dec_select_blocks(q, bounds, pos, blocks)  # not told, every block counts as whole
+    torch.cuda.synchronize()
+    assert gd.device_error(clear=True) == 0 and blocks.tolist() == [[[0, 1, 2]] * 2] * 3
