@@ -402,10 +402,11 @@ cudaError_t launch_block_bounds(const BoundsArgs& a, int D, cudaStream_t st) {
                  : launch(block_bounds_kernel<128>, grid, dim3(kBoundThreads), 0, st, true, a);
 }
 
-// CTAs per item: as many as fit the GPU at one per SM beside the other items',
-// but no more than leave each warp its batch of blocks.  (b = 1, 8 heads, 512
-// blocks: 9.6 us with one, 6.9 with four, 6.4 with eight; CTAs of 512 threads 9.2,
-// 6.9 and 6.9.)
+// CTAs per item: while all items' come to at most two per SM, and no more than
+// leave each warp its batch of blocks.  (b = 1, 8 heads, 512 blocks: 9.6 us with
+// one, 6.9 with four, 6.4 with eight; CTAs of 512 threads 9.2, 6.9 and 6.9.)  Two
+// CTAs fit an SM's shared memory up to about 7,000 blocks; longer rows of so many
+// items run in two waves.
 int select_cluster(int items, int NB, int D, int sms) {
   const int batch = kSelWarps * (32 / (2 * D / 8)) * kBatch;
   int c = 1;
