@@ -271,12 +271,13 @@ size_t dec_long_attn_workspace_size(int Hq, int Hkv, int D);
  * K and V the values that the codes stand for, to float32 accuracy dim by dim,
  * however the scales of groups and keys spread; a probability is held to 2^-30
  * of the row's largest one, an element of q (a group's sum of them: 1/32 of a
- * group's size times that) to 2^-33 of its head's largest.  pos[b] == -1 is a row without keys: its output is zero.  A row
- * with any other pos outside [0, S_max) is not written (error bit 4).  Slots
- * behind pos[b] are not read.  q is taken up to 2^114 in magnitude.  ws: device
- * workspace of dec_long_attn_workspace_size() bytes, 256-byte aligned, any
- * contents; calls that can overlap on the GPU need one each.  Results are
- * reproducible bit for bit.
+ * group's size times that) to 2^-33 of its head's largest.  pos[b] == -1 is a
+ * row without keys: its output is zero.  A row with any other pos outside
+ * [0, S_max) is not written (error bit 4).  Slots behind pos[b] are not read.  q
+ * is taken up to 2^114 in magnitude.  ws: device workspace of
+ * dec_long_attn_workspace_size() bytes, 256-byte aligned, any contents; calls
+ * that can overlap on the GPU need one each.  Results are reproducible bit for
+ * bit.
  */
 int dec_kv4_decode_attn(const float* q, const void* k_codes, const void* k_params, const void* v_codes,
                         const void* v_params, const int32_t* pos, float* o, void* ws, size_t ws_bytes, int B, int Hq,
@@ -288,8 +289,11 @@ int dec_kv4_decode_attn(const float* q, const void* k_codes, const void* k_param
  * the smallest value of each dim (NaNs are passed over).  Call it after the T
  * tokens at slots pos[b] .. pos[b] + T - 1 were written (T == 1: a decode
  * step): every block that holds one of them is computed anew over its slots up
- * to pos[b] + T - 1; the other blocks keep theirs.  A row whose slots leave
- * the cache is left as it was (error bit 4).
+ * to pos[b] + T - 1; the other blocks keep theirs.  T is one for all rows:
+ * where a padded prompt's row is shorter, its blocks' bounds cover the slots
+ * behind its last token too, whatever they hold, and bound its own keys all the
+ * same; a decode step's call computes the block it writes to anew.  A row whose
+ * slots leave the cache is left as it was (error bit 4).
  */
 int dec_block_bounds(const void* k_cache, const int32_t* pos, int T, void* bounds, int B, int Hkv, int D, int S_max,
                      void* stream);
