@@ -418,7 +418,8 @@ __device__ __forceinline__ void state_init(State<F, NT>& st) {
 #pragma unroll
   for (int gr = 0; gr < F::NG; ++gr) st.c2[gr] = 0x3C003C00u;
   st.window = 0;
-  st.lo = st.width = 0u;
+  st.lo = 0u;
+  st.width = 0x10000u;
 }
 
 // NG (s, z) pairs of key r
@@ -460,18 +461,20 @@ __device__ __forceinline__ void raise(State<F, NT>& st, const float (&x)[NT], co
   }
 }
 
-// Windows of scales.  Window e, 1 .. 31, holds s in [2^(e-21), 2^(e-15)), the first
-// one every s below 2^-14, and C = 2^(15-e) takes them below 1, exactly.  6 bits
-// hold the scales of alike keys (a factor of 2 to 3 apart in a unit) without a
-// change, and at the window's lower end still leave 2^-30 of a probability that
-// is held (in both of its halves) to 2^-36 of the largest one.
-constexpr int kWindow = 6;
+// Windows of scales.  Window e, 1 .. 31, holds s in [2^(e-27), 2^(e-15)), and C =
+// 2^(15-e) takes them to [2^-12, 1), exactly (a half has 14 bits down to its
+// subnormals).  Probabilities are held, in both of their halves, to 2^-36 of the
+// largest one; at the window's lower end 2^-24 is left of that, as float32 sums
+// leave.  (Windows of 2^6 leave 2^-30, but keys whose values spread by 2^10 took
+// 124 us in their passes where alike ones take 36.)  Window 0, at first, holds
+// zero alone: the scale of a constant group, such as dims that only pad a head.
+constexpr int kWindow = 12;
 __device__ __forceinline__ uint32_t window_lo(int e) {  // half bits
-  return e > kWindow ? static_cast<uint32_t>(e - kWindow) << 10 : e > 1 ? 1u << (e + 9 - kWindow) : 1u;
+  return e > kWindow ? static_cast<uint32_t>(e - kWindow) << 10 : 1u << max(e + 9 - kWindow, 0);
 }
 // 1 / c of a power of two
 __device__ __forceinline__ float inverse(float c) { return __uint_as_float(0x7F000000u - __float_as_uint(c)); }
-__device__ __forceinline__ uint32_t window_factor(int e) {  // C as half bits; 1 without a window
+__device__ __forceinline__ uint32_t window_factor(int e) {  // C as half bits; 1 in window 0
   return e == 0 ? 0x3C00u : e < 30 ? static_cast<uint32_t>(30 - e) << 10 : 0x400u >> (e - 29);
 }
 template <class F, int NT>
@@ -486,7 +489,7 @@ __device__ __forceinline__ void window_ends(const State<F, NT>& st, uint32_t* lo
     *width = st.width;
   } else {
     *lo = st.window ? window_lo(st.window) << 16 : 0u;
-    *width = (static_cast<uint32_t>(st.window) << 26) - *lo;
+    *width = (st.window ? static_cast<uint32_t>(st.window) << 26 : 0x10000u) - *lo;
   }
 }
 // Group gr's factor as two halves.  All 32 lanes.
@@ -504,7 +507,7 @@ __device__ __forceinline__ void move_windows(State<F, NT>& st, int e, float (&ra
   const uint32_t both = window_factor(e) | static_cast<uint32_t>(127 + (was ? was : 15) - (e ? e : 15)) << 23;
   if constexpr (State<F, NT>::kHeld) {
     st.lo = e ? window_lo(e) << 16 : 0u;
-    st.width = (static_cast<uint32_t>(e) << 26) - st.lo;
+    st.width = (e ? static_cast<uint32_t>(e) << 26 : 0x10000u) - st.lo;
   } else {
     st.window = e;
   }
@@ -548,7 +551,7 @@ __device__ __noinline__ uint2 first_and_alike(uint4 pairs, uint32_t live, int ne
   return make_uint2(served & live, static_cast<uint32_t>(next));
 }
 
-// A unit with a scale outside its group's window (zeros are in none).  The windows
+// A unit with a scale outside its group's window (a zero outside window 0 too).  The windows
 // move to serve all its `live` keys where the scales of each group span no more
 // than a window, or else the first one and those like it.  Returns the keys that
 // are served, as bits.  vw as above, dead keys with a live one's.  All 32 lanes.

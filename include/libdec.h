@@ -269,7 +269,7 @@ size_t dec_long_attn_workspace_size(int Hq, int Hkv, int D);
  * with g = floor(h / (Hq/Hkv)) and keys j = 0 .. pos[b],
  *   o[b][h] = sum_j softmax_j(q[b][h] . K[b][g][j] / sqrt(D)) V[b][g][j]
  * K and V the values that the codes stand for, to float32 accuracy dim by dim,
- * however the scales of groups and keys spread; a probability is held to 2^-30
+ * however the scales of groups and keys spread; a probability is held to 2^-24
  * of the row's largest one, an element of q (a group's sum of them: 1/32 of a
  * group's size times that) to 2^-33 of its head's largest.  pos[b] == -1 is a
  * row without keys: its output is zero.  A row with any other pos outside

@@ -50,7 +50,7 @@ def attend(gd, q, k, v, group, what):  # noqa: F811
 @pytest.mark.parametrize("D,group,G,sizes", [
     (64, 32, 1, (1.0, 1e-3)), (64, 32, 4, (10.0, 1e-4)), (64, 32, 8, (1e-5, 1000.0)),
     (128, 32, 4, (1e3, 1e-5, 1.0, 30.0)), (128, 64, 2, (1e-4, 100.0)), (128, 32, 16, (1e-5, 1e-2, 10.0, 1e4)),
-    (128, 64, 7, (5e3, 1e-5))])
+    (128, 64, 7, (5e3, 1e-5)), (128, 32, 4, (0.0, 1.0, 0.0, 1e-4)), (128, 64, 16, (1.0, 0.0)), (64, 64, 2, (0.0,))])
 def test_groups_of_unlike_scale(gd, D, group, G, sizes, shape):  # noqa: F811
     B, Hkv, S = shape_of(shape, G)
     k, v, q = normal(1, B, Hkv, S, D), normal(2, B, Hkv, S, D), normal(3, B, G * Hkv, D)
