@@ -2,7 +2,7 @@
 
 Argument marshalling only: every function here checks tensor dtypes and
 shapes, passes raw device pointers and sizes to the library and turns a
-non-zero status into ``DecError`` (for the long-cache calls a compiled module,
+non-zero status into ``DecError`` (for the long-cache, 8-bit and expert calls a compiled module,
 ``csrc/binding.cpp``, does it).  All arithmetic runs in the CUDA kernels of
 ``libdec.so``; if the library is missing, every call raises.
 
@@ -77,6 +77,12 @@ _SIGNATURES = {
     "dec_block_bounds": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _P]),
     "dec_select_blocks": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "dec_block_decode_attn": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _S, _I, _I, _I, _I, _I, _P]),
+    "dec_fp8_quant": (_I, [_P, _I, _L, _L, _P, _P, _I, _I, _I, _I, _P]),
+    "dec_fp8_dequant": (_I, [_P, _P, _P, _I, _L, _L, _I, _I, _I, _I, _P]),
+    "dec_fp8_gemm": (_I, [_P, _P, _P, _P, _P, _L, _P, _L, _I, _I, _I, _P]),
+    "dec_moe_route": (_I, [_P, _P, _P, _I, _I, _F, _P, _P, _I, _I, _I, _I, _P]),
+    "dec_moe_workspace_size": (_S, [_I, _I, _I]),
+    "dec_moe_experts": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _I, _I, _I, _I, _I, _P]),
     "dec_state_workspace_size": (_S, [ctypes.POINTER(DecModel), _I, _I]),
     "dec_state_init": (_I, [ctypes.POINTER(DecModel), ctypes.POINTER(DecState), _P]),
     "dec_state_release": (_I, [ctypes.POINTER(DecState)]),
@@ -309,6 +315,49 @@ def dec_select_blocks(q, bounds, pos, blocks, n_first: int = 1, n_last: int = 1,
 def dec_block_decode_attn(q, k_cache, v_cache, pos, blocks, o, ws=None, stream=None):
     """GQA decode attention over the listed 64-key blocks of a bf16 cache; returns the workspace."""
     return (_nat or _native()).block_decode_attn(q, k_cache, v_cache, pos, blocks, o, ws, _handle(stream, k_cache))
+
+
+# ----------------------------------------------------------------------------- 8-bit weights and experts
+
+def dec_fp8_quant(x, codes, scales, block_rows: int = 1, stream=None):
+    """Quantises rows ``x`` (views [rows, K] or [n, rows, K], float32 or bf16) to e4m3 ``codes`` of the same shape
+    (float8_e4m3fn or uint8) with float32 ``scales`` [.., ceil(rows/block_rows), ceil(K/128)], powers of two;
+    ``block_rows`` 1 (activations) or 128 (weights)."""
+    (_nat or _native()).fp8_quant(x, codes, scales, block_rows, _handle(stream, x))
+
+
+def dec_fp8_dequant(codes, scales, out, block_rows: int = 1, stream=None):
+    """Writes what codes stand for, code times scale, to ``out`` (views [rows, K] or [n, rows, K], float32 or bf16)."""
+    (_nat or _native()).fp8_dequant(codes, scales, out, block_rows, _handle(stream, out))
+
+
+def dec_fp8_gemm(x_codes, x_scales, w_codes, w_scales, out, residual=None, stream=None):
+    """``out`` [M, N] = x w^T (+ ``residual``, which may be ``out``) for 8-bit rows (blocks of 1 x 128) and 8-bit
+    weights (blocks of 128 x 128); ``out`` and ``residual`` are float32 rows, strided as they like."""
+    (_nat or _native()).fp8_gemm(x_codes, x_scales, w_codes, w_scales, out, residual, _handle(stream, x_codes))
+
+
+_SCORES = {"softmax": False, "sigmoid": True}
+
+
+def dec_moe_route(y, Wr, ids, weights, bias=None, score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+                  stream=None):
+    """The ``k`` experts of each token: fills ``ids`` (int32 [T, k], best first) and ``weights`` (float32 [T, k])
+    from the scores of ``Wr y`` (``Wr`` bf16 [E, H]); ``bias`` (float32 [E]) is added for the choice only."""
+    if score not in _SCORES:
+        raise DecError(DEC_EINVAL, f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    (_nat or _native()).moe_route(y, Wr, ids, weights, bias, _SCORES[score], renormalise, scale, _handle(stream, y))
+
+
+def moe_workspace_size(T, k, I) -> int:
+    return int(lib().dec_moe_workspace_size(T, k, I))
+
+
+def dec_moe_experts(y, ids, weights, Wg, Wu, Wd, out, residual=None, scales=None, ws=None, stream=None):
+    """``out`` [T, H] = ``residual`` + the weighted sum of each token's chosen gated MLPs (weights bf16 [E, I, H],
+    [E, I, H], [E, H, I], or e4m3 codes with ``scales`` = (of Wg, of Wu, of Wd)); returns the workspace."""
+    sg, su, sd = scales if scales is not None else (None, None, None)
+    return (_nat or _native()).moe_experts(y, ids, weights, Wg, Wu, Wd, out, residual, sg, su, sd, ws, _handle(stream, y))
 
 
 # ----------------------------------------------------------------------------- model / state

@@ -18,9 +18,10 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdec.so")
 BINDING = os.path.join(HERE, "_binding.so")
 UNITS = ["api.cu", "gemv_qkv.cu", "gemv_glu.cu", "gemv_resid.cu", "gemv_head.cu", "attn.cu", "step.cu", "prefill.cu",
-         "select.cu", "tcgemm.cu", "kv4.cu", "long_attn.cu", "blocks.cu", "long_api.cu"]
+         "select.cu", "tcgemm.cu", "kv4.cu", "long_attn.cu", "blocks.cu", "long_api.cu", "fp8.cu", "fp8_gemm.cu",
+         "moe_route.cu", "moe.cu", "fp8_api.cu"]
 HEADERS = ["dec_common.cuh", "dec_kernels.cuh", "dec_attn.cuh", "dec_step.cuh", "dec_launch.cuh", "dec_long.cuh",
-           "dec_host.cuh"]
+           "dec_host.cuh", "dec_tc.cuh", "dec_fp8.cuh", "dec_moe.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -13,9 +13,11 @@
 #include <mutex>
 #include <string>
 
+#include "dec_fp8.cuh"
 #include "dec_host.cuh"
 #include "dec_launch.cuh"
 #include "dec_long.cuh"
+#include "dec_moe.cuh"
 #include "libdec.h"
 
 using namespace dec;
@@ -171,6 +173,10 @@ int device_info(DeviceInfo** out) {
     DEC_CUDA(allow_smem_select());
     DEC_CUDA(allow_smem_long());
     DEC_CUDA(allow_smem_blocks());
+    DEC_CUDA(allow_smem_fp8());
+    DEC_CUDA(allow_smem_fp8_gemm());
+    DEC_CUDA(allow_smem_moe_route());
+    DEC_CUDA(allow_smem_moe());
     DEC_CUDA(prefer_max_carveout(add_rmsnorm_kernel));
     DEC_CUDA(prefer_max_carveout(advance_kernel));
     DEC_CUDA(prefer_max_carveout(set_tokens_kernel));

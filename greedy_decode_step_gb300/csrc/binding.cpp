@@ -1,5 +1,5 @@
-// Native marshalling of the long-cache calls: torch tensors in, libdec entry
-// points out.  These calls take a few microseconds on the GPU, and checking
+// Native marshalling of the long-cache, 8-bit and expert calls: torch tensors
+// in, libdec entry points out.  These calls take a few microseconds on the GPU, and checking
 // seven tensors in Python with a ctypes call behind takes 10; here it is well
 // under one.  Same rules as the Python side: wrong dtypes raise TypeError,
 // layouts ValueError, everything else DecError with the library's codes.
@@ -159,8 +159,8 @@ const int32_t* ints(PyObject* o, int64_t B, int dev, const char* name, bool opti
 }
 
 // The caller's workspace, or one made on the stream that will use it (so that
-// dropping it is safe); `out` gets a new reference to it.
-void* workspace(PyObject* given, int Hq, int Hkv, int D, int dev, const OnDevice& on, size_t* bytes, PyObject** out) {
+// dropping it is safe) with `need` bytes; `out` gets a new reference to it.
+void* workspace(PyObject* given, size_t need, int dev, const OnDevice& on, size_t* bytes, PyObject** out) {
   if (given != Py_None) {
     const at::Tensor& t = tensor(given, "ws");
     expect(cuda_index(t) == dev && t.is_contiguous(), "ws must be contiguous memory on the tensors' device");
@@ -169,7 +169,7 @@ void* workspace(PyObject* given, int Hq, int Hkv, int D, int dev, const OnDevice
     *out = given;
     return t.data_ptr();
   }
-  *bytes = dec_long_attn_workspace_size(Hq, Hkv, D);
+  *bytes = need;
   if (*bytes == 0) {  // sizes that the call itself refuses, with its own code
     Py_INCREF(Py_None);
     *out = Py_None;
@@ -229,7 +229,7 @@ PyObject* kv4_decode_attn(PyObject* const* a) {
   const OnDevice on(c.dev, a[8]);
   size_t bytes;
   PyObject* held = nullptr;
-  void* ws = workspace(a[7], Hq, c.Hkv, c.D, c.dev, on, &bytes, &held);
+  void* ws = workspace(a[7], dec_long_attn_workspace_size(Hq, c.Hkv, c.D), c.dev, on, &bytes, &held);
   const int rc = without_gil([&] {
     return dec_kv4_decode_attn(static_cast<const float*>(q), c.kc, c.kp, c.vc, c.vp, pos, static_cast<float*>(o), ws,
                                bytes, c.B, Hq, c.Hkv, c.D, c.group(), c.S, on.stream);
@@ -299,10 +299,168 @@ PyObject* block_decode_attn(PyObject* const* a) {
   const OnDevice on(dev, a[7]);
   size_t bytes;
   PyObject* held = nullptr;
-  void* ws = workspace(a[6], Hq, Hkv, D, dev, on, &bytes, &held);
+  void* ws = workspace(a[6], dec_long_attn_workspace_size(Hq, Hkv, D), dev, on, &bytes, &held);
   const int rc = without_gil([&] {
     return dec_block_decode_attn(static_cast<const float*>(q), kp, vp, pos, static_cast<const int32_t*>(blocks), n,
                                  static_cast<float*>(o), ws, bytes, B, Hq, Hkv, D, S, on.stream);
+  });
+  if (rc != DEC_OK) Py_DECREF(held);
+  done(rc);
+  return held;
+}
+
+// ----------------------------------------------------------------------------- 8-bit weights and experts
+
+// e4m3 codes, as that type or as bytes: contiguous, of this shape.
+void* codes(PyObject* o, std::initializer_list<int64_t> shape, int index, const char* name) {
+  const at::ScalarType t = tensor(o, name).scalar_type();
+  if (t != at::kByte && t != at::kFloat8_e4m3fn)
+    throw Failure{PyExc_TypeError, 0, std::string(name) + " must be torch.float8_e4m3fn or torch.uint8, got " + str(t)};
+  return gpu(o, t, shape, index, name);
+}
+
+// Float rows [rows, K] or [n, rows, K] with contiguous values, and the codes and scales beside them.
+struct Held {
+  void *x, *c;
+  float* s;
+  int64_t n, rows, K, sm, sr;
+  int bf16, dev;
+  Held(PyObject* xo, PyObject* co, PyObject* so, int64_t block_rows, const char* xn) {
+    const at::Tensor& t = tensor(xo, xn);
+    if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kBFloat16)
+      throw Failure{PyExc_TypeError, 0, std::string(xn) + " must be float32 or bfloat16, got " + str(t.scalar_type())};
+    expect(t.dim() == 2 || t.dim() == 3, std::string(xn) + " must be [rows, K] or [n, rows, K], got " + str(t.sizes()));
+    expect(block_rows >= 1, "block_rows must be 1 or 128");
+    const bool many = t.dim() == 3;
+    n = many ? t.size(0) : 1, rows = t.size(many), K = t.size(1 + many);
+    expect(n <= INT32_MAX && rows <= INT32_MAX && K <= INT32_MAX, std::string(xn) + " is too large");
+    expect(K <= 1 || t.stride(1 + many) == 1, std::string(xn) + " must have contiguous rows");
+    // a dim of one element may carry any stride
+    sm = n > 1 ? t.stride(0) : 0, sr = rows > 1 ? t.stride(many) : 0;
+    bf16 = t.scalar_type() == at::kBFloat16;
+    dev = cuda_index(t);
+    x = t.data_ptr();
+    const int64_t RB = (rows + block_rows - 1) / block_rows, KB = (K + 127) / 128;
+    if (many) {
+      c = codes(co, {n, rows, K}, dev, "codes");
+      s = static_cast<float*>(gpu(so, at::kFloat, {n, RB, KB}, dev, "scales"));
+    } else {
+      c = codes(co, {rows, K}, dev, "codes");
+      s = static_cast<float*>(gpu(so, at::kFloat, {RB, KB}, dev, "scales"));
+    }
+  }
+};
+
+// x, codes, scales, block_rows, stream
+PyObject* fp8_quant(PyObject* const* a) {
+  const int R = as_int(a[3]);
+  const Held h(a[0], a[1], a[2], R, "x");
+  const OnDevice on(h.dev, a[4]);
+  done(without_gil([&] { return dec_fp8_quant(h.x, h.bf16, h.sm, h.sr, h.c, h.s, h.n, h.rows, h.K, R, on.stream); }));
+  Py_RETURN_NONE;
+}
+
+// codes, scales, out, block_rows, stream
+PyObject* fp8_dequant(PyObject* const* a) {
+  const int R = as_int(a[3]);
+  const Held h(a[2], a[0], a[1], R, "out");
+  const OnDevice on(h.dev, a[4]);
+  done(without_gil([&] { return dec_fp8_dequant(h.c, h.s, h.x, h.bf16, h.sm, h.sr, h.n, h.rows, h.K, R, on.stream); }));
+  Py_RETURN_NONE;
+}
+
+// Float rows [M, N] with contiguous values; the stride of their rows.
+float* float_rows(PyObject* o, int64_t M, int64_t N, int dev, const char* name, int64_t* stride) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != at::kFloat)
+    throw Failure{PyExc_TypeError, 0, std::string(name) + " must be torch.Float, got " + str(t.scalar_type())};
+  if (t.dim() != 2 || t.size(0) != M || t.size(1) != N || (N > 1 && t.stride(1) != 1))
+    refuse(std::string(name) + " must be rows [" + std::to_string(M) + ", " + std::to_string(N) +
+           "] with contiguous values, got " + str(t.sizes()) + " strided " + str(t.strides()));
+  if (cuda_index(t) != dev) refuse(std::string(name) + " is on " + t.device().str() + ", other tensors of the call are not");
+  *stride = M > 1 ? t.stride(0) : N;
+  return static_cast<float*>(t.data_ptr());
+}
+
+// x_codes, x_scales, w_codes, w_scales, out, residual, stream
+PyObject* fp8_gemm(PyObject* const* a) {
+  const at::Tensor &x = tensor(a[0], "x_codes"), &w = tensor(a[2], "w_codes");
+  expect(x.dim() == 2 && w.dim() == 2, "x_codes must be [M, K], w_codes [N, K]");
+  const int64_t M = x.size(0), K = x.size(1), N = w.size(0), KB = (K + 127) / 128;
+  expect(M <= INT32_MAX && N <= INT32_MAX && K <= INT32_MAX, "the sizes are too large");
+  const int dev = cuda_index(x);
+  const void* xc = codes(a[0], {M, K}, dev, "x_codes");
+  const void* xs = gpu(a[1], at::kFloat, {M, KB}, dev, "x_scales");
+  const void* wc = codes(a[2], {N, K}, dev, "w_codes");
+  const void* ws = gpu(a[3], at::kFloat, {(N + 127) / 128, KB}, dev, "w_scales");
+  int64_t ldo, ldr = 0;
+  float* out = float_rows(a[4], M, N, dev, "out", &ldo);
+  const float* res = a[5] == Py_None ? nullptr : float_rows(a[5], M, N, dev, "residual", &ldr);
+  const OnDevice on(dev, a[6]);
+  done(without_gil([&] {
+    return dec_fp8_gemm(xc, static_cast<const float*>(xs), wc, static_cast<const float*>(ws), res, ldr, out, ldo, M, N, K,
+                        on.stream);
+  }));
+  Py_RETURN_NONE;
+}
+
+// y, Wr, ids, weights, bias, sigmoid, renormalise, scale, stream
+PyObject* moe_route(PyObject* const* a) {
+  const at::Tensor &y = tensor(a[0], "y"), &w = tensor(a[1], "Wr"), &id = tensor(a[2], "ids");
+  expect(y.dim() == 2 && w.dim() == 2 && id.dim() == 2, "y must be [T, H], Wr [E, H], ids [T, k]");
+  const int64_t T = y.size(0), H = y.size(1), E = w.size(0), k = id.size(1);
+  expect(T <= INT32_MAX && H <= INT32_MAX && E <= INT32_MAX && k <= INT32_MAX, "the sizes are too large");
+  const int dev = cuda_index(y);
+  const void* yp = gpu(a[0], at::kFloat, {T, H}, dev, "y");
+  const void* wp = gpu(a[1], at::kBFloat16, {E, H}, dev, "Wr");
+  void* ids = gpu(a[2], at::kInt, {T, k}, dev, "ids");
+  void* gates = gpu(a[3], at::kFloat, {T, k}, dev, "weights");
+  const void* bias = a[4] == Py_None ? nullptr : gpu(a[4], at::kFloat, {E}, dev, "bias");
+  const int sigmoid = PyObject_IsTrue(a[5]), renorm = PyObject_IsTrue(a[6]);
+  const double scale = PyFloat_AsDouble(a[7]);
+  if (sigmoid < 0 || renorm < 0 || (scale == -1.0 && PyErr_Occurred())) throw Failure{nullptr, -1, ""};
+  const OnDevice on(dev, a[8]);
+  done(without_gil([&] {
+    return dec_moe_route(static_cast<const float*>(yp), wp, static_cast<const float*>(bias), sigmoid, renorm,
+                         static_cast<float>(scale), static_cast<int32_t*>(ids), static_cast<float*>(gates), T, H, E, k,
+                         on.stream);
+  }));
+  Py_RETURN_NONE;
+}
+
+// y, ids, weights, Wg, Wu, Wd, out, residual, Sg, Su, Sd (None: bf16 weights), ws, stream
+PyObject* moe_experts(PyObject* const* a) {
+  const at::Tensor &y = tensor(a[0], "y"), &id = tensor(a[1], "ids"), &g = tensor(a[3], "Wg");
+  expect(y.dim() == 2 && id.dim() == 2 && g.dim() == 3, "y must be [T, H], ids [T, k], Wg [E, I, H]");
+  const int64_t T = y.size(0), H = y.size(1), k = id.size(1), E = g.size(0), I = g.size(1);
+  expect(T <= INT32_MAX && H <= INT32_MAX && E <= INT32_MAX && I <= INT32_MAX && k <= INT32_MAX, "the sizes are too large");
+  const int dev = cuda_index(y);
+  const void* yp = gpu(a[0], at::kFloat, {T, H}, dev, "y");
+  const void* ids = gpu(a[1], at::kInt, {T, k}, dev, "ids");
+  const void* gates = gpu(a[2], at::kFloat, {T, k}, dev, "weights");
+  const bool f8 = a[8] != Py_None;
+  const void *wg, *wu, *wd, *sg = nullptr, *su = nullptr, *sd = nullptr;
+  if (f8) {
+    const int64_t IB = (I + 127) / 128, HB = (H + 127) / 128;
+    wg = codes(a[3], {E, I, H}, dev, "Wg"), wu = codes(a[4], {E, I, H}, dev, "Wu"), wd = codes(a[5], {E, H, I}, dev, "Wd");
+    sg = gpu(a[8], at::kFloat, {E, IB, HB}, dev, "scales of Wg");
+    su = gpu(a[9], at::kFloat, {E, IB, HB}, dev, "scales of Wu");
+    sd = gpu(a[10], at::kFloat, {E, HB, IB}, dev, "scales of Wd");
+  } else {
+    wg = gpu(a[3], at::kBFloat16, {E, I, H}, dev, "Wg"), wu = gpu(a[4], at::kBFloat16, {E, I, H}, dev, "Wu");
+    wd = gpu(a[5], at::kBFloat16, {E, H, I}, dev, "Wd");
+  }
+  void* out = gpu(a[6], at::kFloat, {T, H}, dev, "out");
+  const void* res = a[7] == Py_None ? nullptr : gpu(a[7], at::kFloat, {T, H}, dev, "residual");
+  const OnDevice on(dev, a[12]);
+  size_t bytes;
+  PyObject* held = nullptr;
+  void* ws = workspace(a[11], T > 0 ? dec_moe_workspace_size(T, k, I) : 0, dev, on, &bytes, &held);
+  const int rc = without_gil([&] {
+    return dec_moe_experts(static_cast<const float*>(yp), static_cast<const int32_t*>(ids), static_cast<const float*>(gates),
+                           wg, wu, wd, static_cast<const float*>(sg), static_cast<const float*>(su),
+                           static_cast<const float*>(sd), static_cast<const float*>(res), static_cast<float*>(out), ws,
+                           bytes, T, k, E, H, I, on.stream);
   });
   if (rc != DEC_OK) Py_DECREF(held);
   done(rc);
@@ -353,10 +511,15 @@ PyMethodDef kMethods[] = {DEC_ENTRY(kv4_store, 11),
                           DEC_ENTRY(block_bounds, 5),
                           DEC_ENTRY(select_blocks, 8),
                           DEC_ENTRY(block_decode_attn, 8),
+                          DEC_ENTRY(fp8_quant, 5),
+                          DEC_ENTRY(fp8_dequant, 5),
+                          DEC_ENTRY(fp8_gemm, 7),
+                          DEC_ENTRY(moe_route, 9),
+                          DEC_ENTRY(moe_experts, 13),
                           {"set_error", set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {
-    PyModuleDef_HEAD_INIT, "_binding", "Native marshalling of libdec's long-cache calls.", -1, kMethods, nullptr, nullptr,
+    PyModuleDef_HEAD_INIT, "_binding", "Native marshalling of libdec's short calls.", -1, kMethods, nullptr, nullptr,
     nullptr, nullptr};
 
 }  // namespace

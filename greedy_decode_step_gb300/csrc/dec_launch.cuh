@@ -64,6 +64,10 @@ uint32_t attn_launch_smem(int D);
 // bf16 [outer][inner] row-major tensor map with a box of 64 x box_rows and the
 // 128-byte swizzle (false if the driver refuses it).
 bool make_tmap_sw128(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_rows);
+// [mats][rows][inner] row-major of 2-byte or 1-byte elements, box of 128 bytes x
+// box_rows of one matrix, 128-byte swizzle (false if the driver refuses it).
+bool make_tmap_mats(CUtensorMap* m, const void* base, int bytes, uint64_t inner, uint64_t rows, uint64_t mats,
+                    uint32_t box_rows);
 
 // Batched prompt pass (prefill.cu): rows are (sequence, position) pairs.
 cudaError_t launch_prefill_embed(const int32_t* prompt, int P, int i0, int n, int rows, int H, const uint16_t* embed,

@@ -1,0 +1,54 @@
+// Arguments and launches of the mixture-of-experts layer: the router's choice
+// and the chosen experts' gated MLPs for a decode step's few tokens.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dec_common.cuh"
+
+namespace dec {
+
+constexpr int kMoeMaxTokens = 16;
+constexpr int kMoeMaxChoices = 16;    // experts per token
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxDim = 32768;     // hidden and intermediate sizes
+constexpr int kMoeMaxCtas = 160;      // CTAs of the gate/up launch
+constexpr int kMoeUnit = 64;          // gate rows (and up rows) of one tile
+
+struct MoeRouteArgs {
+  const float* y;                // [T][H]
+  const uint16_t* Wr;            // bf16 [E][H]
+  const float* bias;             // [E] or null
+  int32_t* ids;                  // [T][k]
+  float* gates;                  // [T][k]
+  int H, E, k, sigmoid, renormalise;
+  float scale;
+};
+cudaError_t launch_moe_route(const MoeRouteArgs& a, int T, cudaStream_t st);
+cudaError_t allow_smem_moe_route();
+
+struct MoeCall {
+  const float* y;                // [T][H]
+  const int32_t* ids;            // [T][k], -1: none
+  const float* gates;            // [T][k]
+  const void *wg, *wu, *wd;      // [E][I][H], [E][I][H], [E][H][I]: bf16, or e4m3 codes with scales
+  const float *sg, *su, *sd;     // [E][ceil(rows / 128)][ceil(columns / 128)], null for bf16
+  const float* residual;         // [T][H] or null
+  float* out;                    // [T][H]
+  float* ws;
+  int T, k, E, H, I;
+  uint32_t* err;
+};
+// Workspace: gate and up products of every chosen (token, expert), then the
+// parts of tiles that a CTA took over from the one before it.
+inline size_t moe_main_floats(int T, int k, int I) { return static_cast<size_t>(T) * k * 2 * I; }
+inline size_t moe_workspace_bytes(int T, int k, int I) {
+  return 4 * (((moe_main_floats(T, k, I) + 63) & ~size_t(63)) +
+              static_cast<size_t>(kMoeMaxCtas) * kMoeMaxTokens * 2 * kMoeUnit);
+}
+// 0, or 1 (*why says why) or 3 (a CUDA error)
+int moe_experts(const MoeCall& c, int sms, cudaStream_t st, const char** why);
+cudaError_t allow_smem_moe();
+
+}  // namespace dec

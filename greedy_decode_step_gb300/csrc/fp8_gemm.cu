@@ -1,0 +1,570 @@
+// Matrix product of 8-bit rows and weights with a scale per block of 128, on
+// the 5th-generation tensor cores:
+//
+//   out[m][n] = res[m][n] + sum_kb sx[m][kb] sw[n / 128][kb] P_kb[m][n],
+//   P_kb[m][n] = sum over the 128 values of block kb of xc[m][k] wc[n][k]
+//
+// Products of e4m3 codes are exact; the tensor core adds a block's 128 of them
+// in fp32 (tcgen05.mma kind::f8f6f4, K = 32 per instruction), and the block's
+// sum leaves tensor memory to meet its two scales in fp32 registers.  The
+// scales are any floats, so they cannot ride along in the instruction (its
+// block-scaled form takes powers of two per 32 values).  While the epilogue
+// warps add block kb, the tensor core fills the other of two accumulators with
+// block kb + 1.
+//
+// Two forms of one pipeline (a TMA producer lane, an MMA lane, epilogue warps):
+//
+// * narrow: few rows.  The 128 lanes of an accumulator are weight rows, its
+//   BN columns the rows of x, so a decode step's few rows waste no tensor
+//   time.  Bound by the weight stream: K is split over a cluster of CTAs
+//   until the GPU is full, and the splits are added through distributed shared
+//   memory in rank order.
+// * wide: many rows.  The lanes are 128 rows of x, 256 columns of weight rows,
+//   so that a thread's scale is one register per block and half tile: 128
+//   FMAs and 8 TMEM loads per thread and block where the tensor core is busy
+//   for 512 cycles.  Persistent CTAs, so the store of one tile runs beside the
+//   products of the next.
+//
+// Every wait is bounded (an error bit and an early exit instead of a hang),
+// and tensor memory is released on every path.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "dec_fp8.cuh"
+#include "dec_launch.cuh"
+#include "dec_tc.cuh"
+
+namespace dec {
+namespace {
+
+constexpr int kF8BM = 128;                    // accumulator lanes
+constexpr int kF8BK = kFp8Block;              // K per stage: one scale block, one 128-byte swizzle row
+constexpr uint32_t kF8Tile = kF8BM * kF8BK;   // 16 KB: 128 rows of a stage
+constexpr uint32_t kF8Head = 1024;            // barriers
+constexpr uint32_t kNarrowHead = 2048;        // and two blocks' scales per row
+
+// ----------------------------------------------------------------------------- narrow: weight rows on the lanes
+
+constexpr int kNarrowThreads = 192;
+constexpr int kNarrowMaxStages = 12;
+constexpr int kNarrowMaxSplits = 8;
+
+struct NarrowArgs {
+  CUtensorMap wmap, xmap;  // box 128 rows of wc, BN rows of xc
+  const float *sx, *sw, *residual;
+  float* out;
+  long long ldr, ldo;
+  int M, N, KB, n_tiles, splits, stages;
+  uint32_t* err;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __grid_constant__ NarrowArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + kNarrowMaxStages;
+  uint64_t* accum = empty + kNarrowMaxStages;  // [2] an accumulator holds a block
+  uint64_t* drained = accum + 2;               // [2] it has been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
+  volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);  // a wait ran out: every role ends
+  float(*scales)[BN] = reinterpret_cast<float(*)[BN]>(smem + kF8Head);
+  unsigned char* tiles = smem + kNarrowHead;
+  constexpr uint32_t kXTile = BN * kF8BK, kStage = kF8Tile + kXTile;
+  constexpr uint32_t kCols = tmem_columns(2 * BN);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
+  const int m0 = (tile / a.n_tiles) * kF8BM;  // weight rows
+  const int r0 = (tile % a.n_tiles) * BN;     // rows of x
+  const int kb0 = static_cast<int>(static_cast<long long>(split) * a.KB / a.splits);
+  const int nkb = static_cast<int>(static_cast<long long>(split + 1) * a.KB / a.splits) - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&accum[s], 1);
+      mbar_init(&drained[s], 4);
+    }
+    *stop = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t wpol = l2_policy_evict_first(), xpol = l2_policy_evict_last();
+      // weights (no kernel writes them) go out before the wait for the kernel that makes the rows
+      const int pre = min(nkb, a.stages);
+      for (int i = 0; i < pre; ++i) {
+        mbar_arrive_expect_tx(&full[i], kStage);
+        tma_load_3d(tiles + i * kStage, &a.wmap, (kb0 + i) * kF8BK, m0, 0, &full[i], wpol);
+      }
+      pdl_wait();
+      pdl_launch_dependents();
+      for (int i = 0; i < pre; ++i)
+        tma_load_3d(tiles + i * kStage + kF8Tile, &a.xmap, (kb0 + i) * kF8BK, r0, 0, &full[i], xpol);
+      int issued = pre;
+      for (; issued < nkb; ++issued) {
+        const int s = issued % a.stages;
+        if (!mbar_wait(&empty[s], ((issued / a.stages) - 1) & 1, stop, a.err, kErrWaitEmpty)) *stop = 1;
+        if (*stop) break;
+        mbar_arrive_expect_tx(&full[s], kStage);
+        tma_load_3d(tiles + s * kStage, &a.wmap, (kb0 + issued) * kF8BK, m0, 0, &full[s], wpol);
+        tma_load_3d(tiles + s * kStage + kF8Tile, &a.xmap, (kb0 + issued) * kF8BK, r0, 0, &full[s], xpol);
+      }
+      // an early end waits for its own copies
+      if (*stop)
+        for (int i = max(0, issued - a.stages); i < issued; ++i)
+          if (!tc_wait(&full[i % a.stages], (i / a.stages) & 1, a.err, kErrDrain)) break;
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc_idesc_of(BN, false);
+      for (int i = 0; i < nkb; ++i) {
+        const int s = i % a.stages, b = i & 1;
+        if (!mbar_wait(&full[s], (i / a.stages) & 1, stop, a.err, kErrWaitFull) ||
+            (i >= 2 && !mbar_wait(&drained[b], ((i >> 1) - 1) & 1, stop, a.err, kErrWaitFull)))
+          *stop = 1;
+        if (*stop) break;
+        tc_fence_after();
+        const uint32_t sa = smem_addr(tiles + s * kStage);
+#pragma unroll
+        for (int kk = 0; kk < kF8BK / 32; ++kk)
+          tc_mma_f8(tmem + b * BN, smem_desc_sw128(sa + kk * 32), smem_desc_sw128(sa + kF8Tile + kk * 32), idesc, kk > 0);
+        tc_commit(&empty[s]);
+        tc_commit(&accum[b]);
+      }
+    }
+  } else {
+    pdl_wait();
+    const int q = warp & 3, t = threadIdx.x - 64;
+    const int m = m0 + 32 * q + lane;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    float acc[BN];
+#pragma unroll
+    for (int j = 0; j < BN; ++j) acc[j] = 0.f;
+    // thread t brings row t's scale of every block, one block ahead
+    const bool brings = t < BN && r0 + t < a.M;
+    const float* sx = brings ? a.sx + static_cast<long long>(r0 + t) * a.KB + kb0 : a.sx;
+    const float* sw = a.sw + static_cast<long long>(m0 / kFp8Block) * a.KB + kb0;
+    float nx = brings ? __ldg(sx) : 0.f, nw = __ldg(sw);
+    bool ok = nkb > 0;
+    for (int i = 0; i < nkb; ++i) {
+      const int b = i & 1;
+      if (t < BN) scales[b][t] = nx * nw;
+      if (i + 1 < nkb) {
+        nx = brings ? __ldg(sx + i + 1) : 0.f;
+        nw = __ldg(sw + i + 1);
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      int good = 1;
+      if (lane == 0) good = (mbar_wait(&accum[b], (i >> 1) & 1, stop, a.err, kErrWaitFull) && !*stop) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+      if (!ok) *stop = 1;
+      tc_fence_after();
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < BN; c += 16) {
+          uint32_t v[16];
+          tmem_ld_issue(at + b * BN + c, v);
+          tmem_ld_wait(v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(__uint_as_float(v[j]), scales[b][c + j], acc[c + j]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&drained[b]);
+    }
+    if (a.splits == 1) {
+      if (ok && m < a.N) {
+#pragma unroll
+        for (int j = 0; j < BN; ++j) {
+          const int r = r0 + j;
+          if (r < a.M) a.out[r * a.ldo + m] = acc[j] + (a.residual ? a.residual[r * a.ldr + m] : 0.f);
+        }
+      }
+    } else {
+      // the ring is done: every block's products have been committed
+      float* part = reinterpret_cast<float*>(tiles);
+#pragma unroll
+      for (int j = 0; j < BN; ++j) part[j * kF8BM + 32 * q + lane] = acc[j];
+    }
+  }
+  __syncwarp();
+  if (a.splits > 1) {
+    pdl_wait();  // every thread writes the result here
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const uint32_t local = smem_addr(tiles);
+    const int rows = min(BN, a.M - r0), total = rows * kF8BM, per = (total + a.splits - 1) / a.splits;
+    const int end = min(total, (split + 1) * per);
+    for (int o = split * per + static_cast<int>(threadIdx.x); o < end; o += kNarrowThreads) {
+      const int r = r0 + o / kF8BM, m = m0 + o % kF8BM;
+      float x[kNarrowMaxSplits];
+#pragma unroll
+      for (int k = 0; k < kNarrowMaxSplits; ++k) {
+        x[k] = 0.f;
+        if (k < a.splits) {
+          uint32_t remote;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local + 4u * o), "r"(k));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[k]) : "r"(remote));
+        }
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kNarrowMaxSplits; ++k) sum += x[k];
+      if (m < a.N) a.out[r * a.ldo + m] = sum + (a.residual ? a.residual[r * a.ldr + m] : 0.f);
+    }
+    __syncwarp();
+    // no CTA leaves while others may still read its shared memory
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free(tmem, kCols);
+  }
+}
+
+// ----------------------------------------------------------------------------- wide: rows of x on the lanes
+
+constexpr int kWideThreads = 384;   // warp 0 copies, warp 1 multiplies, warps 4-11 scale and store
+constexpr int kWideBN = 256;
+constexpr int kWideStages = 4;
+constexpr uint32_t kWideStage = kF8Tile + kWideBN * kF8BK;  // 48 KB
+constexpr int kWidePitch = 20;      // floats of a staged row of 16: rows 4 banks apart
+constexpr uint32_t kWideOut = 8 * 32 * kWidePitch * 4;
+constexpr uint32_t kWideSmem = 1024 + kF8Head + kWideStages * kWideStage + kWideOut;
+
+struct WideArgs {
+  CUtensorMap wmap, xmap;  // box 256 rows of wc, 128 rows of xc
+  const float *sx, *sw, *residual;
+  float* out;
+  long long ldr, ldo;
+  int M, N, KB, NB, m_tiles, tiles;
+  int vec;  // rows of the result (and the residual) are 16-byte aligned
+  uint32_t* err;
+};
+
+__global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_constant__ WideArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + kWideStages;
+  uint64_t* accum = empty + kWideStages;
+  uint64_t* drained = accum + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
+  volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);  // a wait ran out: every role ends
+  unsigned char* tiles = smem + kF8Head;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kWideStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&accum[s], 1);
+      mbar_init(&drained[s], 8);
+    }
+    *stop = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 2 * kWideBN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp < 4) {
+    // 128 threads x 72 + 256 x 216 registers = the 384 x 168 of the launch
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0 && lane == 0) {
+      const uint64_t keep = l2_policy_evict_last();
+      int it = 0;
+      for (int tile = blockIdx.x; tile < a.tiles && !*stop; tile += gridDim.x) {
+        const int m0 = (tile % a.m_tiles) * kF8BM, n0 = (tile / a.m_tiles) * kWideBN;
+        for (int kb = 0; kb < a.KB; ++kb, ++it) {
+          const int s = it % kWideStages;
+          if (it >= kWideStages && !mbar_wait(&empty[s], ((it / kWideStages) - 1) & 1, stop, a.err, kErrWaitEmpty)) *stop = 1;
+          if (*stop) break;
+          unsigned char* st = tiles + s * kWideStage;
+          mbar_arrive_expect_tx(&full[s], kWideStage);
+          tma_load_3d(st, &a.xmap, kb * kF8BK, m0, 0, &full[s], keep);
+          tma_load_3d(st + kF8Tile, &a.wmap, kb * kF8BK, n0, 0, &full[s], keep);
+        }
+      }
+      if (*stop)  // an early end waits for its own copies
+        for (int i = max(0, it - kWideStages); i < it; ++i)
+          if (!tc_wait(&full[i % kWideStages], (i / kWideStages) & 1, a.err, kErrDrain)) break;
+    } else if (warp == 1 && lane == 0) {
+      constexpr uint32_t idesc = tc_idesc_of(kWideBN, false);
+      int it = 0;
+      for (int tile = blockIdx.x; tile < a.tiles && !*stop; tile += gridDim.x) {
+        for (int kb = 0; kb < a.KB; ++kb, ++it) {
+          const int s = it % kWideStages, b = it & 1;
+          if (!mbar_wait(&full[s], (it / kWideStages) & 1, stop, a.err, kErrWaitFull) ||
+              (it >= 2 && !mbar_wait(&drained[b], ((it >> 1) - 1) & 1, stop, a.err, kErrWaitFull)))
+            *stop = 1;
+          if (*stop) break;
+          tc_fence_after();
+          const uint32_t sa = smem_addr(tiles + s * kWideStage);
+#pragma unroll
+          for (int kk = 0; kk < kF8BK / 32; ++kk)
+            tc_mma_f8(tmem + b * kWideBN, smem_desc_sw128(sa + kk * 32), smem_desc_sw128(sa + kF8Tile + kk * 32), idesc,
+                      kk > 0);
+          tc_commit(&empty[s]);
+          tc_commit(&accum[b]);
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., columns 128 half ..
+    float* stage = reinterpret_cast<float*>(tiles + kWideStages * kWideStage) + (warp - 4) * 32 * kWidePitch;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * 128;
+    int it = 0;
+    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+      const int m0 = (tile % a.m_tiles) * kF8BM + 32 * q, n0 = (tile / a.m_tiles) * kWideBN + 128 * half;
+      const float* sx = a.sx + static_cast<long long>(min(m0 + lane, a.M - 1)) * a.KB;
+      const float* sw = a.sw + static_cast<long long>(min(n0 / kFp8Block, a.NB - 1)) * a.KB;
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      // the scales of the next block are on their way while this one is added
+      float nx = __ldg(sx), nw = __ldg(sw);
+      int ok = 1;
+      for (int kb = 0; kb < a.KB; ++kb, ++it) {
+        const int b = it & 1;
+        const float s = nx * nw;
+        if (kb + 1 < a.KB) {
+          nx = __ldg(sx + kb + 1);
+          nw = __ldg(sw + kb + 1);
+        }
+        if (lane == 0) ok = (mbar_wait(&accum[b], (it >> 1) & 1, stop, a.err, kErrWaitFull) && !*stop) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[2][16];
+        tmem_ld_issue(at + b * kWideBN, v[0]);
+        tmem_ld_wait(v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (c + 1 < 8) tmem_ld_issue(at + b * kWideBN + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[16 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, acc[16 * c + j]);
+          if (c + 1 < 8) tmem_ld_wait(v[(c + 1) & 1]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&drained[b]);
+      }
+      if (!ok) {
+        *stop = 1;
+        break;
+      }
+      // 16 columns at a time through shared memory, so that 4 lanes write 64 consecutive bytes of a row
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int n = n0 + 16 * c;
+        if (n < a.N) {  // warp-uniform
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float4*>(stage + lane * kWidePitch + 4 * j) =
+                make_float4(acc[16 * c + 4 * j], acc[16 * c + 4 * j + 1], acc[16 * c + 4 * j + 2], acc[16 * c + 4 * j + 3]);
+          __syncwarp();
+          const int col = n + 4 * (lane & 3);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int rr = 8 * p + (lane >> 2), r = m0 + rr;
+            float4 v = *reinterpret_cast<const float4*>(stage + rr * kWidePitch + 4 * (lane & 3));
+            if (r >= a.M || col >= a.N) continue;
+            float* dst = a.out + r * a.ldo + col;
+            const float* add = a.residual ? a.residual + r * a.ldr + col : nullptr;
+            if (a.vec && col + 4 <= a.N) {
+              if (add) {
+                const float4 w = *reinterpret_cast<const float4*>(add);
+                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+              }
+              *reinterpret_cast<float4*>(dst) = v;
+            } else {
+              const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (col + j < a.N) dst[j] = e[j] + (add ? add[j] : 0.f);
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free(tmem, 2 * kWideBN);
+  }
+}
+
+// ----------------------------------------------------------------------------- host side
+
+constexpr uint32_t kNarrowSmemMax = 112 * 1024;  // two CTAs per SM
+
+template <int BN>
+constexpr int narrow_stages() {
+  constexpr uint32_t max = BN <= 64 ? kNarrowSmemMax : 2 * kNarrowSmemMax;
+  constexpr int fit = static_cast<int>((max - 1024 - kNarrowHead) / (kF8Tile + BN * kF8BK));
+  return fit < kNarrowMaxStages ? fit : kNarrowMaxStages;
+}
+template <int BN>
+constexpr uint32_t narrow_smem() {
+  return 1024 + kNarrowHead + narrow_stages<BN>() * (kF8Tile + BN * kF8BK);
+}
+
+// Clusters of `size` CTAs that the device holds at once (cached; -1 where the query fails).
+template <int BN>
+int narrow_clusters(int size) {
+  static std::mutex mu;
+  static int cache[kNarrowMaxSplits + 1] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[size] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size * 64);
+    cfg.blockDim = dim3(kNarrowThreads);
+    cfg.dynamicSmemBytes = narrow_smem<BN>();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<BN>, &cfg) != cudaSuccess || n == 0) {
+      (void)cudaGetLastError();
+      n = -1;
+    }
+    cache[size] = n;
+  }
+  return cache[size];
+}
+
+template <int BN>
+cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
+  static thread_local NarrowArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (!make_tmap_mats(&a.wmap, c.wc, 1, c.K, c.N, 1, kF8BM) || !make_tmap_mats(&a.xmap, c.xc, 1, c.K, c.M, 1, BN)) {
+    *why = "a tensor map could not be made";
+    return cudaErrorInvalidValue;
+  }
+  a.sx = c.sx;
+  a.sw = c.sw;
+  a.residual = c.residual;
+  a.out = c.out;
+  a.ldr = c.ldr;
+  a.ldo = c.ldo;
+  a.M = c.M;
+  a.N = c.N;
+  a.KB = (c.K + kF8BK - 1) / kF8BK;
+  a.n_tiles = (c.M + BN - 1) / BN;
+  a.err = c.err;
+  a.stages = narrow_stages<BN>();
+  const long long tiles = static_cast<long long>(a.n_tiles) * ((c.N + kF8BM - 1) / kF8BM);
+  // K splits: double while every split keeps two blocks and all clusters run at once
+  const long long slots = static_cast<long long>(sms) * (BN <= 64 ? 2 : 1);
+  int splits = 1;
+  while (splits * 2 <= kNarrowMaxSplits && tiles * splits * 2 <= slots && a.KB / (splits * 2) >= 2 &&
+         narrow_clusters<BN>(splits * 2) >= tiles)
+    splits *= 2;
+  a.splits = splits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+  cfg.blockDim = dim3(kNarrowThreads);
+  cfg.dynamicSmemBytes = narrow_smem<BN>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<BN>, a);
+}
+
+cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
+  static thread_local WideArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (!make_tmap_mats(&a.wmap, c.wc, 1, c.K, c.N, 1, kWideBN) || !make_tmap_mats(&a.xmap, c.xc, 1, c.K, c.M, 1, kF8BM)) {
+    *why = "a tensor map could not be made";
+    return cudaErrorInvalidValue;
+  }
+  a.sx = c.sx;
+  a.sw = c.sw;
+  a.residual = c.residual;
+  a.out = c.out;
+  a.ldr = c.ldr;
+  a.ldo = c.ldo;
+  a.M = c.M;
+  a.N = c.N;
+  a.KB = (c.K + kF8BK - 1) / kF8BK;
+  a.NB = (c.N + kFp8Block - 1) / kFp8Block;
+  a.m_tiles = (c.M + kF8BM - 1) / kF8BM;
+  a.tiles = a.m_tiles * ((c.N + kWideBN - 1) / kWideBN);
+  a.err = c.err;
+  auto rows16 = [](const void* p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 4 == 0; };
+  a.vec = rows16(c.out, c.ldo) && (!c.residual || rows16(c.residual, c.ldr));
+  return launch(fp8_wide_kernel, dim3(std::min(a.tiles, sms)), dim3(kWideThreads), kWideSmem, st, true, a);
+}
+
+}  // namespace
+
+int fp8_gemm(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
+  *why = nullptr;
+  cudaError_t e;
+  if (c.M <= 16)
+    e = launch_narrow<16>(c, sms, st, why);
+  else if (c.M <= 32)
+    e = launch_narrow<32>(c, sms, st, why);
+  else if (c.M <= 64)
+    e = launch_narrow<64>(c, sms, st, why);
+  else if (c.M <= 128)
+    e = launch_narrow<128>(c, sms, st, why);
+  else
+    e = launch_wide(c, sms, st, why);
+  if (*why) return 1;
+  if (e != cudaSuccess) {
+    *why = cudaGetErrorString(e);
+    return 3;
+  }
+  return 0;
+}
+
+cudaError_t allow_smem_fp8_gemm() {
+  cudaError_t e;
+  if ((e = allow_smem(fp8_narrow_kernel<16>)) != cudaSuccess) return e;
+  if ((e = allow_smem(fp8_narrow_kernel<32>)) != cudaSuccess) return e;
+  if ((e = allow_smem(fp8_narrow_kernel<64>)) != cudaSuccess) return e;
+  if ((e = allow_smem(fp8_narrow_kernel<128>)) != cudaSuccess) return e;
+  return allow_smem(fp8_wide_kernel);
+}
+
+}  // namespace dec

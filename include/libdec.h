@@ -30,7 +30,7 @@
  *    limit) set bits in a per-device error word read by dec_device_error().
  *  - Numerics: fp32 accumulation of bf16 weights; RMSNorm, RoPE, softmax and
  *    SiLU in fp32 (RoPE angles reduced in fp64); the KV cache stores bf16.
- *  - Batch B is 1..16 (token selection and the long-cache calls take more).
+ *  - Batch B is 1..16 (token selection, the long-cache calls and the 8-bit products take more).
  *    head_dim D is 64 or 128; Hq/Hkv is an integer <= 16.
  */
 #ifndef LIBDEC_H
@@ -327,6 +327,95 @@ int dec_select_blocks(const float* q, const void* bounds, const int32_t* pos, in
 int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cache, const int32_t* pos,
                           const int32_t* blocks, int n_select, float* o, void* ws, size_t ws_bytes, int B, int Hq,
                           int Hkv, int D, int S_max, void* stream);
+
+/* ------------------------------------------------------------------ 8-bit weights, experts */
+
+/*
+ * Weights in 8 bits, and a mixture-of-experts layer in place of the dense MLP:
+ * single calls beside the GEMVs above (the captured decode loop keeps its bf16
+ * weights).  The paper has no counterpart of them.
+ *
+ * 8-bit values are e4m3 codes (1 sign, 4 exponent, 3 fraction bits, largest
+ * value 448, 0x7F a NaN) with one float32 scale s per block of 128 values of a
+ * row, over one row (activations) or 128 rows (weights); a code c stands for
+ * c * s.  A matrix of R rows of K codes (K a multiple of 16) has scales
+ * [ceil(R / block_rows)][ceil(K / 128)]; blocks at the edges are smaller.
+ */
+
+/*
+ * Quantises n matrices of rows of K values.  x: float32 (bf16 == 0) or bf16
+ * (bf16 != 0); row r of matrix i begins at i * stride_mat + r * stride_row
+ * elements (multiples of 16 bytes).  codes [n][rows][K], dense; scales float32
+ * [n][ceil(rows / block_rows)][ceil(K / 128)]; block_rows 1 or 128.  With a the
+ * largest finite magnitude of a block,
+ *   s = the smallest power of two, 2^-126 at least, with a <= 448 s (1 if a == 0)
+ *   c = e4m3(x / s), to nearest, ties to even
+ * and the NaN code for an infinity or a NaN, which no other value is touched
+ * by.  Codes and scales are defined to the bit.  n and rows may be 0.
+ */
+int dec_fp8_quant(const void* x, int bf16, int64_t stride_mat, int64_t stride_row, void* codes, float* scales, int n,
+                  int rows, int K, int block_rows, void* stream);
+
+/*
+ * Reads codes back: out = c * s, rounded once to float32 and for bf16 once
+ * more (any float scales; exact in float32 for powers of two of its range).
+ * out is strided as x above; its rows may not share memory.
+ */
+int dec_fp8_dequant(const void* codes, const float* scales, void* out, int bf16, int64_t stride_mat, int64_t stride_row,
+                    int n, int rows, int K, int block_rows, void* stream);
+
+/*
+ * Product of 8-bit rows x [M][K] (blocks of 1 x 128) and 8-bit weights w [N][K]
+ * (blocks of 128 x 128), any float scales:
+ *   out[m][n] = residual[m][n] + sum_j sx[m][j] sw[n / 128][j] sum_{k in block j} cx[m][k] cw[n][k]
+ * Products of codes are exact; a block's sum is held in fp32, as are the sums
+ * over blocks.  out and residual: float32, rows of N contiguous values that
+ * begin stride_out and stride_residual elements apart (stride_out >= N);
+ * residual may be NULL, or out itself with its stride; other overlaps are not
+ * allowed.  M is 0..2^24.  Results are reproducible bit for bit.
+ */
+int dec_fp8_gemm(const void* x_codes, const float* x_scales, const void* w_codes, const float* w_scales,
+                 const float* residual, int64_t stride_residual, float* out, int64_t stride_out, int M, int N, int K,
+                 void* stream);
+
+/*
+ * The experts of each token.  z = Wr y[t]; the score p of an expert is its
+ * softmax over all E (sigmoid == 0) or its sigmoid (sigmoid != 0).  Chosen are
+ * the k experts of the largest z, or with a bias (float32 [E], else NULL) of
+ * the largest p + bias; equal ones by the lower id, NaN behind every number.
+ * ids: int32 [T][k], best first; weights float32 [T][k]: p, divided by the sum
+ * of the chosen ones' p if renormalise != 0, times scale.  y fp32 [T][H]; Wr
+ * bf16 [E][H].  T is 0..16, E 1..1024, k 1..16 and at most E, H a multiple of 8
+ * up to 32768.
+ */
+int dec_moe_route(const float* y, const void* Wr, const float* bias, int sigmoid, int renormalise, float scale,
+                  int32_t* ids, float* weights, int T, int H, int E, int k, void* stream);
+
+/* Workspace bytes of dec_moe_experts (0: sizes refused). */
+size_t dec_moe_workspace_size(int T, int k, int I);
+
+/*
+ * The chosen experts' gated MLPs, added up:
+ *   out[t] = residual[t] + sum_j weights[t][j] Wd[e] (silu(Wg[e] y[t]) * (Wu[e] y[t])),  e = ids[t][j]
+ * ids[t][j] == -1: no expert (a token without any gets its residual); an
+ * expert listed twice counts twice; an id outside [-1, E) is passed over
+ * (error bit 4).  Sg, Su and Sd all NULL: Wg, Wu bf16 [E][I][H], Wd bf16
+ * [E][H][I], H and I multiples of 8.  Else e4m3 codes of these shapes with
+ * scales of 128 x 128 blocks per expert, [E][ceil(I/128)][ceil(H/128)] and for
+ * Wd [E][ceil(H/128)][ceil(I/128)], H and I multiples of 16.  Activations keep
+ * float32 accuracy: an element of y is held to 2^-24 of itself (8-bit weights:
+ * to 2^-23 of the largest of its 128), and so is one of the MLP's inner
+ * vector.  Each chosen expert's weights are read once.  The weights must be
+ * finite: a NaN or an infinity in an expert reaches every token of the call; a
+ * non-finite element of y reaches its own token only.  y, residual and out
+ * fp32 [T][H]; residual may be NULL or out, and out may be y.  T is 0..16, k
+ * 1..16, E 1..1024, H and I up to 32768.  ws: device workspace of
+ * dec_moe_workspace_size() bytes, 256-byte aligned, any contents; calls that
+ * can overlap on the GPU need one each.  Results are reproducible bit for bit.
+ */
+int dec_moe_experts(const float* y, const int32_t* ids, const float* weights, const void* Wg, const void* Wu, const void* Wd,
+                    const float* Sg, const float* Su, const float* Sd, const float* residual, float* out, void* ws,
+                    size_t ws_bytes, int T, int k, int E, int H, int I, void* stream);
 
 /* ------------------------------------------------------------------ whole step */
 
