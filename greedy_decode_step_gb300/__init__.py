@@ -81,7 +81,7 @@ _SIGNATURES = {
     "dec_fp8_dequant": (_I, [_P, _P, _P, _I, _L, _L, _I, _I, _I, _I, _P]),
     "dec_fp8_gemm": (_I, [_P, _P, _P, _P, _P, _L, _P, _L, _I, _I, _I, _P]),
     "dec_moe_route": (_I, [_P, _P, _P, _I, _I, _F, _P, _P, _I, _I, _I, _I, _P]),
-    "dec_moe_workspace_size": (_S, [_I, _I, _I]),
+    "dec_moe_workspace_size": (_S, [_I, _I, _I, _I]),
     "dec_moe_experts": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _I, _I, _I, _I, _I, _P]),
     "dec_state_workspace_size": (_S, [ctypes.POINTER(DecModel), _I, _I]),
     "dec_state_init": (_I, [ctypes.POINTER(DecModel), ctypes.POINTER(DecState), _P]),
@@ -349,8 +349,8 @@ def dec_moe_route(y, Wr, ids, weights, bias=None, score: str = "softmax", renorm
     (_nat or _native()).moe_route(y, Wr, ids, weights, bias, _SCORES[score], renormalise, scale, _handle(stream, y))
 
 
-def moe_workspace_size(T, k, I) -> int:
-    return int(lib().dec_moe_workspace_size(T, k, I))
+def moe_workspace_size(T, k, H, I) -> int:
+    return int(lib().dec_moe_workspace_size(T, k, H, I))
 
 
 def dec_moe_experts(y, ids, weights, Wg, Wu, Wd, out, residual=None, scales=None, ws=None, stream=None):

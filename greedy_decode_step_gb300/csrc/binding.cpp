@@ -455,7 +455,7 @@ PyObject* moe_experts(PyObject* const* a) {
   const OnDevice on(dev, a[12]);
   size_t bytes;
   PyObject* held = nullptr;
-  void* ws = workspace(a[11], T > 0 ? dec_moe_workspace_size(T, k, I) : 0, dev, on, &bytes, &held);
+  void* ws = workspace(a[11], T > 0 ? dec_moe_workspace_size(T, k, H, I) : 0, dev, on, &bytes, &held);
   const int rc = without_gil([&] {
     return dec_moe_experts(static_cast<const float*>(yp), static_cast<const int32_t*>(ids), static_cast<const float*>(gates),
                            wg, wu, wd, static_cast<const float*>(sg), static_cast<const float*>(su),

@@ -36,16 +36,28 @@ struct MoeCall {
   const float *sg, *su, *sd;     // [E][ceil(rows / 128)][ceil(columns / 128)], null for bf16
   const float* residual;         // [T][H] or null
   float* out;                    // [T][H]
-  float* ws;
+  unsigned char* ws;
   int T, k, E, H, I;
   uint32_t* err;
 };
-// Workspace: gate and up products of every chosen (token, expert), then the
-// parts of tiles that a CTA took over from the one before it.
-inline size_t moe_main_floats(int T, int k, int I) { return static_cast<size_t>(T) * k * 2 * I; }
-inline size_t moe_workspace_bytes(int T, int k, int I) {
-  return 4 * (((moe_main_floats(T, k, I) + 63) & ~size_t(63)) +
-              static_cast<size_t>(kMoeMaxCtas) * kMoeMaxTokens * 2 * kMoeUnit);
+// Workspace (byte offsets): the plan; gate and up products of every chosen
+// (token, expert); the parts of tiles that a CTA took over from the one before
+// it; the split rows of y and of the inner vectors, 1 KB per token and 64 or
+// 128 values.
+constexpr int kMoeRows = kMoeMaxTokens * kMoeMaxChoices;  // (token, expert) pairs
+constexpr int kMoePlanBytes = 4096;
+struct MoeWorkspace {
+  size_t main, cut, xb, hb, bytes;
+};
+inline MoeWorkspace moe_workspace(int T, int k, int H, int I) {
+  auto up = [](size_t n) { return (n + 1023) & ~size_t(1023); };
+  MoeWorkspace w;
+  w.main = kMoePlanBytes;
+  w.cut = w.main + up(static_cast<size_t>(T) * k * 2 * I * 4);
+  w.xb = w.cut + static_cast<size_t>(kMoeMaxCtas) * kMoeMaxTokens * 2 * kMoeUnit * 4;
+  w.hb = w.xb + static_cast<size_t>(T) * ((H + 63) / 64) * 1024;
+  w.bytes = w.hb + static_cast<size_t>(T) * k * ((I + 63) / 64) * 1024;
+  return w;
 }
 // 0, or 1 (*why says why) or 3 (a CUDA error)
 int moe_experts(const MoeCall& c, int sms, cudaStream_t st, const char** why);

@@ -202,11 +202,11 @@ int dec_moe_route(const float* y, const void* Wr, const float* bias, int sigmoid
   return DEC_OK;
 }
 
-size_t dec_moe_workspace_size(int T, int k, int I) {
-  if (check_moe(T, kMoeMaxExperts, 8) != DEC_OK || check_choices(k, kMoeMaxExperts) != DEC_OK ||
-      check_inner(I, false, 8) != DEC_OK)
+size_t dec_moe_workspace_size(int T, int k, int H, int I) {
+  if (check_moe(T, kMoeMaxExperts, H) != DEC_OK || check_choices(k, kMoeMaxExperts) != DEC_OK ||
+      check_inner(I, false, H) != DEC_OK)
     return 0;
-  return moe_workspace_bytes(T, k, I);
+  return moe_workspace(T, k, H, I).bytes;
 }
 
 int dec_moe_experts(const float* y, const int32_t* ids, const float* weights, const void* Wg, const void* Wu, const void* Wd,
@@ -231,7 +231,7 @@ int dec_moe_experts(const float* y, const int32_t* ids, const float* weights, co
   if (residual) DEC_PTR(residual);
   DEC_PTR(out);
   DEC_CHECK(aligned(ws, 256), DEC_EINVAL, "workspace must be non-null and 256-byte aligned");
-  const size_t need = moe_workspace_bytes(T, k, I);
+  const size_t need = moe_workspace(T, k, H, I).bytes;
   DEC_CHECK(ws_bytes >= need, DEC_EINVAL, "experts' workspace has %zu bytes, needs %zu", ws_bytes, need);
   MoeCall c{};
   int sms;
@@ -247,7 +247,7 @@ int dec_moe_experts(const float* y, const int32_t* ids, const float* weights, co
   c.sd = Sd;
   c.residual = residual;
   c.out = out;
-  c.ws = static_cast<float*>(ws);
+  c.ws = static_cast<unsigned char*>(ws);
   c.T = T;
   c.k = k;
   c.E = E;

@@ -3,8 +3,9 @@
 //   out[t] = res[t] + sum over experts e chosen by t, gate weight w:
 //            Wd[e] (w silu(Wg[e] y[t]) * (Wu[e] y[t]))
 //
-// in two launches, gate/up and down, both bound by the stream of the chosen
-// experts' weights: each is read once, whatever number of tokens chose it.
+// Bound by the stream of the chosen experts' weights: each is read once,
+// whatever number of tokens chose it.  Two launches (gate/up and down) stream
+// them; two short ones ahead of each make the activations' operand.
 //
 // The products run on the tensor cores with weight rows on the 128 lanes of an
 // accumulator and the tokens on its columns (tcgen05.mma, M = 128).  fp32
@@ -14,21 +15,28 @@
 //   * bf16 weights: three bf16 parts (24 bits);
 //   * e4m3 weights: five e4m3 parts, each 2^-5 of the one before, of x / s with s
 //     a power of two per token and 128 values (what is left is 2^-23 of the
-//     largest of the 128); every 128 values the column sums leave tensor memory
-//     to meet s and the weights' own block scale in fp32.
-// The parts are made in shared memory beside the weight stream, by four warps
-// that each take every fourth 128-byte chunk of K; columns cost little: 16 for
-// one or two tokens, 48 (bf16) or 80 (e4m3) for 16, next to 128 weight rows.
+//     largest of the 128).
+// After every 128 bytes of K the column sums leave tensor memory and are added
+// in fp32 registers, times s and the weights' own block scale: the tensor core
+// cuts every product at the last place of its running sum, and one accumulator
+// over a whole row of 2560 was off by 1.8e-6 where this is by 1e-7.
+//
+// The parts are made once (moe_prep_kernel for y, moe_act_kernel for the inner
+// vector), as 1 KB blocks per token and chunk that a bulk copy puts beside the
+// weights as they are: eight swizzled rows of 128 bytes, the parts in the
+// first three or five.  A chunk's operand is the blocks of the tokens that chose
+// the expert, N = 8 per token, so its cost follows their number.  (Splitting rows
+// beside the stream, in every CTA, cost 1.1 us a chunk with 16 tokens, three times
+// the time its weights take.)
 //
 // gate/up: a tile is 64 gate rows and the same 64 up rows of an expert.  How
 // many experts are active is known on the device only, so a persistent grid
 // lays all tiles' chunks end to end and gives every CTA an equal run of them;
-// a tile cut between CTAs leaves parts, which the down launch adds, in CTA
-// order, as it reads them.
-// down: a tile is 128 output rows, its K axis all active experts' h one behind
-// the other, split over a cluster of CTAs whose sums meet in distributed shared
-// memory in rank order: results do not depend on timing.  Its first weights
-// are on their way while gate/up still runs.
+// a tile cut between CTAs leaves parts, which moe_act_kernel adds in CTA order.
+// down: a tile is 128 output rows, its K axis all active experts' inner vectors
+// one behind the other, split over a cluster of CTAs whose sums meet in
+// distributed shared memory in rank order: results do not depend on timing.
+// Its first weights are on their way while gate/up still runs.
 //
 // Every wait is bounded (an error bit and an early exit instead of a hang),
 // and tensor memory is released on every path.
@@ -49,24 +57,33 @@
 namespace dec {
 namespace {
 
-constexpr int kMoeThreads = 320;      // warp 0 copies, 1 multiplies, 2-5 take sums off, 6-9 split rows into parts
-constexpr int kMoeSplitWarps = 4;
+constexpr int kMoeThreads = 224;      // warp 0 copies weights, 1 multiplies, 2-5 take sums off, 6 copies activations
+constexpr int kMoeFlat = 256;         // threads of the two short launches
 constexpr uint32_t kMoeATile = 128 * 128;
-constexpr int kMoeRows = kMoeMaxTokens * kMoeMaxChoices;  // (token, expert) pairs
-constexpr uint32_t kMoeSmemMax = 112 * 1024;              // both launches' CTAs share an SM
+constexpr uint32_t kMoeBlock = 1024;  // one token's parts of one chunk
 constexpr int kMoeMaxStages = 8;
+constexpr int kMoeBStages = 4;
 constexpr int kMoeMaxSplits = 8;
 
-template <bool F8, int NT>
-struct Shape {
+template <bool F8>
+struct Parts {
   static constexpr int kParts = F8 ? 5 : 3;
-  static constexpr int kN = (kParts * NT + 15) / 16 * 16;   // columns of the MMA
   static constexpr int kChunk = F8 ? 128 : 64;              // values of K per 128-byte row
-  static constexpr int kVals = kChunk / 32;                 // of them per lane of a splitting warp
-  static constexpr uint32_t kBTile = kN * 128;
-  static constexpr int kBStages = kMoeSplitWarps;
-  static constexpr int kScaleSlots = kBStages + 2;
+  static constexpr int kVals = kChunk / 32;                 // of them per lane of a warp
+  static constexpr uint32_t kScaleAt = kParts * 128;        // e4m3: s behind the parts
+  static constexpr uint32_t kCopy = kParts * 128 + (F8 ? 16 : 0);
 };
+
+// What all launches derive from the ids (made by moe_prep_kernel): the active
+// experts in ascending order, the tokens of each, and one row per (expert,
+// token) pair.
+struct Plan {
+  int active, rows;
+  uint16_t expert[kMoeRows], count[kMoeRows], first[kMoeRows];  // per active expert
+  uint16_t token[kMoeRows], act[kMoeRows];                      // per row
+  float gate[kMoeRows];
+};
+static_assert(sizeof(Plan) <= kMoePlanBytes, "the plan's place in the workspace");
 
 struct MoeArgs {
   CUtensorMap g, u, d;           // boxes of 64, 64 and 128 rows
@@ -76,85 +93,24 @@ struct MoeArgs {
   const float *sg, *su, *sd;
   const float* residual;
   float* out;
-  float *main, *cut;             // workspace
+  Plan* plan;                    // workspace
+  float *main, *cut;
+  unsigned char *xb, *hb;
   int T, k, E, H, I;
   int ctas;                      // of the gate/up launch
-  int splits, stages;
+  int splits;
   uint32_t* err;
 };
-
-// What both launches derive from the ids: the active experts in ascending
-// order, the tokens of each and where their rows begin.
-struct Plan {
-  uint32_t chosen[kMoeMaxExperts / 2];   // 16 token bits per expert
-  uint16_t expert[kMoeRows], tokens[kMoeRows], first[kMoeRows];
-  float gate[kMoeRows];                  // per row (down)
-  int active;
-};
-
-// Called by all threads; ends with a barrier.
-__device__ __forceinline__ void make_plan(Plan& p, const MoeArgs& a, bool gates) {
-  const int n = a.T * a.k;
-  for (int i = threadIdx.x; i < (a.E + 1) / 2; i += kMoeThreads) p.chosen[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kMoeThreads) {
-    const int e = a.ids[i];
-    if (e >= 0 && e < a.E)
-      atomicOr(&p.chosen[e >> 1], (1u << (i / a.k)) << (16 * (e & 1)));
-    else if (e != -1 && blockIdx.x == 0)
-      atomicOr(a.err, kErrPosRange);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int active = 0, rows = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const uint32_t m = e < a.E ? (p.chosen[e >> 1] >> (16 * (e & 1))) & 0xFFFFu : 0u;
-      const uint32_t any = __ballot_sync(0xffffffffu, m != 0);
-      if (any == 0) continue;
-      const int c = __popc(m);
-      int upto = c;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      if (m) {
-        const int at = active + __popc(any & ((1u << lane) - 1));
-        p.expert[at] = static_cast<uint16_t>(e);
-        p.tokens[at] = static_cast<uint16_t>(m);
-        p.first[at] = static_cast<uint16_t>(rows + upto - c);
-      }
-      active += __popc(any);
-      rows += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) p.active = active;
-  }
-  __syncthreads();
-  if (gates) {
-    for (int i = threadIdx.x; i < p.active * kMoeMaxTokens; i += kMoeThreads) {
-      const int at = i / kMoeMaxTokens, t = i % kMoeMaxTokens;
-      const uint32_t m = p.tokens[at];
-      if (!((m >> t) & 1u)) continue;
-      float w = 0.f;  // an expert that a token lists twice counts twice
-      for (int j = 0; j < a.k; ++j)
-        if (a.ids[t * a.k + j] == p.expert[at]) w += a.gates[t * a.k + j];
-      p.gate[p.first[at] + __popc(m & ((1u << t) - 1))] = w;
-    }
-    __syncthreads();
-  }
-}
 
 // The runs of gate/up: W chunks over n CTAs.  A run is at least an eighth of a
 // tile's K axis, so that a tile is cut into nine parts at most.
 struct Runs {
   long long W;
   int n, kch, units;
-  __device__ __forceinline__ Runs(const Plan& p, const MoeArgs& a, int chunk) {
+  __device__ __forceinline__ Runs(int active, const MoeArgs& a, int chunk) {
     kch = (a.H + chunk - 1) / chunk;
     units = (a.I + kMoeUnit - 1) / kMoeUnit;
-    const long long tiles = static_cast<long long>(p.active) * units;
+    const long long tiles = static_cast<long long>(active) * units;
     W = tiles * kch;
     n = static_cast<int>(min(static_cast<long long>(a.ctas), min(8 * tiles, W)));  // no run is empty
   }
@@ -169,29 +125,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Byte offset of this lane's 4 bytes in row `row` of a swizzled tile.
+// Byte offset of this lane's 4 bytes in row `row` < 8 of a swizzled block.
 __device__ __forceinline__ uint32_t part_at(int row, int lane) {
-  return row * 128 + ((((lane >> 2) ^ row) & 7) << 4) + ((lane & 3) << 2);
+  return row * 128 + (((lane >> 2) ^ row) << 4) + ((lane & 3) << 2);
 }
 
-// Three bf16 parts of this lane's two values into rows t, NT + t, 2 NT + t.
-template <int NT>
-__device__ __forceinline__ void put_parts(unsigned char* tile, int t, int lane, const float (&x)[2]) {
+// A warp's two (bf16 parts) or four (e4m3 parts) values per lane into a block.
+__device__ __forceinline__ void put_parts(unsigned char* block, int lane, const float (&x)[2]) {
   float a = x[0], b = x[1];
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
     const uint32_t w = pack_bf16(a, b);
-    *reinterpret_cast<uint32_t*>(tile + part_at(p * NT + t, lane)) = w;
+    *reinterpret_cast<uint32_t*>(block + part_at(p, lane)) = w;
     a -= bf16lo(w);
     b -= bf16hi(w);
   }
 }
 
-// Five e4m3 parts of this lane's four values; returns s (the same in all lanes).
 // s: the largest magnitude of the 128 is at most 224 s, so that what a part
 // leaves, half a step of at most 16, is at most 8 and 2^5 of it fits again.
-template <int NT>
-__device__ __forceinline__ float put_parts(unsigned char* tile, int t, int lane, const float (&x)[4]) {
+__device__ __forceinline__ void put_parts(unsigned char* block, int lane, const float (&x)[4]) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -212,7 +165,7 @@ __device__ __forceinline__ float put_parts(unsigned char* tile, int t, int lane,
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
-    *reinterpret_cast<uint32_t*>(tile + part_at(p * NT + t, lane)) = lo | (static_cast<uint32_t>(hi) << 16);
+    *reinterpret_cast<uint32_t*>(block + part_at(p, lane)) = lo | (static_cast<uint32_t>(hi) << 16);
     if (p < 4) {
       uint32_t h0, h1;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"(lo));
@@ -225,85 +178,191 @@ __device__ __forceinline__ float put_parts(unsigned char* tile, int t, int lane,
       v[3] = (v[3] - f1.y) * 32.f;
     }
   }
-  return __uint_as_float(static_cast<uint32_t>(e) << 23);
+  if (lane == 0) *reinterpret_cast<float*>(block + Parts<true>::kScaleAt) = __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
 
-template <int NT, int PARTS>
-__device__ __forceinline__ void put_zeros(unsigned char* tile, int t, int lane) {
-#pragma unroll
-  for (int p = 0; p < PARTS; ++p) *reinterpret_cast<uint32_t*>(tile + part_at(p * NT + t, lane)) = 0;
+// A lane's consecutive values.
+__device__ __forceinline__ void load_vals(float (&x)[2], const float* src) {
+  const float2 f = *reinterpret_cast<const float2*>(src);
+  x[0] = f.x, x[1] = f.y;
+}
+__device__ __forceinline__ void load_vals(float (&x)[4], const float* src) {
+  const float4 f = *reinterpret_cast<const float4*>(src);
+  x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
 }
 
-// The accumulator's columns of this thread's lane, parts added per token, the smallest first.
-template <bool F8, int NT>
-__device__ __forceinline__ void take_sums(uint32_t taddr, float (&s)[NT]) {
-  using S = Shape<F8, NT>;
-  uint32_t v[S::kN / 16][16];
+// ----------------------------------------------------------------------------- plan and parts of y
+
+// One CTA; ends with a barrier.
+__device__ __forceinline__ void make_plan(Plan& p, const MoeArgs& a) {
+  __shared__ uint32_t chosen[kMoeMaxExperts / 2];  // 16 token bits per expert
+  __shared__ int32_t ids[kMoeRows];
+  __shared__ float gates[kMoeRows];
+  const int n = a.T * a.k;
+  for (int i = threadIdx.x; i < (a.E + 1) / 2; i += kMoeFlat) chosen[i] = 0;
+  for (int i = threadIdx.x; i < n; i += kMoeFlat) {
+    ids[i] = a.ids[i];
+    gates[i] = a.gates[i];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kMoeFlat) {
+    const int e = ids[i];
+    if (e >= 0 && e < a.E)
+      atomicOr(&chosen[e >> 1], (1u << (i / a.k)) << (16 * (e & 1)));
+    else if (e != -1)
+      atomicOr(a.err, kErrPosRange);
+  }
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  int active = 0, rows = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + lane;
+    const uint32_t m = e < a.E ? (chosen[e >> 1] >> (16 * (e & 1))) & 0xFFFFu : 0u;
+    const uint32_t any = __ballot_sync(0xffffffffu, m != 0);
+    if (any == 0) continue;
+    const int c = __popc(m);
+    int upto = c;
 #pragma unroll
-  for (int c = 0; c < S::kN / 16; ++c) tmem_ld_issue(taddr + 16 * c, v[c]);
-#pragma unroll
-  for (int c = 0; c < S::kN / 16; ++c) tmem_ld_wait(v[c]);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    float r = 0.f;
-#pragma unroll
-    for (int p = S::kParts - 1; p >= 0; --p) {
-      const float x = __uint_as_float(v[(p * NT + t) / 16][(p * NT + t) % 16]);
-      r = F8 ? fmaf(r, 0.03125f, x) : r + x;
+    for (int o = 1; o < 32; o *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    s[t] = r;
+    if (m) {
+      const int at = active + __popc(any & ((1u << lane) - 1)), first = rows + upto - c;
+      p.expert[at] = static_cast<uint16_t>(e);
+      p.count[at] = static_cast<uint16_t>(c);
+      p.first[at] = static_cast<uint16_t>(first);
+      int row = first;
+      for (uint32_t left = m; left; left &= left - 1, ++row) {
+        const int t = __ffs(left) - 1;
+        float w = 0.f;  // an expert that a token lists twice counts twice
+        for (int j = 0; j < a.k; ++j)
+          if (ids[t * a.k + j] == e) w += gates[t * a.k + j];
+        p.token[row] = static_cast<uint16_t>(t);
+        p.act[row] = static_cast<uint16_t>(at);
+        p.gate[row] = w;
+      }
+    }
+    active += __popc(any);
+    rows += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (lane == 0) {
+    p.active = active;
+    p.rows = rows;
   }
 }
 
-// ----------------------------------------------------------------------------- shared state of a CTA
+// Block 0: the plan.  Warps of the others: one block of parts each, chunk j of token t at j T + t.
+template <bool F8>
+__global__ void __launch_bounds__(kMoeFlat) moe_prep_kernel(const __grid_constant__ MoeArgs a) {
+  using P = Parts<F8>;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (blockIdx.x == 0) {
+    make_plan(*a.plan, a);
+    return;
+  }
+  const int lane = threadIdx.x & 31, i = (blockIdx.x - 1) * (kMoeFlat / 32) + threadIdx.x / 32;
+  const int j = i / a.T, t = i - j * a.T, k = j * P::kChunk + lane * P::kVals;
+  if (j * P::kChunk >= a.H) return;
+  float x[P::kVals];
+#pragma unroll
+  for (int v = 0; v < P::kVals; ++v) x[v] = 0.f;
+  if (k < a.H) load_vals(x, a.y + static_cast<size_t>(t) * a.H + k);
+  put_parts(a.xb + static_cast<size_t>(i) * kMoeBlock, lane, x);
+}
 
+// The inner vectors: one warp per row and chunk adds a cut tile's parts and splits w silu(g) u.
+// Blocks lie in the order that the down launch reads them: expert, chunk, token.
+template <bool F8>
+__global__ void __launch_bounds__(kMoeFlat) moe_act_kernel(const __grid_constant__ MoeArgs a) {
+  using P = Parts<F8>;
+  pdl_launch_dependents();  // the next launch reads nothing of this one's before its own wait
+  pdl_wait();
+  const Plan& p = *a.plan;
+  const int lane = threadIdx.x & 31, id = blockIdx.x * (kMoeFlat / 32) + threadIdx.x / 32;
+  const int kch = (a.I + P::kChunk - 1) / P::kChunk, row = id / kch, j = id - row * kch;
+  if (row >= p.rows) return;
+  const Runs r(p.active, a, P::kChunk);
+  const int act = p.act[row], rank = row - p.first[act];
+  const int i = j * P::kChunk + lane * P::kVals;
+  float x[P::kVals];
+#pragma unroll
+  for (int v = 0; v < P::kVals; ++v) x[v] = 0.f;
+  if (i < a.I) {
+    const long long pos = (static_cast<long long>(act) * r.units + i / kMoeUnit) * r.kch;
+    const int c0 = r.owner(pos), c1 = r.owner(pos + r.kch - 1);
+    float g[P::kVals], u[P::kVals];
+    load_vals(g, a.main + static_cast<size_t>(row) * 2 * a.I + i);
+    load_vals(u, a.main + (static_cast<size_t>(row) * 2 + 1) * a.I + i);
+    for (int c = c0 + 1; c <= c1; ++c) {
+      const float* src = a.cut + (static_cast<size_t>(c) * kMoeMaxTokens + rank) * (2 * kMoeUnit) + (i & (kMoeUnit - 1));
+      float dg[P::kVals], du[P::kVals];
+      load_vals(dg, src);
+      load_vals(du, src + kMoeUnit);
+#pragma unroll
+      for (int v = 0; v < P::kVals; ++v) {
+        g[v] += dg[v];
+        u[v] += du[v];
+      }
+    }
+    const float w = p.gate[row];
+#pragma unroll
+    for (int v = 0; v < P::kVals; ++v) x[v] = g[v] / (1.f + expf(-g[v])) * u[v] * w;
+  }
+  put_parts(a.hb + (static_cast<size_t>(p.first[act]) * kch + static_cast<size_t>(j) * p.count[act] + rank) * kMoeBlock, lane,
+            x);
+}
+
+// ----------------------------------------------------------------------------- a CTA of the two streaming launches
+
+// NT: the most tokens of a call, 2, 8 or 16.
 template <bool F8, int NT>
 struct Cta {
-  using S = Shape<F8, NT>;
+  using P = Parts<F8>;
   uint64_t *fullA, *emptyA, *fullB, *emptyB, *accum, *drained;
   uint32_t* tmem_slot;
-  volatile int* stop;
-  float (*scales)[kMoeMaxTokens];  // [kScaleSlots] s of every token of a chunk
+  volatile int* stop;  // a wait ran out: every role ends
   Plan* plan;
+  float* total;        // [NT][128] sums of the down launch
   unsigned char *A, *B;
-  int stages;
+  uint32_t tmem;
 
-  static constexpr uint32_t kHead = 1024, kPlan = (sizeof(Plan) + 1023) / 1024 * 1024;
-  static constexpr int kStages = static_cast<int>((kMoeSmemMax - 1024 - kHead - kPlan - S::kBStages * S::kBTile) / kMoeATile) <
-                                         kMoeMaxStages
-                                     ? static_cast<int>((kMoeSmemMax - 1024 - kHead - kPlan - S::kBStages * S::kBTile) /
-                                                        kMoeATile)
-                                     : kMoeMaxStages;
-  static constexpr uint32_t kSmem = 1024 + kHead + kPlan + S::kBStages * S::kBTile + kStages * kMoeATile;
-  static constexpr uint32_t kCols = tmem_columns(2 * S::kN);
+  static constexpr uint32_t kHead = 1024, kPlan = kMoePlanBytes, kTotal = NT * 512, kBTile = NT * kMoeBlock;
+  // up to 8 tokens two CTAs fit an SM, of one launch or of gate/up and down
+  static constexpr uint32_t kMax = NT <= 8 ? 112 * 1024 : 224 * 1024;
+  static constexpr int kFit = static_cast<int>((kMax - 1024 - kHead - kPlan - kTotal - kMoeBStages * kBTile) / kMoeATile);
+  static constexpr int kStages = kFit < kMoeMaxStages ? kFit : kMoeMaxStages;
+  static constexpr uint32_t kSmem = 1024 + kHead + kPlan + kTotal + kMoeBStages * kBTile + kStages * kMoeATile;
+  static constexpr uint32_t kAcc = 8 * NT;                  // columns of an accumulator
+  static constexpr uint32_t kCols = tmem_columns(2 * kAcc);
+  static constexpr int kGroup = NT < 4 ? NT : 4;            // tokens whose sums are loaded together
 
+  // All threads.
   __device__ __forceinline__ explicit Cta(unsigned char* raw) {
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     fullA = reinterpret_cast<uint64_t*>(smem);
     emptyA = fullA + kMoeMaxStages;
     fullB = emptyA + kMoeMaxStages;
-    emptyB = fullB + S::kBStages;
-    accum = emptyB + S::kBStages;
+    emptyB = fullB + kMoeBStages;
+    accum = emptyB + kMoeBStages;
     drained = accum + 2;
     tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
     stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    scales = reinterpret_cast<float(*)[kMoeMaxTokens]>(smem + 512);
-    static_assert((2 * kMoeMaxStages + 2 * S::kBStages + 4) * 8 + 8 <= 512, "barriers");
-    static_assert(512 + S::kScaleSlots * kMoeMaxTokens * 4 <= kHead, "scales");
-    plan = reinterpret_cast<Plan*>(smem + kHead);
-    A = smem + kHead + kPlan;
+    static_assert((2 * kMoeMaxStages + 2 * kMoeBStages + 4) * 8 + 8 <= kHead, "barriers");
+    A = smem + kHead;
     B = A + kStages * kMoeATile;
-  }
-  // All threads; returns the accumulators' address.
-  __device__ __forceinline__ uint32_t begin() {
+    plan = reinterpret_cast<Plan*>(B + kMoeBStages * kBTile);
+    total = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(plan) + kPlan);
     if (threadIdx.x == 0) {
       for (int s = 0; s < kStages; ++s) {
         mbar_init(&fullA[s], 1);
         mbar_init(&emptyA[s], 1);
       }
-      for (int s = 0; s < S::kBStages; ++s) {
+      for (int s = 0; s < kMoeBStages; ++s) {
         mbar_init(&fullB[s], 1);
-        mbar_init(&emptyB[s], 1);
+        mbar_init(&emptyB[s], 4);
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(&accum[s], 1);
@@ -316,9 +375,16 @@ struct Cta {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    return *tmem_slot;
+    tmem = *tmem_slot;
   }
-  __device__ __forceinline__ void end(uint32_t tmem) {
+  // All threads.
+  __device__ __forceinline__ void take_plan(const Plan* from) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(from);
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(Plan) / 4); i += kMoeThreads)
+      reinterpret_cast<uint32_t*>(plan)[i] = src[i];
+    __syncthreads();
+  }
+  __device__ __forceinline__ void end() {
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -333,31 +399,94 @@ struct Cta {
     if (threadIdx.x % 32 == 0) ok = (mbar_wait(bar, parity, stop, err, code) && !*stop) ? 1 : 0;
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
   }
-  // One lane: the copies of the last stages have landed (an early end must not leave them in flight).
-  __device__ __forceinline__ void drain(int issued, uint32_t* err) const {
-    for (int i = max(0, issued - kStages); i < issued; ++i)
-      if (!tc_wait(&fullA[i % kStages], (i / kStages) & 1, err, kErrDrain)) break;
+  // One lane: a free stage of the weights' ring for chunk `it`, null when a wait ran out.
+  __device__ __forceinline__ unsigned char* claim(int it, uint32_t* err) const {
+    const int s = it % kStages;
+    if (it >= kStages && !mbar_wait(&emptyA[s], ((it / kStages) - 1) & 1, stop, err, kErrWaitEmpty)) *stop = 1;
+    if (*stop) {  // an early end waits for the copies that are on their way
+      for (int i = max(0, it - kStages); i < it; ++i)
+        if (!tc_wait(&fullA[i % kStages], (i / kStages) & 1, err, kErrDrain)) break;
+      return nullptr;
+    }
+    mbar_arrive_expect_tx(&fullA[s], kMoeATile);
+    return A + s * kMoeATile;
   }
-  // One lane: the MMAs of chunk `it` into the accumulator at `d`; false when a wait ran out.
-  __device__ __forceinline__ bool multiply(int it, uint32_t d, bool fresh, uint32_t* err) const {
-    const int s = it % kStages, b = it % S::kBStages;
-    if (!mbar_wait(&fullA[s], (it / kStages) & 1, stop, err, kErrWaitFull) ||
-        !mbar_wait(&fullB[b], (it / S::kBStages) & 1, stop, err, kErrWaitFull) || *stop)
+  // Whole warp: chunk `it`'s blocks, lane r's from `src` (n lanes); false when a wait ran out.
+  __device__ __forceinline__ bool bring(int it, int n, const unsigned char* src, uint64_t pol, uint32_t* err) const {
+    const int b = it % kMoeBStages, lane = threadIdx.x & 31;
+    if (it >= kMoeBStages && !warp_wait(&emptyB[b], ((it / kMoeBStages) - 1) & 1, err, kErrWaitEmpty)) {
+      *stop = 1;
+      if (lane == 0)
+        for (int i = max(0, it - kMoeBStages); i < it; ++i)
+          if (!tc_wait(&fullB[i % kMoeBStages], (i / kMoeBStages) & 1, err, kErrDrain)) break;
       return false;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(&fullB[b], n * P::kCopy);
+    __syncwarp();
+    if (lane < n) bulk_copy_g2s(B + b * kBTile + lane * kMoeBlock, src, P::kCopy, &fullB[b], pol);
+    return true;
+  }
+  // One lane: the MMAs of chunk `it` with n tokens; false when a wait ran out.
+  __device__ __forceinline__ bool multiply(int it, int n, uint32_t* err) const {
+    const int s = it % kStages, b = it % kMoeBStages;
+    if (!mbar_wait(&fullA[s], (it / kStages) & 1, stop, err, kErrWaitFull) ||
+        !mbar_wait(&fullB[b], (it / kMoeBStages) & 1, stop, err, kErrWaitFull) ||
+        (it >= 2 && !mbar_wait(&drained[it & 1], ((it >> 1) - 1) & 1, stop, err, kErrWaitFull)) || *stop) {
+      *stop = 1;
+      return false;
+    }
     tc_fence_after();
-    const uint32_t sa = smem_addr(A + s * kMoeATile), sb = smem_addr(B + b * S::kBTile);
-    constexpr uint32_t idesc = tc_idesc_of(S::kN, !F8);
+    const uint32_t sa = smem_addr(A + s * kMoeATile), sb = smem_addr(B + b * kBTile), d = tmem + (it & 1) * kAcc;
+    const uint32_t idesc = tc_idesc_of(8 * ((n + 1) & ~1), !F8);  // columns of a missing last token hold anything
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of K per instruction
       const uint64_t ad = smem_desc_sw128(sa + kk * 32), bd = smem_desc_sw128(sb + kk * 32);
-      const uint32_t more = !fresh || kk > 0;
       if (F8)
-        tc_mma_f8(d, ad, bd, idesc, more);
+        tc_mma_f8(d, ad, bd, idesc, kk > 0);
       else
-        tc_mma(d, ad, bd, idesc, more);
+        tc_mma(d, ad, bd, idesc, kk > 0);
     }
     tc_commit(&emptyA[s]);
-    tc_commit(&emptyB[b]);
+    tc_commit(&accum[it & 1]);
+    return true;
+  }
+  // Whole warp: adds chunk `it`'s sums of n tokens, weights' scale w (1 for bf16); false when a wait ran out.
+  __device__ __forceinline__ bool add(int it, int n, float w, float (&sum)[NT], uint32_t* err) const {
+    if (!warp_wait(&accum[it & 1], (it >> 1) & 1, err, kErrWaitFull)) {
+      *stop = 1;
+      return false;
+    }
+    tc_fence_after();
+    const uint32_t at = tmem + (static_cast<uint32_t>(threadIdx.x & 96) << 16) + (it & 1) * kAcc;
+    const unsigned char* blocks = B + (it % kMoeBStages) * kBTile;
+#pragma unroll
+    for (int t0 = 0; t0 < NT; t0 += kGroup) {
+      if (t0 >= n) break;
+      uint32_t v[kGroup / 2][16];
+#pragma unroll
+      for (int h = 0; h < kGroup / 2; ++h) tmem_ld_issue(at + 8 * (t0 + 2 * h), v[h]);
+#pragma unroll
+      for (int h = 0; h < kGroup / 2; ++h) tmem_ld_wait(v[h]);
+#pragma unroll
+      for (int t = 0; t < kGroup; ++t) {
+        float x = 0.f;  // the smallest part first
+#pragma unroll
+        for (int p = P::kParts - 1; p >= 0; --p) {
+          const float part = __uint_as_float(v[t / 2][8 * (t & 1) + p]);
+          x = F8 ? fmaf(x, 0.03125f, part) : x + part;
+        }
+        if (F8)
+          sum[t0 + t] = fmaf(x, w * *reinterpret_cast<const float*>(blocks + (t0 + t) * kMoeBlock + P::kScaleAt), sum[t0 + t]);
+        else
+          sum[t0 + t] += x;
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) {
+      mbar_arrive(&drained[it & 1]);
+      mbar_arrive(&emptyB[it % kMoeBStages]);
+    }
     return true;
   }
 };
@@ -365,320 +494,183 @@ struct Cta {
 // ----------------------------------------------------------------------------- gate/up
 
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kMoeThreads, 1) moe_gate_up_kernel(const __grid_constant__ MoeArgs a) {
-  using S = Shape<F8, NT>;
+__global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_gate_up_kernel(const __grid_constant__ MoeArgs a) {
+  using P = Parts<F8>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Cta<F8, NT> c(smem_raw);
-  const uint32_t tmem = c.begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
+  c.take_plan(a.plan);
   const Plan& p = *c.plan;
-  make_plan(*c.plan, a, false);
-  const Runs r(p, a, S::kChunk);
+  const Runs r(p.active, a, P::kChunk);
   const int lo = r.begin(blockIdx.x), hi = r.begin(blockIdx.x + 1);
 
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_first();
       int it = 0;
-      for (int pos = lo; pos < hi && !*c.stop;) {
+      bool ok = true;
+      for (int pos = lo; pos < hi && ok;) {
         const int tile = pos / r.kch, j0 = pos - tile * r.kch, n = min(r.kch - j0, hi - pos);
         const int row = (tile % r.units) * kMoeUnit, e = p.expert[tile / r.units];
         for (int j = j0; j < j0 + n; ++j, ++it) {
-          const int s = it % c.kStages;
-          if (it >= c.kStages && !mbar_wait(&c.emptyA[s], ((it / c.kStages) - 1) & 1, c.stop, a.err, kErrWaitEmpty))
-            *c.stop = 1;
-          if (*c.stop) break;
-          mbar_arrive_expect_tx(&c.fullA[s], kMoeATile);
-          tma_load_3d(c.A + s * kMoeATile, &a.g, j * S::kChunk, row, e, &c.fullA[s], pol);
-          tma_load_3d(c.A + s * kMoeATile + kMoeATile / 2, &a.u, j * S::kChunk, row, e, &c.fullA[s], pol);
+          unsigned char* to = c.claim(it, a.err);
+          ok = to != nullptr;
+          if (!ok) break;
+          uint64_t* bar = &c.fullA[it % c.kStages];
+          tma_load_3d(to, &a.g, j * P::kChunk, row, e, bar, pol);
+          tma_load_3d(to + kMoeATile / 2, &a.u, j * P::kChunk, row, e, bar, pol);
         }
         pos += n;
       }
-      if (*c.stop) c.drain(it, a.err);
+    }
+  } else if (warp == 6) {
+    const uint64_t pol = l2_policy_evict_last();
+    int it = 0;
+    bool ok = true;
+    for (int pos = lo; pos < hi && ok;) {
+      const int tile = pos / r.kch, j0 = pos - tile * r.kch, n = min(r.kch - j0, hi - pos);
+      const int act = tile / r.units, count = p.count[act], t = lane < count ? p.token[p.first[act] + lane] : 0;
+      for (int j = j0; j < j0 + n && ok; ++j, ++it)
+        ok = c.bring(it, count, a.xb + (static_cast<size_t>(j) * a.T + t) * kMoeBlock, pol, a.err);
+      pos += n;
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      int it = 0, seg = 0;
-      for (int pos = lo; pos < hi && !*c.stop; ++seg) {
-        const int j0 = pos % r.kch, n = min(r.kch - j0, hi - pos);
-        for (int j = 0; j < n; ++j, ++it) {
-          // e4m3: an accumulator per chunk; bf16: per tile
-          const int b = (F8 ? it : seg) & 1, turn = (F8 ? it : seg) >> 1;
-          if ((F8 || j == 0) && turn > 0 &&
-              !mbar_wait(&c.drained[b], (turn - 1) & 1, c.stop, a.err, kErrWaitFull))
-            *c.stop = 1;
-          if (*c.stop || !c.multiply(it, tmem + b * S::kN, F8 || j == 0, a.err)) {
-            *c.stop = 1;
-            break;
-          }
-          if (F8 || j + 1 == n) tc_commit(&c.accum[b]);
-        }
+      int it = 0;
+      bool ok = true;
+      for (int pos = lo; pos < hi && ok;) {
+        const int tile = pos / r.kch, n = min((tile + 1) * r.kch, hi) - pos, count = p.count[tile / r.units];
+        for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, a.err);
         pos += n;
       }
     }
-  } else if (warp < 6) {
-    const int q = warp & 3, m = 32 * q + lane;  // TMEM lanes; row of the tile: gate below 64, up from 64 on
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16);
+  } else {
+    const int m = (32 * warp + lane) & 127;  // TMEM lane; row of the tile: gate below 64, up from 64 on
     const int IB = (a.I + kFp8Block - 1) / kFp8Block;
-    int it = 0, seg = 0;
+    int it = 0;
     bool ok = true;
-    for (int pos = lo; pos < hi && ok; ++seg) {
+    for (int pos = lo; pos < hi && ok;) {
       const int tile = pos / r.kch, j0 = pos - tile * r.kch, n = min(r.kch - j0, hi - pos);
-      const int act = tile / r.units, ub = tile - act * r.units;
-      const uint32_t tokens = p.tokens[act];
+      const int act = tile / r.units, ub = tile - act * r.units, count = p.count[act];
       float sum[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) sum[t] = 0.f;
+      const float* sw = nullptr;
+      float next = 1.f;
       if (F8) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) sum[t] = 0.f;
-        const float* sw = (m < kMoeUnit ? a.sg : a.su) +
-                          (static_cast<size_t>(p.expert[act]) * IB + ub * kMoeUnit / kFp8Block) * r.kch;
-        float next = __ldg(sw + j0);
-        for (int j = j0; j < j0 + n; ++j, ++it) {
-          const float w = next;
-          if (j + 1 < j0 + n) next = __ldg(sw + j + 1);
-          ok = c.warp_wait(&c.accum[it & 1], (it >> 1) & 1, a.err, kErrWaitFull);
-          if (!ok) break;
-          tc_fence_after();
-          float part[NT];
-          take_sums<F8, NT>(at + (it & 1) * S::kN, part);
-          const float* sx = c.scales[it % S::kScaleSlots];
-#pragma unroll
-          for (int t = 0; t < NT; ++t) sum[t] = fmaf(part[t], w * sx[t], sum[t]);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&c.drained[it & 1]);
-        }
-      } else {
-        ok = c.warp_wait(&c.accum[seg & 1], (seg >> 1) & 1, a.err, kErrWaitFull);
-        if (ok) {
-          tc_fence_after();
-          take_sums<F8, NT>(at + (seg & 1) * S::kN, sum);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&c.drained[seg & 1]);
-        }
+        sw = (m < kMoeUnit ? a.sg : a.su) + (static_cast<size_t>(p.expert[act]) * IB + ub * kMoeUnit / kFp8Block) * r.kch;
+        next = __ldg(sw + j0);
+      }
+      for (int j = j0; j < j0 + n && ok; ++j, ++it) {
+        const float w = next;
+        if (F8 && j + 1 < j0 + n) next = __ldg(sw + j + 1);
+        ok = c.add(it, count, w, sum, a.err);
       }
       if (!ok) break;
       const int i = ub * kMoeUnit + (m & (kMoeUnit - 1));
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if (!((tokens >> t) & 1u)) continue;
-        if (j0 > 0) {
+        if (t >= count) break;
+        if (j0 > 0)
           a.cut[(static_cast<size_t>(blockIdx.x) * kMoeMaxTokens + t) * (2 * kMoeUnit) + m] = sum[t];
-        } else if (i < a.I) {
-          const int row = p.first[act] + __popc(tokens & ((1u << t) - 1));
-          a.main[(static_cast<size_t>(row) * 2 + (m >= kMoeUnit)) * a.I + i] = sum[t];
-        }
+        else if (i < a.I)
+          a.main[(static_cast<size_t>(p.first[act] + t) * 2 + (m >= kMoeUnit)) * a.I + i] = sum[t];
       }
       pos += n;
     }
-    if (!ok) *c.stop = 1;
-  } else {
-    const int mine = warp - 6;
-    int it = mine;
-    for (int pos = lo + mine; pos < hi; pos += kMoeSplitWarps, it += kMoeSplitWarps) {
-      const int tile = pos / r.kch, j = pos - tile * r.kch;
-      const uint32_t tokens = p.tokens[tile / r.units];
-      const int k = j * S::kChunk + lane * S::kVals;
-      float x[NT][S::kVals];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int v = 0; v < S::kVals; ++v) x[t][v] = 0.f;
-        if (((tokens >> t) & 1u) && k < a.H) {
-          const float* src = a.y + static_cast<size_t>(t) * a.H + k;
-          if constexpr (F8) {
-            const float4 f = __ldg(reinterpret_cast<const float4*>(src));
-            x[t][0] = f.x, x[t][1] = f.y, x[t][2] = f.z, x[t][3] = f.w;
-          } else {
-            const float2 f = __ldg(reinterpret_cast<const float2*>(src));
-            x[t][0] = f.x, x[t][1] = f.y;
-          }
-        }
-      }
-      const int b = it % S::kBStages;
-      if (it >= S::kBStages && !c.warp_wait(&c.emptyB[b], ((it / S::kBStages) - 1) & 1, a.err, kErrWaitEmpty)) break;
-      unsigned char* tileB = c.B + b * S::kBTile;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (!((tokens >> t) & 1u)) continue;
-        if constexpr (F8) {
-          const float s = put_parts<NT>(tileB, t, lane, x[t]);
-          if (lane == 0) c.scales[it % S::kScaleSlots][t] = s;
-        } else {
-          put_parts<NT>(tileB, t, lane, x[t]);
-        }
-      }
-      fence_to_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.fullB[b]);
-    }
   }
-  c.end(tmem);
+  c.end();
 }
 
 // ----------------------------------------------------------------------------- down
 
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kMoeThreads, 1) moe_down_kernel(const __grid_constant__ MoeArgs a) {
-  using S = Shape<F8, NT>;
+__global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_down_kernel(const __grid_constant__ MoeArgs a) {
+  using P = Parts<F8>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Cta<F8, NT> c(smem_raw);
-  const uint32_t tmem = c.begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % a.splits, m0 = (blockIdx.x / a.splits) * 128;
+  // the plan was complete before gate/up could begin, and that began before this launch could
+  c.take_plan(a.plan);
   const Plan& p = *c.plan;
-  // ids and gates were complete before gate/up could begin
-  make_plan(*c.plan, a, true);
-  const Runs r(p, a, S::kChunk);
-  const int kch = (a.I + S::kChunk - 1) / S::kChunk, all = p.active * kch;
+  const int kch = (a.I + P::kChunk - 1) / P::kChunk, all = p.active * kch;
   const int lo = static_cast<int>(static_cast<long long>(split) * all / a.splits);
-  const int n = static_cast<int>(static_cast<long long>(split + 1) * all / a.splits) - lo;
-  float* part = reinterpret_cast<float*>(c.A);  // [NT][128] this CTA's sums, once the ring is done
+  const int hi = static_cast<int>(static_cast<long long>(split + 1) * all / a.splits);
 
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_first();
-      int it = 0;
-      for (; it < n; ++it) {
-        const int s = it % c.kStages, act = (lo + it) / kch, j = lo + it - act * kch;
-        if (it >= c.kStages && !mbar_wait(&c.emptyA[s], ((it / c.kStages) - 1) & 1, c.stop, a.err, kErrWaitEmpty)) *c.stop = 1;
-        if (*c.stop) break;
-        mbar_arrive_expect_tx(&c.fullA[s], kMoeATile);
-        tma_load_3d(c.A + s * kMoeATile, &a.d, j * S::kChunk, m0, p.expert[act], &c.fullA[s], pol);
+      int act = lo / kch, j = lo - act * kch;
+      for (int it = 0; it < hi - lo; ++it) {
+        unsigned char* to = c.claim(it, a.err);
+        if (!to) break;
+        tma_load_3d(to, &a.d, j * P::kChunk, m0, p.expert[act], &c.fullA[it % c.kStages], pol);
+        if (++j == kch) {
+          j = 0;
+          ++act;
+        }
       }
-      if (*c.stop) c.drain(it, a.err);
+    }
+  } else if (warp == 6) {
+    pdl_wait();  // the inner vectors
+    const uint64_t pol = l2_policy_evict_last();
+    int it = 0;
+    bool ok = true;
+    for (int pos = lo; pos < hi && ok;) {
+      const int act = pos / kch, j0 = pos - act * kch, n = min(kch - j0, hi - pos), count = p.count[act];
+      const unsigned char* src = a.hb + (static_cast<size_t>(p.first[act]) * kch + static_cast<size_t>(j0) * count + lane) * kMoeBlock;
+      for (int j = 0; j < n && ok; ++j, ++it, src += count * kMoeBlock) ok = c.bring(it, count, src, pol, a.err);
+      pos += n;
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      for (int it = 0; it < n; ++it) {
-        const int b = F8 ? it & 1 : 0;
-        if (F8 && it >= 2 && !mbar_wait(&c.drained[b], ((it >> 1) - 1) & 1, c.stop, a.err, kErrWaitFull)) *c.stop = 1;
-        if (*c.stop || !c.multiply(it, tmem + b * S::kN, F8 || it == 0, a.err)) {
-          *c.stop = 1;
-          break;
-        }
-        if (F8 || it + 1 == n) tc_commit(&c.accum[b]);
+      int it = 0;
+      bool ok = true;
+      for (int pos = lo; pos < hi && ok;) {
+        const int act = pos / kch, n = min((act + 1) * kch, hi) - pos, count = p.count[act];
+        for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, a.err);
+        pos += n;
       }
-    }
-  } else if (warp < 6) {
-    const int q = warp & 3;
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    float sum[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) sum[t] = 0.f;
-    bool ok = true;
-    if (F8) {
-      const int HB = (a.H + kFp8Block - 1) / kFp8Block;
-      auto scale = [&](int it) {
-        const int act = (lo + it) / kch, j = lo + it - act * kch;
-        return __ldg(a.sd + (static_cast<size_t>(p.expert[act]) * HB + m0 / kFp8Block) * kch + j);
-      };
-      float next = n > 0 ? scale(0) : 0.f;
-      for (int it = 0; it < n && ok; ++it) {
-        const float w = next;
-        if (it + 1 < n) next = scale(it + 1);
-        ok = c.warp_wait(&c.accum[it & 1], (it >> 1) & 1, a.err, kErrWaitFull);
-        if (!ok) break;
-        tc_fence_after();
-        float v[NT];
-        take_sums<F8, NT>(at + (it & 1) * S::kN, v);
-        const float* sx = c.scales[it % S::kScaleSlots];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) sum[t] = fmaf(v[t], w * sx[t], sum[t]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.drained[it & 1]);
-      }
-    } else if (n > 0) {
-      ok = c.warp_wait(&c.accum[0], 0, a.err, kErrWaitFull);
-      tc_fence_after();
-      if (ok) take_sums<F8, NT>(at, sum);
-    }
-    if (!ok) *c.stop = 1;
-    // every product of this CTA is done, so the ring's memory is free
-    if (ok) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) part[t * 128 + 32 * q + lane] = sum[t];
     }
   } else {
-    pdl_wait();  // gate and up products
-    const int mine = warp - 6;
-    for (int it = mine; it < n; it += kMoeSplitWarps) {
-      const int act = (lo + it) / kch, j = lo + it - act * kch;
-      const uint32_t tokens = p.tokens[act];
-      const int i = j * S::kChunk + lane * S::kVals, ub = i / kMoeUnit;
-      const bool inside = i < a.I;
-      int c0 = 0, c1 = 0;  // the CTAs that hold parts of this lane's tile
-      if (inside) {
-        const long long pos = (static_cast<long long>(act) * r.units + ub) * r.kch;
-        c0 = r.owner(pos);
-        c1 = r.owner(pos + r.kch - 1);
+    const int m = (32 * warp + lane) & 127, HB = (a.H + kFp8Block - 1) / kFp8Block;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) c.total[t * 128 + m] = 0.f;
+    int it = 0;
+    bool ok = true;
+    for (int pos = lo; pos < hi && ok;) {
+      const int act = pos / kch, j0 = pos - act * kch, n = min(kch - j0, hi - pos), count = p.count[act];
+      float sum[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) sum[t] = 0.f;
+      const float* sw = nullptr;
+      float next = 1.f;
+      if (F8) {
+        sw = a.sd + (static_cast<size_t>(p.expert[act]) * HB + m0 / kFp8Block) * kch;
+        next = __ldg(sw + j0);
       }
-      float x[NT][S::kVals];
-      int row = p.first[act];
+      for (int j = j0; j < j0 + n && ok; ++j, ++it) {
+        const float w = next;
+        if (F8 && j + 1 < j0 + n) next = __ldg(sw + j + 1);
+        ok = c.add(it, count, w, sum, a.err);
+      }
+      // this thread's column of its tokens' sums
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int v = 0; v < S::kVals; ++v) x[t][v] = 0.f;
-        if (!((tokens >> t) & 1u)) continue;
-        if (inside) {
-          float g[S::kVals], u[S::kVals];
-          auto load = [](float(&d)[S::kVals], const float* src) {
-            if constexpr (F8) {
-              const float4 f = *reinterpret_cast<const float4*>(src);
-              d[0] = f.x, d[1] = f.y, d[2] = f.z, d[3] = f.w;
-            } else {
-              const float2 f = *reinterpret_cast<const float2*>(src);
-              d[0] = f.x, d[1] = f.y;
-            }
-          };
-          load(g, a.main + static_cast<size_t>(row) * 2 * a.I + i);
-          load(u, a.main + (static_cast<size_t>(row) * 2 + 1) * a.I + i);
-          for (int cc = c0 + 1; cc <= c1; ++cc) {
-            const float* src = a.cut + (static_cast<size_t>(cc) * kMoeMaxTokens + t) * (2 * kMoeUnit) + (i & (kMoeUnit - 1));
-            float dg[S::kVals], du[S::kVals];
-            load(dg, src);
-            load(du, src + kMoeUnit);
-#pragma unroll
-            for (int v = 0; v < S::kVals; ++v) {
-              g[v] += dg[v];
-              u[v] += du[v];
-            }
-          }
-          const float w = p.gate[row];
-#pragma unroll
-          for (int v = 0; v < S::kVals; ++v) x[t][v] = g[v] / (1.f + expf(-g[v])) * u[v] * w;
-        }
-        ++row;
+        if (t >= count) break;
+        c.total[p.token[p.first[act] + t] * 128 + m] += sum[t];
       }
-      const int b = it % S::kBStages;
-      if (it >= S::kBStages && !c.warp_wait(&c.emptyB[b], ((it / S::kBStages) - 1) & 1, a.err, kErrWaitEmpty)) break;
-      unsigned char* tileB = c.B + b * S::kBTile;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (!((tokens >> t) & 1u)) {  // a token that did not choose the expert
-          put_zeros<NT, S::kParts>(tileB, t, lane);
-          if (F8 && lane == 0) c.scales[it % S::kScaleSlots][t] = 0.f;
-        } else if constexpr (F8) {
-          const float s = put_parts<NT>(tileB, t, lane, x[t]);
-          if (lane == 0) c.scales[it % S::kScaleSlots][t] = s;
-        } else {
-          put_parts<NT>(tileB, t, lane, x[t]);
-        }
-      }
-      fence_to_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.fullB[b]);
+      pos += n;
     }
   }
   __syncwarp();
   pdl_wait();  // the result may be what an earlier kernel reads or writes
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   {
-    const uint32_t local = smem_addr(part);
+    const uint32_t local = smem_addr(c.total);
     const int total = a.T * 128, per = (total + a.splits - 1) / a.splits, end = min(total, (split + 1) * per);
     for (int o = split * per + static_cast<int>(threadIdx.x); o < end; o += kMoeThreads) {
       const int t = o >> 7, m = m0 + (o & 127);
@@ -702,7 +694,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_down_kernel(const __grid_c
   __syncwarp();
   // no CTA leaves while others may still read its shared memory
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  c.end(tmem);
+  c.end();
 }
 
 // ----------------------------------------------------------------------------- host side
@@ -736,12 +728,19 @@ int down_clusters(int size) {
 
 template <bool F8, int NT>
 cudaError_t run_experts(MoeArgs& a, cudaStream_t st) {
-  cudaError_t e = launch(moe_gate_up_kernel<F8, NT>, dim3(a.ctas), dim3(kMoeThreads), Cta<F8, NT>::kSmem, st, true, a);
+  using P = Parts<F8>;
+  constexpr int kWarps = kMoeFlat / 32;
+  const int blocks = a.T * ((a.H + P::kChunk - 1) / P::kChunk), rows = a.T * a.k * ((a.I + P::kChunk - 1) / P::kChunk);
+  cudaError_t e = launch(moe_prep_kernel<F8>, dim3(1 + (blocks + kWarps - 1) / kWarps), dim3(kMoeFlat), 0, st, true, a);
   if (e != cudaSuccess) return e;
-  // K splits of a tile of the down product: as many as run at once
+  e = launch(moe_gate_up_kernel<F8, NT>, dim3(a.ctas), dim3(kMoeThreads), Cta<F8, NT>::kSmem, st, true, a);
+  if (e != cudaSuccess) return e;
+  e = launch(moe_act_kernel<F8>, dim3((rows + kWarps - 1) / kWarps), dim3(kMoeFlat), 0, st, true, a);
+  if (e != cudaSuccess) return e;
+  // K splits of a tile of the down product: the most with which all clusters run at once
   const int tiles = (a.H + 127) / 128;
-  a.splits = 1;
-  while (a.splits * 2 <= kMoeMaxSplits && down_clusters<F8, NT>(a.splits * 2) >= tiles) a.splits *= 2;
+  a.splits = kMoeMaxSplits;
+  while (a.splits > 1 && down_clusters<F8, NT>(a.splits) < tiles) --a.splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * a.splits);
   cfg.blockDim = dim3(kMoeThreads);
@@ -761,7 +760,9 @@ cudaError_t run_experts(MoeArgs& a, cudaStream_t st) {
 
 template <bool F8, int NT>
 cudaError_t allow_one() {
-  cudaError_t e = allow_smem(moe_gate_up_kernel<F8, NT>);
+  cudaError_t e = prefer_max_carveout(moe_prep_kernel<F8>);
+  if (e == cudaSuccess) e = prefer_max_carveout(moe_act_kernel<F8>);
+  if (e == cudaSuccess) e = allow_smem(moe_gate_up_kernel<F8, NT>);
   return e != cudaSuccess ? e : allow_smem(moe_down_kernel<F8, NT>);
 }
 
@@ -787,8 +788,12 @@ int moe_experts(const MoeCall& c, int sms, cudaStream_t st, const char** why) {
   a.sd = c.sd;
   a.residual = c.residual;
   a.out = c.out;
-  a.main = c.ws;
-  a.cut = c.ws + ((moe_main_floats(c.T, c.k, c.I) + 63) & ~size_t(63));
+  const MoeWorkspace w = moe_workspace(c.T, c.k, c.H, c.I);
+  a.plan = reinterpret_cast<Plan*>(c.ws);
+  a.main = reinterpret_cast<float*>(c.ws + w.main);
+  a.cut = reinterpret_cast<float*>(c.ws + w.cut);
+  a.xb = c.ws + w.xb;
+  a.hb = c.ws + w.hb;
   a.T = c.T;
   a.k = c.k;
   a.E = c.E;

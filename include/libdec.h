@@ -392,7 +392,7 @@ int dec_moe_route(const float* y, const void* Wr, const float* bias, int sigmoid
                   int32_t* ids, float* weights, int T, int H, int E, int k, void* stream);
 
 /* Workspace bytes of dec_moe_experts (0: sizes refused). */
-size_t dec_moe_workspace_size(int T, int k, int I);
+size_t dec_moe_workspace_size(int T, int k, int H, int I);
 
 /*
  * The chosen experts' gated MLPs, added up:

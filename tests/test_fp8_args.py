@@ -92,7 +92,7 @@ def test_particular_arguments_of_the_layer(gd):
     refused(gd, "dec_moe_experts", EXPERTS, gd.DEC_EUNSUPPORTED, "multiples of 16", **held, I=72)
     for s in held:
         refused(gd, "dec_moe_experts", EXPERTS, gd.DEC_EINVAL, s, **{**held, s: None})
-    refused(gd, "dec_moe_experts", EXPERTS, gd.DEC_EINVAL, "needs", ws_bytes=gd.moe_workspace_size(4, 2, 64) - 1)
+    refused(gd, "dec_moe_experts", EXPERTS, gd.DEC_EINVAL, "needs", ws_bytes=gd.moe_workspace_size(4, 2, 256, 64) - 1)
     refused(gd, "dec_moe_experts", EXPERTS, gd.DEC_EINVAL, "256-byte", ws=P + 128)
 
 
@@ -103,8 +103,9 @@ def test_calls_without_work_need_no_gpu(gd):
         assert getattr(gd.lib(), name)(*{**good, **change}.values()) == gd.DEC_OK
 
 
-@pytest.mark.parametrize("sizes,word", [((-1, 2, 64), "T must"), ((17, 2, 64), "at most 16"), ((4, 0, 64), "per token"),
-                                        ((4, 17, 64), "per token"), ((4, 2, 60), "I = ")])
+@pytest.mark.parametrize("sizes,word", [((-1, 2, 64, 64), "T must"), ((17, 2, 64, 64), "at most 16"), ((4, 0, 64, 64), "per token"),
+                                        ((4, 17, 64, 64), "per token"), ((4, 2, 64, 60), "I = "),
+                                        ((4, 2, 60, 64), "H = ")])
 def test_a_workspace_size_of_zero_leaves_its_reason(gd, sizes, word):
     assert gd.lib().dec_add_rmsnorm(None, None, None, None, 1, 64, 0.0, None) != gd.DEC_OK  # another call's message
     assert gd.moe_workspace_size(*sizes) == 0

@@ -123,8 +123,8 @@ def choose(seed, T, k, E):
     return ids, torch.rand(T, k, generator=rng(seed + 99), device="cuda")
 
 
-def dirty(T, k, I):
-    n = gd.moe_workspace_size(T, k, I)
+def dirty(T, k, H, I):
+    n = gd.moe_workspace_size(T, k, H, I)
     return torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")  # every float a NaN
 
 
@@ -136,7 +136,7 @@ def close(got, want, bound):
 
 def check(y, ids, w, held, scales, plain, residual=None):
     out = torch.full_like(y, math.nan)
-    ws = dirty(*ids.shape, held[0].shape[1])
+    ws = dirty(*ids.shape, y.shape[1], held[0].shape[1])
     gd.dec_moe_experts(y, ids, w, *held, out, residual=residual, scales=scales, ws=ws)
     close(out, *R.experts(y, ids, w, *plain, residual=residual))
     again = torch.full_like(y, math.nan)
@@ -188,7 +188,7 @@ def test_exact_sums_of_integers(T, H, I, E, k, fp8):
     held = [x.to(dt) for x in (wg, wu, wd)]
     scales = tuple(torch.ones(E, -(-x.shape[1] // 128), -(-x.shape[2] // 128), device="cuda") for x in held) if fp8 else None
     out = torch.zeros(T, H, device="cuda")
-    gd.dec_moe_experts(y, ids, w, *held, out, scales=scales, ws=dirty(T, k, I))
+    gd.dec_moe_experts(y, ids, w, *held, out, scales=scales, ws=dirty(T, k, H, I))
     want = torch.zeros(T, H, dtype=torch.float64, device="cuda")
     for t in range(T):
         for j in range(k):
@@ -311,7 +311,7 @@ def test_layer_in_a_captured_step(T, fp8):
     start = normal(103, T, H)
     r, y = start.clone(), torch.zeros(T, H, device="cuda")
     ids, w = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda")
-    ws = dirty(T, k, I)
+    ws = dirty(T, k, H, I)
 
     def layer(stream=None):
         gd.dec_add_rmsnorm(None, r, gamma, y, eps, stream=stream)
@@ -365,7 +365,7 @@ def test_two_layers_at_once():
         held, scales, plain = make_weights(110 + 20 * i, E, H, I, fp8)
         y = normal(111 + i, T, H)
         ids, w = choose(112 + 40 * i, T, k, E)
-        sets.append((y, ids, w, held, scales, plain, torch.zeros_like(y), dirty(T, k, I), torch.cuda.Stream()))
+        sets.append((y, ids, w, held, scales, plain, torch.zeros_like(y), dirty(T, k, H, I), torch.cuda.Stream()))
     torch.cuda.synchronize()
     for _ in range(40):
         for y, ids, w, held, scales, plain, out, ws, st in sets:
@@ -382,7 +382,7 @@ def test_workspace_is_returned_and_taken():
     ids, w = choose(122, T, k, E)
     out = torch.zeros_like(y)
     ws = gd.dec_moe_experts(y, ids, w, *held, out)
-    assert ws.numel() == gd.moe_workspace_size(T, k, I)
+    assert ws.numel() == gd.moe_workspace_size(T, k, H, I)
     assert gd.dec_moe_experts(y, ids, w, *held, out, ws=ws) is ws
     with pytest.raises(gd.DecError, match="needs"):
         gd.dec_moe_experts(y, ids, w, *held, out, ws=ws[:256])
