@@ -13,7 +13,7 @@ constexpr int kMoeMaxTokens = 16;
 constexpr int kMoeMaxChoices = 16;    // experts per token
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxDim = 32768;     // hidden and intermediate sizes
-constexpr int kMoeMaxCtas = 160;      // CTAs of the gate/up launch
+constexpr int kMoeMaxCtas = 320;      // CTAs of the gate/up launch: two per SM
 constexpr int kMoeUnit = 64;          // gate rows (and up rows) of one tile
 
 struct MoeRouteArgs {

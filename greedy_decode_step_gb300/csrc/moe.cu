@@ -57,12 +57,12 @@
 namespace dec {
 namespace {
 
-constexpr int kMoeThreads = 224;      // warp 0 copies weights, 1 multiplies, 2-5 take sums off, 6 copies activations
+constexpr int kMoeThreads = 256;      // warps 0 and 6 copy weights, 7 activations, 1 multiplies, 2-5 take sums off
 constexpr int kMoeFlat = 256;         // threads of the two short launches
 constexpr uint32_t kMoeATile = 128 * 128;
 constexpr uint32_t kMoeBlock = 1024;  // one token's parts of one chunk
 constexpr int kMoeMaxStages = 8;
-constexpr int kMoeBStages = 4;
+constexpr int kMoeTurns = 8;          // chunks whose activations may be in shared memory at once
 constexpr int kMoeMaxSplits = 8;
 
 template <bool F8>
@@ -86,7 +86,7 @@ struct Plan {
 static_assert(sizeof(Plan) <= kMoePlanBytes, "the plan's place in the workspace");
 
 struct MoeArgs {
-  CUtensorMap g, u, d;           // boxes of 64, 64 and 128 rows
+  CUtensorMap g, u, d;           // boxes of 64 rows
   const float* y;
   const int32_t* ids;
   const float* gates;
@@ -193,64 +193,70 @@ __device__ __forceinline__ void load_vals(float (&x)[4], const float* src) {
 
 // ----------------------------------------------------------------------------- plan and parts of y
 
-// One CTA; ends with a barrier.
+// One CTA.
 __device__ __forceinline__ void make_plan(Plan& p, const MoeArgs& a) {
-  __shared__ uint32_t chosen[kMoeMaxExperts / 2];  // 16 token bits per expert
+  __shared__ uint32_t chosen[kMoeMaxExperts / 2];                       // 16 token bits per expert
+  __shared__ uint16_t act_of[kMoeMaxExperts], first_of[kMoeMaxExperts];  // of active experts
   __shared__ int32_t ids[kMoeRows];
   __shared__ float gates[kMoeRows];
-  const int n = a.T * a.k;
-  for (int i = threadIdx.x; i < (a.E + 1) / 2; i += kMoeFlat) chosen[i] = 0;
-  for (int i = threadIdx.x; i < n; i += kMoeFlat) {
+  const int n = a.T * a.k, i = threadIdx.x;
+  for (int w = i; w < (a.E + 1) / 2; w += kMoeFlat) chosen[w] = 0;
+  static_assert(kMoeRows <= kMoeFlat, "a thread per choice");
+  if (i < n) {
     ids[i] = a.ids[i];
     gates[i] = a.gates[i];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kMoeFlat) {
-    const int e = ids[i];
-    if (e >= 0 && e < a.E)
-      atomicOr(&chosen[e >> 1], (1u << (i / a.k)) << (16 * (e & 1)));
-    else if (e != -1)
-      atomicOr(a.err, kErrPosRange);
+  const int mine = i < n ? ids[i] : -1, t = i / a.k;
+  const bool valid = mine >= 0 && mine < a.E;
+  if (valid)
+    atomicOr(&chosen[mine >> 1], (1u << t) << (16 * (mine & 1)));
+  else if (mine != -1)
+    atomicOr(a.err, kErrPosRange);
+  __syncthreads();
+  if (i < 32) {
+    int active = 0, rows = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + i;
+      const uint32_t m = e < a.E ? (chosen[e >> 1] >> (16 * (e & 1))) & 0xFFFFu : 0u;
+      const uint32_t any = __ballot_sync(0xffffffffu, m != 0);
+      if (any == 0) continue;
+      const int c = __popc(m);
+      int upto = c;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (i >= o) upto += v;
+      }
+      if (m) {
+        const int at = active + __popc(any & ((1u << i) - 1)), first = rows + upto - c;
+        p.expert[at] = static_cast<uint16_t>(e);
+        p.count[at] = static_cast<uint16_t>(c);
+        p.first[at] = static_cast<uint16_t>(first);
+        act_of[e] = static_cast<uint16_t>(at);
+        first_of[e] = static_cast<uint16_t>(first);
+      }
+      active += __popc(any);
+      rows += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (i == 0) {
+      p.active = active;
+      p.rows = rows;
+    }
   }
   __syncthreads();
-  if (threadIdx.x >= 32) return;
-  const int lane = threadIdx.x;
-  int active = 0, rows = 0;
-  for (int e0 = 0; e0 < a.E; e0 += 32) {
-    const int e = e0 + lane;
-    const uint32_t m = e < a.E ? (chosen[e >> 1] >> (16 * (e & 1))) & 0xFFFFu : 0u;
-    const uint32_t any = __ballot_sync(0xffffffffu, m != 0);
-    if (any == 0) continue;
-    const int c = __popc(m);
-    int upto = c;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
+  if (!valid) return;
+  const uint32_t m = (chosen[mine >> 1] >> (16 * (mine & 1))) & 0xFFFFu;
+  float w = 0.f;  // an expert that a token lists twice counts twice
+  for (int j = t * a.k; j < (t + 1) * a.k; ++j)
+    if (ids[j] == mine) {
+      if (j < i) return;  // an earlier listing makes the row
+      w += gates[j];
     }
-    if (m) {
-      const int at = active + __popc(any & ((1u << lane) - 1)), first = rows + upto - c;
-      p.expert[at] = static_cast<uint16_t>(e);
-      p.count[at] = static_cast<uint16_t>(c);
-      p.first[at] = static_cast<uint16_t>(first);
-      int row = first;
-      for (uint32_t left = m; left; left &= left - 1, ++row) {
-        const int t = __ffs(left) - 1;
-        float w = 0.f;  // an expert that a token lists twice counts twice
-        for (int j = 0; j < a.k; ++j)
-          if (ids[t * a.k + j] == e) w += gates[t * a.k + j];
-        p.token[row] = static_cast<uint16_t>(t);
-        p.act[row] = static_cast<uint16_t>(at);
-        p.gate[row] = w;
-      }
-    }
-    active += __popc(any);
-    rows += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  if (lane == 0) {
-    p.active = active;
-    p.rows = rows;
-  }
+  const int row = first_of[mine] + __popc(m & ((1u << t) - 1));
+  p.token[row] = static_cast<uint16_t>(t);
+  p.act[row] = act_of[mine];
+  p.gate[row] = w;
 }
 
 // Block 0: the plan.  Warps of the others: one block of parts each, chunk j of token t at j T + t.
@@ -317,10 +323,30 @@ __global__ void __launch_bounds__(kMoeFlat) moe_act_kernel(const __grid_constant
 
 // ----------------------------------------------------------------------------- a CTA of the two streaming launches
 
-// NT: the most tokens of a call, 2, 8 or 16.
+// Where the chunks' activations lie: a ring of 2 KB slots, a chunk of n tokens
+// in (n + 1) / 2 of them side by side (the ring's end is passed over where they
+// would not fit).  Every role keeps its own copy of this and steps it alike.
+template <int SLOTS>
+struct Ring {
+  int head = 0;
+  __device__ __forceinline__ int take(int n, int* used) {
+    const int want = (n + 1) >> 1;
+    const bool wraps = head + want > SLOTS;
+    const int skip = wraps ? SLOTS - head : 0, at = wraps ? 0 : head;
+    head = at + want;
+    *used = want + skip;
+    return at;
+  }
+};
+
+// NT: the most tokens of a call, 2, 8 or 16.  Two CTAs fit an SM, of one launch
+// or of two: a thread takes about 55 ns to issue a copy, so three warps of each
+// share them, and with one CTA per SM the same stream was 10 % slower.
 template <bool F8, int NT>
 struct Cta {
   using P = Parts<F8>;
+  static constexpr int kSlots = NT <= 2 ? 8 : 16;
+  static constexpr uint32_t kSlot = 2 * kMoeBlock;
   uint64_t *fullA, *emptyA, *fullB, *emptyB, *accum, *drained;
   uint32_t* tmem_slot;
   volatile int* stop;  // a wait ran out: every role ends
@@ -329,14 +355,13 @@ struct Cta {
   unsigned char *A, *B;
   uint32_t tmem;
 
-  static constexpr uint32_t kHead = 1024, kPlan = kMoePlanBytes, kTotal = NT * 512, kBTile = NT * kMoeBlock;
-  // up to 8 tokens two CTAs fit an SM, of one launch or of gate/up and down
-  static constexpr uint32_t kMax = NT <= 8 ? 112 * 1024 : 224 * 1024;
-  static constexpr int kFit = static_cast<int>((kMax - 1024 - kHead - kPlan - kTotal - kMoeBStages * kBTile) / kMoeATile);
-  static constexpr int kStages = kFit < kMoeMaxStages ? kFit : kMoeMaxStages;
-  static constexpr uint32_t kSmem = 1024 + kHead + kPlan + kTotal + kMoeBStages * kBTile + kStages * kMoeATile;
-  static constexpr uint32_t kAcc = 8 * NT;                  // columns of an accumulator
-  static constexpr uint32_t kCols = tmem_columns(2 * kAcc);
+  static constexpr uint32_t kHead = 1024, kPlan = kMoePlanBytes, kTotal = NT * 512;
+  static constexpr int kStages = static_cast<int>((112 * 1024 - 1024 - kHead - kPlan - kTotal - kSlots * kSlot) / kMoeATile);
+  static_assert(kStages >= 4 && kStages <= kMoeMaxStages && kSlots >= NT / 2, "shared memory");
+  static constexpr uint32_t kSmem = 1024 + kHead + kPlan + kTotal + kSlots * kSlot + kStages * kMoeATile;
+  static constexpr int kAccs = NT <= 8 ? 4 : 2;             // accumulators in turn: two CTAs' fit tensor memory
+  static constexpr uint32_t kAcc = 8 * NT;                  // columns of one
+  static constexpr uint32_t kCols = tmem_columns(kAccs * kAcc);
   static constexpr int kGroup = NT < 4 ? NT : 4;            // tokens whose sums are loaded together
 
   // All threads.
@@ -345,26 +370,26 @@ struct Cta {
     fullA = reinterpret_cast<uint64_t*>(smem);
     emptyA = fullA + kMoeMaxStages;
     fullB = emptyA + kMoeMaxStages;
-    emptyB = fullB + kMoeBStages;
-    accum = emptyB + kMoeBStages;
-    drained = accum + 2;
-    tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
+    emptyB = fullB + kMoeTurns;
+    accum = emptyB + kMoeTurns;
+    drained = accum + kAccs;
+    tmem_slot = reinterpret_cast<uint32_t*>(drained + kAccs);
     stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kMoeMaxStages + 2 * kMoeBStages + 4) * 8 + 8 <= kHead, "barriers");
+    static_assert((2 * kMoeMaxStages + 2 * kMoeTurns + 2 * kAccs) * 8 + 8 <= kHead, "barriers");
     A = smem + kHead;
     B = A + kStages * kMoeATile;
-    plan = reinterpret_cast<Plan*>(B + kMoeBStages * kBTile);
+    plan = reinterpret_cast<Plan*>(B + kSlots * kSlot);
     total = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(plan) + kPlan);
     if (threadIdx.x == 0) {
       for (int s = 0; s < kStages; ++s) {
-        mbar_init(&fullA[s], 1);
+        mbar_init(&fullA[s], 2);
         mbar_init(&emptyA[s], 1);
       }
-      for (int s = 0; s < kMoeBStages; ++s) {
+      for (int s = 0; s < kMoeTurns; ++s) {
         mbar_init(&fullB[s], 1);
         mbar_init(&emptyB[s], 4);
       }
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < kAccs; ++s) {
         mbar_init(&accum[s], 1);
         mbar_init(&drained[s], 4);
       }
@@ -399,44 +424,42 @@ struct Cta {
     if (threadIdx.x % 32 == 0) ok = (mbar_wait(bar, parity, stop, err, code) && !*stop) ? 1 : 0;
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
   }
-  // One lane: a free stage of the weights' ring for chunk `it`, null when a wait ran out.
-  __device__ __forceinline__ unsigned char* claim(int it, uint32_t* err) const {
+  // One lane of either weight warp: its half (64 rows) of a free stage for
+  // chunk `it`, null when a wait ran out.
+  __device__ __forceinline__ unsigned char* claim(int it, int half, uint32_t* err) const {
     const int s = it % kStages;
     if (it >= kStages && !mbar_wait(&emptyA[s], ((it / kStages) - 1) & 1, stop, err, kErrWaitEmpty)) *stop = 1;
-    if (*stop) {  // an early end waits for the copies that are on their way
-      for (int i = max(0, it - kStages); i < it; ++i)
-        if (!tc_wait(&fullA[i % kStages], (i / kStages) & 1, err, kErrDrain)) break;
-      return nullptr;
-    }
-    mbar_arrive_expect_tx(&fullA[s], kMoeATile);
-    return A + s * kMoeATile;
+    if (*stop) return nullptr;
+    mbar_arrive_expect_tx(&fullA[s], kMoeATile / 2);
+    return A + s * kMoeATile + half * (kMoeATile / 2);
   }
-  // Whole warp: chunk `it`'s blocks, lane r's from `src` (n lanes); false when a wait ran out.
-  __device__ __forceinline__ bool bring(int it, int n, const unsigned char* src, uint64_t pol, uint32_t* err) const {
-    const int b = it % kMoeBStages, lane = threadIdx.x & 31;
-    if (it >= kMoeBStages && !warp_wait(&emptyB[b], ((it / kMoeBStages) - 1) & 1, err, kErrWaitEmpty)) {
-      *stop = 1;
-      if (lane == 0)
-        for (int i = max(0, it - kMoeBStages); i < it; ++i)
-          if (!tc_wait(&fullB[i % kMoeBStages], (i / kMoeBStages) & 1, err, kErrDrain)) break;
-      return false;
+  // Whole warp: waits until chunk `it`'s activations may be brought; `sizes` holds the slots of the chunks in turn, one
+  // byte each, `tail` is the oldest that holds some, `room` the free slots.  False when a wait ran out.
+  __device__ __forceinline__ bool make_room(int it, int used, uint64_t& sizes, int& tail, int& room, uint32_t* err) const {
+    while (room < used || it - tail >= kMoeTurns) {
+      if (!warp_wait(&emptyB[tail % kMoeTurns], (tail / kMoeTurns) & 1, err, kErrWaitEmpty)) {
+        *stop = 1;
+        return false;
+      }
+      room += static_cast<int>((sizes >> (8 * (tail % kMoeTurns))) & 0xFF);
+      ++tail;
     }
-    if (lane == 0) mbar_arrive_expect_tx(&fullB[b], n * P::kCopy);
-    __syncwarp();
-    if (lane < n) bulk_copy_g2s(B + b * kBTile + lane * kMoeBlock, src, P::kCopy, &fullB[b], pol);
+    room -= used;
+    const int at = 8 * (it % kMoeTurns);
+    sizes = (sizes & ~(0xFFull << at)) | (static_cast<uint64_t>(used) << at);
     return true;
   }
-  // One lane: the MMAs of chunk `it` with n tokens; false when a wait ran out.
-  __device__ __forceinline__ bool multiply(int it, int n, uint32_t* err) const {
-    const int s = it % kStages, b = it % kMoeBStages;
+  // One lane: the MMAs of chunk `it` with n tokens in slot b; false when a wait ran out.
+  __device__ __forceinline__ bool multiply(int it, int n, int b, uint32_t* err) const {
+    const int s = it % kStages, acc = it % kAccs;
     if (!mbar_wait(&fullA[s], (it / kStages) & 1, stop, err, kErrWaitFull) ||
-        !mbar_wait(&fullB[b], (it / kMoeBStages) & 1, stop, err, kErrWaitFull) ||
-        (it >= 2 && !mbar_wait(&drained[it & 1], ((it >> 1) - 1) & 1, stop, err, kErrWaitFull)) || *stop) {
+        !mbar_wait(&fullB[it % kMoeTurns], (it / kMoeTurns) & 1, stop, err, kErrWaitFull) ||
+        (it >= kAccs && !mbar_wait(&drained[acc], ((it / kAccs) - 1) & 1, stop, err, kErrWaitFull)) || *stop) {
       *stop = 1;
       return false;
     }
     tc_fence_after();
-    const uint32_t sa = smem_addr(A + s * kMoeATile), sb = smem_addr(B + b * kBTile), d = tmem + (it & 1) * kAcc;
+    const uint32_t sa = smem_addr(A + s * kMoeATile), sb = smem_addr(B + b * kSlot), d = tmem + acc * kAcc;
     const uint32_t idesc = tc_idesc_of(8 * ((n + 1) & ~1), !F8);  // columns of a missing last token hold anything
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of K per instruction
@@ -447,28 +470,32 @@ struct Cta {
         tc_mma(d, ad, bd, idesc, kk > 0);
     }
     tc_commit(&emptyA[s]);
-    tc_commit(&accum[it & 1]);
+    tc_commit(&accum[acc]);
     return true;
   }
-  // Whole warp: adds chunk `it`'s sums of n tokens, weights' scale w (1 for bf16); false when a wait ran out.
-  __device__ __forceinline__ bool add(int it, int n, float w, float (&sum)[NT], uint32_t* err) const {
-    if (!warp_wait(&accum[it & 1], (it >> 1) & 1, err, kErrWaitFull)) {
+  // Whole warp: adds chunk `it`'s sums of n tokens in slot b, weights' scale w (1 for bf16); false when a wait ran out.
+  __device__ __forceinline__ bool add(int it, int n, int b, float w, float (&sum)[NT], uint32_t* err) const {
+    const int acc = it % kAccs;
+    if (!warp_wait(&accum[acc], (it / kAccs) & 1, err, kErrWaitFull)) {
       *stop = 1;
       return false;
     }
     tc_fence_after();
-    const uint32_t at = tmem + (static_cast<uint32_t>(threadIdx.x & 96) << 16) + (it & 1) * kAcc;
-    const unsigned char* blocks = B + (it % kMoeBStages) * kBTile;
+    const uint32_t at = tmem + (static_cast<uint32_t>(threadIdx.x & 96) << 16) + acc * kAcc;
+    const unsigned char* blocks = B + b * kSlot;
 #pragma unroll
     for (int t0 = 0; t0 < NT; t0 += kGroup) {
       if (t0 >= n) break;
       uint32_t v[kGroup / 2][16];
 #pragma unroll
-      for (int h = 0; h < kGroup / 2; ++h) tmem_ld_issue(at + 8 * (t0 + 2 * h), v[h]);
+      for (int h = 0; h < kGroup / 2; ++h)
+        if (h == 0 || t0 + 2 * h < n) tmem_ld_issue(at + 8 * (t0 + 2 * h), v[h]);
 #pragma unroll
-      for (int h = 0; h < kGroup / 2; ++h) tmem_ld_wait(v[h]);
+      for (int h = 0; h < kGroup / 2; ++h)
+        if (h == 0 || t0 + 2 * h < n) tmem_ld_wait(v[h]);
 #pragma unroll
       for (int t = 0; t < kGroup; ++t) {
+        if (t0 + t >= n) break;
         float x = 0.f;  // the smallest part first
 #pragma unroll
         for (int p = P::kParts - 1; p >= 0; --p) {
@@ -484,17 +511,23 @@ struct Cta {
     tc_fence_before();
     __syncwarp();
     if (threadIdx.x % 32 == 0) {
-      mbar_arrive(&drained[it & 1]);
-      mbar_arrive(&emptyB[it % kMoeBStages]);
+      mbar_arrive(&drained[acc]);
+      mbar_arrive(&emptyB[it % kMoeTurns]);
     }
     return true;
+  }
+  // One lane, at the end of a copying role: an early end waits for the copies that are on their way.
+  __device__ __forceinline__ void drain(uint64_t* bars, int n, int from, int to, uint32_t* err) const {
+    if (*stop)
+      for (int i = max(0, from); i < to; ++i)
+        if (!tc_wait(&bars[i % n], (i / n) & 1, err, kErrDrain)) break;
   }
 };
 
 // ----------------------------------------------------------------------------- gate/up
 
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_gate_up_kernel(const __grid_constant__ MoeArgs a) {
+__global__ void __launch_bounds__(kMoeThreads, 2) moe_gate_up_kernel(const __grid_constant__ MoeArgs a) {
   using P = Parts<F8>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Cta<F8, NT> c(smem_raw);
@@ -506,50 +539,66 @@ __global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_gate_up_kern
   const Runs r(p.active, a, P::kChunk);
   const int lo = r.begin(blockIdx.x), hi = r.begin(blockIdx.x + 1);
 
-  if (warp == 0) {
+  using Slots = Ring<Cta<F8, NT>::kSlots>;
+  if (warp == 0 || warp == 6) {
     if (lane == 0) {
+      const int half = warp == 6;
       const uint64_t pol = l2_policy_evict_first();
+      const CUtensorMap* map = half ? &a.u : &a.g;
       int it = 0;
       bool ok = true;
       for (int pos = lo; pos < hi && ok;) {
         const int tile = pos / r.kch, j0 = pos - tile * r.kch, n = min(r.kch - j0, hi - pos);
         const int row = (tile % r.units) * kMoeUnit, e = p.expert[tile / r.units];
         for (int j = j0; j < j0 + n; ++j, ++it) {
-          unsigned char* to = c.claim(it, a.err);
+          unsigned char* to = c.claim(it, half, a.err);
           ok = to != nullptr;
           if (!ok) break;
-          uint64_t* bar = &c.fullA[it % c.kStages];
-          tma_load_3d(to, &a.g, j * P::kChunk, row, e, bar, pol);
-          tma_load_3d(to + kMoeATile / 2, &a.u, j * P::kChunk, row, e, bar, pol);
+          tma_load_3d(to, map, j * P::kChunk, row, e, &c.fullA[it % c.kStages], pol);
         }
         pos += n;
       }
+      if (half == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
     }
-  } else if (warp == 6) {
+  } else if (warp == 7) {
     const uint64_t pol = l2_policy_evict_last();
-    int it = 0;
+    Slots ring;
+    uint64_t sizes = 0;
+    int it = 0, tail = 0, room = c.kSlots, used;
     bool ok = true;
     for (int pos = lo; pos < hi && ok;) {
       const int tile = pos / r.kch, j0 = pos - tile * r.kch, n = min(r.kch - j0, hi - pos);
       const int act = tile / r.units, count = p.count[act], t = lane < count ? p.token[p.first[act] + lane] : 0;
-      for (int j = j0; j < j0 + n && ok; ++j, ++it)
-        ok = c.bring(it, count, a.xb + (static_cast<size_t>(j) * a.T + t) * kMoeBlock, pol, a.err);
+      for (int j = j0; j < j0 + n; ++j, ++it) {
+        const int at = ring.take(count, &used);
+        ok = c.make_room(it, used, sizes, tail, room, a.err);
+        if (!ok) break;
+        uint64_t* bar = &c.fullB[it % kMoeTurns];
+        if (lane == 0) mbar_arrive_expect_tx(bar, count * P::kCopy);
+        __syncwarp();
+        if (lane < count)
+          bulk_copy_g2s(c.B + at * c.kSlot + lane * kMoeBlock, a.xb + (static_cast<size_t>(j) * a.T + t) * kMoeBlock, P::kCopy,
+                        bar, pol);
+      }
       pos += n;
     }
+    if (lane == 0) c.drain(c.fullB, kMoeTurns, it - kMoeTurns, it, a.err);
   } else if (warp == 1) {
     if (lane == 0) {
-      int it = 0;
+      Slots ring;
+      int it = 0, used;
       bool ok = true;
       for (int pos = lo; pos < hi && ok;) {
         const int tile = pos / r.kch, n = min((tile + 1) * r.kch, hi) - pos, count = p.count[tile / r.units];
-        for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, a.err);
+        for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, ring.take(count, &used), a.err);
         pos += n;
       }
     }
   } else {
     const int m = (32 * warp + lane) & 127;  // TMEM lane; row of the tile: gate below 64, up from 64 on
     const int IB = (a.I + kFp8Block - 1) / kFp8Block;
-    int it = 0;
+    Slots ring;
+    int it = 0, used;
     bool ok = true;
     for (int pos = lo; pos < hi && ok;) {
       const int tile = pos / r.kch, j0 = pos - tile * r.kch, n = min(r.kch - j0, hi - pos);
@@ -566,7 +615,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_gate_up_kern
       for (int j = j0; j < j0 + n && ok; ++j, ++it) {
         const float w = next;
         if (F8 && j + 1 < j0 + n) next = __ldg(sw + j + 1);
-        ok = c.add(it, count, w, sum, a.err);
+        ok = c.add(it, count, ring.take(count, &used), w, sum, a.err);
       }
       if (!ok) break;
       const int i = ub * kMoeUnit + (m & (kMoeUnit - 1));
@@ -587,7 +636,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_gate_up_kern
 // ----------------------------------------------------------------------------- down
 
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_down_kernel(const __grid_constant__ MoeArgs a) {
+__global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const __grid_constant__ MoeArgs a) {
   using P = Parts<F8>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Cta<F8, NT> c(smem_raw);
@@ -600,38 +649,55 @@ __global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_down_kernel(
   const int lo = static_cast<int>(static_cast<long long>(split) * all / a.splits);
   const int hi = static_cast<int>(static_cast<long long>(split + 1) * all / a.splits);
 
-  if (warp == 0) {
+  using Slots = Ring<Cta<F8, NT>::kSlots>;
+  if (warp == 0 || warp == 6) {
     if (lane == 0) {
+      const int half = warp == 6;
       const uint64_t pol = l2_policy_evict_first();
-      int act = lo / kch, j = lo - act * kch;
-      for (int it = 0; it < hi - lo; ++it) {
-        unsigned char* to = c.claim(it, a.err);
+      int act = lo / kch, j = lo - act * kch, it = 0;
+      for (; it < hi - lo; ++it) {
+        unsigned char* to = c.claim(it, half, a.err);
         if (!to) break;
-        tma_load_3d(to, &a.d, j * P::kChunk, m0, p.expert[act], &c.fullA[it % c.kStages], pol);
+        // rows behind the last are filled with zeros
+        tma_load_3d(to, &a.d, j * P::kChunk, m0 + half * 64, p.expert[act], &c.fullA[it % c.kStages], pol);
         if (++j == kch) {
           j = 0;
           ++act;
         }
       }
+      if (half == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
     }
-  } else if (warp == 6) {
+  } else if (warp == 7) {
     pdl_wait();  // the inner vectors
     const uint64_t pol = l2_policy_evict_last();
-    int it = 0;
+    Slots ring;
+    uint64_t sizes = 0;
+    int it = 0, tail = 0, room = c.kSlots, used;
     bool ok = true;
     for (int pos = lo; pos < hi && ok;) {
       const int act = pos / kch, j0 = pos - act * kch, n = min(kch - j0, hi - pos), count = p.count[act];
-      const unsigned char* src = a.hb + (static_cast<size_t>(p.first[act]) * kch + static_cast<size_t>(j0) * count + lane) * kMoeBlock;
-      for (int j = 0; j < n && ok; ++j, ++it, src += count * kMoeBlock) ok = c.bring(it, count, src, pol, a.err);
+      const unsigned char* src = a.hb + (static_cast<size_t>(p.first[act]) * kch + static_cast<size_t>(j0) * count) * kMoeBlock;
+      for (int j = 0; j < n; ++j, ++it, src += count * kMoeBlock) {
+        const int at = ring.take(count, &used);
+        ok = c.make_room(it, used, sizes, tail, room, a.err);
+        if (!ok) break;
+        if (lane == 0) {  // a chunk's blocks lie side by side
+          const uint32_t bytes = (count - 1) * kMoeBlock + P::kCopy;
+          mbar_arrive_expect_tx(&c.fullB[it % kMoeTurns], bytes);
+          bulk_copy_g2s(c.B + at * c.kSlot, src, bytes, &c.fullB[it % kMoeTurns], pol);
+        }
+      }
       pos += n;
     }
+    if (lane == 0) c.drain(c.fullB, kMoeTurns, it - kMoeTurns, it, a.err);
   } else if (warp == 1) {
     if (lane == 0) {
-      int it = 0;
+      Slots ring;
+      int it = 0, used;
       bool ok = true;
       for (int pos = lo; pos < hi && ok;) {
         const int act = pos / kch, n = min((act + 1) * kch, hi) - pos, count = p.count[act];
-        for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, a.err);
+        for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, ring.take(count, &used), a.err);
         pos += n;
       }
     }
@@ -639,7 +705,8 @@ __global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_down_kernel(
     const int m = (32 * warp + lane) & 127, HB = (a.H + kFp8Block - 1) / kFp8Block;
 #pragma unroll
     for (int t = 0; t < NT; ++t) c.total[t * 128 + m] = 0.f;
-    int it = 0;
+    Slots ring;
+    int it = 0, used;
     bool ok = true;
     for (int pos = lo; pos < hi && ok;) {
       const int act = pos / kch, j0 = pos - act * kch, n = min(kch - j0, hi - pos), count = p.count[act];
@@ -655,7 +722,7 @@ __global__ void __launch_bounds__(kMoeThreads, NT <= 8 ? 2 : 1) moe_down_kernel(
       for (int j = j0; j < j0 + n && ok; ++j, ++it) {
         const float w = next;
         if (F8 && j + 1 < j0 + n) next = __ldg(sw + j + 1);
-        ok = c.add(it, count, w, sum, a.err);
+        ok = c.add(it, count, ring.take(count, &used), w, sum, a.err);
       }
       // this thread's column of its tokens' sums
 #pragma unroll
@@ -776,7 +843,7 @@ int moe_experts(const MoeCall& c, int sms, cudaStream_t st, const char** why) {
   std::memset(&a, 0, sizeof(a));
   if (!make_tmap_mats(&a.g, c.wg, bytes, c.H, c.I, c.E, kMoeUnit) ||
       !make_tmap_mats(&a.u, c.wu, bytes, c.H, c.I, c.E, kMoeUnit) ||
-      !make_tmap_mats(&a.d, c.wd, bytes, c.I, c.H, c.E, 128)) {
+      !make_tmap_mats(&a.d, c.wd, bytes, c.I, c.H, c.E, kMoeUnit)) {
     *why = "a tensor map could not be made";
     return 1;
   }
@@ -799,7 +866,7 @@ int moe_experts(const MoeCall& c, int sms, cudaStream_t st, const char** why) {
   a.E = c.E;
   a.H = c.H;
   a.I = c.I;
-  a.ctas = std::min(sms, kMoeMaxCtas);
+  a.ctas = std::min(2 * sms, kMoeMaxCtas);
   a.err = c.err;
   const int nt = c.T <= 2 ? 2 : (c.T <= 8 ? 8 : 16);
   cudaError_t e = f8 ? (nt == 2 ? run_experts<true, 2>(a, st) : nt == 8 ? run_experts<true, 8>(a, st) : run_experts<true, 16>(a, st))

@@ -7,11 +7,12 @@
 //   weight: p, divided by the sum of the chosen ones' if asked, times scale
 //
 // A cluster of 8 CTAs per token, so that one launch serves: each CTA takes an
-// eighth of the experts, a warp per expert with the token's row in shared
-// memory, and puts the logits into CTA 0, whose first warp chooses.  The sums
-// of different experts run in one order, so equal rows of Wr give equal
-// logits.  Bound by latency: the matrix (0.3 to 2 MB) comes from L2 for all
-// tokens but the first to ask.
+// eighth of the experts, a warp per expert, and puts the logits into CTA 0,
+// whose first warp chooses.  The sums of different experts run in one order, so
+// equal rows of Wr give equal logits.  Bound by latency: a warp's first 2048
+// weights are on their way before the wait for the launch that makes y; each
+// lane keeps the best of its own experts and looks anew only after it lost
+// that one.
 #include <cuda_runtime.h>
 
 #include "dec_launch.cuh"
@@ -25,9 +26,11 @@ constexpr int kRouteCluster = 8;
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 
+constexpr int kRouteAhead = 8;  // 16-byte pieces of a row of Wr that a lane holds
+
 // Eight products of bf16 weights, in four sums.
-__device__ __forceinline__ void dot8(const uint4& w, const float* x, float (&acc)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(x), b = *reinterpret_cast<const float4*>(x + 4);
+__device__ __forceinline__ void dot8(const uint4& w, const float* y, float (&acc)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(y)), b = __ldg(reinterpret_cast<const float4*>(y + 4));
   acc[0] = fmaf(bf16lo(w.x), a.x, acc[0]);
   acc[1] = fmaf(bf16hi(w.x), a.y, acc[1]);
   acc[2] = fmaf(bf16lo(w.y), a.z, acc[2]);
@@ -40,22 +43,33 @@ __device__ __forceinline__ void dot8(const uint4& w, const float* x, float (&acc
 
 __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteThreads)
     moe_route_kernel(const MoeRouteArgs a) {
-  extern __shared__ __align__(16) float x[];  // [H]
   __shared__ float z[kMoeMaxExperts];
   __shared__ uint32_t key[kMoeMaxExperts];
   const int rank = blockIdx.x % kRouteCluster, t = blockIdx.x / kRouteCluster;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const float* y = a.y + static_cast<size_t>(t) * a.H;
+  uint4 w[kRouteAhead];
+  auto fetch = [&](int e, int h0) {
+#pragma unroll
+    for (int i = 0; i < kRouteAhead; ++i) {
+      const int h = h0 + (32 * i + lane) * 8;
+      if (h < a.H) w[i] = __ldg(reinterpret_cast<const uint4*>(a.Wr + static_cast<size_t>(e) * a.H + h));
+    }
+  };
+  const int e0 = rank * kRouteWarps + warp;
+  if (e0 < a.E) fetch(e0, 0);  // no kernel writes the weights
   pdl_wait();
   pdl_launch_dependents();
-  const float* y = a.y + static_cast<size_t>(t) * a.H;
-  for (int i = threadIdx.x * 4; i < a.H; i += kRouteThreads * 4)
-    *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(y + i);
-  __syncthreads();
-  for (int e = rank * kRouteWarps + warp; e < a.E; e += kRouteCluster * kRouteWarps) {
-    const uint16_t* w = a.Wr + static_cast<size_t>(e) * a.H;
+  for (int e = e0; e < a.E; e += kRouteCluster * kRouteWarps) {
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int h = lane * 8; h < a.H; h += 256) dot8(__ldg(reinterpret_cast<const uint4*>(w + h)), x + h, acc);
+    for (int h0 = 0; h0 < a.H; h0 += kRouteAhead * 256) {
+      if (e != e0 || h0 > 0) fetch(e, h0);
+#pragma unroll
+      for (int i = 0; i < kRouteAhead; ++i) {
+        const int h = h0 + (32 * i + lane) * 8;
+        if (h < a.H) dot8(w[i], y + h, acc);
+      }
+    }
     const float sum = warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
     if (lane == 0) store_cta0(z + e, __float_as_uint(sum));
   }
@@ -74,47 +88,51 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
     total = warp_sum(total);
   }
   auto score = [&](float v) { return a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / total; };
+  uint32_t best = 0, at = 0;  // of this lane's experts
   for (int e = lane; e < a.E; e += 32) {
-    const float v = (a.bias ? score(z[e]) + a.bias[e] : z[e]) + 0.f;  // -0 and 0 are equal
-    key[e] = v == v ? float_order_key(v) : 1u;                         // 0: taken
+    const float v = (a.bias ? score(z[e]) + a.bias[e] : z[e]) + 0.f;   // -0 and 0 are equal
+    const uint32_t o = v == v ? float_order_key(v) : 1u;                // 0: taken
+    key[e] = o;
+    if (o > best) {
+      best = o;
+      at = e;
+    }
   }
-  __syncwarp();
-  float mine = 0.f, sum = 0.f;
-  int id = 0;
+  uint32_t mine = 0;
   for (int j = 0; j < a.k; ++j) {
-    uint32_t best = 0, at = 0;
-    for (int e = lane; e < a.E; e += 32)
-      if (key[e] > best) {
-        best = key[e];
-        at = e;
-      }
     const uint32_t most = __reduce_max_sync(0xffffffffu, best);
     const uint32_t e = __reduce_min_sync(0xffffffffu, best == most ? at : 0xffffffffu);
-    const float p = score(z[e]);
-    sum += p;
-    if (lane == j) {
-      mine = p;
-      id = static_cast<int>(e);
+    if (lane == j) mine = e;
+    if (best == most && at == e) {
+      key[e] = 0;
+      best = 0;
+      for (int i = lane; i < a.E; i += 32)
+        if (key[i] > best) {
+          best = key[i];
+          at = i;
+        }
     }
-    __syncwarp();
-    if (lane == 0) key[e] = 0;
-    __syncwarp();
+  }
+  const float p = lane < a.k ? score(z[mine]) : 0.f;
+  float sum = 1.f;
+  if (a.renormalise) {
+    sum = 0.f;
+    for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, p, j);
   }
   if (lane < a.k) {
-    a.ids[static_cast<size_t>(t) * a.k + lane] = id;
-    a.gates[static_cast<size_t>(t) * a.k + lane] = (a.renormalise ? mine / sum : mine) * a.scale;
+    a.ids[static_cast<size_t>(t) * a.k + lane] = static_cast<int>(mine);
+    a.gates[static_cast<size_t>(t) * a.k + lane] = p / sum * a.scale;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_moe_route(const MoeRouteArgs& a, int T, cudaStream_t st) {
-  return launch(moe_route_kernel, dim3(T * kRouteCluster), dim3(kRouteThreads), static_cast<size_t>(a.H) * 4, st, true, a);
+  return launch(moe_route_kernel, dim3(T * kRouteCluster), dim3(kRouteThreads), 0, st, true, a);
 }
 
 cudaError_t allow_smem_moe_route() {
-  cudaError_t e = cudaFuncSetAttribute(moe_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeMaxDim * 4);
-  return e != cudaSuccess ? e : prefer_max_carveout(moe_route_kernel);
+  return prefer_max_carveout(moe_route_kernel);
 }
 
 }  // namespace dec
