@@ -40,9 +40,9 @@ struct MoeCall {
   int T, k, E, H, I;
   uint32_t* err;
 };
-// Workspace (byte offsets): the plan; gate and up products of every chosen
-// (token, expert); the parts of tiles that a CTA took over from the one before
-// it; the split rows of y and of the inner vectors, 1 KB per token and 64 or
+// Workspace (byte offsets): the plan and a counter per tile of the down launch;
+// gate and up products of every chosen (token, expert); the parts of tiles that
+// several CTAs share; the split rows of y and of the inner vectors, 1 KB per token and 64 or
 // 128 values.
 constexpr int kMoeRows = kMoeMaxTokens * kMoeMaxChoices;  // (token, expert) pairs
 constexpr int kMoePlanBytes = 4096;
@@ -52,7 +52,7 @@ struct MoeWorkspace {
 inline MoeWorkspace moe_workspace(int T, int k, int H, int I) {
   auto up = [](size_t n) { return (n + 1023) & ~size_t(1023); };
   MoeWorkspace w;
-  w.main = kMoePlanBytes;
+  w.main = kMoePlanBytes + kMoeMaxDim / 128 * 4;
   w.cut = w.main + up(static_cast<size_t>(T) * k * 2 * I * 4);
   w.xb = w.cut + static_cast<size_t>(kMoeMaxCtas) * kMoeMaxTokens * 2 * kMoeUnit * 4;
   w.hb = w.xb + static_cast<size_t>(T) * ((H + 63) / 64) * 1024;

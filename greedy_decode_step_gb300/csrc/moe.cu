@@ -34,9 +34,11 @@
 // lays all tiles' chunks end to end and gives every CTA an equal run of them;
 // a tile cut between CTAs leaves parts, which moe_act_kernel adds in CTA order.
 // down: a tile is 128 output rows, its K axis all active experts' inner vectors
-// one behind the other, split over a cluster of CTAs whose sums meet in
-// distributed shared memory in rank order: results do not depend on timing.
-// Its first weights are on their way while gate/up still runs.
+// one behind the other, split over as many CTAs as run at once.  The last of a
+// tile's CTAs to arrive adds their sums in split order: results do not depend
+// on timing.  (Clusters that add through distributed shared memory hold 120
+// CTAs where 300 run, and took 74 us for the down half of 16 tokens, 8 of 128 8-bit experts, where this takes 48.)  The
+// first weights are on their way while gate/up still runs.
 //
 // Every wait is bounded (an error bit and an early exit instead of a hang),
 // and tensor memory is released on every path.
@@ -47,7 +49,6 @@
 
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 
 #include "dec_fp8.cuh"
 #include "dec_launch.cuh"
@@ -63,7 +64,7 @@ constexpr uint32_t kMoeATile = 128 * 128;
 constexpr uint32_t kMoeBlock = 1024;  // one token's parts of one chunk
 constexpr int kMoeMaxStages = 8;
 constexpr int kMoeTurns = 8;          // chunks whose activations may be in shared memory at once
-constexpr int kMoeMaxSplits = 8;
+constexpr int kMoeMaxSplits = 32;
 
 template <bool F8>
 struct Parts {
@@ -94,7 +95,8 @@ struct MoeArgs {
   const float* residual;
   float* out;
   Plan* plan;                    // workspace
-  float *main, *cut;
+  uint32_t* arrived;             // [tiles of down]
+  float *main, *cut;             // cut: the parts of down's tiles, too
   unsigned char *xb, *hb;
   int T, k, E, H, I;
   int ctas;                      // of the gate/up launch
@@ -266,6 +268,7 @@ __global__ void __launch_bounds__(kMoeFlat) moe_prep_kernel(const __grid_constan
   pdl_wait();
   pdl_launch_dependents();
   if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < (a.H + 127) / 128; i += kMoeFlat) a.arrived[i] = 0;
     make_plan(*a.plan, a);
     return;
   }
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const __grid_c
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Cta<F8, NT> c(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x % a.splits, m0 = (blockIdx.x / a.splits) * 128;
+  const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits, m0 = tile * 128;
   // the plan was complete before gate/up could begin, and that began before this launch could
   c.take_plan(a.plan);
   const Plan& p = *c.plan;
@@ -735,63 +738,54 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const __grid_c
   }
   __syncwarp();
   pdl_wait();  // the result may be what an earlier kernel reads or writes
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  {
-    const uint32_t local = smem_addr(c.total);
-    const int total = a.T * 128, per = (total + a.splits - 1) / a.splits, end = min(total, (split + 1) * per);
-    for (int o = split * per + static_cast<int>(threadIdx.x); o < end; o += kMoeThreads) {
-      const int t = o >> 7, m = m0 + (o & 127);
-      float x[kMoeMaxSplits];
+  __syncthreads();
+  // [tile][split][T][128]
+  const int n4 = a.T * 32;
+  float4* mine = reinterpret_cast<float4*>(a.cut) + (static_cast<size_t>(tile) * a.splits + split) * n4;
+  const float4* sums = reinterpret_cast<const float4*>(c.total);
+  bool last = true;
+  if (a.splits > 1) {
+    for (int i = threadIdx.x; i < n4; i += kMoeThreads) mine[i] = sums[i];
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) *c.tmem_slot = atomicAdd(a.arrived + tile, 1u);  // the slot has served
+    __syncthreads();
+    last = *c.tmem_slot == static_cast<uint32_t>(a.splits - 1);
+    __threadfence();
+  }
+  if (last) {
+    const float4* all4 = mine - static_cast<size_t>(split) * n4;
+    for (int i = threadIdx.x; i < n4; i += kMoeThreads) {
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.splits == 1) sum = sums[i];
+      for (int s0 = 0; s0 < a.splits && a.splits > 1; s0 += 16) {
+        float4 x[16];
 #pragma unroll
-      for (int k = 0; k < kMoeMaxSplits; ++k) {
-        x[k] = 0.f;
-        if (k < a.splits) {
-          uint32_t remote;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local + 4u * o), "r"(k));
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[k]) : "r"(remote));
-        }
+        for (int s = 0; s < 16; ++s)
+          if (s0 + s < a.splits) x[s] = __ldcg(all4 + static_cast<size_t>(s0 + s) * n4 + i);
+#pragma unroll
+        for (int s = 0; s < 16; ++s)
+          if (s0 + s < a.splits) {
+            sum.x += x[s].x;
+            sum.y += x[s].y;
+            sum.z += x[s].z;
+            sum.w += x[s].w;
+          }
       }
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < kMoeMaxSplits; ++k) sum += x[k];
-      const size_t to = static_cast<size_t>(t) * a.H + m;
-      if (m < a.H) a.out[to] = (a.residual ? a.residual[to] : 0.f) + sum;
+      const int m = m0 + 4 * (i & 31);
+      if (m >= a.H) continue;  // H is a multiple of 8
+      const size_t to = static_cast<size_t>(i >> 5) * a.H + m;
+      if (a.residual) {
+        const float4 r = *reinterpret_cast<const float4*>(a.residual + to);
+        sum = make_float4(r.x + sum.x, r.y + sum.y, r.z + sum.z, r.w + sum.w);
+      }
+      *reinterpret_cast<float4*>(a.out + to) = sum;
     }
   }
-  __syncwarp();
-  // no CTA leaves while others may still read its shared memory
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   c.end();
 }
 
 // ----------------------------------------------------------------------------- host side
-
-template <bool F8, int NT>
-int down_clusters(int size) {
-  static std::mutex mu;
-  static int cache[kMoeMaxSplits + 1] = {};
-  std::lock_guard<std::mutex> lock(mu);
-  if (cache[size] == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(size * 64);
-    cfg.blockDim = dim3(kMoeThreads);
-    cfg.dynamicSmemBytes = Cta<F8, NT>::kSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, moe_down_kernel<F8, NT>, &cfg) != cudaSuccess || n == 0) {
-      (void)cudaGetLastError();
-      n = -1;
-    }
-    cache[size] = n;
-  }
-  return cache[size];
-}
 
 template <bool F8, int NT>
 cudaError_t run_experts(MoeArgs& a, cudaStream_t st) {
@@ -804,25 +798,10 @@ cudaError_t run_experts(MoeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch(moe_act_kernel<F8>, dim3((rows + kWarps - 1) / kWarps), dim3(kMoeFlat), 0, st, true, a);
   if (e != cudaSuccess) return e;
-  // K splits of a tile of the down product: the most with which all clusters run at once
+  // K splits of a tile of the down product: as many CTAs as run at once, each with two chunks if all choices differ
   const int tiles = (a.H + 127) / 128;
-  a.splits = kMoeMaxSplits;
-  while (a.splits > 1 && down_clusters<F8, NT>(a.splits) < tiles) --a.splits;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * a.splits);
-  cfg.blockDim = dim3(kMoeThreads);
-  cfg.dynamicSmemBytes = Cta<F8, NT>::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, moe_down_kernel<F8, NT>, a);
+  a.splits = std::max(1, std::min({a.ctas / tiles, kMoeMaxSplits, rows / 2}));
+  return launch(moe_down_kernel<F8, NT>, dim3(tiles * a.splits), dim3(kMoeThreads), Cta<F8, NT>::kSmem, st, true, a);
 }
 
 template <bool F8, int NT>
@@ -857,6 +836,7 @@ int moe_experts(const MoeCall& c, int sms, cudaStream_t st, const char** why) {
   a.out = c.out;
   const MoeWorkspace w = moe_workspace(c.T, c.k, c.H, c.I);
   a.plan = reinterpret_cast<Plan*>(c.ws);
+  a.arrived = reinterpret_cast<uint32_t*>(c.ws + kMoePlanBytes);
   a.main = reinterpret_cast<float*>(c.ws + w.main);
   a.cut = reinterpret_cast<float*>(c.ws + w.cut);
   a.xb = c.ws + w.xb;
