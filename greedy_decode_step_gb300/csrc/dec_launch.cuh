@@ -68,6 +68,8 @@ bool make_tmap_sw128(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
 // box_rows of one matrix, 128-byte swizzle (false if the driver refuses it).
 bool make_tmap_mats(CUtensorMap* m, const void* base, int bytes, uint64_t inner, uint64_t rows, uint64_t mats,
                     uint32_t box_rows);
+// fp32 [rows][inner], rows ld elements apart (16-byte aligned): box 32 x 32, 128-byte swizzle, for stores.
+bool make_tmap_out(CUtensorMap* m, float* base, uint64_t inner, uint64_t rows, uint64_t ld);
 
 // Batched prompt pass (prefill.cu): rows are (sequence, position) pairs.
 cudaError_t launch_prefill_embed(const int32_t* prompt, int P, int i0, int n, int rows, int H, const uint16_t* embed,

@@ -240,31 +240,32 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
 
 // ----------------------------------------------------------------------------- wide: rows of x on the lanes
 
-constexpr int kWideThreads = 384;   // warp 0 copies, warp 1 multiplies, warps 4-11 scale and store
+constexpr int kWideThreads = 384;   // warp 0 copies, 1 and 2 multiply, 4-11 scale and store
 constexpr int kWideBN = 256;
-constexpr int kWideStages = 4;
+constexpr int kWideStages = 3;      // a fourth would leave no room for the second buffer of results
 constexpr uint32_t kWideStage = kF8Tile + kWideBN * kF8BK;  // 48 KB
-constexpr int kWidePitch = 20;      // floats of a staged row of 16: rows 4 banks apart
-constexpr uint32_t kWideOut = 8 * 32 * kWidePitch * 4;
+constexpr uint32_t kWideOut = 8 * 2 * 32 * 128;  // twice 32 rows of 32 results per warp, on their way out
 constexpr uint32_t kWideSmem = 1024 + kF8Head + kWideStages * kWideStage + kWideOut;
 
 struct WideArgs {
   CUtensorMap wmap, xmap;  // box 256 rows of wc, 128 rows of xc
+  CUtensorMap omap;        // of the result, if `bulk`
   const float *sx, *sw, *residual;
   float* out;
   long long ldr, ldo;
   int M, N, KB, NB, m_tiles, tiles;
-  int vec;  // rows of the result (and the residual) are 16-byte aligned
+  int bulk;    // rows of the result are 16-byte aligned: tensor copies store them
+  int vec;     // and rows of the residual, if any
   uint32_t* err;
 };
 
 __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_constant__ WideArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // done: a stage's products are in its accumulator, and the stage may be filled anew
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
-  uint64_t* empty = full + kWideStages;
-  uint64_t* accum = empty + kWideStages;
-  uint64_t* drained = accum + 2;
+  uint64_t* done = full + kWideStages;
+  uint64_t* drained = done + kWideStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);  // a wait ran out: every role ends
   unsigned char* tiles = smem + kF8Head;
@@ -273,12 +274,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   if (threadIdx.x == 0) {
     for (int s = 0; s < kWideStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&done[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&accum[s], 1);
-      mbar_init(&drained[s], 8);
-    }
+    for (int s = 0; s < 2; ++s) mbar_init(&drained[s], 8);
     *stop = 0;
     fence_mbar_init();
   }
@@ -289,53 +287,58 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
+  // 128 threads x 40 + 256 x 232 registers = the 384 x 168 of the launch
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
 
-  if (warp < 4) {
-    // 128 threads x 72 + 256 x 216 registers = the 384 x 168 of the launch
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0 && lane == 0) {
-      const uint64_t keep = l2_policy_evict_last();
-      int it = 0;
-      for (int tile = blockIdx.x; tile < a.tiles && !*stop; tile += gridDim.x) {
-        const int m0 = (tile % a.m_tiles) * kF8BM, n0 = (tile / a.m_tiles) * kWideBN;
-        for (int kb = 0; kb < a.KB; ++kb, ++it) {
-          const int s = it % kWideStages;
-          if (it >= kWideStages && !mbar_wait(&empty[s], ((it / kWideStages) - 1) & 1, stop, a.err, kErrWaitEmpty)) *stop = 1;
-          if (*stop) break;
+  if (warp == 0) {
+    const uint64_t keep = l2_policy_evict_last();
+    int it = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
+      const int m0 = (tile % a.m_tiles) * kF8BM, n0 = (tile / a.m_tiles) * kWideBN;
+      for (int kb = 0; kb < a.KB; ++kb, ++it) {
+        const int s = it % kWideStages;
+        if (it >= kWideStages) ok = warp_wait(&done[s], ((it / kWideStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
+        if (!ok) break;
+        if (elect_one()) {
           unsigned char* st = tiles + s * kWideStage;
           mbar_arrive_expect_tx(&full[s], kWideStage);
           tma_load_3d(st, &a.xmap, kb * kF8BK, m0, 0, &full[s], keep);
           tma_load_3d(st + kF8Tile, &a.wmap, kb * kF8BK, n0, 0, &full[s], keep);
         }
       }
-      if (*stop)  // an early end waits for its own copies
-        for (int i = max(0, it - kWideStages); i < it; ++i)
-          if (!tc_wait(&full[i % kWideStages], (i / kWideStages) & 1, a.err, kErrDrain)) break;
-    } else if (warp == 1 && lane == 0) {
-      constexpr uint32_t idesc = tc_idesc_of(kWideBN, false);
-      int it = 0;
-      for (int tile = blockIdx.x; tile < a.tiles && !*stop; tile += gridDim.x) {
-        for (int kb = 0; kb < a.KB; ++kb, ++it) {
-          const int s = it % kWideStages, b = it & 1;
-          if (!mbar_wait(&full[s], (it / kWideStages) & 1, stop, a.err, kErrWaitFull) ||
-              (it >= 2 && !mbar_wait(&drained[b], ((it >> 1) - 1) & 1, stop, a.err, kErrWaitFull)))
-            *stop = 1;
-          if (*stop) break;
-          tc_fence_after();
-          const uint32_t sa = smem_addr(tiles + s * kWideStage);
-#pragma unroll
-          for (int kk = 0; kk < kF8BK / 32; ++kk)
-            tc_mma_f8(tmem + b * kWideBN, smem_desc_sw128(sa + kk * 32), smem_desc_sw128(sa + kF8Tile + kk * 32), idesc,
-                      kk > 0);
-          tc_commit(&empty[s]);
-          tc_commit(&accum[b]);
-        }
-      }
     }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if (!ok && lane == 0) {  // an early end waits for its own copies
+      *stop = 1;
+      for (int i = max(0, it - kWideStages); i < it; ++i)
+        if (!tc_wait(&full[i % kWideStages], (i / kWideStages) & 1, a.err, kErrDrain)) break;
+    }
+  } else if (warp == 1 || warp == 2) {
+    // every second block each, so that one waits for its next while the other's products are being issued
+    constexpr uint32_t idesc = tc_idesc_of(kWideBN, false);
+    const int b = warp - 1;
+    const int mine = (a.tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    bool ok = true;
+    for (int it = b; it < mine * a.KB; it += 2) {
+      const int s = it % kWideStages;
+      ok = warp_wait(&full[s], (it / kWideStages) & 1, stop, a.err, kErrWaitFull) &&
+           (it < 2 || warp_wait(&drained[b], ((it >> 1) - 1) & 1, stop, a.err, kErrWaitFull));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sa = smem_addr(tiles + s * kWideStage);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kF8BK / 32; ++kk)
+          tc_mma_f8(tmem + b * kWideBN, smem_desc_sw128(sa + kk * 32), smem_desc_sw128(sa + kF8Tile + kk * 32), idesc, kk > 0);
+        tc_commit(&done[s]);
+      }
+      __syncwarp();
+    }
+    if (!ok) *stop = 1;
+  } else if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., columns 128 half ..
-    float* stage = reinterpret_cast<float*>(tiles + kWideStages * kWideStage) + (warp - 4) * 32 * kWidePitch;
+    unsigned char* stages = tiles + kWideStages * kWideStage + (warp - 4) * 2 * 32 * 128;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * 128;
     int it = 0;
     for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
@@ -345,29 +348,35 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-      // the scales of the next block are on their way while this one is added
-      float nx = __ldg(sx), nw = __ldg(sw);
-      int ok = 1;
+      // the scales of the next two blocks are on their way while this one is added
+      float x0 = __ldg(sx), w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
+      if (a.KB > 1) {
+        x1 = __ldg(sx + 1);
+        w1 = __ldg(sw + 1);
+      }
+      bool ok = true;
       for (int kb = 0; kb < a.KB; ++kb, ++it) {
         const int b = it & 1;
-        const float s = nx * nw;
-        if (kb + 1 < a.KB) {
-          nx = __ldg(sx + kb + 1);
-          nw = __ldg(sw + kb + 1);
+        const float s = x0 * w0;
+        x0 = x1;
+        w0 = w1;
+        if (kb + 2 < a.KB) {
+          x1 = __ldg(sx + kb + 2);
+          w1 = __ldg(sw + kb + 2);
         }
-        if (lane == 0) ok = (mbar_wait(&accum[b], (it >> 1) & 1, stop, a.err, kErrWaitFull) && !*stop) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = warp_wait(&done[it % kWideStages], (it / kWideStages) & 1, stop, a.err, kErrWaitFull);
         if (!ok) break;
         tc_fence_after();
-        uint32_t v[2][16];
-        tmem_ld_issue(at + b * kWideBN, v[0]);
-        tmem_ld_wait(v[0]);
+        // 64 columns asked for at once, added while the next 32 come
+        uint32_t v[2][32];
+        tmem_ld_issue32(at + b * kWideBN, v[0]);
+        tmem_ld_wait32(v[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (c + 1 < 8) tmem_ld_issue(at + b * kWideBN + 16 * (c + 1), v[(c + 1) & 1]);
+        for (int c = 0; c < 4; ++c) {
+          if (c + 1 < 4) tmem_ld_issue32(at + b * kWideBN + 32 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[16 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, acc[16 * c + j]);
-          if (c + 1 < 8) tmem_ld_wait(v[(c + 1) & 1]);
+          for (int j = 0; j < 32; ++j) acc[32 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, acc[32 * c + j]);
+          if (c + 1 < 4) tmem_ld_wait32(v[(c + 1) & 1]);
         }
         tc_fence_before();
         __syncwarp();
@@ -377,41 +386,60 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
         *stop = 1;
         break;
       }
-      // 16 columns at a time through shared memory, so that 4 lanes write 64 consecutive bytes of a row
+      // 32 columns at a time through shared memory (rows of 128 bytes, their 16-byte pieces swizzled), so that whole
+      // lines leave: by a tensor copy, which runs beside the next tile, or by 8 lanes a row
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int n = n0 + 16 * c;
-        if (n < a.N) {  // warp-uniform
+      for (int c = 0; c < 4; ++c) {
+        const int n = n0 + 32 * c;
+        if (n < a.N && m0 < a.M) {  // warp-uniform
+          unsigned char* stage = stages + (c & 1) * 32 * 128;
+          if (a.bulk) tma_store_wait_read<1>();  // the one before last has left this buffer
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4*>(stage + lane * kWidePitch + 4 * j) =
-                make_float4(acc[16 * c + 4 * j], acc[16 * c + 4 * j + 1], acc[16 * c + 4 * j + 2], acc[16 * c + 4 * j + 3]);
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(
+                acc[32 * c + 4 * j], acc[32 * c + 4 * j + 1], acc[32 * c + 4 * j + 2], acc[32 * c + 4 * j + 3]);
           __syncwarp();
-          const int col = n + 4 * (lane & 3);
+          const int piece = lane & 7, col = n + 4 * piece;
+          if (!a.bulk || a.residual) {
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const int rr = 8 * p + (lane >> 2), r = m0 + rr;
-            float4 v = *reinterpret_cast<const float4*>(stage + rr * kWidePitch + 4 * (lane & 3));
-            if (r >= a.M || col >= a.N) continue;
-            float* dst = a.out + r * a.ldo + col;
-            const float* add = a.residual ? a.residual + r * a.ldr + col : nullptr;
-            if (a.vec && col + 4 <= a.N) {
-              if (add) {
-                const float4 w = *reinterpret_cast<const float4*>(add);
-                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            for (int p = 0; p < 8; ++p) {
+              const int rr = 4 * p + (lane >> 3), r = m0 + rr;
+              float4* at4 = reinterpret_cast<float4*>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
+              float4 v = *at4;
+              if (r >= a.M || col >= a.N) continue;
+              const float* add = a.residual ? a.residual + r * a.ldr + col : nullptr;
+              if (a.vec && col + 4 <= a.N) {
+                if (add) {
+                  const float4 w = *reinterpret_cast<const float4*>(add);
+                  v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+                }
+              } else if (add) {
+                v.x += add[0];
+                if (col + 1 < a.N) v.y += add[1];
+                if (col + 2 < a.N) v.z += add[2];
+                if (col + 3 < a.N) v.w += add[3];
               }
-              *reinterpret_cast<float4*>(dst) = v;
-            } else {
-              const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (col + j < a.N) dst[j] = e[j] + (add ? add[j] : 0.f);
+              if (a.bulk) {
+                *at4 = v;
+              } else {
+                float* dst = a.out + r * a.ldo + col;
+                dst[0] = v.x;
+                if (col + 1 < a.N) dst[1] = v.y;
+                if (col + 2 < a.N) dst[2] = v.z;
+                if (col + 3 < a.N) dst[3] = v.w;
+              }
             }
+          }
+          if (a.bulk) {
+            fence_to_async();
+            __syncwarp();
+            if (lane == 0) tma_store_2d(&a.omap, stage, n, m0);  // the lane that waits for it
           }
         }
       }
     }
+    if (a.bulk) tma_store_wait_read<0>();  // its memory is in use until then
   }
   __syncwarp();
   tc_fence_before();
@@ -531,7 +559,12 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
   a.tiles = a.m_tiles * ((c.N + kWideBN - 1) / kWideBN);
   a.err = c.err;
   auto rows16 = [](const void* p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 4 == 0; };
-  a.vec = rows16(c.out, c.ldo) && (!c.residual || rows16(c.residual, c.ldr));
+  a.bulk = rows16(c.out, c.ldo) && c.N % 4 == 0;  // a tensor copy cuts a row off at whole 16 bytes only
+  a.vec = c.residual && rows16(c.residual, c.ldr);
+  if (a.bulk && !make_tmap_out(&a.omap, c.out, c.N, c.M, c.ldo)) {
+    *why = "a tensor map could not be made";
+    return cudaErrorInvalidValue;
+  }
   return launch(fp8_wide_kernel, dim3(std::min(a.tiles, sms)), dim3(kWideThreads), kWideSmem, st, true, a);
 }
 
