@@ -53,12 +53,25 @@ constexpr int kNarrowThreads = 192;
 constexpr int kNarrowMaxStages = 12;
 constexpr int kNarrowMaxSplits = 8;
 
+constexpr uint32_t kNarrowSmemMax = 112 * 1024;  // two CTAs per SM
+
+template <int BN>
+constexpr int narrow_stages() {
+  constexpr uint32_t max = BN <= 64 ? kNarrowSmemMax : 2 * kNarrowSmemMax;
+  constexpr int fit = static_cast<int>((max - 1024 - kNarrowHead) / (kF8Tile + BN * kF8BK));
+  return fit < kNarrowMaxStages ? fit : kNarrowMaxStages;
+}
+template <int BN>
+constexpr uint32_t narrow_smem() {
+  return 1024 + kNarrowHead + narrow_stages<BN>() * (kF8Tile + BN * kF8BK);
+}
+
 struct NarrowArgs {
   CUtensorMap wmap, xmap;  // box 128 rows of wc, BN rows of xc
   const float *sx, *sw, *residual;
   float* out;
   long long ldr, ldo;
-  int M, N, KB, n_tiles, splits, stages;
+  int M, N, KB, n_tiles, splits;
   uint32_t* err;
 };
 
@@ -75,6 +88,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
   float(*scales)[BN] = reinterpret_cast<float(*)[BN]>(smem + kF8Head);
   unsigned char* tiles = smem + kNarrowHead;
   constexpr uint32_t kXTile = BN * kF8BK, kStage = kF8Tile + kXTile;
+  constexpr int kStages = narrow_stages<BN>();
   constexpr uint32_t kCols = tmem_columns(2 * BN);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
@@ -84,7 +98,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
   const int nkb = static_cast<int>(static_cast<long long>(split + 1) * a.KB / a.splits) - kb0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -102,50 +116,63 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t wpol = l2_policy_evict_first(), xpol = l2_policy_evict_last();
-      // weights (no kernel writes them) go out before the wait for the kernel that makes the rows
-      const int pre = min(nkb, a.stages);
+    const uint64_t wpol = l2_policy_evict_first(), xpol = l2_policy_evict_last();
+    auto bring_w = [&](int i) {
+      tma_load_3d(tiles + i % kStages * kStage, &a.wmap, (kb0 + i) * kF8BK, m0, 0, &full[i % kStages], wpol);
+    };
+    auto bring_x = [&](int i) {
+      tma_load_3d(tiles + i % kStages * kStage + kF8Tile, &a.xmap, (kb0 + i) * kF8BK, r0, 0, &full[i % kStages], xpol);
+    };
+    // weights (no kernel writes them) go out before the wait for the kernel that makes the rows
+    const int pre = min(nkb, kStages);
+    if (elect_one())
       for (int i = 0; i < pre; ++i) {
         mbar_arrive_expect_tx(&full[i], kStage);
-        tma_load_3d(tiles + i * kStage, &a.wmap, (kb0 + i) * kF8BK, m0, 0, &full[i], wpol);
+        bring_w(i);
       }
-      pdl_wait();
-      pdl_launch_dependents();
-      for (int i = 0; i < pre; ++i)
-        tma_load_3d(tiles + i * kStage + kF8Tile, &a.xmap, (kb0 + i) * kF8BK, r0, 0, &full[i], xpol);
-      int issued = pre;
-      for (; issued < nkb; ++issued) {
-        const int s = issued % a.stages;
-        if (!mbar_wait(&empty[s], ((issued / a.stages) - 1) & 1, stop, a.err, kErrWaitEmpty)) *stop = 1;
-        if (*stop) break;
-        mbar_arrive_expect_tx(&full[s], kStage);
-        tma_load_3d(tiles + s * kStage, &a.wmap, (kb0 + issued) * kF8BK, m0, 0, &full[s], wpol);
-        tma_load_3d(tiles + s * kStage + kF8Tile, &a.xmap, (kb0 + issued) * kF8BK, r0, 0, &full[s], xpol);
+    __syncwarp();
+    pdl_wait();
+    pdl_launch_dependents();
+    if (elect_one())
+      for (int i = 0; i < pre; ++i) bring_x(i);
+    __syncwarp();
+    int it = pre;
+    bool ok = true;
+    for (; it < nkb; ++it) {
+      ok = warp_wait(&empty[it % kStages], ((it / kStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
+      if (!ok) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[it % kStages], kStage);
+        bring_w(it);
+        bring_x(it);
       }
-      // an early end waits for its own copies
-      if (*stop)
-        for (int i = max(0, issued - a.stages); i < issued; ++i)
-          if (!tc_wait(&full[i % a.stages], (i / a.stages) & 1, a.err, kErrDrain)) break;
+      __syncwarp();
+    }
+    if (!ok && lane == 0) {  // an early end waits for its own copies
+      *stop = 1;
+      for (int i = max(0, it - kStages); i < it; ++i)
+        if (!tc_wait(&full[i % kStages], (i / kStages) & 1, a.err, kErrDrain)) break;
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = tc_idesc_of(BN, false);
-      for (int i = 0; i < nkb; ++i) {
-        const int s = i % a.stages, b = i & 1;
-        if (!mbar_wait(&full[s], (i / a.stages) & 1, stop, a.err, kErrWaitFull) ||
-            (i >= 2 && !mbar_wait(&drained[b], ((i >> 1) - 1) & 1, stop, a.err, kErrWaitFull)))
-          *stop = 1;
-        if (*stop) break;
-        tc_fence_after();
-        const uint32_t sa = smem_addr(tiles + s * kStage);
+    constexpr uint32_t idesc = tc_idesc_of(BN, false);
+    bool ok = true;
+    for (int i = 0; i < nkb; ++i) {
+      const int s = i % kStages, b = i & 1;
+      ok = warp_wait(&full[s], (i / kStages) & 1, stop, a.err, kErrWaitFull) &&
+           (i < 2 || warp_wait(&drained[b], ((i >> 1) - 1) & 1, stop, a.err, kErrWaitFull));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sa = smem_addr(tiles + s * kStage);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kF8BK / 32; ++kk)
           tc_mma_f8(tmem + b * BN, smem_desc_sw128(sa + kk * 32), smem_desc_sw128(sa + kF8Tile + kk * 32), idesc, kk > 0);
         tc_commit(&empty[s]);
         tc_commit(&accum[b]);
       }
+      __syncwarp();
     }
+    if (!ok) *stop = 1;
   } else {
     pdl_wait();
     const int q = warp & 3, t = threadIdx.x - 64;
@@ -168,9 +195,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
         nw = __ldg(sw + i + 1);
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      int good = 1;
-      if (lane == 0) good = (mbar_wait(&accum[b], (i >> 1) & 1, stop, a.err, kErrWaitFull) && !*stop) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+      ok = warp_wait(&accum[b], (i >> 1) & 1, stop, a.err, kErrWaitFull);
       if (!ok) *stop = 1;
       tc_fence_after();
       if (ok) {
@@ -452,19 +477,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
 
 // ----------------------------------------------------------------------------- host side
 
-constexpr uint32_t kNarrowSmemMax = 112 * 1024;  // two CTAs per SM
-
-template <int BN>
-constexpr int narrow_stages() {
-  constexpr uint32_t max = BN <= 64 ? kNarrowSmemMax : 2 * kNarrowSmemMax;
-  constexpr int fit = static_cast<int>((max - 1024 - kNarrowHead) / (kF8Tile + BN * kF8BK));
-  return fit < kNarrowMaxStages ? fit : kNarrowMaxStages;
-}
-template <int BN>
-constexpr uint32_t narrow_smem() {
-  return 1024 + kNarrowHead + narrow_stages<BN>() * (kF8Tile + BN * kF8BK);
-}
-
 // Clusters of `size` CTAs that the device holds at once (cached; -1 where the query fails).
 template <int BN>
 int narrow_clusters(int size) {
@@ -512,7 +524,6 @@ cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const 
   a.KB = (c.K + kF8BK - 1) / kF8BK;
   a.n_tiles = (c.M + BN - 1) / BN;
   a.err = c.err;
-  a.stages = narrow_stages<BN>();
   const long long tiles = static_cast<long long>(a.n_tiles) * ((c.N + kF8BM - 1) / kF8BM);
   // K splits: double while every split keeps two blocks and all clusters run at once
   const long long slots = static_cast<long long>(sms) * (BN <= 64 ? 2 : 1);

@@ -421,26 +421,26 @@ struct Cta {
       tmem_free(tmem, kCols);
     }
   }
-  // Whole warp: waits in lane 0, one answer for all.
-  __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) const {
-    int ok = 1;
-    if (threadIdx.x % 32 == 0) ok = (mbar_wait(bar, parity, stop, err, code) && !*stop) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-  }
-  // One lane of either weight warp: its half (64 rows) of a free stage for
-  // chunk `it`, null when a wait ran out.
-  __device__ __forceinline__ unsigned char* claim(int it, int half, uint32_t* err) const {
+  // Whole warp, of either weight warp: a free stage for chunk `it`; false when a wait ran out.
+  __device__ __forceinline__ bool claim(int it, uint32_t* err) const {
     const int s = it % kStages;
-    if (it >= kStages && !mbar_wait(&emptyA[s], ((it / kStages) - 1) & 1, stop, err, kErrWaitEmpty)) *stop = 1;
-    if (*stop) return nullptr;
-    mbar_arrive_expect_tx(&fullA[s], kMoeATile / 2);
-    return A + s * kMoeATile + half * (kMoeATile / 2);
+    if (it >= kStages && !warp_wait(&emptyA[s], ((it / kStages) - 1) & 1, stop, err, kErrWaitEmpty)) {
+      *stop = 1;
+      return false;
+    }
+    return true;
+  }
+  // One lane: half (64 rows) of chunk `it`'s weights from (x, y, z) of a map.
+  __device__ __forceinline__ void bring(int it, int half, const CUtensorMap* map, int x, int y, int z, uint64_t pol) const {
+    uint64_t* bar = &fullA[it % kStages];
+    mbar_arrive_expect_tx(bar, kMoeATile / 2);
+    tma_load_3d(A + it % kStages * kMoeATile + half * (kMoeATile / 2), map, x, y, z, bar, pol);
   }
   // Whole warp: waits until chunk `it`'s activations may be brought; `sizes` holds the slots of the chunks in turn, one
   // byte each, `tail` is the oldest that holds some, `room` the free slots.  False when a wait ran out.
   __device__ __forceinline__ bool make_room(int it, int used, uint64_t& sizes, int& tail, int& room, uint32_t* err) const {
     while (room < used || it - tail >= kMoeTurns) {
-      if (!warp_wait(&emptyB[tail % kMoeTurns], (tail / kMoeTurns) & 1, err, kErrWaitEmpty)) {
+      if (!warp_wait(&emptyB[tail % kMoeTurns], (tail / kMoeTurns) & 1, stop, err, kErrWaitEmpty)) {
         *stop = 1;
         return false;
       }
@@ -452,34 +452,37 @@ struct Cta {
     sizes = (sizes & ~(0xFFull << at)) | (static_cast<uint64_t>(used) << at);
     return true;
   }
-  // One lane: the MMAs of chunk `it` with n tokens in slot b; false when a wait ran out.
+  // Whole warp: the MMAs of chunk `it` with n tokens in slot b; false when a wait ran out.
   __device__ __forceinline__ bool multiply(int it, int n, int b, uint32_t* err) const {
     const int s = it % kStages, acc = it % kAccs;
-    if (!mbar_wait(&fullA[s], (it / kStages) & 1, stop, err, kErrWaitFull) ||
-        !mbar_wait(&fullB[it % kMoeTurns], (it / kMoeTurns) & 1, stop, err, kErrWaitFull) ||
-        (it >= kAccs && !mbar_wait(&drained[acc], ((it / kAccs) - 1) & 1, stop, err, kErrWaitFull)) || *stop) {
+    if (!warp_wait(&fullA[s], (it / kStages) & 1, stop, err, kErrWaitFull) ||
+        !warp_wait(&fullB[it % kMoeTurns], (it / kMoeTurns) & 1, stop, err, kErrWaitFull) ||
+        (it >= kAccs && !warp_wait(&drained[acc], ((it / kAccs) - 1) & 1, stop, err, kErrWaitFull))) {
       *stop = 1;
       return false;
     }
     tc_fence_after();
     const uint32_t sa = smem_addr(A + s * kMoeATile), sb = smem_addr(B + b * kSlot), d = tmem + acc * kAcc;
     const uint32_t idesc = tc_idesc_of(8 * ((n + 1) & ~1), !F8);  // columns of a missing last token hold anything
+    if (elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of K per instruction
-      const uint64_t ad = smem_desc_sw128(sa + kk * 32), bd = smem_desc_sw128(sb + kk * 32);
-      if (F8)
-        tc_mma_f8(d, ad, bd, idesc, kk > 0);
-      else
-        tc_mma(d, ad, bd, idesc, kk > 0);
+      for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of K per instruction
+        const uint64_t ad = smem_desc_sw128(sa + kk * 32), bd = smem_desc_sw128(sb + kk * 32);
+        if (F8)
+          tc_mma_f8(d, ad, bd, idesc, kk > 0);
+        else
+          tc_mma(d, ad, bd, idesc, kk > 0);
+      }
+      tc_commit(&emptyA[s]);
+      tc_commit(&accum[acc]);
     }
-    tc_commit(&emptyA[s]);
-    tc_commit(&accum[acc]);
+    __syncwarp();
     return true;
   }
   // Whole warp: adds chunk `it`'s sums of n tokens in slot b, weights' scale w (1 for bf16); false when a wait ran out.
   __device__ __forceinline__ bool add(int it, int n, int b, float w, float (&sum)[NT], uint32_t* err) const {
     const int acc = it % kAccs;
-    if (!warp_wait(&accum[acc], (it / kAccs) & 1, err, kErrWaitFull)) {
+    if (!warp_wait(&accum[acc], (it / kAccs) & 1, stop, err, kErrWaitFull)) {
       *stop = 1;
       return false;
     }
@@ -544,25 +547,23 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gate_up_kernel(const __gri
 
   using Slots = Ring<Cta<F8, NT>::kSlots>;
   if (warp == 0 || warp == 6) {
-    if (lane == 0) {
-      const int half = warp == 6;
-      const uint64_t pol = l2_policy_evict_first();
-      const CUtensorMap* map = half ? &a.u : &a.g;
-      int it = 0;
-      bool ok = true;
-      for (int pos = lo; pos < hi && ok;) {
-        const int tile = pos / r.kch, j0 = pos - tile * r.kch, n = min(r.kch - j0, hi - pos);
-        const int row = (tile % r.units) * kMoeUnit, e = p.expert[tile / r.units];
-        for (int j = j0; j < j0 + n; ++j, ++it) {
-          unsigned char* to = c.claim(it, half, a.err);
-          ok = to != nullptr;
-          if (!ok) break;
-          tma_load_3d(to, map, j * P::kChunk, row, e, &c.fullA[it % c.kStages], pol);
-        }
-        pos += n;
+    const int half = warp == 6;
+    const uint64_t pol = l2_policy_evict_first();
+    const CUtensorMap* map = half ? &a.u : &a.g;
+    int it = 0;
+    bool ok = true;
+    for (int pos = lo; pos < hi && ok;) {
+      const int tile = pos / r.kch, j0 = pos - tile * r.kch, n = min(r.kch - j0, hi - pos);
+      const int row = (tile % r.units) * kMoeUnit, e = p.expert[tile / r.units];
+      for (int j = j0; j < j0 + n; ++j, ++it) {
+        ok = c.claim(it, a.err);
+        if (!ok) break;
+        if (elect_one()) c.bring(it, half, map, j * P::kChunk, row, e, pol);
+        __syncwarp();
       }
-      if (half == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
+      pos += n;
     }
+    if (half == 0 && lane == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
   } else if (warp == 7) {
     const uint64_t pol = l2_policy_evict_last();
     Slots ring;
@@ -587,15 +588,13 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gate_up_kernel(const __gri
     }
     if (lane == 0) c.drain(c.fullB, kMoeTurns, it - kMoeTurns, it, a.err);
   } else if (warp == 1) {
-    if (lane == 0) {
-      Slots ring;
-      int it = 0, used;
-      bool ok = true;
-      for (int pos = lo; pos < hi && ok;) {
-        const int tile = pos / r.kch, n = min((tile + 1) * r.kch, hi) - pos, count = p.count[tile / r.units];
-        for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, ring.take(count, &used), a.err);
-        pos += n;
-      }
+    Slots ring;
+    int it = 0, used;
+    bool ok = true;
+    for (int pos = lo; pos < hi && ok;) {
+      const int tile = pos / r.kch, n = min((tile + 1) * r.kch, hi) - pos, count = p.count[tile / r.units];
+      for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, ring.take(count, &used), a.err);
+      pos += n;
     }
   } else {
     const int m = (32 * warp + lane) & 127;  // TMEM lane; row of the tile: gate below 64, up from 64 on
@@ -654,22 +653,20 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const __grid_c
 
   using Slots = Ring<Cta<F8, NT>::kSlots>;
   if (warp == 0 || warp == 6) {
-    if (lane == 0) {
-      const int half = warp == 6;
-      const uint64_t pol = l2_policy_evict_first();
-      int act = lo / kch, j = lo - act * kch, it = 0;
-      for (; it < hi - lo; ++it) {
-        unsigned char* to = c.claim(it, half, a.err);
-        if (!to) break;
-        // rows behind the last are filled with zeros
-        tma_load_3d(to, &a.d, j * P::kChunk, m0 + half * 64, p.expert[act], &c.fullA[it % c.kStages], pol);
-        if (++j == kch) {
-          j = 0;
-          ++act;
-        }
+    const int half = warp == 6;
+    const uint64_t pol = l2_policy_evict_first();
+    int act = lo / kch, j = lo - act * kch, it = 0;
+    for (; it < hi - lo; ++it) {
+      if (!c.claim(it, a.err)) break;
+      // rows behind the last are filled with zeros
+      if (elect_one()) c.bring(it, half, &a.d, j * P::kChunk, m0 + half * 64, p.expert[act], pol);
+      __syncwarp();
+      if (++j == kch) {
+        j = 0;
+        ++act;
       }
-      if (half == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
     }
+    if (half == 0 && lane == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
   } else if (warp == 7) {
     pdl_wait();  // the inner vectors
     const uint64_t pol = l2_policy_evict_last();
@@ -684,25 +681,24 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const __grid_c
         const int at = ring.take(count, &used);
         ok = c.make_room(it, used, sizes, tail, room, a.err);
         if (!ok) break;
-        if (lane == 0) {  // a chunk's blocks lie side by side
+        if (elect_one()) {  // a chunk's blocks lie side by side
           const uint32_t bytes = (count - 1) * kMoeBlock + P::kCopy;
           mbar_arrive_expect_tx(&c.fullB[it % kMoeTurns], bytes);
           bulk_copy_g2s(c.B + at * c.kSlot, src, bytes, &c.fullB[it % kMoeTurns], pol);
         }
+        __syncwarp();
       }
       pos += n;
     }
     if (lane == 0) c.drain(c.fullB, kMoeTurns, it - kMoeTurns, it, a.err);
   } else if (warp == 1) {
-    if (lane == 0) {
-      Slots ring;
-      int it = 0, used;
-      bool ok = true;
-      for (int pos = lo; pos < hi && ok;) {
-        const int act = pos / kch, n = min((act + 1) * kch, hi) - pos, count = p.count[act];
-        for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, ring.take(count, &used), a.err);
-        pos += n;
-      }
+    Slots ring;
+    int it = 0, used;
+    bool ok = true;
+    for (int pos = lo; pos < hi && ok;) {
+      const int act = pos / kch, n = min((act + 1) * kch, hi) - pos, count = p.count[act];
+      for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, ring.take(count, &used), a.err);
+      pos += n;
     }
   } else {
     const int m = (32 * warp + lane) & 127, HB = (a.H + kFp8Block - 1) / kFp8Block;
