@@ -55,43 +55,39 @@ __device__ __forceinline__ float scaled(float x, float inv) {
 }
 
 template <bool BF16>
-struct Vec {  // 16 bytes of a source row
+struct Vec {  // 16 bytes of a source row, as they came
   static constexpr int kN = BF16 ? 8 : 4;
-  float v[kN];
-  __device__ __forceinline__ void load(const void* p) {
-    const uint4 w = __ldg(static_cast<const uint4*>(p));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (BF16) {
-        v[2 * i] = bf16lo(u[i]);
-        v[2 * i + 1] = bf16hi(u[i]);
-      } else {
-        v[i] = __uint_as_float(u[i]);
-      }
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] = 0.f;
+  uint4 w;
+  __device__ __forceinline__ void load(const void* p) { w = __ldg(static_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float value(int i) const {
+    const uint32_t u = BF16 ? (i / 2 == 0 ? w.x : i / 2 == 1 ? w.y : i / 2 == 2 ? w.z : w.w)
+                            : (i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
+    return BF16 ? (i & 1 ? bf16hi(u) : bf16lo(u)) : __uint_as_float(u);
   }
   __device__ __forceinline__ uint32_t top() const {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) m = max(m, finite_magnitude(v[i]));
+    for (int i = 0; i < kN; ++i) m = max(m, finite_magnitude(value(i)));
     return m;
   }
   __device__ __forceinline__ void store(uint8_t* p, float inv) const {
-    uint32_t w[kN / 4];
+    uint32_t c[kN / 4];
 #pragma unroll
     for (int i = 0; i < kN / 4; ++i)
-      w[i] = e4m3_pair(scaled(v[4 * i], inv), scaled(v[4 * i + 1], inv)) |
-             (e4m3_pair(scaled(v[4 * i + 2], inv), scaled(v[4 * i + 3], inv)) << 16);
+      c[i] = e4m3_pair(scaled(value(4 * i), inv), scaled(value(4 * i + 1), inv)) |
+             (e4m3_pair(scaled(value(4 * i + 2), inv), scaled(value(4 * i + 3), inv)) << 16);
     if (kN == 8)
-      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[kN / 4 - 1]);
+      *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[kN / 4 - 1]);
     else
-      *reinterpret_cast<uint32_t*>(p) = w[0];
+      *reinterpret_cast<uint32_t*>(p) = c[0];
   }
+};
+
+// Rows of one launch: flat row f0 + i of all matrices' rows laid end to end.
+// Launches are cut so that every index below fits 32 bits.
+struct Slice {
+  uint32_t mat, row, rows;  // first matrix, first row in it, rows
 };
 
 template <bool BF16>
@@ -99,32 +95,30 @@ __device__ __forceinline__ const char* source(const Fp8QuantArgs& a, long long m
   return static_cast<const char*>(a.x) + (mat * a.sm + row * a.sr + k) * (BF16 ? 2 : 4);
 }
 
-// 1 x 128 blocks: LANES lanes per block, kUnroll blocks of a lane in flight.
+// 1 x 128 blocks: 128 / kN lanes per block, kUnroll blocks of a lane in flight.
 template <bool BF16>
-__global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const Fp8QuantArgs a) {
+__global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const Fp8QuantArgs a, const Slice s) {
   constexpr int kN = Vec<BF16>::kN, kLanes = kFp8Block / kN, kPer = kQuantThreads / kLanes, kUnroll = 4;
   pdl_wait();
   pdl_launch_dependents();
-  const int KB = (a.K + kFp8Block - 1) / kFp8Block;
-  const long long blocks = static_cast<long long>(a.n) * a.rows * KB;
+  const uint32_t KB = (a.K + kFp8Block - 1) / kFp8Block, blocks = s.rows * KB;
   const int sub = threadIdx.x / kLanes, in = threadIdx.x % kLanes;
   // consecutive blocks of a CTA lie side by side in memory; the loop's bound is CTA-uniform, so that the shuffles
   // below are met by whole warps
-  for (long long b0 = static_cast<long long>(blockIdx.x) * kPer * kUnroll; b0 < blocks;
-       b0 += static_cast<long long>(gridDim.x) * kPer * kUnroll) {
+  for (uint32_t b0 = blockIdx.x * (kPer * kUnroll); b0 < blocks; b0 += gridDim.x * (kPer * kUnroll)) {
     Vec<BF16> x[kUnroll];
-    long long row[kUnroll];
+    long long flat[kUnroll];  // row among all codes, or -1
     int k[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const long long b = b0 + u * kPer + sub;
-      row[u] = b < blocks ? b / KB : -1;
-      k[u] = static_cast<int>(b - row[u] * KB) * kFp8Block + in * kN;
-      if (row[u] >= 0 && k[u] < a.K) {
-        const long long mat = row[u] / a.rows;
-        x[u].load(source<BF16>(a, mat, row[u] - mat * a.rows, k[u]));
-      } else {
-        x[u].zero();
+      const uint32_t b = b0 + u * kPer + sub, i = b / KB;
+      k[u] = static_cast<int>(b - i * KB) * kFp8Block + in * kN;
+      flat[u] = -1;
+      x[u].zero();
+      if (b < blocks) {
+        const uint32_t r = s.row + i, m = r / a.rows;
+        flat[u] = static_cast<long long>(s.mat) * a.rows + r;
+        if (k[u] < a.K) x[u].load(source<BF16>(a, s.mat + m, r - m * a.rows, k[u]));
       }
     }
 #pragma unroll
@@ -133,93 +127,110 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const Fp8Quan
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const uint32_t e = scale_exponent(top);
-      if (row[u] < 0) continue;
-      if (k[u] < a.K) x[u].store(a.codes + row[u] * a.K + k[u], __uint_as_float((254u - e) << 23));
-      if (in == 0) a.scales[row[u] * KB + k[u] / kFp8Block] = __uint_as_float(e << 23);
+      if (flat[u] < 0) continue;
+      if (k[u] < a.K) x[u].store(a.codes + flat[u] * a.K + k[u], __uint_as_float((254u - e) << 23));
+      if (in == 0) a.scales[flat[u] * KB + k[u] / kFp8Block] = __uint_as_float(e << 23);
     }
   }
 }
 
-// 128 x 128 blocks: one CTA per block.
 template <bool BF16>
-__global__ void __launch_bounds__(kQuantThreads) quant_tiles_kernel(const Fp8QuantArgs a) {
+constexpr int kTileCtas = BF16 ? 3 : 2;  // per SM
+
+// 128 x 128 blocks: one CTA per block, which it holds in registers as it came.
+template <bool BF16>
+__global__ void __launch_bounds__(kQuantThreads, kTileCtas<BF16>) quant_tiles_kernel(const Fp8QuantArgs a) {
   constexpr int kN = Vec<BF16>::kN, kLanes = kFp8Block / kN, kRows = kQuantThreads / kLanes, kUnroll = kFp8Block / kRows;
-  __shared__ uint32_t tops[kQuantThreads / 32];
+  __shared__ uint32_t tops[2][kQuantThreads / 32];
   pdl_wait();
-  pdl_launch_dependents();
+  // no early start for the next launch: it may read these as weights, ahead of its own wait
   const int KB = (a.K + kFp8Block - 1) / kFp8Block, RB = (a.rows + kFp8Block - 1) / kFp8Block;
   const long long tiles = static_cast<long long>(a.n) * RB * KB;
   const int sub = threadIdx.x / kLanes, in = threadIdx.x % kLanes;
-  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+  int turn = 0;
+  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
     const long long mb = tile / KB, mat = mb / RB;
     const int k = static_cast<int>(tile - mb * KB) * kFp8Block + in * kN;
-    const long long r0 = (mb - mat * RB) * kFp8Block + sub;
+    const int r0 = static_cast<int>(mb - mat * RB) * kFp8Block + sub;
     Vec<BF16> x[kUnroll];
-    uint32_t top = 0;
+    const char* src = source<BF16>(a, mat, r0, k);
+    const long long step = kRows * a.sr * (BF16 ? 2 : 4);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (r0 + u * kRows < a.rows && k < a.K)
-        x[u].load(source<BF16>(a, mat, r0 + u * kRows, k));
+        x[u].load(src + u * step);
       else
         x[u].zero();
     }
+    uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) top = max(top, x[u].top());
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) tops[threadIdx.x / 32] = top;
-    __syncthreads();
+    if ((threadIdx.x & 31) == 0) tops[turn][threadIdx.x / 32] = top;
+    __syncthreads();  // two sets of maxima in turn: one barrier a block
 #pragma unroll
-    for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, tops[w]);
-    __syncthreads();
+    for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, tops[turn][w]);
     const uint32_t e = scale_exponent(top);
     const float inv = __uint_as_float((254u - e) << 23);
     if (threadIdx.x == 0) a.scales[tile] = __uint_as_float(e << 23);
     if (k < a.K) {
+      uint8_t* dst = a.codes + (mat * a.rows + r0) * a.K + k;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
-        if (r0 + u * kRows < a.rows) x[u].store(a.codes + (mat * a.rows + r0 + u * kRows) * a.K + k, inv);
+        if (r0 + u * kRows < a.rows) x[u].store(dst + static_cast<long long>(u) * kRows * a.K, inv);
     }
   }
 }
 
-// 16 codes per thread and step: one scale holds for all of them (K is a multiple of 16).
+// 4 (float32) or 8 (bf16) codes per thread and step, so that a warp writes 512
+// bytes side by side; one scale holds for all of them (K is a multiple of 16).
 template <bool BF16>
-__global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const Fp8DequantArgs a) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int KB = (a.K + kFp8Block - 1) / kFp8Block, per_row = a.K / 16;
-  const long long RB = (static_cast<long long>(a.rows) + a.block_rows - 1) / a.block_rows;
-  const long long total = static_cast<long long>(a.n) * a.rows * per_row;
-  for (long long i = static_cast<long long>(blockIdx.x) * kQuantThreads + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kQuantThreads) {
-    const long long row = i / per_row, mat = row / a.rows, r = row - mat * a.rows;
-    const int k = static_cast<int>(i - row * per_row) * 16;
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.codes) + i);
-    const float s = __ldg(a.scales + (mat * RB + r / a.block_rows) * KB + k / kFp8Block);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    float v[16];
+__global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const Fp8DequantArgs a, const Slice s) {
+  constexpr int kN = BF16 ? 8 : 4, kUnroll = 4;
+  pdl_wait();  // and no early start, as above
+  const uint32_t KB = (a.K + kFp8Block - 1) / kFp8Block, per_row = a.K / kN, total = s.rows * per_row;
+  const uint32_t RB = (static_cast<uint32_t>(a.rows) + a.block_rows - 1) / a.block_rows;
+  for (uint32_t i0 = blockIdx.x * (kQuantThreads * kUnroll) + threadIdx.x; i0 < total;
+       i0 += gridDim.x * (kQuantThreads * kUnroll)) {
+    uint2 w[kUnroll];
+    float scale[kUnroll];
+    char* dst[kUnroll];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t h;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(u[j / 2] >> (16 * (j & 1)))));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      v[2 * j] = f.x * s;
-      v[2 * j + 1] = f.y * s;
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t i = i0 + u * kQuantThreads, f = i / per_row, r = s.row + f, m = r / a.rows;
+      const uint32_t k = (i - f * per_row) * kN, mat = s.mat + m, row = r - m * a.rows;
+      dst[u] = nullptr;
+      if (i >= total) continue;
+      const uint8_t* src = a.codes + (static_cast<long long>(s.mat) * a.rows + r) * a.K + k;
+      w[u] = BF16 ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(__ldg(reinterpret_cast<const uint32_t*>(src)), 0u);
+      const uint32_t rb = a.block_rows == 1 ? row : row / kFp8Block;
+      scale[u] = __ldg(a.scales + (static_cast<long long>(mat) * RB + rb) * KB + k / kFp8Block);
+      dst[u] = static_cast<char*>(a.out) + (mat * a.sm + row * a.sr + k) * (BF16 ? 2 : 4);
     }
-    char* dst = static_cast<char*>(a.out) + (mat * a.sm + r * a.sr + k) * (BF16 ? 2 : 4);
-    if (BF16) {
-      uint32_t p[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        p[j] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int u = 0; u < kUnroll; ++u) {
+      if (!dst[u]) continue;
+      float v[kN];
+#pragma unroll
+      for (int j = 0; j < kN / 2; ++j) {
+        uint32_t h;
+        const uint32_t c = j < 2 ? w[u].x : w[u].y;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c >> (16 * (j & 1)))));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        v[2 * j] = f.x * scale[u];
+        v[2 * j + 1] = f.y * scale[u];
       }
-      reinterpret_cast<uint4*>(dst)[0] = make_uint4(p[0], p[1], p[2], p[3]);
-      reinterpret_cast<uint4*>(dst)[1] = make_uint4(p[4], p[5], p[6], p[7]);
-    } else {
+      if constexpr (BF16) {
+        uint32_t p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        reinterpret_cast<float4*>(dst)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+          p[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(dst[u]) = make_uint4(p[0], p[1], p[2], p[3]);
+      } else {
+        *reinterpret_cast<float4*>(dst[u]) = make_float4(v[0], v[1], v[2], v[3]);
+      }
     }
   }
 }
@@ -228,26 +239,45 @@ int grid_of(long long items, int sms) {
   return static_cast<int>(std::max(1ll, std::min<long long>(items, static_cast<long long>(sms) * 8)));
 }
 
+// Calls f(slice) for row ranges of at most 2^31 / per_row rows, until one fails.
+template <typename F>
+cudaError_t in_slices(int n, int rows, long long per_row, F f) {
+  const long long all = static_cast<long long>(n) * rows, most = std::max(1ll, (1ll << 31) / per_row - 1);
+  for (long long at = 0; at < all;) {
+    const Slice s{static_cast<uint32_t>(at / rows), static_cast<uint32_t>(at % rows),
+                  static_cast<uint32_t>(std::min(all - at, std::min(most, (1ll << 31) - rows)))};
+    const cudaError_t e = f(s);
+    if (e != cudaSuccess) return e;
+    at += s.rows;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, bool bf16, int block_rows, int sms, cudaStream_t st) {
   const long long KB = (a.K + kFp8Block - 1) / kFp8Block;
-  if (block_rows == 1) {
-    const long long per = 4ll * kQuantThreads * (bf16 ? 8 : 4) / kFp8Block;
-    const int grid = grid_of((static_cast<long long>(a.n) * a.rows * KB + per - 1) / per, sms);
-    return bf16 ? launch(quant_rows_kernel<true>, dim3(grid), dim3(kQuantThreads), 0, st, true, a)
-                : launch(quant_rows_kernel<false>, dim3(grid), dim3(kQuantThreads), 0, st, true, a);
-  }
-  const int grid = grid_of(static_cast<long long>(a.n) * ((a.rows + kFp8Block - 1) / kFp8Block) * KB, sms);
+  if (block_rows == 1)
+    return in_slices(a.n, a.rows, KB, [&](const Slice& s) {
+      const long long per = 4ll * kQuantThreads * (bf16 ? 8 : 4) / kFp8Block;
+      const int grid = grid_of((s.rows * KB + per - 1) / per, sms);
+      return bf16 ? launch(quant_rows_kernel<true>, dim3(grid), dim3(kQuantThreads), 0, st, true, a, s)
+                  : launch(quant_rows_kernel<false>, dim3(grid), dim3(kQuantThreads), 0, st, true, a, s);
+    });
+  // as many CTAs as run at once: each takes the same number of blocks, but for one
+  const long long tiles = static_cast<long long>(a.n) * ((a.rows + kFp8Block - 1) / kFp8Block) * KB;
+  const int grid = static_cast<int>(std::min<long long>(tiles, sms * (bf16 ? kTileCtas<true> : kTileCtas<false>)));
   return bf16 ? launch(quant_tiles_kernel<true>, dim3(grid), dim3(kQuantThreads), 0, st, true, a)
               : launch(quant_tiles_kernel<false>, dim3(grid), dim3(kQuantThreads), 0, st, true, a);
 }
 
 cudaError_t launch_fp8_dequant(const Fp8DequantArgs& a, bool bf16, int sms, cudaStream_t st) {
-  const long long total = static_cast<long long>(a.n) * a.rows * (a.K / 16);
-  const int grid = grid_of((total + kQuantThreads - 1) / kQuantThreads, sms);
-  return bf16 ? launch(dequant_kernel<true>, dim3(grid), dim3(kQuantThreads), 0, st, true, a)
-              : launch(dequant_kernel<false>, dim3(grid), dim3(kQuantThreads), 0, st, true, a);
+  const long long per_row = a.K / (bf16 ? 8 : 4);
+  return in_slices(a.n, a.rows, per_row, [&](const Slice& s) {
+    const int grid = grid_of((s.rows * per_row + 4 * kQuantThreads - 1) / (4 * kQuantThreads), sms);
+    return bf16 ? launch(dequant_kernel<true>, dim3(grid), dim3(kQuantThreads), 0, st, true, a, s)
+                : launch(dequant_kernel<false>, dim3(grid), dim3(kQuantThreads), 0, st, true, a, s);
+  });
 }
 
 // The same shared-memory carveout as the kernels that follow them, so that those may start beside them.

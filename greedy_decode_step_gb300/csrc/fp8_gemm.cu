@@ -21,8 +21,8 @@
 //   memory in rank order.
 // * wide: many rows.  The lanes are 128 rows of x, 256 columns of weight rows,
 //   so that a thread's scale is one register per block and half tile: 128
-//   FMAs and 8 TMEM loads per thread and block where the tensor core is busy
-//   for 512 cycles.  Persistent CTAs, so the store of one tile runs beside the
+//   FMAs and 4 TMEM loads per thread and block, next to 685 cycles of the tensor
+//   core.  Persistent CTAs, so the store of one tile runs beside the
 //   products of the next.
 //
 // Every wait is bounded (an error bit and an early exit instead of a hang),
@@ -45,7 +45,7 @@ constexpr int kF8BM = 128;                    // accumulator lanes
 constexpr int kF8BK = kFp8Block;              // K per stage: one scale block, one 128-byte swizzle row
 constexpr uint32_t kF8Tile = kF8BM * kF8BK;   // 16 KB: 128 rows of a stage
 constexpr uint32_t kF8Head = 1024;            // barriers
-constexpr uint32_t kNarrowHead = 2048;        // and two blocks' scales per row
+constexpr uint32_t kNarrowHead = 2048;        // and two blocks' scales per row of x
 
 // ----------------------------------------------------------------------------- narrow: weight rows on the lanes
 
@@ -57,8 +57,7 @@ constexpr uint32_t kNarrowSmemMax = 112 * 1024;  // two CTAs per SM
 
 template <int BN>
 constexpr int narrow_stages() {
-  constexpr uint32_t max = BN <= 64 ? kNarrowSmemMax : 2 * kNarrowSmemMax;
-  constexpr int fit = static_cast<int>((max - 1024 - kNarrowHead) / (kF8Tile + BN * kF8BK));
+  constexpr int fit = static_cast<int>((kNarrowSmemMax - 1024 - kNarrowHead) / (kF8Tile + BN * kF8BK));
   return fit < kNarrowMaxStages ? fit : kNarrowMaxStages;
 }
 template <int BN>
@@ -123,7 +122,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
     auto bring_x = [&](int i) {
       tma_load_3d(tiles + i % kStages * kStage + kF8Tile, &a.xmap, (kb0 + i) * kF8BK, r0, 0, &full[i % kStages], xpol);
     };
-    // weights (no kernel writes them) go out before the wait for the kernel that makes the rows
+    // weights go out before the wait for the kernel that makes the rows (the kernels that make weights let nothing start
+    // before they are complete)
     const int pre = min(nkb, kStages);
     if (elect_one())
       for (int i = 0; i < pre; ++i) {
@@ -266,14 +266,19 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
 // ----------------------------------------------------------------------------- wide: rows of x on the lanes
 
 constexpr int kWideThreads = 384;   // warp 0 copies, 1 and 2 multiply, 4-11 scale and store
-constexpr int kWideBN = 256;
-constexpr int kWideStages = 3;      // a fourth would leave no room for the second buffer of results
-constexpr uint32_t kWideStage = kF8Tile + kWideBN * kF8BK;  // 48 KB
+constexpr int kWideMaxStages = 6;
 constexpr uint32_t kWideOut = 8 * 2 * 32 * 128;  // twice 32 rows of 32 results per warp, on their way out
-constexpr uint32_t kWideSmem = 1024 + kF8Head + kWideStages * kWideStage + kWideOut;
+template <int BN>
+struct Wide {  // BN weight rows per tile: 64, 128, 192 or 256
+  static constexpr uint32_t kStage = kF8Tile + BN * kF8BK;
+  static constexpr int kFit = static_cast<int>((kSmemMax - 1024 - kF8Head - kWideOut) / kStage);
+  static constexpr int kStages = kFit < kWideMaxStages ? kFit : kWideMaxStages;  // 3 at 256
+  static constexpr uint32_t kSmem = 1024 + kF8Head + kStages * kStage + kWideOut;
+  static constexpr int kChunks = BN / 64;  // of 32 columns, per epilogue warp
+};
 
 struct WideArgs {
-  CUtensorMap wmap, xmap;  // box 256 rows of wc, 128 rows of xc
+  CUtensorMap wmap, xmap;  // box BN rows of wc, 128 rows of xc
   CUtensorMap omap;        // of the result, if `bulk`
   const float *sx, *sw, *residual;
   float* out;
@@ -284,7 +289,10 @@ struct WideArgs {
   uint32_t* err;
 };
 
+template <int BN>
 __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_constant__ WideArgs a) {
+  constexpr int kWideBN = BN, kWideStages = Wide<BN>::kStages, kChunks = Wide<BN>::kChunks;
+  constexpr uint32_t kWideStage = Wide<BN>::kStage, kCols = tmem_columns(2 * BN);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // done: a stage's products are in its accumulator, and the stage may be filled anew
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
     *stop = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, 2 * kWideBN);
+  if (warp == 1) tmem_alloc(tmem_slot, kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -362,32 +370,38 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
     if (!ok) *stop = 1;
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., columns 128 half ..
+    const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., columns BN / 2 half ..
     unsigned char* stages = tiles + kWideStages * kWideStage + (warp - 4) * 2 * 32 * 128;
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * 128;
-    int it = 0;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * (BN / 2);
+    int it = 0, turn = 0;
     for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-      const int m0 = (tile % a.m_tiles) * kF8BM + 32 * q, n0 = (tile / a.m_tiles) * kWideBN + 128 * half;
+      const int m0 = (tile % a.m_tiles) * kF8BM + 32 * q, n0 = (tile / a.m_tiles) * BN + BN / 2 * half;
       const float* sx = a.sx + static_cast<long long>(min(m0 + lane, a.M - 1)) * a.KB;
-      const float* sw = a.sw + static_cast<long long>(min(n0 / kFp8Block, a.NB - 1)) * a.KB;
-      float acc[128];
+      // the columns of a warp lie in one block of weight rows, at BN = 192 in two
+      const int nb = n0 / kFp8Block, cut = BN == 192 ? (nb + 1) * kFp8Block - n0 : BN;
+      const float* sw = a.sw + static_cast<long long>(min(nb, a.NB - 1)) * a.KB;
+      const float* sv = a.sw + static_cast<long long>(min(nb + 1, a.NB - 1)) * a.KB;
+      float acc[BN / 2];
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      for (int j = 0; j < BN / 2; ++j) acc[j] = 0.f;
       // the scales of the next two blocks are on their way while this one is added
-      float x0 = __ldg(sx), w0 = __ldg(sw), x1 = 0.f, w1 = 0.f;
+      float x0 = __ldg(sx), w0 = __ldg(sw), v0 = BN == 192 ? __ldg(sv) : 0.f, x1 = 0.f, w1 = 0.f, v1 = 0.f;
       if (a.KB > 1) {
         x1 = __ldg(sx + 1);
         w1 = __ldg(sw + 1);
+        if (BN == 192) v1 = __ldg(sv + 1);
       }
       bool ok = true;
       for (int kb = 0; kb < a.KB; ++kb, ++it) {
         const int b = it & 1;
-        const float s = x0 * w0;
+        const float s = x0 * w0, s2 = x0 * v0;
         x0 = x1;
         w0 = w1;
+        v0 = v1;
         if (kb + 2 < a.KB) {
           x1 = __ldg(sx + kb + 2);
           w1 = __ldg(sw + kb + 2);
+          if (BN == 192) v1 = __ldg(sv + kb + 2);
         }
         ok = warp_wait(&done[it % kWideStages], (it / kWideStages) & 1, stop, a.err, kErrWaitFull);
         if (!ok) break;
@@ -397,11 +411,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
         tmem_ld_issue32(at + b * kWideBN, v[0]);
         tmem_ld_wait32(v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c + 1 < 4) tmem_ld_issue32(at + b * kWideBN + 32 * (c + 1), v[(c + 1) & 1]);
+        for (int c = 0; c < kChunks; ++c) {
+          if (c + 1 < kChunks) tmem_ld_issue32(at + b * kWideBN + 32 * (c + 1), v[(c + 1) & 1]);
+          const float f = BN == 192 && 32 * c >= cut ? s2 : s;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) acc[32 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, acc[32 * c + j]);
-          if (c + 1 < 4) tmem_ld_wait32(v[(c + 1) & 1]);
+          for (int j = 0; j < 32; ++j) acc[32 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), f, acc[32 * c + j]);
+          if (c + 1 < kChunks) tmem_ld_wait32(v[(c + 1) & 1]);
         }
         tc_fence_before();
         __syncwarp();
@@ -414,10 +429,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       // 32 columns at a time through shared memory (rows of 128 bytes, their 16-byte pieces swizzled), so that whole
       // lines leave: by a tensor copy, which runs beside the next tile, or by 8 lanes a row
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < kChunks; ++c) {
         const int n = n0 + 32 * c;
         if (n < a.N && m0 < a.M) {  // warp-uniform
-          unsigned char* stage = stages + (c & 1) * 32 * 128;
+          unsigned char* stage = stages + (turn & 1) * 32 * 128;
+          ++turn;
           if (a.bulk) tma_store_wait_read<1>();  // the one before last has left this buffer
           __syncwarp();
 #pragma unroll
@@ -471,13 +487,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_free(tmem, 2 * kWideBN);
+    tmem_free(tmem, kCols);
   }
 }
 
 // ----------------------------------------------------------------------------- host side
 
-// Clusters of `size` CTAs that the device holds at once (cached; -1 where the query fails).
+// Clusters of `size` CTAs that run at once, cached.  The occupancy query counts
+// one CTA per SM wherever tensor memory is used; two fit here.
 template <int BN>
 int narrow_clusters(int size) {
   static std::mutex mu;
@@ -500,9 +517,49 @@ int narrow_clusters(int size) {
       (void)cudaGetLastError();
       n = -1;
     }
-    cache[size] = n;
+    cache[size] = 2 * n;
   }
   return cache[size];
+}
+
+// K splits: double while every split keeps two blocks and all clusters run at
+// once (76 clusters of 4, four more than fit, took 13.2 us where 2 take 8).
+template <int BN>
+int narrow_splits(long long tiles, int KB, int sms) {
+  int splits = 1;
+  while (splits * 2 <= kNarrowMaxSplits && tiles * splits * 2 <= 2ll * sms && KB / (splits * 2) >= 2 &&
+         narrow_clusters<BN>(splits * 2) >= tiles)
+    splits *= 2;
+  return splits;
+}
+
+// Which form is quickest, by what each took per wave of CTAs and block of K
+// (us, measured over M = 16 .. 2048 with K = 2560 and 8960, within 20 %):
+//   narrow, 16 or 32 rows, two CTAs per SM:  5 + waves (0.37 or 0.45 KB / splits)
+//   wide, tiles of 64, 128, 192, 256 columns: 4.5 + waves (0.5 + 0.214, 0.270, 0.372 or 0.456 KB)
+// e.g. 64 x 9728 x 2560: 10.9 narrow, 9.0 wide 64, 15.2 wide 256; 512 x 1536 x
+// 8960: 31 narrow, 20 wide 64; 509 x 6144 x 2560: 16.9, 13.8, 15.8 wide 128, 192,
+// 256; 2048 x 9728 x 2560: 59, 62, 52.
+enum Form { kNarrow16, kNarrow32, kWide64, kWide128, kWide192, kWide256 };
+Form best_form(const Fp8GemmCall& c, int sms) {
+  const int KB = (c.K + kF8BK - 1) / kF8BK;
+  auto up = [](long long a, long long b) { return (a + b - 1) / b; };
+  Form best = kWide256;
+  double least = 1e30;
+  auto offer = [&](Form f, double us) {
+    if (us < least) {
+      least = us;
+      best = f;
+    }
+  };
+  const long long n128 = up(c.N, kF8BM), t16 = up(c.M, 16) * n128, t32 = up(c.M, 32) * n128, m128 = up(c.M, kF8BM);
+  const int s16 = narrow_splits<16>(t16, KB, sms), s32 = narrow_splits<32>(t32, KB, sms);
+  offer(kNarrow16, 5.0 + up(t16 * s16, 2 * sms) * 0.37 * up(KB, s16));
+  if (c.M > 16) offer(kNarrow32, 5.0 + up(t32 * s32, 2 * sms) * 0.45 * up(KB, s32));
+  const Form wide[4] = {kWide64, kWide128, kWide192, kWide256};
+  const double per[4] = {0.214, 0.270, 0.372, 0.456};
+  for (int i = 0; i < 4; ++i) offer(wide[i], 4.5 + up(m128 * up(c.N, 64 * (i + 1)), sms) * (0.5 + per[i] * KB));
+  return best;
 }
 
 template <int BN>
@@ -525,12 +582,7 @@ cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const 
   a.n_tiles = (c.M + BN - 1) / BN;
   a.err = c.err;
   const long long tiles = static_cast<long long>(a.n_tiles) * ((c.N + kF8BM - 1) / kF8BM);
-  // K splits: double while every split keeps two blocks and all clusters run at once
-  const long long slots = static_cast<long long>(sms) * (BN <= 64 ? 2 : 1);
-  int splits = 1;
-  while (splits * 2 <= kNarrowMaxSplits && tiles * splits * 2 <= slots && a.KB / (splits * 2) >= 2 &&
-         narrow_clusters<BN>(splits * 2) >= tiles)
-    splits *= 2;
+  const int splits = narrow_splits<BN>(tiles, a.KB, sms);
   a.splits = splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
@@ -549,10 +601,11 @@ cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const 
   return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<BN>, a);
 }
 
+template <int BN>
 cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
   static thread_local WideArgs a;
   std::memset(&a, 0, sizeof(a));
-  if (!make_tmap_mats(&a.wmap, c.wc, 1, c.K, c.N, 1, kWideBN) || !make_tmap_mats(&a.xmap, c.xc, 1, c.K, c.M, 1, kF8BM)) {
+  if (!make_tmap_mats(&a.wmap, c.wc, 1, c.K, c.N, 1, BN) || !make_tmap_mats(&a.xmap, c.xc, 1, c.K, c.M, 1, kF8BM)) {
     *why = "a tensor map could not be made";
     return cudaErrorInvalidValue;
   }
@@ -567,7 +620,7 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
   a.KB = (c.K + kF8BK - 1) / kF8BK;
   a.NB = (c.N + kFp8Block - 1) / kFp8Block;
   a.m_tiles = (c.M + kF8BM - 1) / kF8BM;
-  a.tiles = a.m_tiles * ((c.N + kWideBN - 1) / kWideBN);
+  a.tiles = a.m_tiles * ((c.N + BN - 1) / BN);
   a.err = c.err;
   auto rows16 = [](const void* p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 4 == 0; };
   a.bulk = rows16(c.out, c.ldo) && c.N % 4 == 0;  // a tensor copy cuts a row off at whole 16 bytes only
@@ -576,7 +629,7 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
     *why = "a tensor map could not be made";
     return cudaErrorInvalidValue;
   }
-  return launch(fp8_wide_kernel, dim3(std::min(a.tiles, sms)), dim3(kWideThreads), kWideSmem, st, true, a);
+  return launch(fp8_wide_kernel<BN>, dim3(std::min(a.tiles, sms)), dim3(kWideThreads), Wide<BN>::kSmem, st, true, a);
 }
 
 }  // namespace
@@ -584,16 +637,14 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
 int fp8_gemm(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
   *why = nullptr;
   cudaError_t e;
-  if (c.M <= 16)
-    e = launch_narrow<16>(c, sms, st, why);
-  else if (c.M <= 32)
-    e = launch_narrow<32>(c, sms, st, why);
-  else if (c.M <= 64)
-    e = launch_narrow<64>(c, sms, st, why);
-  else if (c.M <= 128)
-    e = launch_narrow<128>(c, sms, st, why);
-  else
-    e = launch_wide(c, sms, st, why);
+  switch (best_form(c, sms)) {
+    case kNarrow16: e = launch_narrow<16>(c, sms, st, why); break;
+    case kNarrow32: e = launch_narrow<32>(c, sms, st, why); break;
+    case kWide64: e = launch_wide<64>(c, sms, st, why); break;
+    case kWide128: e = launch_wide<128>(c, sms, st, why); break;
+    case kWide192: e = launch_wide<192>(c, sms, st, why); break;
+    default: e = launch_wide<256>(c, sms, st, why); break;
+  }
   if (*why) return 1;
   if (e != cudaSuccess) {
     *why = cudaGetErrorString(e);
@@ -606,9 +657,10 @@ cudaError_t allow_smem_fp8_gemm() {
   cudaError_t e;
   if ((e = allow_smem(fp8_narrow_kernel<16>)) != cudaSuccess) return e;
   if ((e = allow_smem(fp8_narrow_kernel<32>)) != cudaSuccess) return e;
-  if ((e = allow_smem(fp8_narrow_kernel<64>)) != cudaSuccess) return e;
-  if ((e = allow_smem(fp8_narrow_kernel<128>)) != cudaSuccess) return e;
-  return allow_smem(fp8_wide_kernel);
+  if ((e = allow_smem(fp8_wide_kernel<64>)) != cudaSuccess) return e;
+  if ((e = allow_smem(fp8_wide_kernel<128>)) != cudaSuccess) return e;
+  if ((e = allow_smem(fp8_wide_kernel<192>)) != cudaSuccess) return e;
+  return allow_smem(fp8_wide_kernel<256>);
 }
 
 }  // namespace dec

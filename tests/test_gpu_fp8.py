@@ -237,6 +237,26 @@ def test_reproducible_captured_and_on_another_stream(M):
     assert torch.equal(out, 2.0 * first)  # a power of two changes no rounding
 
 
+@pytest.mark.parametrize("M", [1, 300])
+def test_weights_made_right_before_the_product(M):
+    """The rows first, then the weights, then the product, without a pause: it reads no weights of the pass before."""
+    N, K = 4096, 2048
+    x = normal(55, M, K)
+    ws = [normal(56 + i, N, K).bfloat16() for i in range(3)]
+    xc, xs = empty_codes(x, 1)
+    wc, wsc = empty_codes(ws[0], 128)
+    outs = [torch.zeros(M, N, device="cuda") for _ in range(12)]
+    for i, out in enumerate(outs):
+        gd.dec_fp8_quant(x, xc, xs)
+        gd.dec_fp8_quant(ws[i % 3], wc, wsc, block_rows=128)
+        gd.dec_fp8_gemm(xc, xs, wc, wsc, out)
+    for i in range(3):
+        gd.dec_fp8_quant(ws[i], wc, wsc, block_rows=128)
+        want, bound = R.gemm(xc, xs, wc, wsc)
+        for out in outs[i::3]:
+            close(out, want, bound)
+
+
 def test_two_products_at_once():
     a, b = operands(60, 16, 700, 2048), operands(61, 300, 900, 1024)
     oa, ob = torch.zeros(16, 700, device="cuda"), torch.zeros(300, 900, device="cuda")
