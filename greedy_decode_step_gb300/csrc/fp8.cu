@@ -65,18 +65,31 @@ struct Vec {  // 16 bytes of a source row, as they came
                             : (i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
     return BF16 ? (i & 1 ? bf16hi(u) : bf16lo(u)) : __uint_as_float(u);
   }
+  // Bits of the largest magnitude, as a float's: 0x7F800000 or more if a value is not finite.
   __device__ __forceinline__ uint32_t top() const {
+    if (BF16) {
+      const uint32_t k = 0x7FFF7FFFu;  // two at a time
+      const uint32_t m = __vmaxu2(__vmaxu2(w.x & k, w.y & k), __vmaxu2(w.z & k, w.w & k));
+      return max(m & 0xFFFF0000u, m << 16);
+    }
+    const uint32_t k = 0x7FFFFFFFu;
+    return max(max(w.x & k, w.y & k), max(w.z & k, w.w & k));
+  }
+  // The same over the finite values.
+  __device__ __forceinline__ uint32_t finite_top() const {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kN; ++i) m = max(m, finite_magnitude(value(i)));
     return m;
   }
+  // ALL: every value is finite.
+  template <bool ALL>
   __device__ __forceinline__ void store(uint8_t* p, float inv) const {
+    auto v = [&](int i) { return ALL ? value(i) * inv : scaled(value(i), inv); };
     uint32_t c[kN / 4];
 #pragma unroll
     for (int i = 0; i < kN / 4; ++i)
-      c[i] = e4m3_pair(scaled(value(4 * i), inv), scaled(value(4 * i + 1), inv)) |
-             (e4m3_pair(scaled(value(4 * i + 2), inv), scaled(value(4 * i + 3), inv)) << 16);
+      c[i] = e4m3_pair(v(4 * i), v(4 * i + 1)) | (e4m3_pair(v(4 * i + 2), v(4 * i + 3)) << 16);
     if (kN == 8)
       *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[kN / 4 - 1]);
     else
@@ -126,9 +139,22 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const Fp8Quan
       uint32_t top = x[u].top();
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool all = top < 0x7F800000u;
+      if (__any_sync(0xffffffffu, !all)) {  // rare: once more without the infinities and NaNs
+        top = x[u].finite_top();
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
       const uint32_t e = scale_exponent(top);
       if (flat[u] < 0) continue;
-      if (k[u] < a.K) x[u].store(a.codes + flat[u] * a.K + k[u], __uint_as_float((254u - e) << 23));
+      if (k[u] < a.K) {
+        uint8_t* dst = a.codes + flat[u] * a.K + k[u];
+        const float inv = __uint_as_float((254u - e) << 23);
+        if (all)
+          x[u].template store<true>(dst, inv);
+        else
+          x[u].template store<false>(dst, inv);
+      }
       if (in == 0) a.scales[flat[u] * KB + k[u] / kFp8Block] = __uint_as_float(e << 23);
     }
   }
@@ -148,7 +174,7 @@ __global__ void __launch_bounds__(kQuantThreads, kTileCtas<BF16>) quant_tiles_ke
   const long long tiles = static_cast<long long>(a.n) * RB * KB;
   const int sub = threadIdx.x / kLanes, in = threadIdx.x % kLanes;
   int turn = 0;
-  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
+  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const long long mb = tile / KB, mat = mb / RB;
     const int k = static_cast<int>(tile - mb * KB) * kFp8Block + in * kN;
     const int r0 = static_cast<int>(mb - mat * RB) * kFp8Block + sub;
@@ -162,22 +188,42 @@ __global__ void __launch_bounds__(kQuantThreads, kTileCtas<BF16>) quant_tiles_ke
       else
         x[u].zero();
     }
+    // two sets of maxima in turn: one barrier a block
+    auto meet = [&](uint32_t top) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      if ((threadIdx.x & 31) == 0) tops[turn][threadIdx.x / 32] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, tops[turn][w]);
+      turn ^= 1;
+      return top;
+    };
     uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) top = max(top, x[u].top());
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) tops[turn][threadIdx.x / 32] = top;
-    __syncthreads();  // two sets of maxima in turn: one barrier a block
+    top = meet(top);
+    const bool all = top < 0x7F800000u;
+    if (!all) {  // rare: once more without the infinities and NaNs
+      top = 0;
 #pragma unroll
-    for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, tops[turn][w]);
+      for (int u = 0; u < kUnroll; ++u) top = max(top, x[u].finite_top());
+      top = meet(top);
+    }
     const uint32_t e = scale_exponent(top);
     const float inv = __uint_as_float((254u - e) << 23);
     if (threadIdx.x == 0) a.scales[tile] = __uint_as_float(e << 23);
     if (k < a.K) {
       uint8_t* dst = a.codes + (mat * a.rows + r0) * a.K + k;
+      const long long next = static_cast<long long>(kRows) * a.K;
+      if (all) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        if (r0 + u * kRows < a.rows) x[u].store(dst + static_cast<long long>(u) * kRows * a.K, inv);
+        for (int u = 0; u < kUnroll; ++u)
+          if (r0 + u * kRows < a.rows) x[u].template store<true>(dst + u * next, inv);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (r0 + u * kRows < a.rows) x[u].template store<false>(dst + u * next, inv);
+      }
     }
   }
 }
