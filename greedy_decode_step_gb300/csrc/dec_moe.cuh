@@ -40,21 +40,22 @@ struct MoeCall {
   int T, k, E, H, I;
   uint32_t* err;
 };
-// Workspace (byte offsets): the plan and a counter per tile of the down launch;
-// gate and up products of every chosen (token, expert); the parts of tiles that
-// several CTAs share; the split rows of y and of the inner vectors, 1 KB per token and 64 or
+// Workspace (byte offsets): the plan; gate and up products of every chosen
+// (token, expert); the parts of tiles that a CTA took over from the one before
+// it; the sums of the down launch's CTAs; the split rows of y and of the inner vectors, 1 KB per token and 64 or
 // 128 values.
 constexpr int kMoeRows = kMoeMaxTokens * kMoeMaxChoices;  // (token, expert) pairs
 constexpr int kMoePlanBytes = 4096;
 struct MoeWorkspace {
-  size_t main, cut, xb, hb, bytes;
+  size_t main, cut, sums, xb, hb, bytes;
 };
 inline MoeWorkspace moe_workspace(int T, int k, int H, int I) {
   auto up = [](size_t n) { return (n + 1023) & ~size_t(1023); };
   MoeWorkspace w;
-  w.main = kMoePlanBytes + kMoeMaxDim / 128 * 4;
+  w.main = kMoePlanBytes;
   w.cut = w.main + up(static_cast<size_t>(T) * k * 2 * I * 4);
-  w.xb = w.cut + static_cast<size_t>(kMoeMaxCtas) * kMoeMaxTokens * 2 * kMoeUnit * 4;
+  w.sums = w.cut + static_cast<size_t>(kMoeMaxCtas) * kMoeMaxTokens * 2 * kMoeUnit * 4;
+  w.xb = w.sums + static_cast<size_t>(kMoeMaxCtas) * kMoeMaxTokens * 128 * 4;
   w.hb = w.xb + static_cast<size_t>(T) * ((H + 63) / 64) * 1024;
   w.bytes = w.hb + static_cast<size_t>(T) * k * ((I + 63) / 64) * 1024;
   return w;

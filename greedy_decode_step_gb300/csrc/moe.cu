@@ -5,7 +5,8 @@
 //
 // Bound by the stream of the chosen experts' weights: each is read once,
 // whatever number of tokens chose it.  Two launches (gate/up and down) stream
-// them; two short ones ahead of each make the activations' operand.
+// them, a short one adds the parts of the result; from three tokens on, a short
+// one ahead of each makes the activations' operand.
 //
 // The products run on the tensor cores with weight rows on the 128 lanes of an
 // accumulator and the tokens on its columns (tcgen05.mma, M = 128).  fp32
@@ -21,24 +22,27 @@
 // cuts every product at the last place of its running sum, and one accumulator
 // over a whole row of 2560 was off by 1.8e-6 where this is by 1e-7.
 //
-// The parts are made once (moe_prep_kernel for y, moe_act_kernel for the inner
-// vector), as 1 KB blocks per token and chunk that a bulk copy puts beside the
-// weights as they are: eight swizzled rows of 128 bytes, the parts in the
-// first three or five.  A chunk's operand is the blocks of the tokens that chose
-// the expert, N = 8 per token, so its cost follows their number.  (Splitting rows
-// beside the stream, in every CTA, cost 1.1 us a chunk with 16 tokens, three times
-// the time its weights take.)
+// The parts are 1 KB blocks per token and chunk: eight swizzled rows of 128
+// bytes, the parts in the first three or five.  A chunk's operand is the blocks
+// of the tokens that chose the expert, N = 8 per token, so its cost follows their
+// number.  For one or two tokens four warps of every CTA make them beside the
+// stream; for more they are made once (moe_prep_kernel for y, moe_act_kernel for
+// the inner vectors) and brought by bulk copies.  (With 16 tokens four warps
+// took 1.1 us a chunk, three times what its weights take; with one token the two
+// launches cost 44 us a layer where this takes 37.)
 //
 // gate/up: a tile is 64 gate rows and the same 64 up rows of an expert.  How
 // many experts are active is known on the device only, so a persistent grid
 // lays all tiles' chunks end to end and gives every CTA an equal run of them;
 // a tile cut between CTAs leaves parts, which moe_act_kernel adds in CTA order.
 // down: a tile is 128 output rows, its K axis all active experts' inner vectors
-// one behind the other, split over as many CTAs as run at once.  The last of a
-// tile's CTAs to arrive adds their sums in split order: results do not depend
-// on timing.  (Clusters that add through distributed shared memory hold 120
-// CTAs where 300 run, and took 74 us for the down half of 16 tokens, 8 of 128 8-bit experts, where this takes 48.)  The
-// first weights are on their way while gate/up still runs.
+// one behind the other, split over as many CTAs as run at once; their sums are
+// added in split order by moe_sum_kernel, so results do not depend on timing.
+// (Clusters that add through distributed shared memory hold 120 CTAs where 300
+// run: 74 us for the down half of 16 tokens, 8 of 128 8-bit experts, against 48.
+// The last of a tile's CTAs to arrive adding all 25 parts took 9 us at the end of
+// 16 tokens, three times the launch that spreads it.)  The first weights are on
+// their way while gate/up still runs.
 //
 // Every wait is bounded (an error bit and an early exit instead of a hang),
 // and tensor memory is released on every path.
@@ -58,7 +62,9 @@
 namespace dec {
 namespace {
 
-constexpr int kMoeThreads = 256;      // warps 0 and 6 copy weights, 7 activations, 1 multiplies, 2-5 take sums off
+// warps 0 and 6 copy weights, 1 multiplies, 2-5 take sums off, 7 copies activations (7-10 split them)
+constexpr int kMoeThreads = 256, kMoeThreadsOwn = 352;
+constexpr int kMoeOwnWarps = 4;
 constexpr int kMoeFlat = 256;         // threads of the two short launches
 constexpr uint32_t kMoeATile = 128 * 128;
 constexpr uint32_t kMoeBlock = 1024;  // one token's parts of one chunk
@@ -95,8 +101,7 @@ struct MoeArgs {
   const float* residual;
   float* out;
   Plan* plan;                    // workspace
-  uint32_t* arrived;             // [tiles of down]
-  float *main, *cut;             // cut: the parts of down's tiles, too
+  float *main, *cut, *sums;
   unsigned char *xb, *hb;
   int T, k, E, H, I;
   int ctas;                      // of the gate/up launch
@@ -261,6 +266,43 @@ __device__ __forceinline__ void make_plan(Plan& p, const MoeArgs& a) {
   p.gate[row] = w;
 }
 
+// The plan of at most two tokens, by one warp of every CTA that needs it, experts in the order of their first listing.
+__device__ __forceinline__ void make_small_plan(Plan& p, const MoeArgs& a, bool report) {
+  const int lane = threadIdx.x & 31, n = a.T * a.k;
+  static_assert(2 * kMoeMaxChoices <= 32, "a lane per choice");
+  const int e = lane < n ? a.ids[lane] : -1;
+  const float g = lane < n ? a.gates[lane] : 0.f;
+  const bool valid = e >= 0 && e < a.E;
+  if (report && !valid && e != -1) atomicOr(a.err, kErrPosRange);
+  const uint32_t same = __match_any_sync(0xffffffffu, valid ? e : -1 - lane);
+  const uint32_t first_token = a.k < 32 ? (1u << a.k) - 1 : 0xffffffffu;
+  const bool leads = valid && lane == __ffs(same) - 1;
+  const int count = ((same & first_token) != 0) + ((same & ~first_token) != 0);
+  const uint32_t leaders = __ballot_sync(0xffffffffu, leads), pairs = __ballot_sync(0xffffffffu, leads && count == 2);
+  float w0 = 0.f, w1 = 0.f;  // an expert that a token lists twice counts twice
+  for (int j = 0; j < n; ++j) {
+    const float gj = __shfl_sync(0xffffffffu, g, j);
+    if ((same >> j) & 1u) (j < a.k ? w0 : w1) += gj;
+  }
+  if (leads) {
+    const uint32_t before = (1u << lane) - 1;
+    const int at = __popc(leaders & before);
+    int row = at + __popc(pairs & before);
+    p.expert[at] = static_cast<uint16_t>(e);
+    p.count[at] = static_cast<uint16_t>(count);
+    p.first[at] = static_cast<uint16_t>(row);
+    if (same & first_token) {
+      p.token[row] = 0;
+      p.gate[row++] = w0;
+    }
+    if (same & ~first_token) {
+      p.token[row] = 1;
+      p.gate[row] = w1;
+    }
+  }
+  if (lane == 0) p.active = __popc(leaders);
+}
+
 // Block 0: the plan.  Warps of the others: one block of parts each, chunk j of token t at j T + t.
 template <bool F8>
 __global__ void __launch_bounds__(kMoeFlat) moe_prep_kernel(const __grid_constant__ MoeArgs a) {
@@ -268,7 +310,6 @@ __global__ void __launch_bounds__(kMoeFlat) moe_prep_kernel(const __grid_constan
   pdl_wait();
   pdl_launch_dependents();
   if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < (a.H + 127) / 128; i += kMoeFlat) a.arrived[i] = 0;
     make_plan(*a.plan, a);
     return;
   }
@@ -282,26 +323,26 @@ __global__ void __launch_bounds__(kMoeFlat) moe_prep_kernel(const __grid_constan
   put_parts(a.xb + static_cast<size_t>(i) * kMoeBlock, lane, x);
 }
 
-// The inner vectors: one warp per row and chunk adds a cut tile's parts and splits w silu(g) u.
-// Blocks lie in the order that the down launch reads them: expert, chunk, token.
+// w silu(g) u of this lane's values of chunk j in row `row`, which is token `rank` of active expert `act`: the products of
+// gate/up, and the parts of a tile that CTAs c0 + 1 .. c1 took over.
 template <bool F8>
-__global__ void __launch_bounds__(kMoeFlat) moe_act_kernel(const __grid_constant__ MoeArgs a) {
+struct Inner {
   using P = Parts<F8>;
-  pdl_launch_dependents();  // the next launch reads nothing of this one's before its own wait
-  pdl_wait();
-  const Plan& p = *a.plan;
-  const int lane = threadIdx.x & 31, id = blockIdx.x * (kMoeFlat / 32) + threadIdx.x / 32;
-  const int kch = (a.I + P::kChunk - 1) / P::kChunk, row = id / kch, j = id - row * kch;
-  if (row >= p.rows) return;
-  const Runs r(p.active, a, P::kChunk);
-  const int act = p.act[row], rank = row - p.first[act];
-  const int i = j * P::kChunk + lane * P::kVals;
-  float x[P::kVals];
+  int i, c0, c1, row, rank;
+  bool inside;
+  __device__ __forceinline__ Inner(const MoeArgs& a, const Runs& r, int act, int row_, int rank_, int j)
+      : i(j * P::kChunk + static_cast<int>(threadIdx.x & 31) * P::kVals), c0(0), c1(0), row(row_), rank(rank_) {
+    inside = i < a.I;
+    if (inside) {
+      const long long pos = (static_cast<long long>(act) * r.units + i / kMoeUnit) * r.kch;
+      c0 = r.owner(pos);
+      c1 = r.owner(pos + r.kch - 1);
+    }
+  }
+  __device__ __forceinline__ void get(const MoeArgs& a, float w, float (&x)[P::kVals]) const {
 #pragma unroll
-  for (int v = 0; v < P::kVals; ++v) x[v] = 0.f;
-  if (i < a.I) {
-    const long long pos = (static_cast<long long>(act) * r.units + i / kMoeUnit) * r.kch;
-    const int c0 = r.owner(pos), c1 = r.owner(pos + r.kch - 1);
+    for (int v = 0; v < P::kVals; ++v) x[v] = 0.f;
+    if (!inside) return;
     float g[P::kVals], u[P::kVals];
     load_vals(g, a.main + static_cast<size_t>(row) * 2 * a.I + i);
     load_vals(u, a.main + (static_cast<size_t>(row) * 2 + 1) * a.I + i);
@@ -316,12 +357,53 @@ __global__ void __launch_bounds__(kMoeFlat) moe_act_kernel(const __grid_constant
         u[v] += du[v];
       }
     }
-    const float w = p.gate[row];
 #pragma unroll
     for (int v = 0; v < P::kVals; ++v) x[v] = g[v] / (1.f + expf(-g[v])) * u[v] * w;
   }
-  put_parts(a.hb + (static_cast<size_t>(p.first[act]) * kch + static_cast<size_t>(j) * p.count[act] + rank) * kMoeBlock, lane,
-            x);
+};
+
+// The inner vectors' blocks, one warp per row and chunk, in the order that the down launch reads them: expert, chunk,
+// token.  The plan was complete before gate/up could begin, and that began before this launch could.
+template <bool F8>
+__global__ void __launch_bounds__(kMoeFlat) moe_act_kernel(const __grid_constant__ MoeArgs a) {
+  using P = Parts<F8>;
+  pdl_launch_dependents();  // the next launch reads nothing of this one's before its own wait
+  const Plan& p = *a.plan;
+  const int lane = threadIdx.x & 31, id = blockIdx.x * (kMoeFlat / 32) + threadIdx.x / 32;
+  const int kch = (a.I + P::kChunk - 1) / P::kChunk, row = id / kch, j = id - row * kch;
+  const bool live = row < p.rows;
+  const int act = live ? p.act[row] : 0, first = live ? p.first[act] : 0, count = live ? p.count[act] : 0;
+  const float w = live ? p.gate[row] : 0.f;
+  const Runs r(p.active, a, P::kChunk);
+  const Inner<F8> inner(a, r, act, row, row - first, live ? j : kch);
+  pdl_wait();
+  if (!live) return;
+  float x[P::kVals];
+  inner.get(a, w, x);
+  put_parts(a.hb + (static_cast<size_t>(first) * kch + static_cast<size_t>(j) * count + row - first) * kMoeBlock, lane, x);
+}
+
+// The result: the sums of a tile's CTAs in split order, on top of the residual.
+__global__ void __launch_bounds__(128) moe_sum_kernel(const __grid_constant__ MoeArgs a) {
+  const int per = a.H / 4, id = blockIdx.x * 128 + threadIdx.x, t = id / per, m = 4 * (id - t * per);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (t >= a.T) return;
+  const size_t to = static_cast<size_t>(t) * a.H + m;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f), res = sum;
+  if (a.residual) res = *reinterpret_cast<const float4*>(a.residual + to);
+  // [tile][split][T][128]
+  const float* src = a.sums + (static_cast<size_t>(m / 128) * a.splits * a.T + t) * 128 + m % 128;
+  for (int s0 = 0; s0 < a.splits; s0 += 16) {
+    float4 x[16];
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+      if (s0 + s < a.splits) x[s] = *reinterpret_cast<const float4*>(src + static_cast<size_t>(s0 + s) * a.T * 128);
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+      if (s0 + s < a.splits) sum = make_float4(sum.x + x[s].x, sum.y + x[s].y, sum.z + x[s].z, sum.w + x[s].w);
+  }
+  *reinterpret_cast<float4*>(a.out + to) = make_float4(res.x + sum.x, res.y + sum.y, res.z + sum.z, res.w + sum.w);
 }
 
 // ----------------------------------------------------------------------------- a CTA of the two streaming launches
@@ -348,6 +430,8 @@ struct Ring {
 template <bool F8, int NT>
 struct Cta {
   using P = Parts<F8>;
+  static constexpr bool kOwn = NT == 2;  // makes its own plan and blocks
+  static constexpr int kThreads = kOwn ? kMoeThreadsOwn : kMoeThreads;
   static constexpr int kSlots = NT <= 2 ? 8 : 16;
   static constexpr uint32_t kSlot = 2 * kMoeBlock;
   uint64_t *fullA, *emptyA, *fullB, *emptyB, *accum, *drained;
@@ -408,9 +492,27 @@ struct Cta {
   // All threads.
   __device__ __forceinline__ void take_plan(const Plan* from) {
     const uint32_t* src = reinterpret_cast<const uint32_t*>(from);
-    for (int i = threadIdx.x; i < static_cast<int>(sizeof(Plan) / 4); i += kMoeThreads)
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(Plan) / 4); i += kThreads)
       reinterpret_cast<uint32_t*>(plan)[i] = src[i];
     __syncthreads();
+  }
+  __device__ __forceinline__ void get_plan(const MoeArgs& a, bool report) {
+    if (!kOwn) return take_plan(a.plan);
+    if (threadIdx.x < 32) make_small_plan(*plan, a, report);
+    __syncthreads();
+  }
+  // Whole warp, of those that split rows: room for chunk `it` (NT = 2: one slot each); null when a wait ran out.
+  __device__ __forceinline__ unsigned char* own_slot(int it, uint32_t* err) const {
+    if (it >= kMoeTurns && !warp_wait(&emptyB[it % kMoeTurns], ((it / kMoeTurns) - 1) & 1, stop, err, kErrWaitEmpty)) {
+      *stop = 1;
+      return nullptr;
+    }
+    return B + it % kMoeTurns * kSlot;
+  }
+  __device__ __forceinline__ void own_done(int it) const {
+    fence_to_async();
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(&fullB[it % kMoeTurns]);
   }
   __device__ __forceinline__ void end() {
     __syncwarp();
@@ -533,14 +635,14 @@ struct Cta {
 // ----------------------------------------------------------------------------- gate/up
 
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kMoeThreads, 2) moe_gate_up_kernel(const __grid_constant__ MoeArgs a) {
+__global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_gate_up_kernel(const __grid_constant__ MoeArgs a) {
   using P = Parts<F8>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Cta<F8, NT> c(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  c.take_plan(a.plan);
+  c.get_plan(a, blockIdx.x == 0);
   const Plan& p = *c.plan;
   const Runs r(p.active, a, P::kChunk);
   const int lo = r.begin(blockIdx.x), hi = r.begin(blockIdx.x + 1);
@@ -564,6 +666,24 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gate_up_kernel(const __gri
       pos += n;
     }
     if (half == 0 && lane == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
+  } else if (c.kOwn && warp >= 7) {
+    const int mine = warp - 7;
+    for (int it = mine, pos = lo + mine; pos < hi; it += kMoeOwnWarps, pos += kMoeOwnWarps) {
+      const int tile = pos / r.kch, act = tile / r.units, first = p.first[act], count = p.count[act];
+      const int k = (pos - tile * r.kch) * P::kChunk + lane * P::kVals;
+      float x[2][P::kVals];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int v = 0; v < P::kVals; ++v) x[t][v] = 0.f;
+        if (t < count && k < a.H) load_vals(x[t], a.y + static_cast<size_t>(p.token[first + t]) * a.H + k);
+      }
+      unsigned char* slot = c.own_slot(it, a.err);
+      if (!slot) break;
+      put_parts(slot, lane, x[0]);
+      if (count == 2) put_parts(slot + kMoeBlock, lane, x[1]);
+      c.own_done(it);
+    }
   } else if (warp == 7) {
     const uint64_t pol = l2_policy_evict_last();
     Slots ring;
@@ -638,14 +758,15 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_gate_up_kernel(const __gri
 // ----------------------------------------------------------------------------- down
 
 template <bool F8, int NT>
-__global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const __grid_constant__ MoeArgs a) {
+__global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_down_kernel(const __grid_constant__ MoeArgs a) {
   using P = Parts<F8>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Cta<F8, NT> c(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits, m0 = tile * 128;
-  // the plan was complete before gate/up could begin, and that began before this launch could
-  c.take_plan(a.plan);
+  // the plan (or what it is made of) was complete before gate/up could begin, and that began before this launch could
+  c.get_plan(a, false);
+  pdl_launch_dependents();
   const Plan& p = *c.plan;
   const int kch = (a.I + P::kChunk - 1) / P::kChunk, all = p.active * kch;
   const int lo = static_cast<int>(static_cast<long long>(split) * all / a.splits);
@@ -667,6 +788,22 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const __grid_c
       }
     }
     if (half == 0 && lane == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
+  } else if (c.kOwn && warp >= 7) {
+    pdl_wait();  // gate and up products
+    const Runs r(p.active, a, P::kChunk);
+    const int mine = warp - 7;
+    for (int it = mine; it < hi - lo; it += kMoeOwnWarps) {
+      const int act = (lo + it) / kch, j = lo + it - act * kch, first = p.first[act], count = p.count[act];
+      const Inner<F8> one(a, r, act, first, 0, j), two(a, r, act, first + 1, 1, j);
+      float x[2][P::kVals];
+      one.get(a, p.gate[first], x[0]);
+      if (count == 2) two.get(a, p.gate[first + 1], x[1]);
+      unsigned char* slot = c.own_slot(it, a.err);
+      if (!slot) break;
+      put_parts(slot, lane, x[0]);
+      if (count == 2) put_parts(slot + kMoeBlock, lane, x[1]);
+      c.own_done(it);
+    }
   } else if (warp == 7) {
     pdl_wait();  // the inner vectors
     const uint64_t pol = l2_policy_evict_last();
@@ -733,51 +870,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const __grid_c
     }
   }
   __syncwarp();
-  pdl_wait();  // the result may be what an earlier kernel reads or writes
+  pdl_wait();  // every thread: the launches before are complete before this one is
   __syncthreads();
   // [tile][split][T][128]
   const int n4 = a.T * 32;
-  float4* mine = reinterpret_cast<float4*>(a.cut) + (static_cast<size_t>(tile) * a.splits + split) * n4;
-  const float4* sums = reinterpret_cast<const float4*>(c.total);
-  bool last = true;
-  if (a.splits > 1) {
-    for (int i = threadIdx.x; i < n4; i += kMoeThreads) mine[i] = sums[i];
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) *c.tmem_slot = atomicAdd(a.arrived + tile, 1u);  // the slot has served
-    __syncthreads();
-    last = *c.tmem_slot == static_cast<uint32_t>(a.splits - 1);
-    __threadfence();
-  }
-  if (last) {
-    const float4* all4 = mine - static_cast<size_t>(split) * n4;
-    for (int i = threadIdx.x; i < n4; i += kMoeThreads) {
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.splits == 1) sum = sums[i];
-      for (int s0 = 0; s0 < a.splits && a.splits > 1; s0 += 16) {
-        float4 x[16];
-#pragma unroll
-        for (int s = 0; s < 16; ++s)
-          if (s0 + s < a.splits) x[s] = __ldcg(all4 + static_cast<size_t>(s0 + s) * n4 + i);
-#pragma unroll
-        for (int s = 0; s < 16; ++s)
-          if (s0 + s < a.splits) {
-            sum.x += x[s].x;
-            sum.y += x[s].y;
-            sum.z += x[s].z;
-            sum.w += x[s].w;
-          }
-      }
-      const int m = m0 + 4 * (i & 31);
-      if (m >= a.H) continue;  // H is a multiple of 8
-      const size_t to = static_cast<size_t>(i >> 5) * a.H + m;
-      if (a.residual) {
-        const float4 r = *reinterpret_cast<const float4*>(a.residual + to);
-        sum = make_float4(r.x + sum.x, r.y + sum.y, r.z + sum.z, r.w + sum.w);
-      }
-      *reinterpret_cast<float4*>(a.out + to) = sum;
-    }
-  }
+  float4* mine = reinterpret_cast<float4*>(a.sums) + (static_cast<size_t>(tile) * a.splits + split) * n4;
+  for (int i = threadIdx.x; i < n4; i += c.kThreads) mine[i] = reinterpret_cast<const float4*>(c.total)[i];
   c.end();
 }
 
@@ -786,24 +884,28 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const __grid_c
 template <bool F8, int NT>
 cudaError_t run_experts(MoeArgs& a, cudaStream_t st) {
   using P = Parts<F8>;
+  using C = Cta<F8, NT>;
   constexpr int kWarps = kMoeFlat / 32;
   const int blocks = a.T * ((a.H + P::kChunk - 1) / P::kChunk), rows = a.T * a.k * ((a.I + P::kChunk - 1) / P::kChunk);
-  cudaError_t e = launch(moe_prep_kernel<F8>, dim3(1 + (blocks + kWarps - 1) / kWarps), dim3(kMoeFlat), 0, st, true, a);
-  if (e != cudaSuccess) return e;
-  e = launch(moe_gate_up_kernel<F8, NT>, dim3(a.ctas), dim3(kMoeThreads), Cta<F8, NT>::kSmem, st, true, a);
-  if (e != cudaSuccess) return e;
-  e = launch(moe_act_kernel<F8>, dim3((rows + kWarps - 1) / kWarps), dim3(kMoeFlat), 0, st, true, a);
+  cudaError_t e = cudaSuccess;
+  if (!C::kOwn) e = launch(moe_prep_kernel<F8>, dim3(1 + (blocks + kWarps - 1) / kWarps), dim3(kMoeFlat), 0, st, true, a);
+  if (e == cudaSuccess) e = launch(moe_gate_up_kernel<F8, NT>, dim3(a.ctas), dim3(C::kThreads), C::kSmem, st, true, a);
+  if (!C::kOwn && e == cudaSuccess)
+    e = launch(moe_act_kernel<F8>, dim3((rows + kWarps - 1) / kWarps), dim3(kMoeFlat), 0, st, true, a);
   if (e != cudaSuccess) return e;
   // K splits of a tile of the down product: as many CTAs as run at once, each with two chunks if all choices differ
   const int tiles = (a.H + 127) / 128;
   a.splits = std::max(1, std::min({a.ctas / tiles, kMoeMaxSplits, rows / 2}));
-  return launch(moe_down_kernel<F8, NT>, dim3(tiles * a.splits), dim3(kMoeThreads), Cta<F8, NT>::kSmem, st, true, a);
+  e = launch(moe_down_kernel<F8, NT>, dim3(tiles * a.splits), dim3(C::kThreads), C::kSmem, st, true, a);
+  if (e != cudaSuccess) return e;
+  return launch(moe_sum_kernel, dim3((a.T * (a.H / 4) + 127) / 128), dim3(128), 0, st, true, a);
 }
 
 template <bool F8, int NT>
 cudaError_t allow_one() {
   cudaError_t e = prefer_max_carveout(moe_prep_kernel<F8>);
   if (e == cudaSuccess) e = prefer_max_carveout(moe_act_kernel<F8>);
+  if (e == cudaSuccess) e = prefer_max_carveout(moe_sum_kernel);
   if (e == cudaSuccess) e = allow_smem(moe_gate_up_kernel<F8, NT>);
   return e != cudaSuccess ? e : allow_smem(moe_down_kernel<F8, NT>);
 }
@@ -832,9 +934,9 @@ int moe_experts(const MoeCall& c, int sms, cudaStream_t st, const char** why) {
   a.out = c.out;
   const MoeWorkspace w = moe_workspace(c.T, c.k, c.H, c.I);
   a.plan = reinterpret_cast<Plan*>(c.ws);
-  a.arrived = reinterpret_cast<uint32_t*>(c.ws + kMoePlanBytes);
   a.main = reinterpret_cast<float*>(c.ws + w.main);
   a.cut = reinterpret_cast<float*>(c.ws + w.cut);
+  a.sums = reinterpret_cast<float*>(c.ws + w.sums);
   a.xb = c.ws + w.xb;
   a.hb = c.ws + w.hb;
   a.T = c.T;
