@@ -36,6 +36,7 @@
 
 #include "dec_fp8.cuh"
 #include "dec_launch.cuh"
+#include "dec_long.cuh"
 #include "dec_tc.cuh"
 
 namespace dec {
@@ -267,13 +268,19 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
 
 constexpr int kWideThreads = 384;   // warp 0 copies, 1 and 2 multiply, 4-11 scale and store
 constexpr int kWideMaxStages = 6;
-constexpr uint32_t kWideOut = 8 * 2 * 32 * 128;  // twice 32 rows of 32 results per warp, on their way out
-template <int BN>
-struct Wide {  // BN weight rows per tile: 64, 128, 192 or 256
-  static constexpr uint32_t kStage = kF8Tile + BN * kF8BK;
-  static constexpr int kFit = static_cast<int>((kSmemMax - 1024 - kF8Head - kWideOut) / kStage);
-  static constexpr int kStages = kFit < kWideMaxStages ? kFit : kWideMaxStages;  // 3 at 256
-  static constexpr uint32_t kSmem = 1024 + kF8Head + kStages * kStage + kWideOut;
+// Tiles of BN weight rows, 64, 128, 192 or 256, by 128 rows of x; PAIR: by 256,
+// 128 in each of two CTAs (cta_group::2) that hold half of the weight rows each.
+// A pair reads two thirds of the bytes from L2 and shared memory per product,
+// and the tensor core takes 512 cycles a block where it takes 685 alone.
+template <int BN, bool PAIR>
+struct Wide {
+  static constexpr int kBRows = PAIR ? BN / 2 : BN;  // weight rows of a CTA
+  static constexpr uint32_t kStage = kF8Tile + kBRows * kF8BK;
+  static constexpr int kBufs = PAIR ? 3 : 2;  // 32 rows of 32 results per warp, on their way out
+  static constexpr uint32_t kOut = 8 * kBufs * 32 * 128;
+  static constexpr int kFit = static_cast<int>((kSmemMax - 1024 - kF8Head - kOut) / kStage);
+  static constexpr int kStages = kFit < kWideMaxStages ? kFit : kWideMaxStages;  // 3 at 256, 4 as a pair
+  static constexpr uint32_t kSmem = 1024 + kF8Head + kStages * kStage + kOut;
   static constexpr int kChunks = BN / 64;  // of 32 columns, per epilogue warp
 };
 
@@ -289,10 +296,11 @@ struct WideArgs {
   uint32_t* err;
 };
 
-template <int BN>
+template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_constant__ WideArgs a) {
-  constexpr int kWideBN = BN, kWideStages = Wide<BN>::kStages, kChunks = Wide<BN>::kChunks;
-  constexpr uint32_t kWideStage = Wide<BN>::kStage, kCols = tmem_columns(2 * BN);
+  using W = Wide<BN, PAIR>;
+  constexpr int kWideStages = W::kStages, kChunks = W::kChunks, kCtas = PAIR ? 2 : 1;
+  constexpr uint32_t kWideStage = W::kStage, kCols = tmem_columns(2 * BN);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // done: a stage's products are in its accumulator, and the stage may be filled anew
@@ -303,18 +311,28 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);  // a wait ran out: every role ends
   unsigned char* tiles = smem + kF8Head;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? blockIdx.x & 1 : 0, first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kWideStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&done[s], 1);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(&drained[s], 8);
+    for (int s = 0; s < 2; ++s) mbar_init(&drained[s], 8 * kCtas);
     *stop = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, kCols);
+  if (warp == 1) {
+    if (PAIR)
+      tmem_alloc_pair(tmem_slot, kCols);
+    else
+      tmem_alloc(tmem_slot, kCols);
+  }
   tc_fence_before();
+  if (PAIR) {  // the other CTA's barriers are set up, too
+    cluster_arrive();
+    cluster_wait();
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -327,30 +345,36 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
     const uint64_t keep = l2_policy_evict_last();
     int it = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
-      const int m0 = (tile % a.m_tiles) * kF8BM, n0 = (tile / a.m_tiles) * kWideBN;
+    for (int tile = first; tile < a.tiles && ok; tile += step) {
+      const int m0 = (tile % a.m_tiles * kCtas + rank) * kF8BM, n0 = (tile / a.m_tiles) * BN + rank * W::kBRows;
       for (int kb = 0; kb < a.KB; ++kb, ++it) {
         const int s = it % kWideStages;
         if (it >= kWideStages) ok = warp_wait(&done[s], ((it / kWideStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
         if (!ok) break;
         if (elect_one()) {
           unsigned char* st = tiles + s * kWideStage;
-          mbar_arrive_expect_tx(&full[s], kWideStage);
-          tma_load_3d(st, &a.xmap, kb * kF8BK, m0, 0, &full[s], keep);
-          tma_load_3d(st + kF8Tile, &a.wmap, kb * kF8BK, n0, 0, &full[s], keep);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], kCtas * kWideStage);
+          if (PAIR) {  // both CTAs' copies complete on the even one's barrier
+            const uint32_t bar = in_even(&full[s]);
+            tma_load_3d_pair(st, &a.xmap, kb * kF8BK, m0, 0, bar, keep);
+            tma_load_3d_pair(st + kF8Tile, &a.wmap, kb * kF8BK, n0, 0, bar, keep);
+          } else {
+            tma_load_3d(st, &a.xmap, kb * kF8BK, m0, 0, &full[s], keep);
+            tma_load_3d(st + kF8Tile, &a.wmap, kb * kF8BK, n0, 0, &full[s], keep);
+          }
         }
       }
     }
-    if (!ok && lane == 0) {  // an early end waits for its own copies
+    if (!ok && lane == 0) {  // an early end waits for its own copies (a pair's: those that complete here)
       *stop = 1;
       for (int i = max(0, it - kWideStages); i < it; ++i)
         if (!tc_wait(&full[i % kWideStages], (i / kWideStages) & 1, a.err, kErrDrain)) break;
     }
-  } else if (warp == 1 || warp == 2) {
+  } else if ((warp == 1 || warp == 2) && rank == 0) {
     // every second block each, so that one waits for its next while the other's products are being issued
-    constexpr uint32_t idesc = tc_idesc_of(kWideBN, false);
+    constexpr uint32_t idesc = PAIR ? tc_idesc_pair(BN) : tc_idesc_of(BN, false);
     const int b = warp - 1;
-    const int mine = (a.tiles - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const int mine = (a.tiles - first + step - 1) / step;
     bool ok = true;
     for (int it = b; it < mine * a.KB; it += 2) {
       const int s = it % kWideStages;
@@ -361,9 +385,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       const uint32_t sa = smem_addr(tiles + s * kWideStage);
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kF8BK / 32; ++kk)
-          tc_mma_f8(tmem + b * kWideBN, smem_desc_sw128(sa + kk * 32), smem_desc_sw128(sa + kF8Tile + kk * 32), idesc, kk > 0);
-        tc_commit(&done[s]);
+        for (int kk = 0; kk < kF8BK / 32; ++kk) {
+          const uint64_t ad = smem_desc_sw128(sa + kk * 32), bd = smem_desc_sw128(sa + kF8Tile + kk * 32);
+          if (PAIR)
+            tc_mma_f8_pair(tmem + b * BN, ad, bd, idesc, kk > 0);
+          else
+            tc_mma_f8(tmem + b * BN, ad, bd, idesc, kk > 0);
+        }
+        if (PAIR)
+          tc_commit_pair(&done[s]);
+        else
+          tc_commit(&done[s]);
       }
       __syncwarp();
     }
@@ -371,26 +403,39 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., columns BN / 2 half ..
-    unsigned char* stages = tiles + kWideStages * kWideStage + (warp - 4) * 2 * 32 * 128;
+    unsigned char* stages = tiles + kWideStages * kWideStage + (warp - 4) * W::kBufs * 32 * 128;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + half * (BN / 2);
-    int it = 0, turn = 0;
-    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-      const int m0 = (tile % a.m_tiles) * kF8BM + 32 * q, n0 = (tile / a.m_tiles) * BN + BN / 2 * half;
-      const float* sx = a.sx + static_cast<long long>(min(m0 + lane, a.M - 1)) * a.KB;
+    auto release = [&](int b) {  // this warp has read accumulator b
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR)
+          mbar_arrive_cluster(in_even(&drained[b]));
+        else
+          mbar_arrive(&drained[b]);
+      }
+    };
+    int it = 0, turn = 0, m0, n0, cut;
+    const float *sx, *sw, *sv;
+    float x0, w0, v0, x1, w1, v1;
+    auto open = [&](int tile) {  // its place, and the scales of its first two blocks
+      m0 = (tile % a.m_tiles * kCtas + rank) * kF8BM + 32 * q;
+      n0 = (tile / a.m_tiles) * BN + BN / 2 * half;
       // the columns of a warp lie in one block of weight rows, at BN = 192 in two
-      const int nb = n0 / kFp8Block, cut = BN == 192 ? (nb + 1) * kFp8Block - n0 : BN;
-      const float* sw = a.sw + static_cast<long long>(min(nb, a.NB - 1)) * a.KB;
-      const float* sv = a.sw + static_cast<long long>(min(nb + 1, a.NB - 1)) * a.KB;
+      const int nb = n0 / kFp8Block;
+      cut = BN == 192 ? (nb + 1) * kFp8Block - n0 : BN;
+      sx = a.sx + static_cast<long long>(min(m0 + lane, a.M - 1)) * a.KB;
+      sw = a.sw + static_cast<long long>(min(nb, a.NB - 1)) * a.KB;
+      sv = a.sw + static_cast<long long>(min(nb + 1, a.NB - 1)) * a.KB;
+      const int one = a.KB > 1;
+      x0 = __ldg(sx), w0 = __ldg(sw), v0 = BN == 192 ? __ldg(sv) : 0.f;
+      x1 = __ldg(sx + one), w1 = __ldg(sw + one), v1 = BN == 192 ? __ldg(sv + one) : 0.f;
+    };
+    open(first);
+    for (int tile = first; tile < a.tiles; tile += step) {
       float acc[BN / 2];
 #pragma unroll
       for (int j = 0; j < BN / 2; ++j) acc[j] = 0.f;
-      // the scales of the next two blocks are on their way while this one is added
-      float x0 = __ldg(sx), w0 = __ldg(sw), v0 = BN == 192 ? __ldg(sv) : 0.f, x1 = 0.f, w1 = 0.f, v1 = 0.f;
-      if (a.KB > 1) {
-        x1 = __ldg(sx + 1);
-        w1 = __ldg(sw + 1);
-        if (BN == 192) v1 = __ldg(sv + 1);
-      }
       bool ok = true;
       for (int kb = 0; kb < a.KB; ++kb, ++it) {
         const int b = it & 1;
@@ -408,33 +453,34 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
         tc_fence_after();
         // 64 columns asked for at once, added while the next 32 come
         uint32_t v[2][32];
-        tmem_ld_issue32(at + b * kWideBN, v[0]);
+        tmem_ld_issue32(at + b * BN, v[0]);
         tmem_ld_wait32(v[0]);
+        if (kChunks == 1) release(b);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          if (c + 1 < kChunks) tmem_ld_issue32(at + b * kWideBN + 32 * (c + 1), v[(c + 1) & 1]);
+          if (c + 1 < kChunks) tmem_ld_issue32(at + b * BN + 32 * (c + 1), v[(c + 1) & 1]);
           const float f = BN == 192 && 32 * c >= cut ? s2 : s;
 #pragma unroll
           for (int j = 0; j < 32; ++j) acc[32 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), f, acc[32 * c + j]);
           if (c + 1 < kChunks) tmem_ld_wait32(v[(c + 1) & 1]);
+          if (c + 2 == kChunks) release(b);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&drained[b]);
       }
       if (!ok) {
         *stop = 1;
         break;
       }
+      const int out_m = m0, out_n = n0;
+      open(min(tile + step, a.tiles - 1));  // the next tile's scales come while this one's results leave
       // 32 columns at a time through shared memory (rows of 128 bytes, their 16-byte pieces swizzled), so that whole
       // lines leave: by a tensor copy, which runs beside the next tile, or by 8 lanes a row
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        const int n = n0 + 32 * c;
-        if (n < a.N && m0 < a.M) {  // warp-uniform
-          unsigned char* stage = stages + (turn & 1) * 32 * 128;
+        const int n = out_n + 32 * c;
+        if (n < a.N && out_m < a.M) {  // warp-uniform
+          unsigned char* stage = stages + turn % W::kBufs * 32 * 128;
           ++turn;
-          if (a.bulk) tma_store_wait_read<1>();  // the one before last has left this buffer
+          if (a.bulk) tma_store_wait_read<W::kBufs - 1>();  // what this buffer held has left
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -445,7 +491,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
           if (!a.bulk || a.residual) {
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
-              const int rr = 4 * p + (lane >> 3), r = m0 + rr;
+              const int rr = 4 * p + (lane >> 3), r = out_m + rr;
               float4* at4 = reinterpret_cast<float4*>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
               float4 v = *at4;
               if (r >= a.M || col >= a.N) continue;
@@ -475,7 +521,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
           if (a.bulk) {
             fence_to_async();
             __syncwarp();
-            if (lane == 0) tma_store_2d(&a.omap, stage, n, m0);  // the lane that waits for it
+            if (lane == 0) tma_store_2d(&a.omap, stage, n, out_m);  // the lane that waits for it
           }
         }
       }
@@ -484,10 +530,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   }
   __syncwarp();
   tc_fence_before();
+  if (PAIR) {  // neither CTA leaves while the other may reach into it
+    cluster_arrive();
+    cluster_wait();
+  }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_free(tmem, kCols);
+    if (PAIR)
+      tmem_free_pair(tmem, kCols);
+    else
+      tmem_free(tmem, kCols);
   }
 }
 
@@ -534,17 +587,18 @@ int narrow_splits(long long tiles, int KB, int sms) {
 }
 
 // Which form is quickest, by what each took per wave of CTAs and block of K
-// (us, measured over M = 16 .. 2048 with K = 2560 and 8960, within 20 %):
-//   narrow, 16 or 32 rows, two CTAs per SM:  5 + waves (0.37 or 0.45 KB / splits)
-//   wide, tiles of 64, 128, 192, 256 columns: 4.5 + waves (0.5 + 0.214, 0.270, 0.372 or 0.456 KB)
-// e.g. 64 x 9728 x 2560: 10.9 narrow, 9.0 wide 64, 15.2 wide 256; 512 x 1536 x
-// 8960: 31 narrow, 20 wide 64; 509 x 6144 x 2560: 16.9, 13.8, 15.8 wide 128, 192,
-// 256; 2048 x 9728 x 2560: 59, 62, 52.
-enum Form { kNarrow16, kNarrow32, kWide64, kWide128, kWide192, kWide256 };
+// (us, fitted to M = 16 .. 8192 with K = 2560 and 8960, within 10 %):
+//   narrow, 16 or 32 rows, two CTAs per SM:          5 + waves (0.37 or 0.45 KB / splits)
+//   wide, tiles of 64, 128, 192, 256 columns, pairs: 4 + waves (0.8, 1.6, 1.9, 2.2, 3.1 +
+//                                                               0.214, 0.27, 0.36, 0.456, 0.39 KB)
+// e.g. 64 x 9728 x 2560: 10.9 narrow, 9.0 wide 64; 512 x 1536 x 8960: 31 narrow,
+// 20.6 wide 64, 38 wide 256; 509 x 6144 x 2560: 17.6, 13.0, 16.0, 15.9 wide 128,
+// 192, 256 and pairs; 8192 x 9728 x 2560: 225, 200, 182, 175.
+enum Form { kNarrow16, kNarrow32, kWide64, kWide128, kWide192, kWide256, kPairs };
 Form best_form(const Fp8GemmCall& c, int sms) {
   const int KB = (c.K + kF8BK - 1) / kF8BK;
   auto up = [](long long a, long long b) { return (a + b - 1) / b; };
-  Form best = kWide256;
+  Form best = kPairs;
   double least = 1e30;
   auto offer = [&](Form f, double us) {
     if (us < least) {
@@ -557,8 +611,9 @@ Form best_form(const Fp8GemmCall& c, int sms) {
   offer(kNarrow16, 5.0 + up(t16 * s16, 2 * sms) * 0.37 * up(KB, s16));
   if (c.M > 16) offer(kNarrow32, 5.0 + up(t32 * s32, 2 * sms) * 0.45 * up(KB, s32));
   const Form wide[4] = {kWide64, kWide128, kWide192, kWide256};
-  const double per[4] = {0.214, 0.270, 0.372, 0.456};
-  for (int i = 0; i < 4; ++i) offer(wide[i], 4.5 + up(m128 * up(c.N, 64 * (i + 1)), sms) * (0.5 + per[i] * KB));
+  const double tile[4] = {0.8, 1.6, 1.9, 2.2}, block[4] = {0.214, 0.27, 0.36, 0.456};
+  for (int i = 0; i < 4; ++i) offer(wide[i], 4.0 + up(m128 * up(c.N, 64 * (i + 1)), sms) * (tile[i] + block[i] * KB));
+  offer(kPairs, 4.0 + up(up(c.M, 2 * kF8BM) * up(c.N, 256), sms / 2) * (3.1 + 0.39 * KB));
   return best;
 }
 
@@ -601,11 +656,11 @@ cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const 
   return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<BN>, a);
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
   static thread_local WideArgs a;
   std::memset(&a, 0, sizeof(a));
-  if (!make_tmap_mats(&a.wmap, c.wc, 1, c.K, c.N, 1, BN) || !make_tmap_mats(&a.xmap, c.xc, 1, c.K, c.M, 1, kF8BM)) {
+  if (!make_tmap_mats(&a.wmap, c.wc, 1, c.K, c.N, 1, Wide<BN, PAIR>::kBRows) || !make_tmap_mats(&a.xmap, c.xc, 1, c.K, c.M, 1, kF8BM)) {
     *why = "a tensor map could not be made";
     return cudaErrorInvalidValue;
   }
@@ -619,7 +674,8 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
   a.N = c.N;
   a.KB = (c.K + kF8BK - 1) / kF8BK;
   a.NB = (c.N + kFp8Block - 1) / kFp8Block;
-  a.m_tiles = (c.M + kF8BM - 1) / kF8BM;
+  constexpr int kCtas = PAIR ? 2 : 1, kRows = kF8BM * kCtas;
+  a.m_tiles = (c.M + kRows - 1) / kRows;
   a.tiles = a.m_tiles * ((c.N + BN - 1) / BN);
   a.err = c.err;
   auto rows16 = [](const void* p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 4 == 0; };
@@ -629,7 +685,21 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
     *why = "a tensor map could not be made";
     return cudaErrorInvalidValue;
   }
-  return launch(fp8_wide_kernel<BN>, dim3(std::min(a.tiles, sms)), dim3(kWideThreads), Wide<BN>::kSmem, st, true, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min(a.tiles, sms / kCtas) * kCtas);
+  cfg.blockDim = dim3(kWideThreads);
+  cfg.dynamicSmemBytes = Wide<BN, PAIR>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fp8_wide_kernel<BN, PAIR>, a);
 }
 
 }  // namespace
@@ -640,10 +710,11 @@ int fp8_gemm(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
   switch (best_form(c, sms)) {
     case kNarrow16: e = launch_narrow<16>(c, sms, st, why); break;
     case kNarrow32: e = launch_narrow<32>(c, sms, st, why); break;
-    case kWide64: e = launch_wide<64>(c, sms, st, why); break;
-    case kWide128: e = launch_wide<128>(c, sms, st, why); break;
-    case kWide192: e = launch_wide<192>(c, sms, st, why); break;
-    default: e = launch_wide<256>(c, sms, st, why); break;
+    case kWide64: e = launch_wide<64, false>(c, sms, st, why); break;
+    case kWide128: e = launch_wide<128, false>(c, sms, st, why); break;
+    case kWide192: e = launch_wide<192, false>(c, sms, st, why); break;
+    case kWide256: e = launch_wide<256, false>(c, sms, st, why); break;
+    default: e = launch_wide<256, true>(c, sms, st, why); break;
   }
   if (*why) return 1;
   if (e != cudaSuccess) {
@@ -657,10 +728,11 @@ cudaError_t allow_smem_fp8_gemm() {
   cudaError_t e;
   if ((e = allow_smem(fp8_narrow_kernel<16>)) != cudaSuccess) return e;
   if ((e = allow_smem(fp8_narrow_kernel<32>)) != cudaSuccess) return e;
-  if ((e = allow_smem(fp8_wide_kernel<64>)) != cudaSuccess) return e;
-  if ((e = allow_smem(fp8_wide_kernel<128>)) != cudaSuccess) return e;
-  if ((e = allow_smem(fp8_wide_kernel<192>)) != cudaSuccess) return e;
-  return allow_smem(fp8_wide_kernel<256>);
+  if ((e = allow_smem(fp8_wide_kernel<64, false>)) != cudaSuccess) return e;
+  if ((e = allow_smem(fp8_wide_kernel<128, false>)) != cudaSuccess) return e;
+  if ((e = allow_smem(fp8_wide_kernel<192, false>)) != cudaSuccess) return e;
+  if ((e = allow_smem(fp8_wide_kernel<256, false>)) != cudaSuccess) return e;
+  return allow_smem(fp8_wide_kernel<256, true>);
 }
 
 }  // namespace dec
