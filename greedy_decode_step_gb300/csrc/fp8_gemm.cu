@@ -336,33 +336,47 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
-  pdl_launch_dependents();
   // 128 threads x 40 + 256 x 232 registers = the 384 x 168 of the launch
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
 
   if (warp == 0) {
     const uint64_t keep = l2_policy_evict_last();
+    // a pair's copies complete on the even CTA's barrier
+    auto bring = [&](const CUtensorMap* map, int it, uint32_t at, int kb, int row) {
+      const int s = it % kWideStages;
+      unsigned char* to = tiles + s * kWideStage + at;
+      if (PAIR)
+        tma_load_3d_pair(to, map, kb * kF8BK, row, 0, in_even(&full[s]), keep);
+      else
+        tma_load_3d(to, map, kb * kF8BK, row, 0, &full[s], keep);
+    };
+    auto expect = [&](int it) {
+      if (rank == 0) mbar_arrive_expect_tx(&full[it % kWideStages], kCtas * kWideStage);
+    };
+    // weights go out before the wait for the kernel that makes the rows, as in the narrow form
+    const int pre = first < a.tiles ? min(a.KB, kWideStages) : 0;
+    if (elect_one())
+      for (int i = 0; i < pre; ++i) {
+        expect(i);
+        bring(&a.wmap, i, kF8Tile, i, first / a.m_tiles * BN + rank * W::kBRows);
+      }
+    __syncwarp();
+    pdl_wait();
+    pdl_launch_dependents();
     int it = 0;
     bool ok = true;
     for (int tile = first; tile < a.tiles && ok; tile += step) {
       const int m0 = (tile % a.m_tiles * kCtas + rank) * kF8BM, n0 = (tile / a.m_tiles) * BN + rank * W::kBRows;
       for (int kb = 0; kb < a.KB; ++kb, ++it) {
-        const int s = it % kWideStages;
-        if (it >= kWideStages) ok = warp_wait(&done[s], ((it / kWideStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
+        if (it >= kWideStages)
+          ok = warp_wait(&done[it % kWideStages], ((it / kWideStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
         if (!ok) break;
         if (elect_one()) {
-          unsigned char* st = tiles + s * kWideStage;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], kCtas * kWideStage);
-          if (PAIR) {  // both CTAs' copies complete on the even one's barrier
-            const uint32_t bar = in_even(&full[s]);
-            tma_load_3d_pair(st, &a.xmap, kb * kF8BK, m0, 0, bar, keep);
-            tma_load_3d_pair(st + kF8Tile, &a.wmap, kb * kF8BK, n0, 0, bar, keep);
-          } else {
-            tma_load_3d(st, &a.xmap, kb * kF8BK, m0, 0, &full[s], keep);
-            tma_load_3d(st + kF8Tile, &a.wmap, kb * kF8BK, n0, 0, &full[s], keep);
-          }
+          if (it >= pre) expect(it);
+          bring(&a.xmap, it, 0, kb, m0);
+          if (it >= pre) bring(&a.wmap, it, kF8Tile, kb, n0);
         }
+        __syncwarp();
       }
     }
     if (!ok && lane == 0) {  // an early end waits for its own copies (a pair's: those that complete here)
@@ -431,6 +445,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       x0 = __ldg(sx), w0 = __ldg(sw), v0 = BN == 192 ? __ldg(sv) : 0.f;
       x1 = __ldg(sx + one), w1 = __ldg(sw + one), v1 = BN == 192 ? __ldg(sv + one) : 0.f;
     };
+    pdl_wait();  // the rows' scales and the residual
     open(first);
     for (int tile = first; tile < a.tiles; tile += step) {
       float acc[BN / 2];
