@@ -694,7 +694,7 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
   a.tiles = a.m_tiles * ((c.N + BN - 1) / BN);
   a.err = c.err;
   auto rows16 = [](const void* p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 4 == 0; };
-  a.bulk = rows16(c.out, c.ldo) && c.N % 4 == 0;  // a tensor copy cuts a row off at whole 16 bytes only
+  a.bulk = rows16(c.out, c.ldo) && c.ldo < (1ll << 36) && c.N % 4 == 0;  // a tensor copy cuts a row off at whole 16 bytes only
   a.vec = c.residual && rows16(c.residual, c.ldr);
   if (a.bulk && !make_tmap_out(&a.omap, c.out, c.N, c.M, c.ldo)) {
     *why = "a tensor map could not be made";
@@ -719,8 +719,10 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
 
 }  // namespace
 
-int fp8_gemm(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
+int fp8_gemm(const Fp8GemmCall& call, int sms, cudaStream_t st, const char** why) {
   *why = nullptr;
+  Fp8GemmCall c = call;
+  if (c.M == 1) c.ldo = c.ldr = (static_cast<long long>(c.N) + 3) / 4 * 4;  // one row's strides mean nothing
   cudaError_t e;
   switch (best_form(c, sms)) {
     case kNarrow16: e = launch_narrow<16>(c, sms, st, why); break;

@@ -351,7 +351,8 @@ int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cac
  *   s = the smallest power of two, 2^-126 at least, with a <= 448 s (1 if a == 0)
  *   c = e4m3(x / s), to nearest, ties to even
  * and the NaN code for an infinity or a NaN, which no other value is touched
- * by.  Codes and scales are defined to the bit.  n and rows may be 0.
+ * by.  Codes and scales are defined to the bit, and memory of their own.  n and
+ * rows may be 0.
  */
 int dec_fp8_quant(const void* x, int bf16, int64_t stride_mat, int64_t stride_row, void* codes, float* scales, int n,
                   int rows, int K, int block_rows, void* stream);
@@ -403,11 +404,11 @@ size_t dec_moe_workspace_size(int T, int k, int H, int I);
  * [E][H][I], H and I multiples of 8.  Else e4m3 codes of these shapes with
  * scales of 128 x 128 blocks per expert, [E][ceil(I/128)][ceil(H/128)] and for
  * Wd [E][ceil(H/128)][ceil(I/128)], H and I multiples of 16.  Activations keep
- * float32 accuracy: an element of y is held to 2^-24 of itself (8-bit weights:
- * to 2^-23 of the largest of its 128), and so is one of the MLP's inner
- * vector.  Each chosen expert's weights are read once.  The weights must be
- * finite: a NaN or an infinity in an expert reaches every token of the call; a
- * non-finite element of y reaches its own token only.  y, residual and out
+ * float32 accuracy: an element of y (up to 2^127) is held to 2^-24 of itself or
+ * 2^-133, whichever is more (8-bit weights: to 2^-23 of the largest of its 128),
+ * and so is one of the MLP's inner vector.  Each chosen expert's
+ * weights are read once.  A NaN or an infinity in an expert reaches the tokens
+ * that chose it (as NaN, it may be), one in y its own token.  y, residual and out
  * fp32 [T][H]; residual may be NULL or out, and out may be y.  T is 0..16, k
  * 1..16, E 1..1024, H and I up to 32768.  ws: device workspace of
  * dec_moe_workspace_size() bytes, 256-byte aligned, any contents; calls that

@@ -172,6 +172,35 @@ def test_residual_and_views(M):
     assert torch.equal(same, out)
 
 
+# sizes that take each form of the product (16 and 32 rows, tiles of 64, 128, 192 and 256 columns, pairs of CTAs),
+# ragged on both sides, with rows of the result that are whole 16 bytes and that are not
+FORMS = [(9, 700, 1040), (40, 1530, 8960), (130, 4100, 656), (250, 9000, 400), (500, 6140, 1040), (385, 9700, 144),
+         (1000, 9730, 528), (2050, 9729, 272), (2047, 9700, 1040), (2041, 9702, 2576), (2040, 9704, 2576), (4200, 5003, 144)]
+
+
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_every_form(M, N, K):
+    ops = operands(80, M, N, K)
+    res = normal(85, M, N)
+    want, bound = R.gemm(*ops, residual=res)
+    out = torch.full((M, N), math.nan, device="cuda")
+    gd.dec_fp8_gemm(*ops, out, residual=res)
+    close(out, want, bound)
+    again = res.clone()
+    gd.dec_fp8_gemm(*ops, again, residual=again)
+    assert torch.equal(again, out)
+
+
+def test_one_row_takes_any_strides():
+    ops = operands(86, 1, 333, 160)
+    want, bound = R.gemm(*ops)
+    out = torch.zeros(1, 333, device="cuda")
+    ptr = [t.data_ptr() for t in ops]
+    assert gd.lib().dec_fp8_gemm(*ptr, out.data_ptr(), 0, out.data_ptr(), 0, 1, 333, 160, None) == gd.DEC_OK
+    torch.cuda.synchronize()
+    close(out, want, bound)
+
+
 @pytest.mark.parametrize("M", [5, 60, 200])
 def test_a_nan_stays_in_its_row_and_column(M):
     N, K = 200, 400

@@ -268,6 +268,28 @@ def test_a_nan_stays_with_its_token(fp8):
     assert torch.equal(out[[0, 3, 5]], clean[[0, 3, 5]])
 
 
+@pytest.mark.parametrize("T", [2, 7, 16])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_nan_in_an_expert_stays_with_its_tokens(T, fp8):
+    H, I, E, k = 512, 320, 9, 2
+    y, res = normal(170, T, H), normal(171, T, H)
+    held, scales, plain = make_weights(172, E, H, I, fp8)
+    ids, w = choose(173, T, k, E)
+    ids[0] = torch.tensor([4, 1], dtype=torch.int32, device="cuda")
+    ids[1] = torch.tensor([1, 7], dtype=torch.int32, device="cuda")
+    clean = check(y, ids, w, held, scales, plain, res)
+    for i in range(3):
+        m = held[i].view(torch.uint8 if fp8 else torch.int16)
+        was = m[4, 33, 65].clone()
+        m[4, 33, 65] = 0x7F if fp8 else 0x7FC0
+        out = torch.zeros_like(y)
+        gd.dec_moe_experts(y, ids, w, *held, out, residual=res, scales=scales)
+        hit = (ids == 4).any(-1)
+        assert torch.equal(torch.isnan(out).any(-1), hit) and bool(hit[0]) and not bool(hit[1])
+        assert torch.equal(out[~hit], clean[~hit])
+        m[4, 33, 65] = was
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_results_over_their_inputs(fp8):
     T, H, I, E, k = 7, 528, 224, 9, 3
