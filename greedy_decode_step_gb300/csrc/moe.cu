@@ -122,7 +122,12 @@ struct Runs {
     n = static_cast<int>(min(static_cast<long long>(a.ctas), min(8 * tiles, W)));  // no run is empty
   }
   __device__ __forceinline__ int begin(int c) const { return c >= n ? static_cast<int>(W) : static_cast<int>(W * c / n); }
-  __device__ __forceinline__ int owner(long long pos) const { return static_cast<int>(((pos + 1) * n - 1) / W); }
+  // The CTA whose run holds chunk `pos`; in 32 bits where they do, a quarter of the instructions.
+  __device__ __forceinline__ int owner(long long pos) const {
+    const unsigned long long x = static_cast<unsigned long long>(pos + 1) * n - 1;
+    if (static_cast<unsigned long long>(W) * n <= 0xFFFFFFFFull) return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(W));
+    return static_cast<int>(x / static_cast<unsigned long long>(W));
+  }
 };
 
 // ----------------------------------------------------------------------------- parts of an activation row
@@ -343,14 +348,22 @@ struct Inner {
 #pragma unroll
     for (int v = 0; v < P::kVals; ++v) x[v] = 0.f;
     if (!inside) return;
-    float g[P::kVals], u[P::kVals];
+    // the products and the first part, which is the only one as a rule, in flight together
+    float g[P::kVals], u[P::kVals], dg[P::kVals], du[P::kVals];
+    const size_t part = kMoeMaxTokens * 2 * kMoeUnit;
+    const float* src = a.cut + (static_cast<size_t>(c0 + 1) * kMoeMaxTokens + rank) * (2 * kMoeUnit) + (i & (kMoeUnit - 1));
     load_vals(g, a.main + static_cast<size_t>(row) * 2 * a.I + i);
     load_vals(u, a.main + (static_cast<size_t>(row) * 2 + 1) * a.I + i);
-    for (int c = c0 + 1; c <= c1; ++c) {
-      const float* src = a.cut + (static_cast<size_t>(c) * kMoeMaxTokens + rank) * (2 * kMoeUnit) + (i & (kMoeUnit - 1));
-      float dg[P::kVals], du[P::kVals];
+    if (c1 > c0) {
       load_vals(dg, src);
       load_vals(du, src + kMoeUnit);
+    }
+    for (int c = c0 + 1; c <= c1; ++c) {
+      if (c > c0 + 1) {
+        src += part;
+        load_vals(dg, src);
+        load_vals(du, src + kMoeUnit);
+      }
 #pragma unroll
       for (int v = 0; v < P::kVals; ++v) {
         g[v] += dg[v];
@@ -789,15 +802,25 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_down_kernel(cons
     }
     if (half == 0 && lane == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
   } else if (c.kOwn && warp >= 7) {
-    pdl_wait();  // gate and up products
     const Runs r(p.active, a, P::kChunk);
     const int mine = warp - 7;
+    // the next chunk's places are worked out while this one's values come
+    auto place = [&](int it) {
+      const int act = min(lo + it, all - 1) / kch, j = lo + it - act * kch;
+      return Inner<F8>(a, r, act, p.first[act], 0, j);
+    };
+    Inner<F8> at = place(hi > lo ? mine : 0);
+    pdl_wait();  // gate and up products
     for (int it = mine; it < hi - lo; it += kMoeOwnWarps) {
-      const int act = (lo + it) / kch, j = lo + it - act * kch, first = p.first[act], count = p.count[act];
-      const Inner<F8> one(a, r, act, first, 0, j), two(a, r, act, first + 1, 1, j);
+      const int act = (lo + it) / kch, count = p.count[act];
+      Inner<F8> two = at;
+      ++two.row;
+      ++two.rank;
       float x[2][P::kVals];
-      one.get(a, p.gate[first], x[0]);
-      if (count == 2) two.get(a, p.gate[first + 1], x[1]);
+      const float w = p.gate[at.row];
+      at.get(a, w, x[0]);
+      if (count == 2) two.get(a, p.gate[two.row], x[1]);
+      if (it + kMoeOwnWarps < hi - lo) at = place(it + kMoeOwnWarps);
       unsigned char* slot = c.own_slot(it, a.err);
       if (!slot) break;
       put_parts(slot, lane, x[0]);
