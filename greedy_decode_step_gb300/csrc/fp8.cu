@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const Fp8Quan
 }
 
 template <bool BF16>
-constexpr int kTileCtas = BF16 ? 3 : 2;  // per SM
+constexpr int kTileCtas = BF16 ? 4 : 2;  // per SM
 
 // 128 x 128 blocks: one CTA per block, which it holds in registers as it came.
 template <bool BF16>
