@@ -97,10 +97,24 @@ struct Vec {  // 16 bytes of a source row, as they came
   }
 };
 
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994): with 2^s >= d and
+// m = floor(2^(31 + s) / d) + 1, m d exceeds 2^(31 + s) by at most 2^s.  The
+// index divisions were a third of the read-back's instructions.
+struct Divisor {
+  uint32_t d, m, s;
+  explicit Divisor(uint32_t by) : d(by), m(0), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>((1ull << (31 + s)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return s == 0 ? n : __umulhi(n, m) >> (s - 1); }
+};
+
 // Rows of one launch: flat row f0 + i of all matrices' rows laid end to end.
 // Launches are cut so that every index below fits 32 bits.
 struct Slice {
   uint32_t mat, row, rows;  // first matrix, first row in it, rows
+  Divisor per_row, per_mat;  // items of a row, rows of a matrix
 };
 
 template <bool BF16>
@@ -124,12 +138,12 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const Fp8Quan
     int k[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t b = b0 + u * kPer + sub, i = b / KB;
+      const uint32_t b = b0 + u * kPer + sub, i = s.per_row(b);
       k[u] = static_cast<int>(b - i * KB) * kFp8Block + in * kN;
       flat[u] = -1;
       x[u].zero();
       if (b < blocks) {
-        const uint32_t r = s.row + i, m = r / a.rows;
+        const uint32_t r = s.row + i, m = s.per_mat(r);
         flat[u] = static_cast<long long>(s.mat) * a.rows + r;
         if (k[u] < a.K) x[u].load(source<BF16>(a, s.mat + m, r - m * a.rows, k[u]));
       }
@@ -243,7 +257,7 @@ __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const Fp8Dequant
     char* dst[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t i = i0 + u * kQuantThreads, f = i / per_row, r = s.row + f, m = r / a.rows;
+      const uint32_t i = i0 + u * kQuantThreads, f = s.per_row(i), r = s.row + f, m = s.per_mat(r);
       const uint32_t k = (i - f * per_row) * kN, mat = s.mat + m, row = r - m * a.rows;
       dst[u] = nullptr;
       if (i >= total) continue;
@@ -291,7 +305,8 @@ cudaError_t in_slices(int n, int rows, long long per_row, F f) {
   const long long all = static_cast<long long>(n) * rows, most = std::max(1ll, (1ll << 31) / per_row - 1);
   for (long long at = 0; at < all;) {
     const Slice s{static_cast<uint32_t>(at / rows), static_cast<uint32_t>(at % rows),
-                  static_cast<uint32_t>(std::min(all - at, std::min(most, (1ll << 31) - rows)))};
+                  static_cast<uint32_t>(std::min(all - at, std::min(most, (1ll << 31) - rows))),
+                  Divisor(static_cast<uint32_t>(per_row)), Divisor(static_cast<uint32_t>(rows))};
     const cudaError_t e = f(s);
     if (e != cudaSuccess) return e;
     at += s.rows;

@@ -148,7 +148,8 @@ def check(y, ids, w, held, scales, plain, residual=None):
 SIZES = [  # T, H, I, E, k
     (1, 256, 704, 8, 2), (1, 16, 16, 1, 1), (2, 128, 64, 4, 4), (1, 2560, 1216, 64, 8), (3, 272, 144, 5, 2),
     (8, 1536, 896, 20, 10), (9, 400, 208, 33, 3), (16, 512, 128, 16, 16), (16, 1536, 896, 80, 10), (13, 2064, 80, 200, 7),
-    (1, 4096, 64, 6, 1), (16, 64, 2048, 3, 2), (5, 1168, 1040, 1024, 16)]
+    (1, 4096, 64, 6, 1), (16, 64, 2048, 3, 2), (5, 1168, 1040, 1024, 16), (16, 128, 64, 1024, 16), (2, 144, 80, 40, 16),
+    (16, 32768, 48, 2, 1), (2, 64, 32768, 2, 2), (4, 32768, 32, 3, 3)]
 
 
 @pytest.mark.parametrize("fp8", [False, True])
