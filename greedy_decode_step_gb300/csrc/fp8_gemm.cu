@@ -46,7 +46,9 @@ constexpr int kF8BM = 128;                    // accumulator lanes
 constexpr int kF8BK = kFp8Block;              // K per stage: one scale block, one 128-byte swizzle row
 constexpr uint32_t kF8Tile = kF8BM * kF8BK;   // 16 KB: 128 rows of a stage
 constexpr uint32_t kF8Head = 1024;            // barriers
-constexpr uint32_t kNarrowHead = 2048;        // and two blocks' scales per row of x
+constexpr int kNarrowGroup = 8;               // blocks whose scales are fetched together
+constexpr int kNarrowAccs = 4;                // accumulators in turn
+constexpr uint32_t kNarrowHead = 3072;        // barriers, and two groups' scales per row of x
 
 // ----------------------------------------------------------------------------- narrow: weight rows on the lanes
 
@@ -81,15 +83,16 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + kNarrowMaxStages;
-  uint64_t* accum = empty + kNarrowMaxStages;  // [2] an accumulator holds a block
-  uint64_t* drained = accum + 2;               // [2] it has been read
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
+  uint64_t* accum = empty + kNarrowMaxStages;  // an accumulator holds a block
+  uint64_t* drained = accum + kNarrowAccs;     // it has been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + kNarrowAccs);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);  // a wait ran out: every role ends
-  float(*scales)[BN] = reinterpret_cast<float(*)[BN]>(smem + kF8Head);
+  float(*scales)[BN] = reinterpret_cast<float(*)[BN]>(smem + kF8Head);  // [2 groups x blocks]
+  static_assert(kF8Head + 2 * kNarrowGroup * BN * 4 <= kNarrowHead, "scales");
   unsigned char* tiles = smem + kNarrowHead;
   constexpr uint32_t kXTile = BN * kF8BK, kStage = kF8Tile + kXTile;
   constexpr int kStages = narrow_stages<BN>();
-  constexpr uint32_t kCols = tmem_columns(2 * BN);
+  constexpr uint32_t kCols = tmem_columns(kNarrowAccs * BN);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits;
   const int m0 = (tile / a.n_tiles) * kF8BM;  // weight rows
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kNarrowAccs; ++s) {
       mbar_init(&accum[s], 1);
       mbar_init(&drained[s], 4);
     }
@@ -158,9 +161,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
     constexpr uint32_t idesc = tc_idesc_of(BN, false);
     bool ok = true;
     for (int i = 0; i < nkb; ++i) {
-      const int s = i % kStages, b = i & 1;
+      const int s = i % kStages, b = i % kNarrowAccs;
       ok = warp_wait(&full[s], (i / kStages) & 1, stop, a.err, kErrWaitFull) &&
-           (i < 2 || warp_wait(&drained[b], ((i >> 1) - 1) & 1, stop, a.err, kErrWaitFull));
+           (i < kNarrowAccs || warp_wait(&drained[b], ((i / kNarrowAccs) - 1) & 1, stop, a.err, kErrWaitFull));
       if (!ok) break;
       tc_fence_after();
       const uint32_t sa = smem_addr(tiles + s * kStage);
@@ -182,21 +185,29 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
     float acc[BN];
 #pragma unroll
     for (int j = 0; j < BN; ++j) acc[j] = 0.f;
-    // thread t brings row t's scale of every block, one block ahead
-    const bool brings = t < BN && r0 + t < a.M;
-    const float* sx = brings ? a.sx + static_cast<long long>(r0 + t) * a.KB + kb0 : a.sx;
+    // the 128 threads bring the products of a group's scales, the next group's while this one is added
+    constexpr int kEach = kNarrowGroup * BN / 128;
     const float* sw = a.sw + static_cast<long long>(m0 / kFp8Block) * a.KB + kb0;
-    float nx = brings ? __ldg(sx) : 0.f, nw = __ldg(sw);
+    float next[kEach];
+    auto fetch = [&](int first) {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int i = first + (t + 128 * e) / BN, r = r0 + t % BN;
+        next[e] = i < nkb && r < a.M ? __ldg(a.sx + static_cast<long long>(r) * a.KB + kb0 + i) * __ldg(sw + i) : 0.f;
+      }
+    };
+    fetch(0);
     bool ok = nkb > 0;
     for (int i = 0; i < nkb; ++i) {
-      const int b = i & 1;
-      if (t < BN) scales[b][t] = nx * nw;
-      if (i + 1 < nkb) {
-        nx = brings ? __ldg(sx + i + 1) : 0.f;
-        nw = __ldg(sw + i + 1);
+      const int b = i % kNarrowAccs, turn = i / kNarrowGroup & 1;
+      if (i % kNarrowGroup == 0) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) scales[turn * kNarrowGroup + (t + 128 * e) / BN][t % BN] = next[e];
+        fetch(i + kNarrowGroup);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
       }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      ok = warp_wait(&accum[b], (i >> 1) & 1, stop, a.err, kErrWaitFull);
+      const float* scale = scales[turn * kNarrowGroup + i % kNarrowGroup];
+      ok = warp_wait(&accum[b], (i / kNarrowAccs) & 1, stop, a.err, kErrWaitFull);
       if (!ok) *stop = 1;
       tc_fence_after();
       if (ok) {
@@ -206,7 +217,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
           tmem_ld_issue(at + b * BN + c, v);
           tmem_ld_wait(v);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(__uint_as_float(v[j]), scales[b][c + j], acc[c + j]);
+          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(__uint_as_float(v[j]), scale[c + j], acc[c + j]);
         }
       }
       tc_fence_before();
