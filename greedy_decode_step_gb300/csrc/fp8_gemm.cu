@@ -499,13 +499,24 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       const int out_m = m0, out_n = n0;
       open(min(tile + step, a.tiles - 1));  // the next tile's scales come while this one's results leave
       // 32 columns at a time through shared memory (rows of 128 bytes, their 16-byte pieces swizzled), so that whole
-      // lines leave: by a tensor copy, which runs beside the next tile, or by 8 lanes a row
+      // lines leave: by a tensor copy, which runs beside the next tile, or by a warp a row
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const int n = out_n + 32 * c;
         if (n < a.N && out_m < a.M) {  // warp-uniform
           unsigned char* stage = stages + turn % W::kBufs * 32 * 128;
           ++turn;
+          // all loads of the residual before anything is written: they are in flight together, and beside what follows
+          const int row8 = lane >> 3, piece = lane & 7;
+          float4 add[8];
+          if (a.bulk && a.vec) {  // 8 lanes a row
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+              const int r = out_m + 4 * p + row8, col = n + 4 * piece;
+              add[p] = r < a.M && col < a.N ? *reinterpret_cast<const float4*>(a.residual + r * a.ldr + col)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
           if (a.bulk) tma_store_wait_read<W::kBufs - 1>();  // what this buffer held has left
           __syncwarp();
 #pragma unroll
@@ -513,34 +524,34 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
             *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(
                 acc[32 * c + 4 * j], acc[32 * c + 4 * j + 1], acc[32 * c + 4 * j + 2], acc[32 * c + 4 * j + 3]);
           __syncwarp();
-          const int piece = lane & 7, col = n + 4 * piece;
-          if (!a.bulk || a.residual) {
+          if (a.bulk && a.vec) {
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
-              const int rr = 4 * p + (lane >> 3), r = out_m + rr;
+              const int rr = 4 * p + row8;
               float4* at4 = reinterpret_cast<float4*>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
-              float4 v = *at4;
-              if (r >= a.M || col >= a.N) continue;
-              const float* add = a.residual ? a.residual + r * a.ldr + col : nullptr;
-              if (a.vec && col + 4 <= a.N) {
-                if (add) {
-                  const float4 w = *reinterpret_cast<const float4*>(add);
-                  v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-                }
-              } else if (add) {
-                v.x += add[0];
-                if (col + 1 < a.N) v.y += add[1];
-                if (col + 2 < a.N) v.z += add[2];
-                if (col + 3 < a.N) v.w += add[3];
+              const float4 v = *at4;
+              *at4 = make_float4(v.x + add[p].x, v.y + add[p].y, v.z + add[p].z, v.w + add[p].w);
+            }
+          } else if (!a.bulk || a.residual) {  // a lane a column, 8 rows at once: rows that are not whole 16 bytes
+            const int col = n + lane;
+#pragma unroll
+            for (int r8 = 0; r8 < 32; r8 += 8) {
+              float v[8], w[8];
+              float* at1[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int rr = r8 + k, r = out_m + rr;
+                w[k] = a.residual && r < a.M && col < a.N ? a.residual[r * a.ldr + col] : 0.f;
+                at1[k] = reinterpret_cast<float*>(stage + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4)) + (lane & 3);
+                v[k] = *at1[k];
               }
-              if (a.bulk) {
-                *at4 = v;
-              } else {
-                float* dst = a.out + r * a.ldo + col;
-                dst[0] = v.x;
-                if (col + 1 < a.N) dst[1] = v.y;
-                if (col + 2 < a.N) dst[2] = v.z;
-                if (col + 3 < a.N) dst[3] = v.w;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int r = out_m + r8 + k;
+                if (a.bulk)
+                  *at1[k] = v[k] + w[k];
+                else if (r < a.M && col < a.N)
+                  a.out[r * a.ldo + col] = v[k] + w[k];
               }
             }
           }
