@@ -533,25 +533,30 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
               *at4 = make_float4(v.x + add[p].x, v.y + add[p].y, v.z + add[p].z, v.w + add[p].w);
             }
           } else if (!a.bulk || a.residual) {  // a lane a column, 8 rows at once: rows that are not whole 16 bytes
-            const int col = n + lane;
-#pragma unroll
-            for (int r8 = 0; r8 < 32; r8 += 8) {
-              float v[8], w[8];
-              float* at1[8];
+            const int rows = min(32, a.M - out_m);
+            const bool in = n + lane < a.N;
+            float* dst = a.out + static_cast<long long>(out_m) * a.ldo + n + lane;
+            const float* res = a.residual ? a.residual + static_cast<long long>(out_m) * a.ldr + n + lane : nullptr;
+            unsigned char* from = stage + 4 * (lane & 3);
+#pragma unroll 1
+            for (int r8 = 0; r8 < rows; r8 += 8, from += 8 * 128) {
+              float v[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const int rr = r8 + k, r = out_m + rr;
-                w[k] = a.residual && r < a.M && col < a.N ? a.residual[r * a.ldr + col] : 0.f;
-                at1[k] = reinterpret_cast<float*>(stage + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4)) + (lane & 3);
-                v[k] = *at1[k];
+                v[k] = 0.f;
+                if (res && in && r8 + k < rows) v[k] = *res;
+                if (res) res += a.ldr;
               }
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int r = out_m + r8 + k;
-                if (a.bulk)
-                  *at1[k] = v[k] + w[k];
-                else if (r < a.M && col < a.N)
-                  a.out[r * a.ldo + col] = v[k] + w[k];
+              for (int k = 0; k < 8; ++k)
+                v[k] += *reinterpret_cast<const float*>(from + k * 128 + (((lane >> 2) ^ k) << 4));
+              if (a.bulk) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) *reinterpret_cast<float*>(from + k * 128 + (((lane >> 2) ^ k) << 4)) = v[k];
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k, dst += a.ldo)
+                  if (in && r8 + k < rows) *dst = v[k];
               }
             }
           }
