@@ -438,7 +438,7 @@ PyObject* moe_experts(PyObject* const* a) {
   const void* yp = gpu(a[0], at::kFloat, {T, H}, dev, "y");
   const void* ids = gpu(a[1], at::kInt, {T, k}, dev, "ids");
   const void* gates = gpu(a[2], at::kFloat, {T, k}, dev, "weights");
-  const bool f8 = a[8] != Py_None;
+  const bool f8 = a[8] != Py_None || a[9] != Py_None || a[10] != Py_None;
   const void *wg, *wu, *wd, *sg = nullptr, *su = nullptr, *sd = nullptr;
   if (f8) {
     const int64_t IB = (I + 127) / 128, HB = (H + 127) / 128;

@@ -116,8 +116,8 @@ int dec_fp8_dequant(const void* codes, const float* scales, void* out, int bf16,
   DEC_WORDS(scales);
   DEC_PTR(out);
   DEC_TRY(check_strides(stride_mat, stride_row, bf16));
-  DEC_CHECK((n == 1 || stride_mat) && (rows == 1 || stride_row), DEC_EINVAL,
-            "rows read back may not share memory (a stride of zero)");
+  DEC_CHECK((n == 1 || stride_mat >= K) && (rows == 1 || stride_row >= K), DEC_EINVAL,
+            "rows read back may not share memory: strides of K = %d at least", K);
   int sms;
   uint32_t* err;
   DEC_TRY(host_device(&sms, &err));

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
       tma_load_3d(tiles + i % kStages * kStage + kF8Tile, &a.xmap, (kb0 + i) * kF8BK, r0, 0, &full[i % kStages], xpol);
     };
     // weights go out before the wait for the kernel that makes the rows (the kernels that make weights let nothing start
-    // before they are complete)
+    // before they are complete, and `early_start` sees to a single row)
     const int pre = min(nkb, kStages);
     if (elect_one())
       for (int i = 0; i < pre; ++i) {
@@ -659,6 +659,10 @@ Form best_form(const Fp8GemmCall& c, int sms) {
   return best;
 }
 
+// The kernel ahead may still run when weights are fetched.  The quantiser of rows
+// lets that happen, and a single row of weights may be its work.
+int early_start(const Fp8GemmCall& c) { return c.N > 1; }
+
 template <int BN>
 cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
   static thread_local NarrowArgs a;
@@ -692,7 +696,7 @@ cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const 
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].val.programmaticStreamSerializationAllowed = early_start(c);
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<BN>, a);
@@ -734,7 +738,7 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].val.programmaticStreamSerializationAllowed = early_start(c);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = kCtas;
   attr[1].val.clusterDim.y = 1;

@@ -60,6 +60,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
       if (h < a.H) to[i] = __ldg(reinterpret_cast<const uint4*>(a.Wr + static_cast<size_t>(e) * a.H + h));
     }
   };
+  cluster_arrive();
   const int e0 = rank * kRouteWarps + warp;
   // two experts a warp at once; the weights are complete before the launch that makes y begins
   fetch(w[0], e0, 0);
@@ -69,6 +70,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
   for (int i = threadIdx.x; i < a.H / 4; i += kRouteThreads)
     y[(i / 64) * 64 + (i & 1) * 32 + (i / 2) % 32] = __ldg(reinterpret_cast<const float4*>(a.y + static_cast<size_t>(t) * a.H) + i);
   __syncthreads();
+  cluster_wait();  // CTA 0 has started: its shared memory may be written
   for (int e = e0; e < a.E; e += 2 * kStep) {
     float acc[2][4] = {};
     for (int h0 = 0; h0 < a.H; h0 += kSpan) {

@@ -340,6 +340,10 @@ int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cac
  * row, over one row (activations) or 128 rows (weights); a code c stands for
  * c * s.  A matrix of R rows of K codes (K a multiple of 16) has scales
  * [ceil(R / block_rows)][ceil(K / 128)]; blocks at the edges are smaller.
+ *
+ * Weights (of a product, a router, experts) may be fetched while the launch
+ * ahead of the call still runs.  What dec_fp8_quant with block_rows 128 and
+ * dec_fp8_dequant make may be used as weights by the very next call.
  */
 
 /*
@@ -360,7 +364,8 @@ int dec_fp8_quant(const void* x, int bf16, int64_t stride_mat, int64_t stride_ro
 /*
  * Reads codes back: out = c * s, rounded once to float32 and for bf16 once
  * more (any float scales; exact in float32 for powers of two of its range).
- * out is strided as x above; its rows may not share memory.
+ * out is strided as x above; its rows may not share memory (strides of K at
+ * least).
  */
 int dec_fp8_dequant(const void* codes, const float* scales, void* out, int bf16, int64_t stride_mat, int64_t stride_row,
                     int n, int rows, int K, int block_rows, void* stream);
@@ -370,10 +375,11 @@ int dec_fp8_dequant(const void* codes, const float* scales, void* out, int bf16,
  * (blocks of 128 x 128), any float scales:
  *   out[m][n] = residual[m][n] + sum_j sx[m][j] sw[n / 128][j] sum_{k in block j} cx[m][k] cw[n][k]
  * Products of codes are exact; a block's sum is held in fp32, as are the sums
- * over blocks.  out and residual: float32, rows of N contiguous values that
- * begin stride_out and stride_residual elements apart (stride_out >= N);
- * residual may be NULL, or out itself with its stride; other overlaps are not
- * allowed.  M is 0..2^24.  Results are reproducible bit for bit.
+ * over blocks and the product of two scales (below 2^-126 it loses bits).  out
+ * and residual: float32, rows of N contiguous values that begin stride_out and
+ * stride_residual elements apart (stride_out >= N); residual may be NULL, or out
+ * itself with its stride; other overlaps are not allowed.  M is 0..2^24.
+ * Results are reproducible bit for bit.
  */
 int dec_fp8_gemm(const void* x_codes, const float* x_scales, const void* w_codes, const float* w_scales,
                  const float* residual, int64_t stride_residual, float* out, int64_t stride_out, int M, int N, int K,

@@ -61,6 +61,8 @@ def test_sizes_of_codes(gd, name, good):
 def test_particular_arguments(gd):
     for s in ("sm", "sr"):
         refused(gd, "dec_fp8_dequant", DEQUANT, gd.DEC_EINVAL, "share memory", **{s: 0})
+    for s in ("sm", "sr"):
+        refused(gd, "dec_fp8_dequant", DEQUANT, gd.DEC_EINVAL, "share memory", **{s: 248})
     refused(gd, "dec_fp8_gemm", GEMM, gd.DEC_EINVAL, "N must", N=0)
     refused(gd, "dec_fp8_gemm", GEMM, gd.DEC_EUNSUPPORTED, "2^24", N=(1 << 24) + 1, ldo=1 << 25)
     refused(gd, "dec_fp8_gemm", GEMM, gd.DEC_EUNSUPPORTED, "2^40", N=1 << 24, M=1 << 20, ldo=1 << 24)
@@ -203,5 +205,7 @@ def test_python_layer(gd):
         gd.dec_moe_experts(y, ids, w, bf[0], bf[1], bf[0], y.clone())
     with pytest.raises(TypeError):
         gd.dec_moe_experts(y, ids, w, *f8, y.clone(), scales=(sc[0], None, sc[0]))
+    with pytest.raises(TypeError):
+        gd.dec_moe_experts(y, ids, w, *bf, y.clone(), scales=(None, sc[0], sc[0]))
     with pytest.raises(gd.DecError, match="shape"):
         gd.dec_moe_experts(y, ids, w, *f8, y.clone(), scales=(sc[0], sc[0], torch.zeros(E, 2, 1)))

@@ -191,6 +191,28 @@ def test_every_form(M, N, K):
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("M,N,K", [(500, 6140, 1040), (2047, 9700, 272), (2047, 9702, 272)])
+def test_rows_of_unlike_alignment(M, N, K):
+    """Many rows whose residual or result is not aligned as the other is: the same bits, and nothing beside them."""
+    ops = operands(87, M, N, K)
+    res = normal(88, M, N)
+    want = torch.empty(M, N, device="cuda")
+    gd.dec_fp8_gemm(*ops, want, residual=res)
+    close(want, *R.gemm(*ops, residual=res))
+    for left, right in ((1, 2), (4, 4), (8, 3)):
+        odd = torch.zeros(M, left + N + right, device="cuda")[:, left:left + N]
+        odd.copy_(res)
+        out = torch.full((M, N), math.nan, device="cuda")
+        gd.dec_fp8_gemm(*ops, out, residual=odd)
+        assert torch.equal(out, want)
+        pad = torch.full((M + 2, left + N + right), 7.0, device="cuda")
+        view = pad[1:M + 1, left:left + N]
+        gd.dec_fp8_gemm(*ops, view, residual=res)
+        assert torch.equal(view, want)
+        view.fill_(7.0)
+        assert bool((pad == 7.0).all())
+
+
 def test_one_row_takes_any_strides():
     ops = operands(86, 1, 333, 160)
     want, bound = R.gemm(*ops)
@@ -281,6 +303,26 @@ def test_weights_made_right_before_the_product(M):
         gd.dec_fp8_gemm(xc, xs, wc, wsc, out)
     for i in range(3):
         gd.dec_fp8_quant(ws[i], wc, wsc, block_rows=128)
+        want, bound = R.gemm(xc, xs, wc, wsc)
+        for out in outs[i::3]:
+            close(out, want, bound)
+
+
+@pytest.mark.parametrize("M", [1, 3000])
+def test_one_row_of_weights_made_right_before_the_product(M):
+    """One row's blocks are the same for both kinds: the quantiser of rows may have made it."""
+    K = 1 << 14
+    x = normal(65, M, K)
+    ws = [normal(66 + i, 1, K) for i in range(3)]
+    xc, xs = empty_codes(x, 1)
+    wc, wsc = empty_codes(ws[0], 1)
+    gd.dec_fp8_quant(x, xc, xs)
+    outs = [torch.zeros(M, 1, device="cuda") for _ in range(12)]
+    for i, out in enumerate(outs):
+        gd.dec_fp8_quant(ws[i % 3], wc, wsc)
+        gd.dec_fp8_gemm(xc, xs, wc, wsc, out)
+    for i in range(3):
+        gd.dec_fp8_quant(ws[i], wc, wsc)
         want, bound = R.gemm(xc, xs, wc, wsc)
         for out in outs[i::3]:
             close(out, want, bound)
