@@ -307,7 +307,10 @@ struct WideArgs {
   uint32_t* err;
 };
 
-template <int BN, bool PAIR>
+// PLAIN: no residual, and tensor copies store the rows.  (With the other paths in
+// one kernel its loop over blocks took 7 % longer: 8191 x 2560 x 19456 in 406 us
+// where 378.)
+template <int BN, bool PAIR, bool PLAIN>
 __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_constant__ WideArgs a) {
   using W = Wide<BN, PAIR>;
   constexpr int kWideStages = W::kStages, kChunks = W::kChunks, kCtas = PAIR ? 2 : 1;
@@ -347,85 +350,104 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // 128 threads x 40 + 256 x 232 registers = the 384 x 168 of the launch
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-
-  if (warp == 0) {
-    const uint64_t keep = l2_policy_evict_last();
-    // a pair's copies complete on the even CTA's barrier
-    auto bring = [&](const CUtensorMap* map, int it, uint32_t at, int kb, int row) {
-      const int s = it % kWideStages;
-      unsigned char* to = tiles + s * kWideStage + at;
-      if (PAIR)
-        tma_load_3d_pair(to, map, kb * kF8BK, row, 0, in_even(&full[s]), keep);
-      else
-        tma_load_3d(to, map, kb * kF8BK, row, 0, &full[s], keep);
-    };
-    auto expect = [&](int it) {
-      if (rank == 0) mbar_arrive_expect_tx(&full[it % kWideStages], kCtas * kWideStage);
-    };
-    // weights go out before the wait for the kernel that makes the rows, as in the narrow form
-    const int pre = first < a.tiles ? min(a.KB, kWideStages) : 0;
-    if (elect_one())
-      for (int i = 0; i < pre; ++i) {
-        expect(i);
-        bring(&a.wmap, i, kF8Tile, i, first / a.m_tiles * BN + rank * W::kBRows);
-      }
+  auto leave = [&] {  // every thread, at its end
     __syncwarp();
-    pdl_wait();
-    pdl_launch_dependents();
-    int it = 0;
-    bool ok = true;
-    for (int tile = first; tile < a.tiles && ok; tile += step) {
-      const int m0 = (tile % a.m_tiles * kCtas + rank) * kF8BM, n0 = (tile / a.m_tiles) * BN + rank * W::kBRows;
-      for (int kb = 0; kb < a.KB; ++kb, ++it) {
-        if (it >= kWideStages)
-          ok = warp_wait(&done[it % kWideStages], ((it / kWideStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
+    tc_fence_before();
+    if (PAIR) {  // neither CTA leaves while the other may reach into it
+      cluster_arrive();
+      cluster_wait();
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kWideThreads) : "memory");
+  };
+  // 128 threads x 40 + 256 x 232 registers = the 384 x 168 of the launch.  What runs with fewer or more stands in its
+  // own branch to the end of the kernel: a value that one side holds in its 200th register would not fit the other.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      const uint64_t keep = l2_policy_evict_last();
+      // a pair's copies complete on the even CTA's barrier
+      auto bring = [&](const CUtensorMap* map, int it, uint32_t at, int kb, int row) {
+        const int s = it % kWideStages;
+        unsigned char* to = tiles + s * kWideStage + at;
+        if (PAIR)
+          tma_load_3d_pair(to, map, kb * kF8BK, row, 0, in_even(&full[s]), keep);
+        else
+          tma_load_3d(to, map, kb * kF8BK, row, 0, &full[s], keep);
+      };
+      auto expect = [&](int it) {
+        if (rank == 0) mbar_arrive_expect_tx(&full[it % kWideStages], kCtas * kWideStage);
+      };
+      // weights go out before the wait for the kernel that makes the rows, as in the narrow form
+      const int pre = first < a.tiles ? min(a.KB, kWideStages) : 0;
+      if (elect_one())
+        for (int i = 0; i < pre; ++i) {
+          expect(i);
+          bring(&a.wmap, i, kF8Tile, i, first / a.m_tiles * BN + rank * W::kBRows);
+        }
+      __syncwarp();
+      pdl_wait();
+      pdl_launch_dependents();
+      int it = 0;
+      bool ok = true;
+      for (int tile = first; tile < a.tiles && ok; tile += step) {
+        const int m0 = (tile % a.m_tiles * kCtas + rank) * kF8BM, n0 = (tile / a.m_tiles) * BN + rank * W::kBRows;
+        for (int kb = 0; kb < a.KB; ++kb, ++it) {
+          if (it >= kWideStages)
+            ok = warp_wait(&done[it % kWideStages], ((it / kWideStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
+          if (!ok) break;
+          if (elect_one()) {
+            if (it >= pre) expect(it);
+            bring(&a.xmap, it, 0, kb, m0);
+            if (it >= pre) bring(&a.wmap, it, kF8Tile, kb, n0);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok && lane == 0) {  // an early end waits for its own copies (a pair's: those that complete here)
+        *stop = 1;
+        for (int i = max(0, it - kWideStages); i < it; ++i)
+          if (!tc_wait(&full[i % kWideStages], (i / kWideStages) & 1, a.err, kErrDrain)) break;
+      }
+    } else if ((warp == 1 || warp == 2) && rank == 0) {
+      // every second block each, so that one waits for its next while the other's products are being issued
+      constexpr uint32_t idesc = PAIR ? tc_idesc_pair(BN) : tc_idesc_of(BN, false);
+      const int b = warp - 1;
+      const int mine = (a.tiles - first + step - 1) / step;
+      bool ok = true;
+      for (int it = b; it < mine * a.KB; it += 2) {
+        const int s = it % kWideStages;
+        ok = warp_wait(&full[s], (it / kWideStages) & 1, stop, a.err, kErrWaitFull) &&
+             (it < 2 || warp_wait(&drained[b], ((it >> 1) - 1) & 1, stop, a.err, kErrWaitFull));
         if (!ok) break;
+        tc_fence_after();
+        const uint32_t sa = smem_addr(tiles + s * kWideStage);
         if (elect_one()) {
-          if (it >= pre) expect(it);
-          bring(&a.xmap, it, 0, kb, m0);
-          if (it >= pre) bring(&a.wmap, it, kF8Tile, kb, n0);
+  #pragma unroll
+          for (int kk = 0; kk < kF8BK / 32; ++kk) {
+            const uint64_t ad = smem_desc_sw128(sa + kk * 32), bd = smem_desc_sw128(sa + kF8Tile + kk * 32);
+            if (PAIR)
+              tc_mma_f8_pair(tmem + b * BN, ad, bd, idesc, kk > 0);
+            else
+              tc_mma_f8(tmem + b * BN, ad, bd, idesc, kk > 0);
+          }
+          if (PAIR)
+            tc_commit_pair(&done[s]);
+          else
+            tc_commit(&done[s]);
         }
         __syncwarp();
       }
+      if (!ok) *stop = 1;
     }
-    if (!ok && lane == 0) {  // an early end waits for its own copies (a pair's: those that complete here)
-      *stop = 1;
-      for (int i = max(0, it - kWideStages); i < it; ++i)
-        if (!tc_wait(&full[i % kWideStages], (i / kWideStages) & 1, a.err, kErrDrain)) break;
-    }
-  } else if ((warp == 1 || warp == 2) && rank == 0) {
-    // every second block each, so that one waits for its next while the other's products are being issued
-    constexpr uint32_t idesc = PAIR ? tc_idesc_pair(BN) : tc_idesc_of(BN, false);
-    const int b = warp - 1;
-    const int mine = (a.tiles - first + step - 1) / step;
-    bool ok = true;
-    for (int it = b; it < mine * a.KB; it += 2) {
-      const int s = it % kWideStages;
-      ok = warp_wait(&full[s], (it / kWideStages) & 1, stop, a.err, kErrWaitFull) &&
-           (it < 2 || warp_wait(&drained[b], ((it >> 1) - 1) & 1, stop, a.err, kErrWaitFull));
-      if (!ok) break;
+    leave();
+    if (warp == 1) {
       tc_fence_after();
-      const uint32_t sa = smem_addr(tiles + s * kWideStage);
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < kF8BK / 32; ++kk) {
-          const uint64_t ad = smem_desc_sw128(sa + kk * 32), bd = smem_desc_sw128(sa + kF8Tile + kk * 32);
-          if (PAIR)
-            tc_mma_f8_pair(tmem + b * BN, ad, bd, idesc, kk > 0);
-          else
-            tc_mma_f8(tmem + b * BN, ad, bd, idesc, kk > 0);
-        }
-        if (PAIR)
-          tc_commit_pair(&done[s]);
-        else
-          tc_commit(&done[s]);
-      }
-      __syncwarp();
+      if (PAIR)
+        tmem_free_pair(tmem, kCols);
+      else
+        tmem_free(tmem, kCols);
     }
-    if (!ok) *stop = 1;
-  } else if (warp >= 4) {
+  } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., columns BN / 2 half ..
     unsigned char* stages = tiles + kWideStages * kWideStage + (warp - 4) * W::kBufs * 32 * 128;
@@ -509,7 +531,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
           // all loads of the residual before anything is written: they are in flight together, and beside what follows
           const int row8 = lane >> 3, piece = lane & 7;
           float4 add[8];
-          if (a.bulk && a.vec) {  // 8 lanes a row
+          if (!PLAIN && a.bulk && a.vec) {  // 8 lanes a row
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
               const int r = out_m + 4 * p + row8, col = n + 4 * piece;
@@ -517,14 +539,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
                                             : make_float4(0.f, 0.f, 0.f, 0.f);
             }
           }
-          if (a.bulk) tma_store_wait_read<W::kBufs - 1>();  // what this buffer held has left
+          if (PLAIN || a.bulk) tma_store_wait_read<W::kBufs - 1>();  // what this buffer held has left
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(
                 acc[32 * c + 4 * j], acc[32 * c + 4 * j + 1], acc[32 * c + 4 * j + 2], acc[32 * c + 4 * j + 3]);
           __syncwarp();
-          if (a.bulk && a.vec) {
+          if (!PLAIN && a.bulk && a.vec) {
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
               const int rr = 4 * p + row8;
@@ -532,7 +554,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
               const float4 v = *at4;
               *at4 = make_float4(v.x + add[p].x, v.y + add[p].y, v.z + add[p].z, v.w + add[p].w);
             }
-          } else if (!a.bulk || a.residual) {  // a lane a column, 8 rows at once: rows that are not whole 16 bytes
+          } else if (!PLAIN && (!a.bulk || a.residual)) {  // a lane a column, 8 rows at once: rows that are not whole 16 bytes
             const int rows = min(32, a.M - out_m);
             const bool in = n + lane < a.N;
             float* dst = a.out + static_cast<long long>(out_m) * a.ldo + n + lane;
@@ -560,7 +582,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
               }
             }
           }
-          if (a.bulk) {
+          if (PLAIN || a.bulk) {
             fence_to_async();
             __syncwarp();
             if (lane == 0) tma_store_2d(&a.omap, stage, n, out_m);  // the lane that waits for it
@@ -568,21 +590,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
         }
       }
     }
-    if (a.bulk) tma_store_wait_read<0>();  // its memory is in use until then
-  }
-  __syncwarp();
-  tc_fence_before();
-  if (PAIR) {  // neither CTA leaves while the other may reach into it
-    cluster_arrive();
-    cluster_wait();
-  }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    if (PAIR)
-      tmem_free_pair(tmem, kCols);
-    else
-      tmem_free(tmem, kCols);
+    if (PLAIN || a.bulk) tma_store_wait_read<0>();  // its memory is in use until then
+    leave();
   }
 }
 
@@ -745,7 +754,14 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fp8_wide_kernel<BN, PAIR>, a);
+  return a.bulk && !c.residual ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<BN, PAIR, true>, a)
+                               : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<BN, PAIR, false>, a);
+}
+
+template <int BN, bool PAIR>
+cudaError_t allow_wide() {
+  const cudaError_t e = allow_smem(fp8_wide_kernel<BN, PAIR, true>);
+  return e != cudaSuccess ? e : allow_smem(fp8_wide_kernel<BN, PAIR, false>);
 }
 
 }  // namespace
@@ -776,11 +792,11 @@ cudaError_t allow_smem_fp8_gemm() {
   cudaError_t e;
   if ((e = allow_smem(fp8_narrow_kernel<16>)) != cudaSuccess) return e;
   if ((e = allow_smem(fp8_narrow_kernel<32>)) != cudaSuccess) return e;
-  if ((e = allow_smem(fp8_wide_kernel<64, false>)) != cudaSuccess) return e;
-  if ((e = allow_smem(fp8_wide_kernel<128, false>)) != cudaSuccess) return e;
-  if ((e = allow_smem(fp8_wide_kernel<192, false>)) != cudaSuccess) return e;
-  if ((e = allow_smem(fp8_wide_kernel<256, false>)) != cudaSuccess) return e;
-  return allow_smem(fp8_wide_kernel<256, true>);
+  if ((e = allow_wide<64, false>()) != cudaSuccess) return e;
+  if ((e = allow_wide<128, false>()) != cudaSuccess) return e;
+  if ((e = allow_wide<192, false>()) != cudaSuccess) return e;
+  if ((e = allow_wide<256, false>()) != cudaSuccess) return e;
+  return allow_wide<256, true>();
 }
 
 }  // namespace dec

@@ -191,6 +191,17 @@ def test_every_form(M, N, K):
     assert torch.equal(again, out)
 
 
+# tiles of 64, 128, 192 and 256 columns, one and several of a CTA, pairs
+@pytest.mark.parametrize("M,N,K", [(130, 4100, 656), (250, 9000, 400), (500, 6140, 1040), (385, 9700, 144), (1000, 9732, 528),
+                                   (2047, 9700, 1040), (2050, 9728, 272), (2040, 9704, 2576)])
+def test_every_form_without_a_residual(M, N, K):
+    ops = operands(89, M, N, K)
+    want, bound = R.gemm(*ops)
+    out = torch.full((M, N), math.nan, device="cuda")
+    gd.dec_fp8_gemm(*ops, out)
+    close(out, want, bound)
+
+
 @pytest.mark.parametrize("M,N,K", [(500, 6140, 1040), (2047, 9700, 272), (2047, 9702, 272)])
 def test_rows_of_unlike_alignment(M, N, K):
     """Many rows whose residual or result is not aligned as the other is: the same bits, and nothing beside them."""
