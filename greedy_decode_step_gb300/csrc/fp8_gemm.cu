@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
     asm volatile("bar.sync 1, %0;" ::"n"(kWideThreads) : "memory");
   };
   // 128 threads x 40 + 256 x 232 registers = the 384 x 168 of the launch.  What runs with fewer or more stands in its
-  // own branch to the end of the kernel: a value that one side holds in its 200th register would not fit the other.
+  // own branch to the end of the kernel, so that no value has to be held in one place by both.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
@@ -416,8 +416,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       bool ok = true;
       for (int it = b; it < mine * a.KB; it += 2) {
         const int s = it % kWideStages;
-        ok = warp_wait(&full[s], (it / kWideStages) & 1, stop, a.err, kErrWaitFull) &&
-             (it < 2 || warp_wait(&drained[b], ((it >> 1) - 1) & 1, stop, a.err, kErrWaitFull));
+        // The accumulator first: once block it - 2 has been read, every block before it, the one that held this stage
+        // among them, is done.  Of an odd number of stages a warp sees every second phase only, and asked too early
+        // the parity would answer for the phase before the last.
+        ok = (it < 2 || warp_wait(&drained[b], ((it >> 1) - 1) & 1, stop, a.err, kErrWaitFull)) &&
+             warp_wait(&full[s], (it / kWideStages) & 1, stop, a.err, kErrWaitFull);
         if (!ok) break;
         tc_fence_after();
         const uint32_t sa = smem_addr(tiles + s * kWideStage);

@@ -202,6 +202,22 @@ def test_every_form_without_a_residual(M, N, K):
     close(out, want, bound)
 
 
+# three and five stages, a few blocks a tile, many tiles a CTA: blocks that arrive out of order
+@pytest.mark.parametrize("M,N,K", [(2050, 9729, 272), (2050, 9728, 272), (4200, 14588, 288), (250, 9000, 400), (385, 9700, 144)])
+def test_short_rows_again_and_again(M, N, K):
+    ops = operands(90, M, N, K)
+    res = normal(91, M, N)
+    for r in (None, res):
+        want, bound = R.gemm(*ops, residual=r)
+        first = torch.full((M, N), math.nan, device="cuda")
+        gd.dec_fp8_gemm(*ops, first, residual=r)
+        close(first, want, bound)
+        out = torch.empty_like(first)
+        for _ in range(25):
+            gd.dec_fp8_gemm(*ops, out, residual=r)
+            assert torch.equal(out, first)
+
+
 @pytest.mark.parametrize("M,N,K", [(500, 6140, 1040), (2047, 9700, 272), (2047, 9702, 272)])
 def test_rows_of_unlike_alignment(M, N, K):
     """Many rows whose residual or result is not aligned as the other is: the same bits, and nothing beside them."""
