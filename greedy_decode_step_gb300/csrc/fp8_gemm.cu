@@ -487,6 +487,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       float acc[BN / 2];
 #pragma unroll
       for (int j = 0; j < BN / 2; ++j) acc[j] = 0.f;
+      if (!PLAIN && a.residual && m0 + lane < a.M) {  // a lane's row of the residual is in L2 by the time it is added
+        const float* res = a.residual + static_cast<long long>(m0 + lane) * a.ldr + n0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (n0 + 32 * c < a.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(res + 32 * c));
+      }
       bool ok = true;
       for (int kb = 0; kb < a.KB; ++kb, ++it) {
         const int b = it & 1;
