@@ -283,36 +283,40 @@ constexpr int kWideMaxStages = 6;
 // 128 in each of two CTAs (cta_group::2) that hold half of the weight rows each.
 // A pair reads two thirds of the bytes from L2 and shared memory per product,
 // and the tensor core takes 512 cycles a block where it takes 685 alone.
-template <int BN, bool PAIR>
+//
+// How results leave: as they are, by tensor copies; the same on top of a residual
+// that tensor copies bring into the staging rows while the tile is multiplied;
+// or row by row, where rows of either are not whole 16 bytes.  (Each in a kernel
+// of its own: with all in one the loop over blocks took 7 % longer, 8191 x 2560 x
+// 19456 in 406 us where 378.)
+enum Out { kPlain, kAdd, kRows };
+
+template <int BN, bool PAIR, Out OUT>
 struct Wide {
   static constexpr int kBRows = PAIR ? BN / 2 : BN;  // weight rows of a CTA
   static constexpr uint32_t kStage = kF8Tile + kBRows * kF8BK;
-  static constexpr int kBufs = PAIR ? 3 : 2;  // 32 rows of 32 results per warp, on their way out
+  static constexpr int kBufs = !PAIR ? 2 : OUT == kAdd ? 4 : 3;  // 32 rows of 32 results per warp, on their way out
   static constexpr uint32_t kOut = 8 * kBufs * 32 * 128;
   static constexpr int kFit = static_cast<int>((kSmemMax - 1024 - kF8Head - kOut) / kStage);
-  static constexpr int kStages = kFit < kWideMaxStages ? kFit : kWideMaxStages;  // 3 at 256, 4 as a pair
+  static constexpr int kStages = kFit < kWideMaxStages ? kFit : kWideMaxStages;  // 3 at 256, 4 as a pair (3 with a residual)
   static constexpr uint32_t kSmem = 1024 + kF8Head + kStages * kStage + kOut;
   static constexpr int kChunks = BN / 64;  // of 32 columns, per epilogue warp
 };
 
 struct WideArgs {
   CUtensorMap wmap, xmap;  // box BN rows of wc, 128 rows of xc
-  CUtensorMap omap;        // of the result, if `bulk`
+  CUtensorMap omap, rmap;  // of the result, if `bulk`, and of the residual for kAdd
   const float *sx, *sw, *residual;
   float* out;
   long long ldr, ldo;
   int M, N, KB, NB, m_tiles, tiles;
-  int bulk;    // rows of the result are 16-byte aligned: tensor copies store them
-  int vec;     // and rows of the residual, if any
+  int bulk;    // rows of the result are whole 16 bytes: tensor copies store them
   uint32_t* err;
 };
 
-// PLAIN: no residual, and tensor copies store the rows.  (With the other paths in
-// one kernel its loop over blocks took 7 % longer: 8191 x 2560 x 19456 in 406 us
-// where 378.)
-template <int BN, bool PAIR, bool PLAIN>
+template <int BN, bool PAIR, Out OUT>
 __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_constant__ WideArgs a) {
-  using W = Wide<BN, PAIR>;
+  using W = Wide<BN, PAIR, OUT>;
   constexpr int kWideStages = W::kStages, kChunks = W::kChunks, kCtas = PAIR ? 2 : 1;
   constexpr uint32_t kWideStage = W::kStage, kCols = tmem_columns(2 * BN);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -323,6 +327,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   uint64_t* drained = done + kWideStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);  // a wait ran out: every role ends
+  uint64_t* came = reinterpret_cast<uint64_t*>(smem + kF8Head / 2);     // kAdd: a warp's staging rows hold the residual
+  static_assert((2 * kWideMaxStages + 3) * 8 <= kF8Head / 2 && 8 * W::kBufs * 8 <= kF8Head / 2, "barriers");
   unsigned char* tiles = smem + kF8Head;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? blockIdx.x & 1 : 0, first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
@@ -333,6 +339,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       mbar_init(&done[s], 1);
     }
     for (int s = 0; s < 2; ++s) mbar_init(&drained[s], 8 * kCtas);
+    if (OUT == kAdd)
+      for (int s = 0; s < 8 * W::kBufs; ++s) mbar_init(&came[s], 1);
     *stop = 0;
     fence_mbar_init();
   }
@@ -466,6 +474,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       }
     };
     int it = 0, turn = 0, m0, n0, cut;
+    came += (warp - 4) * W::kBufs;
+    uint32_t phases = 0, coming = 0;  // a bit per buffer: the phase to wait for, a copy on its way
+    auto bring = [&](int c) {         // chunk c of the residual of the tile at (m0, n0), into a buffer that is free
+      const int buf = c % W::kBufs;
+      coming |= 1u << buf;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&came[buf], 32 * 128);
+        tma_load_2d(stages + buf * 32 * 128, &a.rmap, n0 + 32 * c, m0, &came[buf], l2_policy_evict_first());
+      }
+    };
     const float *sx, *sw, *sv;
     float x0, w0, v0, x1, w1, v1;
     auto open = [&](int tile) {  // its place, and the scales of its first two blocks
@@ -487,7 +505,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       float acc[BN / 2];
 #pragma unroll
       for (int j = 0; j < BN / 2; ++j) acc[j] = 0.f;
-      if (!PLAIN && a.residual && m0 + lane < a.M) {  // a lane's row of the residual is in L2 by the time it is added
+      if (OUT == kAdd && m0 < a.M) {
+        tma_store_wait_read<0>();  // the tile before has left the buffers
+#pragma unroll
+        for (int c = 0; c < kChunks && c < W::kBufs; ++c)
+          if (n0 + 32 * c < a.N) bring(c);
+      }
+      if (OUT == kRows && a.residual && m0 + lane < a.M) {  // a lane's row of the residual is in L2 by the time it is added
         const float* res = a.residual + static_cast<long long>(m0 + lane) * a.ldr + n0;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
@@ -528,42 +552,59 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
         break;
       }
       const int out_m = m0, out_n = n0;
-      open(min(tile + step, a.tiles - 1));  // the next tile's scales come while this one's results leave
       // 32 columns at a time through shared memory (rows of 128 bytes, their 16-byte pieces swizzled), so that whole
       // lines leave: by a tensor copy, which runs beside the next tile, or by a warp a row
+      auto mine = [&](unsigned char* stage, int j) { return reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)); };
+      auto send = [&](unsigned char* stage, int n) {  // by the lane that waits for it
+        fence_to_async();
+        __syncwarp();
+        if (lane == 0) tma_store_2d(&a.omap, stage, n, out_m);
+      };
+      if (OUT == kAdd) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const int n = out_n + 32 * c, buf = c % W::kBufs;
+          if (ok && n < a.N && out_m < a.M) {  // warp-uniform
+            unsigned char* stage = stages + buf * 32 * 128;
+            ok = warp_wait(&came[buf], phases >> buf & 1, stop, a.err, kErrWaitFull);
+            if (ok) {
+              phases ^= 1u << buf;
+              coming &= ~(1u << buf);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float4 r = *mine(stage, j);
+                *mine(stage, j) = make_float4(acc[32 * c + 4 * j] + r.x, acc[32 * c + 4 * j + 1] + r.y,
+                                              acc[32 * c + 4 * j + 2] + r.z, acc[32 * c + 4 * j + 3] + r.w);
+              }
+              send(stage, n);
+              if (c + W::kBufs < kChunks && n + 32 * W::kBufs < a.N) {
+                tma_store_wait_read<0>();
+                bring(c + W::kBufs);
+              }
+            }
+          }
+        }
+        if (!ok) {
+          *stop = 1;
+          break;
+        }
+        open(min(tile + step, a.tiles - 1));
+        continue;
+      }
+      open(min(tile + step, a.tiles - 1));  // the next tile's scales come while this one's results leave
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const int n = out_n + 32 * c;
         if (n < a.N && out_m < a.M) {  // warp-uniform
           unsigned char* stage = stages + turn % W::kBufs * 32 * 128;
           ++turn;
-          // all loads of the residual before anything is written: they are in flight together, and beside what follows
-          const int row8 = lane >> 3, piece = lane & 7;
-          float4 add[8];
-          if (!PLAIN && a.bulk && a.vec) {  // 8 lanes a row
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
-              const int r = out_m + 4 * p + row8, col = n + 4 * piece;
-              add[p] = r < a.M && col < a.N ? *reinterpret_cast<const float4*>(a.residual + r * a.ldr + col)
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-          }
-          if (PLAIN || a.bulk) tma_store_wait_read<W::kBufs - 1>();  // what this buffer held has left
+          if (OUT == kPlain || a.bulk) tma_store_wait_read<W::kBufs - 1>();  // what this buffer held has left
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(
-                acc[32 * c + 4 * j], acc[32 * c + 4 * j + 1], acc[32 * c + 4 * j + 2], acc[32 * c + 4 * j + 3]);
-          __syncwarp();
-          if (!PLAIN && a.bulk && a.vec) {
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
-              const int rr = 4 * p + row8;
-              float4* at4 = reinterpret_cast<float4*>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
-              const float4 v = *at4;
-              *at4 = make_float4(v.x + add[p].x, v.y + add[p].y, v.z + add[p].z, v.w + add[p].w);
-            }
-          } else if (!PLAIN && (!a.bulk || a.residual)) {  // a lane a column, 8 rows at once: rows that are not whole 16 bytes
+            *mine(stage, j) = make_float4(acc[32 * c + 4 * j], acc[32 * c + 4 * j + 1], acc[32 * c + 4 * j + 2], acc[32 * c + 4 * j + 3]);
+          if (OUT == kRows) {  // a lane a column, 8 rows at once
+            __syncwarp();
             const int rows = min(32, a.M - out_m);
             const bool in = n + lane < a.N;
             float* dst = a.out + static_cast<long long>(out_m) * a.ldo + n + lane;
@@ -591,15 +632,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
               }
             }
           }
-          if (PLAIN || a.bulk) {
-            fence_to_async();
-            __syncwarp();
-            if (lane == 0) tma_store_2d(&a.omap, stage, n, out_m);  // the lane that waits for it
-          }
+          if (OUT == kPlain || a.bulk) send(stage, n);
         }
       }
     }
-    if (PLAIN || a.bulk) tma_store_wait_read<0>();  // its memory is in use until then
+    if (OUT == kAdd && lane == 0)  // after an early end only: its own copies
+      for (int buf = 0; buf < W::kBufs; ++buf)
+        if (coming >> buf & 1) tc_wait(&came[buf], phases >> buf & 1, a.err, kErrDrain);
+    if (OUT != kRows || a.bulk) tma_store_wait_read<0>();  // its memory is in use until then
     leave();
   }
 }
@@ -720,11 +760,31 @@ cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const 
   return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<BN>, a);
 }
 
+template <int BN, bool PAIR, Out OUT>
+cudaError_t start_wide(const WideArgs& a, int sms, int early, cudaStream_t st) {
+  constexpr int kCtas = PAIR ? 2 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min(a.tiles, sms / kCtas) * kCtas);
+  cfg.blockDim = dim3(kWideThreads);
+  cfg.dynamicSmemBytes = Wide<BN, PAIR, OUT>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = early;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fp8_wide_kernel<BN, PAIR, OUT>, a);
+}
+
 template <int BN, bool PAIR>
 cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
   static thread_local WideArgs a;
   std::memset(&a, 0, sizeof(a));
-  if (!make_tmap_mats(&a.wmap, c.wc, 1, c.K, c.N, 1, Wide<BN, PAIR>::kBRows) || !make_tmap_mats(&a.xmap, c.xc, 1, c.K, c.M, 1, kF8BM)) {
+  if (!make_tmap_mats(&a.wmap, c.wc, 1, c.K, c.N, 1, Wide<BN, PAIR, kPlain>::kBRows) || !make_tmap_mats(&a.xmap, c.xc, 1, c.K, c.M, 1, kF8BM)) {
     *why = "a tensor map could not be made";
     return cudaErrorInvalidValue;
   }
@@ -738,39 +798,28 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
   a.N = c.N;
   a.KB = (c.K + kF8BK - 1) / kF8BK;
   a.NB = (c.N + kFp8Block - 1) / kFp8Block;
-  constexpr int kCtas = PAIR ? 2 : 1, kRows = kF8BM * kCtas;
-  a.m_tiles = (c.M + kRows - 1) / kRows;
+  constexpr int kTileRows = kF8BM * (PAIR ? 2 : 1);
+  a.m_tiles = (c.M + kTileRows - 1) / kTileRows;
   a.tiles = a.m_tiles * ((c.N + BN - 1) / BN);
   a.err = c.err;
   auto rows16 = [](const void* p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 4 == 0; };
   a.bulk = rows16(c.out, c.ldo) && c.ldo < (1ll << 36) && c.N % 4 == 0;  // a tensor copy cuts a row off at whole 16 bytes only
-  a.vec = c.residual && rows16(c.residual, c.ldr);
-  if (a.bulk && !make_tmap_out(&a.omap, c.out, c.N, c.M, c.ldo)) {
+  const bool add = a.bulk && c.residual && rows16(c.residual, c.ldr) && c.ldr >= c.N && c.ldr < (1ll << 36);
+  if ((a.bulk && !make_tmap_out(&a.omap, c.out, c.N, c.M, c.ldo)) ||
+      (add && !make_tmap_out(&a.rmap, const_cast<float*>(c.residual), c.N, c.M, c.ldr))) {
     *why = "a tensor map could not be made";
     return cudaErrorInvalidValue;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(a.tiles, sms / kCtas) * kCtas);
-  cfg.blockDim = dim3(kWideThreads);
-  cfg.dynamicSmemBytes = Wide<BN, PAIR>::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = early_start(c);
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCtas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
-  return a.bulk && !c.residual ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<BN, PAIR, true>, a)
-                               : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<BN, PAIR, false>, a);
+  const int early = early_start(c);
+  if (add) return start_wide<BN, PAIR, kAdd>(a, sms, early, st);
+  return a.bulk && !c.residual ? start_wide<BN, PAIR, kPlain>(a, sms, early, st) : start_wide<BN, PAIR, kRows>(a, sms, early, st);
 }
 
 template <int BN, bool PAIR>
 cudaError_t allow_wide() {
-  const cudaError_t e = allow_smem(fp8_wide_kernel<BN, PAIR, true>);
-  return e != cudaSuccess ? e : allow_smem(fp8_wide_kernel<BN, PAIR, false>);
+  cudaError_t e = allow_smem(fp8_wide_kernel<BN, PAIR, kPlain>);
+  if (e == cudaSuccess) e = allow_smem(fp8_wide_kernel<BN, PAIR, kAdd>);
+  return e != cudaSuccess ? e : allow_smem(fp8_wide_kernel<BN, PAIR, kRows>);
 }
 
 }  // namespace
