@@ -694,6 +694,9 @@ int narrow_splits(long long tiles, int KB, int sms) {
 // e.g. 64 x 9728 x 2560: 10.9 narrow, 9.0 wide 64; 512 x 1536 x 8960: 31 narrow,
 // 20.6 wide 64, 38 wide 256; 509 x 6144 x 2560: 17.6, 13.0, 16.0, 15.9 wide 128,
 // 192, 256 and pairs; 8192 x 9728 x 2560: 225, 200, 182, 175.
+// Tiles of 192 and 256 columns hold two thirds and half of a residual's chunks ahead
+// where pairs hold all: 4096 x 9728 x 528 in 72 us, 61 as pairs; 2050 x 9728 x 272 in
+// 37, 32; 4096 x 2560 x 9728 in 97 (192), 117 as pairs.
 enum Form { kNarrow16, kNarrow32, kWide64, kWide128, kWide192, kWide256, kPairs };
 Form best_form(const Fp8GemmCall& c, int sms) {
   const int KB = (c.K + kF8BK - 1) / kF8BK;
@@ -712,7 +715,11 @@ Form best_form(const Fp8GemmCall& c, int sms) {
   if (c.M > 16) offer(kNarrow32, 5.0 + up(t32 * s32, 2 * sms) * 0.45 * up(KB, s32));
   const Form wide[4] = {kWide64, kWide128, kWide192, kWide256};
   const double tile[4] = {0.8, 1.6, 1.9, 2.2}, block[4] = {0.214, 0.27, 0.36, 0.456};
-  for (int i = 0; i < 4; ++i) offer(wide[i], 4.0 + up(m128 * up(c.N, 64 * (i + 1)), sms) * (tile[i] + block[i] * KB));
+  const double wait[4] = {0.0, 0.0, 1.0, 2.0};  // for a residual, from the second wave on
+  for (int i = 0; i < 4; ++i) {
+    const long long waves = up(m128 * up(c.N, 64 * (i + 1)), sms);
+    offer(wide[i], 4.0 + waves * (tile[i] + block[i] * KB) + (c.residual ? (waves - 1) * wait[i] : 0.0));
+  }
   offer(kPairs, 4.0 + up(up(c.M, 2 * kF8BM) * up(c.N, 256), sms / 2) * (3.1 + 0.39 * KB));
   return best;
 }

@@ -218,7 +218,7 @@ def test_short_rows_again_and_again(M, N, K):
             assert torch.equal(out, first)
 
 
-@pytest.mark.parametrize("M,N,K", [(500, 6140, 1040), (2047, 9700, 272), (2047, 9702, 272)])
+@pytest.mark.parametrize("M,N,K", [(500, 6140, 1040), (2047, 9700, 272), (2047, 9702, 272), (1000, 9732, 528)])
 def test_rows_of_unlike_alignment(M, N, K):
     """Many rows whose residual or result is not aligned as the other is: the same bits, and nothing beside them."""
     ops = operands(87, M, N, K)
