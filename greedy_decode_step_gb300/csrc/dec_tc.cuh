@@ -228,6 +228,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
       : "memory");
 }
 
+// Asks the same box into L2, with no other effect.
+__device__ __forceinline__ void tma_prefetch_3d(const void* map, int x, int y, int z, uint64_t policy) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile.L2::cache_hint [%0, {%1, %2, %3}], %4;" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "l"(policy)
+               : "memory");
+}
+
 // 2-D tensor copy shared -> global of the box at (x, y); x * element size a
 // multiple of 16 bytes, inside the tensor (what leaves it behind is cut off).
 __device__ __forceinline__ void tma_store_2d(const void* map, const void* src, int x, int y) {

@@ -126,24 +126,19 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
     auto bring_x = [&](int i) {
       tma_load_3d(tiles + i % kStages * kStage + kF8Tile, &a.xmap, (kb0 + i) * kF8BK, r0, 0, &full[i % kStages], xpol);
     };
-    // weights go out before the wait for the kernel that makes the rows (the kernels that make weights let nothing start
-    // before they are complete, and `early_start` sees to a single row)
+    // Ahead of the wait the first weights are asked into L2 only: whichever launch made them, theirs are the bytes that the
+    // copies behind the wait bring.  (Copies issued here would read what the launch ahead has not written yet, or not
+    // made visible: only the wait does that.)
     const int pre = min(nkb, kStages);
     if (elect_one())
-      for (int i = 0; i < pre; ++i) {
-        mbar_arrive_expect_tx(&full[i], kStage);
-        bring_w(i);
-      }
+      for (int i = 0; i < pre; ++i) tma_prefetch_3d(&a.wmap, (kb0 + i) * kF8BK, m0, 0, wpol);
     __syncwarp();
     pdl_wait();
     pdl_launch_dependents();
-    if (elect_one())
-      for (int i = 0; i < pre; ++i) bring_x(i);
-    __syncwarp();
-    int it = pre;
+    int it = 0;
     bool ok = true;
     for (; it < nkb; ++it) {
-      ok = warp_wait(&empty[it % kStages], ((it / kStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
+      ok = it < kStages || warp_wait(&empty[it % kStages], ((it / kStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
       if (!ok) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&full[it % kStages], kStage);
@@ -382,16 +377,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
         else
           tma_load_3d(to, map, kb * kF8BK, row, 0, &full[s], keep);
       };
-      auto expect = [&](int it) {
-        if (rank == 0) mbar_arrive_expect_tx(&full[it % kWideStages], kCtas * kWideStage);
-      };
-      // weights go out before the wait for the kernel that makes the rows, as in the narrow form
+      // the first weights into L2 ahead of the wait, as in the narrow form
       const int pre = first < a.tiles ? min(a.KB, kWideStages) : 0;
       if (elect_one())
-        for (int i = 0; i < pre; ++i) {
-          expect(i);
-          bring(&a.wmap, i, kF8Tile, i, first / a.m_tiles * BN + rank * W::kBRows);
-        }
+        for (int i = 0; i < pre; ++i) tma_prefetch_3d(&a.wmap, i * kF8BK, first / a.m_tiles * BN + rank * W::kBRows, 0, keep);
       __syncwarp();
       pdl_wait();
       pdl_launch_dependents();
@@ -404,9 +393,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
             ok = warp_wait(&done[it % kWideStages], ((it / kWideStages) - 1) & 1, stop, a.err, kErrWaitEmpty);
           if (!ok) break;
           if (elect_one()) {
-            if (it >= pre) expect(it);
+            if (rank == 0) mbar_arrive_expect_tx(&full[it % kWideStages], kCtas * kWideStage);
             bring(&a.xmap, it, 0, kb, m0);
-            if (it >= pre) bring(&a.wmap, it, kF8Tile, kb, n0);
+            bring(&a.wmap, it, kF8Tile, kb, n0);
           }
           __syncwarp();
         }
@@ -724,10 +713,6 @@ Form best_form(const Fp8GemmCall& c, int sms) {
   return best;
 }
 
-// The kernel ahead may still run when weights are fetched.  The quantiser of rows
-// lets that happen, and a single row of weights may be its work.
-int early_start(const Fp8GemmCall& c) { return c.N > 1; }
-
 template <int BN>
 cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const char** why) {
   static thread_local NarrowArgs a;
@@ -761,14 +746,14 @@ cudaError_t launch_narrow(const Fp8GemmCall& c, int sms, cudaStream_t st, const 
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = early_start(c);
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<BN>, a);
 }
 
 template <int BN, bool PAIR, Out OUT>
-cudaError_t start_wide(const WideArgs& a, int sms, int early, cudaStream_t st) {
+cudaError_t start_wide(const WideArgs& a, int sms, cudaStream_t st) {
   constexpr int kCtas = PAIR ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(std::min(a.tiles, sms / kCtas) * kCtas);
@@ -777,7 +762,7 @@ cudaError_t start_wide(const WideArgs& a, int sms, int early, cudaStream_t st) {
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = early;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = kCtas;
   attr[1].val.clusterDim.y = 1;
@@ -817,9 +802,8 @@ cudaError_t launch_wide(const Fp8GemmCall& c, int sms, cudaStream_t st, const ch
     *why = "a tensor map could not be made";
     return cudaErrorInvalidValue;
   }
-  const int early = early_start(c);
-  if (add) return start_wide<BN, PAIR, kAdd>(a, sms, early, st);
-  return a.bulk && !c.residual ? start_wide<BN, PAIR, kPlain>(a, sms, early, st) : start_wide<BN, PAIR, kRows>(a, sms, early, st);
+  if (add) return start_wide<BN, PAIR, kAdd>(a, sms, st);
+  return a.bulk && !c.residual ? start_wide<BN, PAIR, kPlain>(a, sms, st) : start_wide<BN, PAIR, kRows>(a, sms, st);
 }
 
 template <int BN, bool PAIR>

@@ -341,9 +341,10 @@ int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cac
  * c * s.  A matrix of R rows of K codes (K a multiple of 16) has scales
  * [ceil(R / block_rows)][ceil(K / 128)]; blocks at the edges are smaller.
  *
- * Weights (of a product, a router, experts) may be fetched while the launch
- * ahead of the call still runs.  What dec_fp8_quant with block_rows 128 and
- * dec_fp8_dequant make may be used as weights by the very next call.
+ * Weights of a router may be fetched while the launch ahead of the call still
+ * runs.  The other calls take weights that the launch ahead of them writes,
+ * whatever launch that is; what dec_fp8_dequant makes may be used by a router,
+ * too.
  */
 
 /*
