@@ -183,7 +183,6 @@ __global__ void __launch_bounds__(kQuantThreads, kTileCtas<BF16>) quant_tiles_ke
   constexpr int kN = Vec<BF16>::kN, kLanes = kFp8Block / kN, kRows = kQuantThreads / kLanes, kUnroll = kFp8Block / kRows;
   __shared__ uint32_t tops[2][kQuantThreads / 32];
   pdl_wait();
-  // no early start for the next launch: it may read these as weights, ahead of its own wait
   const int KB = (a.K + kFp8Block - 1) / kFp8Block, RB = (a.rows + kFp8Block - 1) / kFp8Block;
   const long long tiles = static_cast<long long>(a.n) * RB * KB;
   const int sub = threadIdx.x / kLanes, in = threadIdx.x % kLanes;
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(kQuantThreads, kTileCtas<BF16>) quant_tiles_ke
 template <bool BF16>
 __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const Fp8DequantArgs a, const Slice s) {
   constexpr int kN = BF16 ? 8 : 4, kUnroll = 4;
-  pdl_wait();  // and no early start, as above
+  pdl_wait();  // and no early start for the next launch: a GEMV may fetch this as its weights, ahead of its own wait
   const uint32_t KB = (a.K + kFp8Block - 1) / kFp8Block, per_row = a.K / kN, total = s.rows * per_row;
   const uint32_t RB = (static_cast<uint32_t>(a.rows) + a.block_rows - 1) / a.block_rows;
   for (uint32_t i0 = blockIdx.x * (kQuantThreads * kUnroll) + threadIdx.x; i0 < total;

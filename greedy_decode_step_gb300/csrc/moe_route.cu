@@ -10,7 +10,7 @@
 // eighth of the experts, a warp per two experts with the token's row in shared
 // memory, and puts the logits into CTA 0, which chooses.  The sums of different
 // experts run in one order, so equal rows of Wr give equal logits.  Bound by
-// latency: a warp's first weights, 4096 of each expert, are on their way before
+// latency: a warp's first weights, 4096 of each expert, are on their way to L2 before
 // the wait for the launch that makes y; up to 256 experts are ranked at once, by
 // counting the better ones of each (64 experts: 1200 cycles where eight rounds of a
 // warp's maximum took 3000).
@@ -62,11 +62,18 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
   };
   cluster_arrive();
   const int e0 = rank * kRouteWarps + warp;
-  // two experts a warp at once; the weights are complete before the launch that makes y begins
-  fetch(w[0], e0, 0);
-  fetch(w[1], e0 + kStep, 0);
+  // two experts a warp at once: ahead of the wait into L2 only, as the launch ahead may be the one that writes them
+  auto ask = [&](int e) {
+    if (e >= a.E) return;
+    for (int h = 64 * lane; h < min(a.H, kSpan); h += 64 * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.Wr + static_cast<size_t>(e) * a.H + h));
+  };
+  ask(e0);
+  ask(e0 + kStep);
   pdl_wait();
   pdl_launch_dependents();
+  fetch(w[0], e0, 0);
+  fetch(w[1], e0 + kStep, 0);
   for (int i = threadIdx.x; i < a.H / 4; i += kRouteThreads)
     y[(i / 64) * 64 + (i & 1) * 32 + (i / 2) % 32] = __ldg(reinterpret_cast<const float4*>(a.y + static_cast<size_t>(t) * a.H) + i);
   __syncthreads();

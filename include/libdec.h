@@ -341,10 +341,10 @@ int dec_block_decode_attn(const float* q, const void* k_cache, const void* v_cac
  * c * s.  A matrix of R rows of K codes (K a multiple of 16) has scales
  * [ceil(R / block_rows)][ceil(K / 128)]; blocks at the edges are smaller.
  *
- * Weights of a router may be fetched while the launch ahead of the call still
- * runs.  The other calls take weights that the launch ahead of them writes,
- * whatever launch that is; what dec_fp8_dequant makes may be used by a router,
- * too.
+ * These calls take weights that the launch right ahead of them writes, whatever
+ * launch that is.  (The bf16 GEMVs above may fetch theirs while it still runs:
+ * after weights are written, by dec_fp8_dequant too, another launch belongs
+ * between.)
  */
 
 /*

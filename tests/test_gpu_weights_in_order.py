@@ -59,3 +59,34 @@ def test_product(M, N, K):
     g.replay()
     for i, out in enumerate(outs):
         assert torch.equal(out, want[i % 3])
+
+
+@pytest.mark.parametrize("T,H,E,k", [(1, 256, 8, 2), (1, 2560, 64, 8), (16, 1536, 80, 10), (4, 16384, 1024, 16)])
+def test_router(T, H, E, k):
+    y = normal(11, T, H)
+    sets = [(normal(12 + i, E, H) / H ** 0.5).bfloat16() for i in range(3)]
+    new = lambda: (torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(T, k, device="cuda"))
+    want = []
+    for w in sets:
+        torch.cuda.synchronize()
+        want.append(new())
+        gd.dec_moe_route(y, w, *want[-1])
+    assert not torch.equal(want[0][1], want[1][1]) and not torch.equal(want[1][1], want[2][1])
+    w, outs = torch.zeros_like(sets[0]), [new() for _ in range(9)]
+
+    def run():
+        for i, out in enumerate(outs):
+            w.copy_(sets[i % 3])
+            gd.dec_moe_route(y, w, *out)
+
+    torch.cuda.synchronize()
+    run()
+    for i, out in enumerate(outs):
+        assert torch.equal(out[0], want[i % 3][0]) and torch.equal(out[1], want[i % 3][1])
+        out[1].zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    g.replay()
+    for i, out in enumerate(outs):
+        assert torch.equal(out[0], want[i % 3][0]) and torch.equal(out[1], want[i % 3][1])
