@@ -168,9 +168,19 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
     __syncwarp();
   }
   const uint32_t mine = lane < a.k ? chosen[lane] : 0u;
-  // renormalised: the largest logit is the first choice's, and the sum over all cancels
-  if (!a.sigmoid && !whole) top = z[chosen[0]];
-  const float p = lane < a.k ? score(z[mine]) : 0.f;
+  const float v = z[mine], most = warp_max(lane < a.k ? v : -INFINITY);
+  float p = 0.f;
+  if (lane < a.k) {
+    // Renormalised, a common factor of the chosen scores cancels: it is taken so that the largest is a half at least (1
+    // for a softmax), however small they are.  For a sigmoid e^-c with c = min(0, the largest logit): e^v / (1 + e^v)
+    // becomes e^(v - c) / (1 + e^v).
+    if (!a.renormalise || !(total == total))  // as it is, or NaN for one among all the logits
+      p = score(v);
+    else if (!a.sigmoid)
+      p = expf(v - most);
+    else
+      p = v >= 0.f ? score(v) : expf(v - fminf(most, 0.f)) / (1.f + expf(v));
+  }
   const float sum = a.renormalise ? warp_sum(p) : 1.f;
   if (lane < a.k) {
     a.ids[static_cast<size_t>(t) * a.k + lane] = static_cast<int>(mine);
