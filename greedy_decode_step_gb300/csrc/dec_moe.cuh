@@ -24,6 +24,7 @@ struct MoeRouteArgs {
   float* gates;                  // [T][k]
   int H, E, k, sigmoid, renormalise;
   float scale;
+  int ahead, bufs;               // pieces in flight and buffers of a warp: set by the launch
 };
 cudaError_t launch_moe_route(const MoeRouteArgs& a, int T, cudaStream_t st);
 cudaError_t allow_smem_moe_route();

@@ -391,6 +391,8 @@ int dec_fp8_gemm(const void* x_codes, const float* x_scales, const void* w_codes
  * softmax over all E (sigmoid == 0) or its sigmoid (sigmoid != 0).  Chosen are
  * the k experts of the largest z, or with a bias (float32 [E], else NULL) of
  * the largest p + bias; equal ones by the lower id, NaN behind every number.
+ * The choice is that of 64 bits: logits are held to 2^-34 H max|Wr[e]| max|y[t]|
+ * or better, p + bias where it decides in doubles.
  * ids: int32 [T][k], best first; weights float32 [T][k]: p, divided by the sum
  * of the chosen ones' p if renormalise != 0, times scale.  y fp32 [T][H]; Wr
  * bf16 [E][H].  T is 0..16, E 1..1024, k 1..16 and at most E, H a multiple of 8
