@@ -1,6 +1,7 @@
 // C-ABI of the 8-bit weight operators and the mixture-of-experts layer:
 // argument checks and launches.  Declarations and contracts are in
 // include/libdec.h.
+#include <algorithm>
 #include <cmath>
 
 #include "dec_fp8.cuh"
@@ -53,6 +54,22 @@ int check_strides(long long sm, long long sr, int bf16) {
   DEC_CHECK(sm >= 0 && sr >= 0 && sm % per == 0 && sr % per == 0, DEC_EINVAL,
             "matrix and row strides must be non-negative multiples of 16 bytes");
   return DEC_OK;
+}
+
+// Whether no two of n x rows rows of K elements, at matrix and row strides sm and sr, have an element in common.
+bool rows_apart(int n, long long sm, int rows, long long sr, int K) {
+  if (n > 1 && sm < K) return false;
+  if (rows > 1 && sr < K) return false;
+  if (n == 1 || rows == 1) return true;
+  // rows whose places differ by i of the larger stride and by j of the other, in opposite directions
+  using Wide = __int128;
+  const bool mats = sm >= sr;
+  const Wide far = mats ? sm : sr, near = mats ? sr : sm, nf = mats ? n : rows, nn = mats ? rows : n;
+  for (Wide i = 1; i < nf && i * far < (nn - 1) * near + K; ++i) {
+    const Wide j = std::min(i * far / near, nn - 1), left = i * far - j * near;
+    if (left < K || (j + 1 < nn && near - left < K)) return false;
+  }
+  return true;
 }
 
 int check_moe(int T, int E, int H) {
@@ -116,8 +133,9 @@ int dec_fp8_dequant(const void* codes, const float* scales, void* out, int bf16,
   DEC_WORDS(scales);
   DEC_PTR(out);
   DEC_TRY(check_strides(stride_mat, stride_row, bf16));
-  DEC_CHECK((n == 1 || stride_mat >= K) && (rows == 1 || stride_row >= K), DEC_EINVAL,
-            "rows read back may not share memory: strides of K = %d at least", K);
+  DEC_CHECK(rows_apart(n, stride_mat, rows, stride_row, K), DEC_EINVAL,
+            "rows read back may not share memory: of %d x %d rows of %d, %lld and %lld apart, some do", n, rows, K,
+            static_cast<long long>(stride_mat), static_cast<long long>(stride_row));
   int sms;
   uint32_t* err;
   DEC_TRY(host_device(&sms, &err));

@@ -365,8 +365,7 @@ int dec_fp8_quant(const void* x, int bf16, int64_t stride_mat, int64_t stride_ro
 /*
  * Reads codes back: out = c * s, rounded once to float32 and for bf16 once
  * more (any float scales; exact in float32 for powers of two of its range).
- * out is strided as x above; its rows may not share memory (strides of K at
- * least).
+ * out is strided as x above; no two of its rows may share memory.
  */
 int dec_fp8_dequant(const void* codes, const float* scales, void* out, int bf16, int64_t stride_mat, int64_t stride_row,
                     int n, int rows, int K, int block_rows, void* stream);
