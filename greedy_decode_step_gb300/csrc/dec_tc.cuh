@@ -62,6 +62,13 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, uint32_t
   return true;
 }
 
+// One thread, after an early end: waits (bounded) until what `asked` stages were asked for, stage i on barrier i % n in
+// its phase i / n, has come.  Earlier phases are over: a stage is asked for anew only then.
+__device__ __forceinline__ void drain_ring(uint64_t* bars, int n, int asked, uint32_t* err) {
+  for (int i = max(0, asked - n); i < asked; ++i)
+    if (!tc_wait(&bars[i % n], (i / n) & 1, err, kErrDrain)) break;
+}
+
 // 8-bit operands (e4m3 A and B), K = 32 per instruction.
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -114,6 +121,13 @@ __device__ __forceinline__ uint32_t in_even(const void* p) {
   uint32_t at;
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(p)));
   return at;
+}
+// A word into the other CTA of a pair, at the address of this one's.
+__device__ __forceinline__ void store_other(const void* p, uint32_t v) {
+  uint32_t at, rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank ^ 1u));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 // What it orders is tensor memory (by the tcgen05 fences around it), so the default scope does; .release.cluster would
 // wait for this SM's global stores, 1000 cycles a block.

@@ -25,8 +25,12 @@
 //   core.  Persistent CTAs, so the store of one tile runs beside the
 //   products of the next.
 //
-// Every wait is bounded (an error bit and an early exit instead of a hang),
-// and tensor memory is released on every path.
+// Every wait on an mbarrier is bounded: an error bit and an early end instead of a
+// hang, in which one thread waits, bounded as well, for the copies and products
+// that are still on their way before shared and tensor memory are given up.
+// Cluster barriers and the allocation of tensor memory have no limit of their own:
+// a cluster's CTAs are resident together, every role comes to its end, and a kernel
+// holds no more tensor memory than leaves room for all CTAs of an SM.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -87,6 +91,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
   uint64_t* drained = accum + kNarrowAccs;     // it has been read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + kNarrowAccs);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);  // a wait ran out: every role ends
+  volatile int* ends = stop + 1;                                        // stages asked for, and multiplied
   float(*scales)[BN] = reinterpret_cast<float(*)[BN]>(smem + kF8Head);  // [2 groups x blocks]
   static_assert(kF8Head + 2 * kNarrowGroup * BN * 4 <= kNarrowHead, "scales");
   unsigned char* tiles = smem + kNarrowHead;
@@ -147,15 +152,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
       }
       __syncwarp();
     }
-    if (!ok && lane == 0) {  // an early end waits for its own copies
-      *stop = 1;
-      for (int i = max(0, it - kStages); i < it; ++i)
-        if (!tc_wait(&full[i % kStages], (i / kStages) & 1, a.err, kErrDrain)) break;
-    }
+    if (!ok) *stop = 1;
+    if (lane == 0) ends[0] = it;
   } else if (warp == 1) {
     constexpr uint32_t idesc = tc_idesc_of(BN, false);
     bool ok = true;
-    for (int i = 0; i < nkb; ++i) {
+    int i = 0;
+    for (; i < nkb; ++i) {
       const int s = i % kStages, b = i % kNarrowAccs;
       ok = warp_wait(&full[s], (i / kStages) & 1, stop, a.err, kErrWaitFull) &&
            (i < kNarrowAccs || warp_wait(&drained[b], ((i / kNarrowAccs) - 1) & 1, stop, a.err, kErrWaitFull));
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
       __syncwarp();
     }
     if (!ok) *stop = 1;
+    if (lane == 0) ends[1] = i;
   } else {
     pdl_wait();
     const int q = warp & 3, t = threadIdx.x - 64;
@@ -265,6 +269,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    if (*stop) {  // after an early end: copies and products that are still on their way
+      if (lane == 0) {
+        drain_ring(full, kStages, ends[0], a.err);
+        drain_ring(empty, kStages, ends[1], a.err);
+      }
+      __syncwarp();
+    }
     tc_fence_after();
     tmem_free(tmem, kCols);
   }
@@ -322,8 +333,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
   uint64_t* drained = done + kWideStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);  // a wait ran out: every role ends
+  volatile int* ends = stop + 1;  // stages that each CTA asked for, and the last that each issuing warp multiplied
   uint64_t* came = reinterpret_cast<uint64_t*>(smem + kF8Head / 2);     // kAdd: a warp's staging rows hold the residual
-  static_assert((2 * kWideMaxStages + 3) * 8 <= kF8Head / 2 && 8 * W::kBufs * 8 <= kF8Head / 2, "barriers");
+  static_assert((2 * kWideMaxStages + 5) * 8 <= kF8Head / 2 && 8 * W::kBufs * 8 <= kF8Head / 2, "barriers");
   unsigned char* tiles = smem + kF8Head;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? blockIdx.x & 1 : 0, first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
@@ -357,6 +369,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
     __syncwarp();
     tc_fence_before();
     if (PAIR) {  // neither CTA leaves while the other may reach into it
+      if (*stop && lane == 0) store_other(const_cast<int*>(stop), 1);
       cluster_arrive();
       cluster_wait();
     }
@@ -400,10 +413,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
           __syncwarp();
         }
       }
-      if (!ok && lane == 0) {  // an early end waits for its own copies (a pair's: those that complete here)
-        *stop = 1;
-        for (int i = max(0, it - kWideStages); i < it; ++i)
-          if (!tc_wait(&full[i % kWideStages], (i / kWideStages) & 1, a.err, kErrDrain)) break;
+      if (!ok) *stop = 1;
+      if (lane == 0) {
+        if (PAIR)
+          store_cta0(const_cast<int*>(ends + rank), it);
+        else
+          ends[0] = it;
       }
     } else if ((warp == 1 || warp == 2) && rank == 0) {
       // every second block each, so that one waits for its next while the other's products are being issued
@@ -411,7 +426,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       const int b = warp - 1;
       const int mine = (a.tiles - first + step - 1) / step;
       bool ok = true;
-      for (int it = b; it < mine * a.KB; it += 2) {
+      int it = b;
+      for (; it < mine * a.KB; it += 2) {
         const int s = it % kWideStages;
         // The accumulator first: once block it - 2 has been read, every block before it, the one that held this stage
         // among them, is done.  Of an odd number of stages a warp sees every second phase only, and asked too early
@@ -438,8 +454,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
         __syncwarp();
       }
       if (!ok) *stop = 1;
+      if (lane == 0) ends[2 + b] = it - 2;  // below 0: none
     }
     leave();
+    if (*stop) {  // after an early end of either CTA: copies and products that are still on their way
+      if (warp == 1 && lane == 0 && rank == 0) {
+        drain_ring(full, kWideStages, PAIR ? max(ends[0], ends[1]) : ends[0], a.err);
+        for (int b = 0; b < 2; ++b)
+          if (ends[2 + b] >= 0) tc_wait(&done[ends[2 + b] % kWideStages], (ends[2 + b] / kWideStages) & 1, a.err, kErrDrain);
+      }
+      __syncwarp();
+      if (PAIR) cluster_arrive();
+      if (PAIR) cluster_wait();
+    }
     if (warp == 1) {
       tc_fence_after();
       if (PAIR)
@@ -630,6 +657,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
         if (coming >> buf & 1) tc_wait(&came[buf], phases >> buf & 1, a.err, kErrDrain);
     if (OUT != kRows || a.bulk) tma_store_wait_read<0>();  // its memory is in use until then
     leave();
+    if (PAIR && *stop) {  // as above
+      cluster_arrive();
+      cluster_wait();
+    }
   }
 }
 
