@@ -44,8 +44,11 @@
 // 16 tokens, three times the launch that spreads it.)  The first weights are on
 // their way while gate/up still runs.
 //
-// Every wait is bounded (an error bit and an early exit instead of a hang),
-// and tensor memory is released on every path.
+// Every wait on an mbarrier is bounded: an error bit and an early end instead of a
+// hang, in which one thread waits, bounded as well, for the copies and products
+// that are still on their way before shared and tensor memory are given up.  (The
+// allocation of tensor memory has no limit of its own: CTAs hold no more than leaves
+// room for all of an SM.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -450,6 +453,7 @@ struct Cta {
   uint64_t *fullA, *emptyA, *fullB, *emptyB, *accum, *drained;
   uint32_t* tmem_slot;
   volatile int* stop;  // a wait ran out: every role ends
+  volatile int* ends;  // chunks whose weights' halves and activations were asked for, and that were multiplied
   Plan* plan;
   float* total;        // [NT][128] sums of the down launch
   unsigned char *A, *B;
@@ -475,7 +479,8 @@ struct Cta {
     drained = accum + kAccs;
     tmem_slot = reinterpret_cast<uint32_t*>(drained + kAccs);
     stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kMoeMaxStages + 2 * kMoeTurns + 2 * kAccs) * 8 + 8 <= kHead, "barriers");
+    ends = stop + 1;
+    static_assert((2 * kMoeMaxStages + 2 * kMoeTurns + 2 * kAccs) * 8 + 24 <= kHead, "barriers");
     A = smem + kHead;
     B = A + kStages * kMoeATile;
     plan = reinterpret_cast<Plan*>(B + kSlots * kSlot);
@@ -494,6 +499,7 @@ struct Cta {
         mbar_init(&drained[s], 4);
       }
       *stop = 0;
+      for (int i = 0; i < 4; ++i) ends[i] = 0;
       fence_mbar_init();
     }
     if (threadIdx.x / 32 == 1) tmem_alloc(tmem_slot, kCols);
@@ -527,11 +533,21 @@ struct Cta {
     __syncwarp();
     if (threadIdx.x % 32 == 0) mbar_arrive(&fullB[it % kMoeTurns]);
   }
-  __device__ __forceinline__ void end() {
+  __device__ __forceinline__ void end(uint32_t* err) {
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x / 32 == 1) {
+      if (*stop) {  // after an early end: copies and products that are still on their way
+        if (threadIdx.x % 32 == 0) {
+          // a chunk with one half asked for: the other's arrival is made good, so that its phase ends with that half
+          for (int i = min(ends[0], ends[1]); i < max(ends[0], ends[1]); ++i) mbar_arrive(&fullA[i % kStages]);
+          drain_ring(fullA, kStages, max(ends[0], ends[1]), err);
+          if (!kOwn) drain_ring(fullB, kMoeTurns, ends[2], err);
+          drain_ring(emptyA, kStages, ends[3], err);
+        }
+        __syncwarp();
+      }
       tc_fence_after();
       tmem_free(tmem, kCols);
     }
@@ -637,12 +653,6 @@ struct Cta {
     }
     return true;
   }
-  // One lane, at the end of a copying role: an early end waits for the copies that are on their way.
-  __device__ __forceinline__ void drain(uint64_t* bars, int n, int from, int to, uint32_t* err) const {
-    if (*stop)
-      for (int i = max(0, from); i < to; ++i)
-        if (!tc_wait(&bars[i % n], (i / n) & 1, err, kErrDrain)) break;
-  }
 };
 
 // ----------------------------------------------------------------------------- gate/up
@@ -678,7 +688,7 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_gate_up_kernel(c
       }
       pos += n;
     }
-    if (half == 0 && lane == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
+    if (lane == 0) c.ends[half] = it;
   } else if (c.kOwn && warp >= 7) {
     const int mine = warp - 7;
     for (int it = mine, pos = lo + mine; pos < hi; it += kMoeOwnWarps, pos += kMoeOwnWarps) {
@@ -719,7 +729,7 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_gate_up_kernel(c
       }
       pos += n;
     }
-    if (lane == 0) c.drain(c.fullB, kMoeTurns, it - kMoeTurns, it, a.err);
+    if (lane == 0) c.ends[2] = it;
   } else if (warp == 1) {
     Slots ring;
     int it = 0, used;
@@ -729,6 +739,7 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_gate_up_kernel(c
       for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, ring.take(count, &used), a.err);
       pos += n;
     }
+    if (lane == 0) c.ends[3] = it - !ok;
   } else {
     const int m = (32 * warp + lane) & 127;  // TMEM lane; row of the tile: gate below 64, up from 64 on
     const int IB = (a.I + kFp8Block - 1) / kFp8Block;
@@ -765,7 +776,7 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_gate_up_kernel(c
       pos += n;
     }
   }
-  c.end();
+  c.end(a.err);
 }
 
 // ----------------------------------------------------------------------------- down
@@ -800,7 +811,7 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_down_kernel(cons
         ++act;
       }
     }
-    if (half == 0 && lane == 0) c.drain(c.fullA, c.kStages, it - c.kStages, it, a.err);
+    if (lane == 0) c.ends[half] = it;
   } else if (c.kOwn && warp >= 7) {
     const Runs r(p.active, a, P::kChunk);
     const int mine = warp - 7;
@@ -850,7 +861,7 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_down_kernel(cons
       }
       pos += n;
     }
-    if (lane == 0) c.drain(c.fullB, kMoeTurns, it - kMoeTurns, it, a.err);
+    if (lane == 0) c.ends[2] = it;
   } else if (warp == 1) {
     Slots ring;
     int it = 0, used;
@@ -860,6 +871,7 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_down_kernel(cons
       for (int j = 0; j < n && ok; ++j, ++it) ok = c.multiply(it, count, ring.take(count, &used), a.err);
       pos += n;
     }
+    if (lane == 0) c.ends[3] = it - !ok;
   } else {
     const int m = (32 * warp + lane) & 127, HB = (a.H + kFp8Block - 1) / kFp8Block;
 #pragma unroll
@@ -899,7 +911,7 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_down_kernel(cons
   const int n4 = a.T * 32;
   float4* mine = reinterpret_cast<float4*>(a.sums) + (static_cast<size_t>(tile) * a.splits + split) * n4;
   for (int i = threadIdx.x; i < n4; i += c.kThreads) mine[i] = reinterpret_cast<const float4*>(c.total)[i];
-  c.end();
+  c.end(a.err);
 }
 
 // ----------------------------------------------------------------------------- host side
