@@ -666,33 +666,37 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
 
 // ----------------------------------------------------------------------------- host side
 
-// Clusters of `size` CTAs that run at once, cached.  The occupancy query counts
-// one CTA per SM wherever tensor memory is used; two fit here.
+// Clusters of `size` CTAs that run at once on the current device, 0 if the
+// query fails; what it answered is kept per device.  It counts one CTA per SM
+// wherever tensor memory is used; two fit here.
 template <int BN>
 int narrow_clusters(int size) {
+  constexpr int kDevices = 64;
   static std::mutex mu;
-  static int cache[kNarrowMaxSplits + 1] = {};
+  static int cache[kDevices][kNarrowMaxSplits + 1] = {};
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool keep = dev >= 0 && dev < kDevices;
   std::lock_guard<std::mutex> lock(mu);
-  if (cache[size] == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(size * 64);
-    cfg.blockDim = dim3(kNarrowThreads);
-    cfg.dynamicSmemBytes = narrow_smem<BN>();
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<BN>, &cfg) != cudaSuccess || n == 0) {
-      (void)cudaGetLastError();
-      n = -1;
-    }
-    cache[size] = 2 * n;
+  if (keep && cache[dev][size] != 0) return cache[dev][size];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size * 64);
+  cfg.blockDim = dim3(kNarrowThreads);
+  cfg.dynamicSmemBytes = narrow_smem<BN>();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fp8_narrow_kernel<BN>, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
   }
-  return cache[size];
+  if (keep) cache[dev][size] = 2 * n;
+  return 2 * n;
 }
 
 // K splits: double while every split keeps two blocks and all clusters run at
