@@ -58,7 +58,7 @@ template <bool BF16>
 struct Vec {  // 16 bytes of a source row, as they came
   static constexpr int kN = BF16 ? 8 : 4;
   uint4 w;
-  __device__ __forceinline__ void load(const void* p) { w = __ldg(static_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const void* p) { w = *static_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ float value(int i) const {
     const uint32_t u = BF16 ? (i / 2 == 0 ? w.x : i / 2 == 1 ? w.y : i / 2 == 2 ? w.z : w.w)
@@ -261,9 +261,9 @@ __global__ void __launch_bounds__(kQuantThreads) dequant_kernel(const Fp8Dequant
       dst[u] = nullptr;
       if (i >= total) continue;
       const uint8_t* src = a.codes + (static_cast<long long>(s.mat) * a.rows + r) * a.K + k;
-      w[u] = BF16 ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(__ldg(reinterpret_cast<const uint32_t*>(src)), 0u);
+      w[u] = BF16 ? *reinterpret_cast<const uint2*>(src) : make_uint2(*reinterpret_cast<const uint32_t*>(src), 0u);
       const uint32_t rb = a.block_rows == 1 ? row : row / kFp8Block;
-      scale[u] = __ldg(a.scales + (static_cast<long long>(mat) * RB + rb) * KB + k / kFp8Block);
+      scale[u] = a.scales[(static_cast<long long>(mat) * RB + rb) * KB + k / kFp8Block];
       dst[u] = static_cast<char*>(a.out) + (mat * a.sm + row * a.sr + k) * (BF16 ? 2 : 4);
     }
 #pragma unroll

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) fp8_narrow_kernel(const __g
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
         const int i = first + (t + 128 * e) / BN, r = r0 + t % BN;
-        next[e] = i < nkb && r < a.M ? __ldg(a.sx + static_cast<long long>(r) * a.KB + kb0 + i) * __ldg(sw + i) : 0.f;
+        next[e] = i < nkb && r < a.M ? a.sx[static_cast<long long>(r) * a.KB + kb0 + i] * sw[i] : 0.f;
       }
     };
     fetch(0);
@@ -512,8 +512,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
       sw = a.sw + static_cast<long long>(min(nb, a.NB - 1)) * a.KB;
       sv = a.sw + static_cast<long long>(min(nb + 1, a.NB - 1)) * a.KB;
       const int one = a.KB > 1;
-      x0 = __ldg(sx), w0 = __ldg(sw), v0 = BN == 192 ? __ldg(sv) : 0.f;
-      x1 = __ldg(sx + one), w1 = __ldg(sw + one), v1 = BN == 192 ? __ldg(sv + one) : 0.f;
+      x0 = *sx, w0 = *sw, v0 = BN == 192 ? *sv : 0.f;
+      x1 = sx[one], w1 = sw[one], v1 = BN == 192 ? sv[one] : 0.f;
     };
     pdl_wait();  // the rows' scales and the residual
     open(first);
@@ -541,9 +541,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) fp8_wide_kernel(const __grid_
         w0 = w1;
         v0 = v1;
         if (kb + 2 < a.KB) {
-          x1 = __ldg(sx + kb + 2);
-          w1 = __ldg(sw + kb + 2);
-          if (BN == 192) v1 = __ldg(sv + kb + 2);
+          x1 = sx[kb + 2];
+          w1 = sw[kb + 2];
+          if (BN == 192) v1 = sv[kb + 2];
         }
         ok = warp_wait(&done[it % kWideStages], (it / kWideStages) & 1, stop, a.err, kErrWaitFull);
         if (!ok) break;

@@ -756,11 +756,11 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_gate_up_kernel(c
       float next = 1.f;
       if (F8) {
         sw = (m < kMoeUnit ? a.sg : a.su) + (static_cast<size_t>(p.expert[act]) * IB + ub * kMoeUnit / kFp8Block) * r.kch;
-        next = __ldg(sw + j0);
+        next = sw[j0];
       }
       for (int j = j0; j < j0 + n && ok; ++j, ++it) {
         const float w = next;
-        if (F8 && j + 1 < j0 + n) next = __ldg(sw + j + 1);
+        if (F8 && j + 1 < j0 + n) next = sw[j + 1];
         ok = c.add(it, count, ring.take(count, &used), w, sum, a.err);
       }
       if (!ok) break;
@@ -888,11 +888,11 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_down_kernel(cons
       float next = 1.f;
       if (F8) {
         sw = a.sd + (static_cast<size_t>(p.expert[act]) * HB + m0 / kFp8Block) * kch;
-        next = __ldg(sw + j0);
+        next = sw[j0];
       }
       for (int j = j0; j < j0 + n && ok; ++j, ++it) {
         const float w = next;
-        if (F8 && j + 1 < j0 + n) next = __ldg(sw + j + 1);
+        if (F8 && j + 1 < j0 + n) next = sw[j + 1];
         ok = c.add(it, count, ring.take(count, &used), w, sum, a.err);
       }
       // this thread's column of its tokens' sums

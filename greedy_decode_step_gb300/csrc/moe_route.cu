@@ -141,7 +141,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
   ahead = now;
   uint32_t largest = 0;  // bits of the largest |y|
   for (int i = threadIdx.x; i < a.H / 4; i += kRouteThreads) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(a.y + static_cast<size_t>(t) * a.H) + i);
+    const float4 v = *(reinterpret_cast<const float4*>(a.y + static_cast<size_t>(t) * a.H) + i);
     y[(i / 64) * 64 + (i & 1) * 32 + (i / 2) % 32] = v;
     const uint32_t k = 0x7FFFFFFFu;
     largest = max(largest, max(max(__float_as_uint(v.x) & k, __float_as_uint(v.y) & k),
