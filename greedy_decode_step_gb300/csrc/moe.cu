@@ -820,7 +820,8 @@ __global__ void __launch_bounds__(Cta<F8, NT>::kThreads, 2) moe_down_kernel(cons
       const int act = min(lo + it, all - 1) / kch, j = lo + it - act * kch;
       return Inner<F8>(a, r, act, p.first[act], 0, j);
     };
-    Inner<F8> at = place(hi > lo ? mine : 0);
+    // without a chunk (with no expert at all there is none) there is no place: j behind the last
+    Inner<F8> at = hi > lo ? place(mine) : Inner<F8>(a, r, 0, 0, 0, kch);
     pdl_wait();  // gate and up products
     for (int it = mine; it < hi - lo; it += kMoeOwnWarps) {
       const int act = (lo + it) / kch, count = p.count[act];

@@ -99,3 +99,18 @@ def test_weights_behind_2_to_the_31(fp8):
             held[i][e] = (0.02 * normal(91 + i + 3 * e, *held[i].shape[1:])).to(dt)
     y, w = normal(95, T, H), torch.rand(T, k, generator=rng(96), device="cuda")
     check(y, ids, w, held, scales, list(zip(held, scales)) if fp8 else held)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 2, 3, 16])
+@pytest.mark.parametrize("I", [16, 64, 320])
+def test_no_expert_at_all(T, I, fp8):
+    """Inner vectors of less than one chunk, one and several, and nothing to compute of them."""
+    H, E, k = 272, 5, 3
+    y, res = normal(60, T, H), normal(61, T, H)
+    held, scales, plain = make_weights(62, E, H, I, fp8)
+    ids, w = torch.full((T, k), -1, dtype=torch.int32, device="cuda"), torch.rand(T, k, device="cuda")
+    assert torch.equal(check(y, ids, w, held, scales, plain, res), res)
+    assert not check(y, ids, w, held, scales, plain).any()
+    ids[T - 1, 1] = 4  # and one expert of one token
+    check(y, ids, w, held, scales, plain)
