@@ -375,8 +375,8 @@ int dec_fp8_dequant(const void* codes, const float* scales, void* out, int bf16,
  * (blocks of 128 x 128), any float scales:
  *   out[m][n] = residual[m][n] + sum_j sx[m][j] sw[n / 128][j] sum_{k in block j} cx[m][k] cw[n][k]
  * Products of codes are exact; a block's sum is held in fp32, as are the sums
- * over blocks and the product of two scales (below 2^-126 it loses bits).  out
- * and residual: float32, rows of N contiguous values that begin stride_out and
+ * over blocks and the product of two scales (below 2^-126 it loses bits, from
+ * 2^128 on it leaves no finite results).  out and residual: float32, rows of N contiguous values that begin stride_out and
  * stride_residual elements apart (stride_out >= N); residual may be NULL, or out
  * itself with its stride; other overlaps are not allowed.  M is 0..2^24.
  * Results are reproducible bit for bit.
@@ -414,8 +414,9 @@ size_t dec_moe_workspace_size(int T, int k, int H, int I);
  * Wd [E][ceil(H/128)][ceil(I/128)], H and I multiples of 16.  Activations keep
  * float32 accuracy: an element of y (up to 2^127) is held to 2^-24 of itself or
  * 2^-133, whichever is more (8-bit weights: to 2^-23 of the largest of its 128),
- * and so is one of the MLP's inner vector.  Each chosen expert's
- * weights are read once.  A NaN or an infinity in an expert reaches the tokens
+ * and so is one of the MLP's inner vector.  What a block's scale and 1/224 of the
+ * largest of 128 activations come to is held in fp32, as with dec_fp8_gemm.
+ * Each chosen expert's weights are read once.  A NaN or an infinity in an expert reaches the tokens
  * that chose it (as NaN, it may be), one in y its own token.  y, residual and out
  * fp32 [T][H]; residual may be NULL or out, and out may be y.  T is 0..16, k
  * 1..16, E 1..1024, H and I up to 32768.  ws: device workspace of
