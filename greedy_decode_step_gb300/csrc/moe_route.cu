@@ -10,23 +10,24 @@
 // Logits are pairs of floats: a sum that starts at 1.5 2^m, m from the largest
 // weight and value, takes whole steps of 2^(m - 23), and what each product
 // leaves goes to a sum of its own (four operations a product in place of one).
-// With W and Y the largest magnitudes, what 32 products leave is 2^-10 W Y at
-// most, off by 2^-29 W Y, so a logit is by 2^-34 H W Y (in random rows of 256 to 4096 by
-// a thousandth of that, 2^-35 to 2^-38 of a logit).  Scores with a bias are compared
-// in float32 first, and in doubles where two lie too close for it: there are two
-// double operations a clock and SM.
+// With W and Y the largest magnitudes, what the up to 40 products of such a sum leave is
+// 2^-15 W Y each, added up in float32, so that a logit is off by 2^-34 H W Y at most (in
+// random rows of 256 to 4096 by a thousandth of that, 2^-35 to 2^-38 of a logit).  Scores
+// with a bias are compared in float32 first, and in doubles where two lie too close for
+// it: there are two double operations a clock and SM.
 //
 // A cluster of 8 CTAs per token, so that one launch serves: each CTA takes an
 // eighth of the experts, a warp for one after the other with the token's row in
-// shared memory, and puts the logits into CTA 0, which chooses.  The sums of different
-// experts run in one order, so equal rows of Wr give equal logits.  Bound by
-// latency, from 128 experts on by the instructions of the sums (76 for 8 products of a
-// warp, 2 a cycle and SM): one token of 2560, 64 experts 4.7 us, 16 tokens and 128
-// experts 8.3 (3.4 and 7.2 with float32 sums and weights fetched ahead of the wait).  The first weights are on their way to
-// L2 before the wait for the launch that makes y; the loops are short, as unrolled over
-// a row they wait for their instructions (16 tokens, 1024 experts of 4096: 162 us, 87);
-// up to 256 experts are ranked at once, by counting the better ones of each (64 experts:
-// 1200 cycles where eight rounds of a warp's maximum took 3000).
+// shared memory, and puts the logits into CTA 0, which chooses.  The sums of
+// different experts run in one order, so equal rows of Wr give equal logits.
+// Bound by latency, from 128 experts on by the instructions of the sums (76 for 8
+// products of a warp, 2 a cycle and SM): one token of 2560, 64 experts 4.7 us, 16
+// tokens and 128 experts 8.3 (3.4 and 7.2 with float32 sums and weights fetched
+// ahead of the wait).  The first weights are on their way to L2 before the wait for
+// the launch that makes y; the loops are short, as unrolled over a row they wait for
+// their instructions (16 tokens, 1024 experts of 4096: 162 us, 87); up to 256
+// experts are ranked at once, by counting the better ones of each (64 experts: 1200
+// cycles where eight rounds of a warp's maximum took 3000).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -168,7 +169,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
     for (int h = now.h + 8 * lane; h < h1; h += 256, w += 32) most = top_pairs(most, *w);
     w = first;
     most = max(most >> 16, most & 0xFFFFu);
-    // a sum of 32 products is below 2^(we + ye - 247), and 2^m four times that
+    // a product is below 2^(we + ye - 252), a sum of 40 of them below 40 / 128 of 2^m
     const int we = static_cast<int>(most >> 7), m = we + ye - 118;  // exponents with their bias of 127
     const bool plain = __any_sync(0xffffffffu, we == 255 || ye == 255 || m > 253);
     const float from = plain ? 0.f : __uint_as_float((static_cast<uint32_t>(max(m, 27)) << 23) | 0x400000u);
