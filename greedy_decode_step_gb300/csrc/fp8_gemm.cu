@@ -52,7 +52,7 @@ constexpr uint32_t kF8Tile = kF8BM * kF8BK;   // 16 KB: 128 rows of a stage
 constexpr uint32_t kF8Head = 1024;            // barriers
 constexpr int kNarrowGroup = 8;               // blocks whose scales are fetched together
 constexpr int kNarrowAccs = 4;                // accumulators in turn
-constexpr uint32_t kNarrowHead = 3072;        // barriers, and two groups' scales per row of x
+constexpr uint32_t kNarrowHead = kF8Head + 2 * kNarrowGroup * 32 * 4;  // barriers, and two groups' scales per row of x
 
 // ----------------------------------------------------------------------------- narrow: weight rows on the lanes
 
